@@ -23,6 +23,7 @@ LHS_ERRBIT_BAD_TOKEN = 1
 LHS_ERRBIT_MALFORMED = 2
 LHS_ERRBIT_NONFINITE = 4
 LHS_ERRBIT_TIMEOUT = 8
+LHS_ERRBIT_BAD_PARAM = 16
 LHS_F32, LHS_F16, LHS_BF16, LHS_Q8_0, LHS_FP8_E4M3 = 0, 1, 2, 3, 4
 LHS_WIRE_F32, LHS_WIRE_F16, LHS_WIRE_I8 = 0, 1, 2
 LHS_NOALLOC_SCRATCH_BYTES = 4 * 1024 * 1024
@@ -38,6 +39,8 @@ ABI_SYMBOLS = (
     "lhs_logits_topk_launches", "lhs_logits_topk", "lhs_logits", "lhs_logits_topk_noalloc", "lhs_wire_bytes",
     "lhs_wire_encode",
     "lhs_wire_decode", "lhs_wire_response_bytes", "lhs_wire_encode_response", "lhs_wire_decode_response",
+    "lhs_i8_init", "lhs_i8_message", "lhs_i8_quantize", "lhs_i8_workspace", "lhs_i8_matmul", "lhs_i8_logits",
+    "lhs_sample",
     "lhs_selftest_bounded_wait", "lhs_strerror",
     "lhs_last_cuda_error", "lhs_version",
 )
@@ -58,6 +61,12 @@ class lhs_table(ctypes.Structure):
                 ("row_bytes", ctypes.c_int64)]
 
 
+class lhs_i8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
+                ("hidden", ctypes.c_int32), ("header", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -72,7 +81,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     P, i32, i64, u32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                             ctypes.c_uint32, ctypes.c_size_t)
-    T = ctypes.POINTER(lhs_table)
+    T, Q = ctypes.POINTER(lhs_table), ctypes.POINTER(lhs_i8)
     sig = {
         "lhs_table_init": (ctypes.c_int, [T, P, i64, i32, i32]),
         "lhs_table_info": (ctypes.c_int, [T, P, P, P, P]),
@@ -101,6 +110,13 @@ def lib() -> ctypes.CDLL:
         "lhs_wire_encode_response": (ctypes.c_int, [i32, P, i32, i32, i32, u32, ctypes.c_float, P, sz,
                                                     P, P]),
         "lhs_wire_decode_response": (ctypes.c_int, [i32, P, sz, i32, i32, P, P, P]),
+        "lhs_i8_init": (ctypes.c_int, [Q, P, i64, P, i64, i64, i32]),
+        "lhs_i8_message": (ctypes.c_int, [Q, P, sz, i32, i32, i32]),
+        "lhs_i8_quantize": (ctypes.c_int, [Q, P, i32, i64, P, P]),
+        "lhs_i8_workspace": (ctypes.c_int, [Q, i64, P]),
+        "lhs_i8_matmul": (ctypes.c_int, [Q, Q, P, i32, i64, P, sz, P, P]),
+        "lhs_i8_logits": (ctypes.c_int, [Q, P, i32, i64, i64, P, i32, i64, P, sz, P, P]),
+        "lhs_sample": (ctypes.c_int, [P, i32, i64, i64, i64, P, P, P, P, P, P, P, P, P]),
         "lhs_selftest_bounded_wait": (ctypes.c_int, [P, i64, P]),
         "lhs_strerror": (ctypes.c_char_p, [ctypes.c_int]),
         "lhs_last_cuda_error": (ctypes.c_int, []),
@@ -455,6 +471,178 @@ def lhs_wire_decode_response(fmt: int, buf: torch.Tensor, seq_len: int, hidden: 
                                           _dev(out, "x") if seq_len else None, _dev(err, "err"),
                                           _stream(stream)), "lhs_wire_decode_response")
     return out, err
+
+
+_WIDE = {torch.float32: LHS_F32, torch.float16: LHS_F16, torch.bfloat16: LHS_BF16}
+
+
+def _wide_rows(t: torch.Tensor, name: str):
+    """(address, dtype code, row stride in elements) of a 2-D CUDA tensor of
+    f32, f16 or bf16 whose rows are contiguous; rows may lie any distance
+    apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _WIDE:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be two-dimensional with contiguous rows")
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), _WIDE[t.dtype], stride
+
+
+class I8Rows:
+    """Rows of int8 codes with one scale each (``lhs_i8``).  Keeps the tensors
+    alive for as long as the descriptor is used."""
+
+    def __init__(self, c: lhs_i8, *tensors: torch.Tensor):
+        self.c = c
+        self.tensors = tensors
+
+    @property
+    def rows(self):
+        return self.c.rows
+
+    @property
+    def hidden(self):
+        return self.c.hidden
+
+    @property
+    def codes(self):
+        """The codes [rows, hidden] (int8 view; plain rows only)."""
+        return self.tensors[0][:, :self.hidden]
+
+    @property
+    def scales(self):
+        """The scales [rows] (plain rows only)."""
+        return self.tensors[1]
+
+    @property
+    def device(self):
+        return self.tensors[0].device
+
+
+def lhs_i8_init(codes: torch.Tensor, scales: torch.Tensor, hidden: int) -> I8Rows:
+    """Rows over ``codes`` (int8 [rows, >= hidden], contiguous rows any
+    distance apart) and ``scales`` (f32 [rows])."""
+    if not codes.is_cuda or not scales.is_cuda:
+        raise ValueError("codes and scales must be CUDA tensors")
+    if codes.dtype != torch.int8 or scales.dtype != torch.float32:
+        raise ValueError("codes must be int8 and scales float32")
+    if codes.dim() != 2 or (codes.shape[1] > 1 and codes.stride(1) != 1) or codes.shape[1] < hidden:
+        raise ValueError("codes must be two-dimensional with contiguous rows of at least hidden codes")
+    rows = codes.shape[0]
+    if scales.dim() != 1 or scales.shape[0] != rows:
+        raise ValueError("one scale for each row")
+    c = lhs_i8()
+    _check(lib().lhs_i8_init(ctypes.byref(c), codes.data_ptr(),
+                             codes.stride(0) if rows > 1 else codes.shape[1], scales.data_ptr(),
+                             4 * (scales.stride(0) if rows > 1 else 1), rows, hidden), "lhs_i8_init")
+    return I8Rows(c, codes, scales)
+
+
+def lhs_i8_message(buf: torch.Tensor, seq_len: int, hidden: int, response: bool = False) -> I8Rows:
+    """The positions of an i8 request (or single-layer response) message, as
+    rows for :func:`lhs_i8_matmul`; nothing is copied."""
+    c = lhs_i8()
+    _check(lib().lhs_i8_message(ctypes.byref(c), _dev(buf, "buf"), buf.numel() * buf.element_size(),
+                                12 if response else 16, seq_len, hidden), "lhs_i8_message")
+    return I8Rows(c, buf)
+
+
+def lhs_i8_quantize(x: torch.Tensor, codes=None, scales=None, err=None, stream=None):
+    """Quantise rows of ``x`` (f32, f16 or bf16 [rows, hidden]) to int8 with one
+    scale each.  Without ``codes`` the rows lie on 16-byte boundaries, as a
+    table's must.  Returns (I8Rows, err word)."""
+    p, dt, stride = _wide_rows(x, "x")
+    n, h = x.shape
+    if codes is None:
+        codes = torch.zeros((n, (h + 15) // 16 * 16), dtype=torch.int8, device=x.device)
+    if scales is None:
+        scales = torch.empty(n, dtype=torch.float32, device=x.device)
+    err = _err_word(err, x.device)
+    t = lhs_i8_init(codes, scales, h)
+    if t.rows != n:
+        raise ValueError("codes must have one row for each row of x")
+    _check(lib().lhs_i8_quantize(ctypes.byref(t.c), p, dt, stride, _dev(err, "err"), _stream(stream)),
+           "lhs_i8_quantize")
+    return t, err
+
+
+def lhs_i8_workspace(table: I8Rows, tokens: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().lhs_i8_workspace(ctypes.byref(table.c), tokens, ctypes.byref(b)), "lhs_i8_workspace")
+    return b.value
+
+
+def _i8_out(table: I8Rows, tokens: int, out_dtype, out, ws):
+    if out is None:
+        out = torch.empty((tokens, table.rows), dtype=out_dtype or torch.float32, device=table.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out is not of out_dtype")
+    if tuple(out.shape) != (tokens, table.rows):
+        raise ValueError("out must be [tokens, table rows]")
+    if ws is None:
+        ws = torch.empty(max(256, lhs_i8_workspace(table, tokens)), dtype=torch.uint8, device=table.device)
+    return out, ws
+
+
+def lhs_i8_matmul(a: I8Rows, table: I8Rows, out_dtype=None, out=None, ws=None, err=None, stream=None):
+    """Logits [a.rows, table.rows] of coded tokens against an i8 table, in
+    ``out_dtype`` (float32 by default, float16 or bfloat16).  Returns (out,
+    err word)."""
+    out, ws = _i8_out(table, a.rows, out_dtype, out, ws)
+    err = _err_word(err, table.device)
+    p, dt, stride = _wide_rows(out, "out")
+    _check(lib().lhs_i8_matmul(ctypes.byref(a.c), ctypes.byref(table.c), p, dt, stride, _dev(ws, "ws"),
+                               ws.numel() * ws.element_size(), _dev(err, "err"), _stream(stream)),
+           "lhs_i8_matmul")
+    return out, err
+
+
+def lhs_i8_logits(table: I8Rows, x: torch.Tensor, out_dtype=None, out=None, ws=None, err=None, stream=None):
+    """Logits of wide residuals ``x`` (f32, f16 or bf16 [tokens, hidden]),
+    quantised per token on the way.  Returns (out, err word)."""
+    xp, xdt, xstride = _wide_rows(x, "x")
+    if x.shape[1] != table.hidden:
+        raise ValueError("x and the table differ in hidden")
+    out, ws = _i8_out(table, x.shape[0], out_dtype, out, ws)
+    err = _err_word(err, table.device)
+    p, dt, stride = _wide_rows(out, "out")
+    _check(lib().lhs_i8_logits(ctypes.byref(table.c), xp, xdt, xstride, x.shape[0], p, dt, stride,
+                               _dev(ws, "ws"), ws.numel() * ws.element_size(), _dev(err, "err"),
+                               _stream(stream)), "lhs_i8_logits")
+    return out, err
+
+
+def _per_row(t, n: int, dtype, name: str):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n:
+        raise ValueError(f"{name} must be {dtype} with one entry for each row")
+    return _dev(t, name)
+
+
+def lhs_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None,
+               ids=None, probs=None, want_probs: bool = True, err=None, stream=None):
+    """One token per row of ``logits`` (f32, f16 or bf16 [rows, vocab]), drawn
+    with the random numbers ``u`` (f32 [rows], in [0, 1)).  temperature, top_p
+    and min_p are f32 [rows], top_k is int32 [rows]; None turns a filter off.
+    Returns (ids, probs|None, err word)."""
+    p, dt, stride = _wide_rows(logits, "logits")
+    n, v = logits.shape
+    dev = logits.device
+    ids = torch.empty(n, dtype=torch.int32, device=dev) if ids is None else ids
+    if want_probs and probs is None:
+        probs = torch.empty(n, dtype=torch.float32, device=dev)
+    err = _err_word(err, dev)
+    f = torch.float32
+    _check(lib().lhs_sample(p, dt, stride, n, v, _per_row(u, n, f, "u"),
+                            _per_row(temperature, n, f, "temperature"),
+                            _per_row(top_k, n, torch.int32, "top_k"), _per_row(top_p, n, f, "top_p"),
+                            _per_row(min_p, n, f, "min_p"), _per_row(ids, n, torch.int32, "ids"),
+                            _per_row(probs, n, f, "probs") if want_probs else None, _dev(err, "err"),
+                            _stream(stream)), "lhs_sample")
+    return ids, (probs if want_probs else None), err
 
 
 def lhs_selftest_bounded_wait(timeout_ns: int, err=None, device=None, stream=None):

@@ -58,6 +58,8 @@ extern "C" {
 #define LHS_ERRBIT_NONFINITE 4  /* i8 encode of a non-finite value; f16-table
                                    lm_head residual outside the f16 range */
 #define LHS_ERRBIT_TIMEOUT 8    /* a bounded on-device wait gave up */
+#define LHS_ERRBIT_BAD_PARAM 16 /* lhs_sample: a row's parameter or random number
+                                   is outside its range */
 
 /* ---- table element types and wire formats ------------------------------ */
 typedef enum {
@@ -327,6 +329,117 @@ LHS_API int lhs_wire_encode_response(int32_t fmt, const void *d_x, int32_t x_dty
 LHS_API int lhs_wire_decode_response(int32_t fmt, const void *d_buf, size_t buf_bytes,
                                      int32_t seq_len, int32_t hidden, float *d_x,
                                      int32_t *d_err, void *stream);
+
+/* ---- rows in 8 bits: an i8 table, and products with it ------------------ */
+
+/* Rows of int8 codes with one f32 scale each; row r stands for the values
+ * code[r][j] * scale[r].  It describes a table quantised per channel (one
+ * vocabulary row = one channel), tokens quantised one by one, or the
+ * positions of an i8 residual message where they lie. */
+typedef struct {
+    const int8_t *codes;  /* device; row r at codes + r*stride */
+    const float *scales;  /* device, 4-byte aligned; row r's scale lies
+                             r*scale_stride bytes further on */
+    int64_t rows;         /* 0 <= rows <= 2^31-1 */
+    int64_t stride;       /* bytes between rows, >= hidden */
+    int64_t scale_stride; /* bytes between scales, a multiple of 4, >= 4 */
+    int32_t hidden;       /* codes per row; 1 <= hidden <= 2^24 */
+    int32_t header;       /* 0: plain rows; 16 / 12: positions of a request /
+                             response message behind a header of that size */
+} lhs_i8;
+
+/* Fill *t after checking the arguments.  Does not touch device memory. */
+LHS_API int lhs_i8_init(lhs_i8 *t, const int8_t *d_codes, int64_t stride, const float *d_scales,
+                        int64_t scale_stride, int64_t rows, int32_t hidden);
+
+/* *t = the positions of an i8 request message (header 16) or single-layer
+ * response message (header 12) of seq_len positions in d_buf, 4-byte
+ * aligned; hidden % 4 == 0 (so that every scale is 4-byte aligned).  Nothing
+ * is copied: the product reads the message itself, and checks it there (see
+ * lhs_i8_matmul).  Errors: LHS_ERR_INVALID_ARG, LHS_ERR_BUFFER_TOO_SMALL
+ * (buf_bytes below the message's size). */
+LHS_API int lhs_i8_message(lhs_i8 *t, const void *d_buf, size_t buf_bytes, int32_t header,
+                           int32_t seq_len, int32_t hidden);
+
+/* Quantise rows of d_x (x_dtype LHS_F32, LHS_F16 or LHS_BF16; row r at
+ * element r*x_stride, x_stride >= hidden) into t's codes and scales, which
+ * the caller owns and which are written here.  The rule is the i8 wire
+ * format's: scale = f32(max|x| / 127), code = clamp(rne(f32(x / scale)),
+ * -127, 127); an all-zero row has scale 0 and codes 0; a row that holds
+ * inf or NaN sets LHS_ERRBIT_NONFINITE and is written as scale 0, codes 0.
+ * Bytes between hidden and stride are left as they are.  d_x aligned to its
+ * element size.  rows == 0 enqueues nothing.  t must describe plain rows.
+ * Errors: LHS_ERR_INVALID_ARG, LHS_ERR_CUDA. */
+LHS_API int lhs_i8_quantize(const lhs_i8 *t, const void *d_x, int32_t x_dtype, int64_t x_stride,
+                            int32_t *d_err, void *stream);
+
+/* Workspace bytes of one lhs_i8_matmul / lhs_i8_logits call of `tokens`
+ * rows against `table`. */
+LHS_API int lhs_i8_workspace(const lhs_i8 *table, int64_t tokens, size_t *bytes);
+
+/* Product of tokens and channels in 8 bits:
+ *   out[t][c] = round(f32(sum_j a[t][j] * w[c][j]) * a_scale[t] * w_scale[c])
+ * The sum of the codes' products is exact (integers); it is rounded once to
+ * binary32, then multiplied by the token's scale and by the channel's, one
+ * binary32 rounding each, and rounded to out_dtype (LHS_F32, LHS_F16 or
+ * LHS_BF16; beyond the f16 range +-inf).  Codes may hold -128.
+ *   table : plain rows; codes 16-byte aligned, stride a multiple of 16,
+ *           hidden <= 131071 (the largest sum stays below 2^31)
+ *   a     : any lhs_i8 of the same hidden.  Where it describes a message,
+ *           a header whose seq_len is not a->rows sets LHS_ERRBIT_MALFORMED
+ *           and makes every result NaN; a position whose zero point is not
+ *           0 sets it and makes that token's results NaN.
+ *   d_out : row t at element t*out_stride (out_stride >= table->rows),
+ *           aligned to its element size; nothing else is written
+ *   d_ws  : 256-byte aligned, >= lhs_i8_workspace bytes, overwritten
+ * a->rows == 0 or table->rows == 0 enqueues nothing.  Errors:
+ * LHS_ERR_INVALID_ARG, LHS_ERR_BUFFER_TOO_SMALL, LHS_ERR_CUDA. */
+LHS_API int lhs_i8_matmul(const lhs_i8 *a, const lhs_i8 *table, void *d_out, int32_t out_dtype,
+                          int64_t out_stride, void *d_ws, size_t ws_bytes, int32_t *d_err,
+                          void *stream);
+
+/* lhs_i8_matmul for tokens that arrive wide: each row of d_x is quantised on
+ * the way as lhs_i8_quantize does it (its codes only pass through the
+ * workspace).  The tied lm_head over an i8 table. */
+LHS_API int lhs_i8_logits(const lhs_i8 *table, const void *d_x, int32_t x_dtype, int64_t x_stride,
+                          int64_t tokens, void *d_out, int32_t out_dtype, int64_t out_stride,
+                          void *d_ws, size_t ws_bytes, int32_t *d_err, void *stream);
+
+/* ---- sampling ------------------------------------------------------------ */
+
+/* Draw one token per row of logits with temperature, top-k, top-p and min-p
+ * from a given random number.  For row r, in this order:
+ *   w[i] = exp((logit[i] - max) / temperature[r])
+ *   top-k: the top_k[r] largest logits stay (equal logits: lower ids first);
+ *          top_k <= 0 or >= vocab: all of them
+ *   top-p: of those, by descending logit (equal: lower ids first), the
+ *          shortest head whose weights sum to at least top_p[r] of theirs
+ *   min-p: of those, the ones with w[i] >= min_p[r] (the largest weight is 1)
+ *   the token is the first id, in ascending order of ids, at which the
+ *   running sum of the weights that stayed passes u[r] times their total.
+ * A temperature of 0 takes the largest logit (the lowest id of equal ones);
+ * others are clamped to [2^-100, 2^100].  A logit of -inf is a masked token
+ * and is never drawn.  Weights are evaluated to about 2^-36 of themselves
+ * and summed as integers, so the result does not depend on the order of the
+ * sums; a weight below about 2^-45 of the row's largest counts as 0.
+ *   d_logits : LHS_F32, LHS_F16 or LHS_BF16, row r at element r*stride
+ *              (stride >= vocab), aligned to its element size
+ *   d_u      : f32 [rows], each in [0, 1)
+ *   d_temperature, d_top_p, d_min_p : f32 [rows]; d_top_k : int32 [rows];
+ *              each may be NULL: temperature 1, the filter off
+ *   d_ids    : int32 [rows]
+ *   d_probs  : f32 [rows] or NULL: the weight of the drawn token over the
+ *              total of those that stayed
+ * A row without a logit above -inf gives id -1 and probability 0.  A row
+ * holding NaN or +inf does too and sets LHS_ERRBIT_NONFINITE; a row with
+ * temperature not finite or < 0, top_p outside (0, 1], min_p outside
+ * [0, 1] or u outside [0, 1) does too and sets LHS_ERRBIT_BAD_PARAM.
+ * rows == 0 enqueues nothing; 1 <= vocab <= 2^31-1.  No workspace.
+ * Errors: LHS_ERR_INVALID_ARG, LHS_ERR_CUDA. */
+LHS_API int lhs_sample(const void *d_logits, int32_t dtype, int64_t stride, int64_t rows,
+                       int64_t vocab, const float *d_u, const float *d_temperature,
+                       const int32_t *d_top_k, const float *d_top_p, const float *d_min_p,
+                       int32_t *d_ids, float *d_probs, int32_t *d_err, void *stream);
 
 /* Diagnostic: launch one tiny kernel whose wait on an on-chip barrier is
  * never satisfied, bounded by timeout_ns; the kernel gives up, sets
