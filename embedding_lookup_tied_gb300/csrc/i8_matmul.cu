@@ -2,26 +2,64 @@
 // (sum_j a[t][j] w[c][j]) * a_scale[t] * w_scale[c], integers summed exactly
 // (ADR-0008 "Remote Embeddings and lm_head Service", POST /v1/logits, over a
 // table and residuals in the i8 form of ADR-0009 "Wire Format Evolution").
+//
+// The 5th-generation tensor cores of this chip multiply f16 far faster than
+// integers, and an 8-bit code is exact in f16, as is a product of two in the
+// f32 accumulator.  So the table stays in 8 bits in HBM and on its way into
+// shared memory, and is widened to f16 on the SM, straight into tensor memory:
+//   TMA -> shared memory (codes) -> registers (f16) -> TMEM (operand A),
+// while the tokens, few next to the table's rows, are written out as f16 once
+// by a first kernel and staged by TMA as operand B.  A pair of CTAs owns 256
+// channels x up to 256 tokens (tcgen05 cta_group::2: each CTA holds 128
+// channels and half of the tokens' tile).
+//
+// Exact sums.  f32 sums of integers are exact while they stay within 2^24.  A
+// partial sum over some k is at most 128 * sum|a|; the first kernel leaves,
+// for each token, the largest sum|a| over 128 codes, b, so n = floor(2^24 /
+// (128 b)) blocks of 128 (at least 8) may be summed in the tensor cores.  Longer
+// sums are taken out every n blocks and added up as 32-bit integers.
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+
+#include <mutex>
 
 #include "decode.cuh"
 
 namespace lhs {
-namespace {
 
-constexpr int kPrepThreads = 256;
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // lm_head.cu
+
+namespace {
 
 __host__ __device__ constexpr int64_t align_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
-// Workspace: the tokens' codes [tokens][kpad] (zeros past hidden), then their
-// scales.
-int64_t kpad_of(int hidden) { return align_up(hidden, 64); }
-int64_t scales_offset(int hidden, int64_t tokens) { return align_up(tokens * kpad_of(hidden), 256); }
+constexpr int kStageK = 128;  // codes per ring stage
+
+// Workspace: the tokens as f16 [tokens][kpad] (zeros past hidden), their
+// scales, and each one's largest sum|a| over a block of 128 codes.
+struct Layout {
+    int kpad;
+    int64_t scales, peaks, bytes;
+};
+Layout layout_of(int hidden, int64_t tokens) {
+    Layout l;
+    l.kpad = static_cast<int>(align_up(hidden, kStageK));
+    l.scales = align_up(tokens * l.kpad * 2, 256);
+    l.peaks = l.scales + align_up(tokens * 4, 256);
+    l.bytes = l.peaks + align_up(tokens * 4, 256);
+    return l;
+}
+
+// ---------------------------------------------------------------------------
+// tokens: codes as f16, scale, peak
+// ---------------------------------------------------------------------------
+constexpr int kPrepThreads = 256;
+constexpr int kPrepWarps = kPrepThreads / 32;
+constexpr int kPrepSteps = 6;  // blocks of 128 a warp keeps in registers: rows up to 6,144 values
 
 // Where a coded token set is a message, whether its header names another
 // seq_len (the words lie before the first position).
 __device__ __forceinline__ bool message_mismatch(const lhs_i8 &a) {
-    if (!a.header) return false;
     const uint8_t *buf = reinterpret_cast<const uint8_t *>(a.scales) - a.header;
     return ld_dep(reinterpret_cast<const uint32_t *>(buf) + 1) != static_cast<uint32_t>(a.rows);
 }
@@ -37,150 +75,660 @@ __device__ __forceinline__ float coded_scale(const lhs_i8 &a, int64_t r, int32_t
     return s;
 }
 
-// One CTA per token: its codes and its scale into the workspace.
+// Four codes (small integers) as f16, and the warp's sum of their magnitudes.
+__device__ __forceinline__ int store_codes(__half *dst, const int (&q)[4]) {
+    const __half2 a = __floats2half2_rn(static_cast<float>(q[0]), static_cast<float>(q[1]));
+    const __half2 b = __floats2half2_rn(static_cast<float>(q[2]), static_cast<float>(q[3]));
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    return __reduce_add_sync(0xFFFFFFFFu, abs(q[0]) + abs(q[1]) + abs(q[2]) + abs(q[3]));
+}
+
+// Values j .. j+3 of a row (zeros past hidden).
+template <int DT>
+__device__ __forceinline__ void load4(const typename Elem<DT>::T *row, int j, int hidden, bool vec,
+                                      float (&v)[4]) {
+    using E = Elem<DT>;
+    if (vec && j + 4 <= hidden) {
+        if (DT == LHS_F32) {
+            const float4 w = ld_dep(reinterpret_cast<const float4 *>(row + j));
+            v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+        } else {
+            const ushort4 w = ld_dep(reinterpret_cast<const ushort4 *>(row + j));
+            v[0] = E::widen(static_cast<typename E::T>(w.x)); v[1] = E::widen(static_cast<typename E::T>(w.y));
+            v[2] = E::widen(static_cast<typename E::T>(w.z)); v[3] = E::widen(static_cast<typename E::T>(w.w));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = j + i < hidden ? E::widen(ld_dep(row + j + i)) : 0.0f;
+    }
+}
+
+// One CTA per wide token; a warp takes blocks of 128 values, four to a lane,
+// and keeps the first kPrepSteps of them in registers between the maximum and
+// the codes.
 template <int DT>
 __global__ void __launch_bounds__(kPrepThreads)
-    i8_prep_wide_kernel(const typename Elem<DT>::T *x, int64_t x_stride, int64_t tokens, int hidden, int kpad,
-                        int8_t *codes, float *scales, int32_t *err) {
-    using E = Elem<DT>;
-    __shared__ float sm_m[kPrepThreads / 32];
-    __shared__ int sm_f[kPrepThreads / 32];
-    pdl_trigger();
+    i8_prep_wide_kernel(const typename Elem<DT>::T *x, int64_t x_stride, bool vec, int64_t tokens, int hidden,
+                        int kpad, __half *codes, float *scales, int32_t *peaks, int32_t *err) {
+    __shared__ float sm_m[kPrepWarps];
+    __shared__ int sm_f[kPrepWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int blocks = kpad / kStageK;
     pdl_wait();
+    pdl_trigger();  // after the wait: the product streams the table before its own, and an earlier
+                    // kernel of the stream may be the one that quantised it
     for (int64_t r = blockIdx.x; r < tokens; r += gridDim.x) {
-        const typename E::T *row = x + r * x_stride;
+        const typename Elem<DT>::T *row = x + r * x_stride;
+        float v[kPrepSteps][4];
         float m = 0.0f;
         int bad = 0;
-        for (int j = threadIdx.x; j < hidden; j += kPrepThreads) {
-            const float v = E::widen(ld_dep(row + j));
-            if (isfinite(v)) m = fmaxf(m, fabsf(v));
-            else bad = 1;
+        auto scan = [&](const float (&w)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (isfinite(w[i])) m = fmaxf(m, fabsf(w[i]));
+                else bad = 1;
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < kPrepSteps; ++s)
+            if (warp + s * kPrepWarps < blocks)
+                load4<DT>(row, (warp + s * kPrepWarps) * kStageK + lane * 4, hidden, vec, v[s]);
+#pragma unroll
+        for (int s = 0; s < kPrepSteps; ++s)
+            if (warp + s * kPrepWarps < blocks) scan(v[s]);
+        for (int b = warp + kPrepSteps * kPrepWarps; b < blocks; b += kPrepWarps) {
+            float w[4];
+            load4<DT>(row, b * kStageK + lane * 4, hidden, vec, w);
+            scan(w);
         }
         block_max_or(m, bad, sm_m, sm_f);
         const float scale = bad ? 0.0f : __fdiv_rn(m, 127.0f);
         const float rcp = __frcp_rn(scale);
-        for (int j = threadIdx.x; j < kpad; j += kPrepThreads)
-            codes[r * kpad + j] =
-                j < hidden ? static_cast<int8_t>(i8_code(E::widen(ld_dep(row + j)), scale, rcp)) : int8_t(0);
+        int peak = 0;
+        auto emit = [&](const float (&w)[4], int b) {
+            int q[4];
+            i8_codes<4>(w, scale, rcp, q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = static_cast<int8_t>(q[i]);
+            peak = max(peak, store_codes(codes + r * kpad + b * kStageK + lane * 4, q));
+        };
+#pragma unroll
+        for (int s = 0; s < kPrepSteps; ++s)
+            if (warp + s * kPrepWarps < blocks) emit(v[s], warp + s * kPrepWarps);
+        for (int b = warp + kPrepSteps * kPrepWarps; b < blocks; b += kPrepWarps) {
+            float w[4];
+            load4<DT>(row, b * kStageK + lane * 4, hidden, vec, w);
+            emit(w, b);
+        }
+        if (lane == 0) sm_f[warp] = peak;
+        __syncthreads();
         if (threadIdx.x == 0) {
+            for (int w = 1; w < kPrepWarps; ++w) peak = max(peak, sm_f[w]);
+            peaks[r] = peak;
             scales[r] = scale;
             if (bad) set_err(err, LHS_ERRBIT_NONFINITE);
         }
+        __syncthreads();
     }
 }
 
+// One CTA per coded token.
 __global__ void __launch_bounds__(kPrepThreads)
-    i8_prep_coded_kernel(const lhs_i8 a, int kpad, int8_t *codes, float *scales, int32_t *err) {
-    pdl_trigger();
+    i8_prep_coded_kernel(const lhs_i8 a, bool words, int kpad, __half *codes, float *scales, int32_t *peaks,
+                         int32_t *err) {
+    __shared__ int sm_f[kPrepWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
+    pdl_trigger();  // after the wait, as above
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const int8_t *row = a.codes + r * a.stride;
-        for (int j = threadIdx.x; j < kpad; j += kPrepThreads)
-            codes[r * kpad + j] = j < a.hidden ? ld_dep(row + j) : int8_t(0);
-        if (threadIdx.x == 0) scales[r] = coded_scale(a, r, err);
+        int peak = 0;
+        for (int b = warp; b < kpad / kStageK; b += kPrepWarps) {
+            const int j = b * kStageK + lane * 4;
+            int q[4];
+            if (words && j + 4 <= a.hidden) {
+                const uint32_t w = ld_dep(reinterpret_cast<const uint32_t *>(row + j));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = static_cast<int8_t>(w >> (8 * i));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = j + i < a.hidden ? ld_dep(row + j + i) : 0;
+            }
+            peak = max(peak, store_codes(codes + r * kpad + j, q));
+        }
+        if (lane == 0) sm_f[warp] = peak;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kPrepWarps; ++w) peak = max(peak, sm_f[w]);
+            peaks[r] = peak;
+            scales[r] = coded_scale(a, r, err);
+        }
+        __syncthreads();
     }
 }
 
-template <int OD>
-__device__ __forceinline__ void store_out(void *out, int64_t i, float v) {
-    if (OD == LHS_F32) reinterpret_cast<float *>(out)[i] = v;
-    else if (OD == LHS_F16) reinterpret_cast<__half *>(out)[i] = __float2half_rn(v);
+// ---------------------------------------------------------------------------
+// product
+// ---------------------------------------------------------------------------
+constexpr int kCtaRows = 128;                       // channels per CTA: TMEM lanes
+constexpr int kPairRows = 2 * kCtaRows;
+constexpr int kConvWarps = 8;                       // widen the codes, take the sums out
+constexpr int kThreads = 32 * (kConvWarps + 3);     // + table producer, token producer, MMA issuer
+constexpr int kTableStageBytes = kCtaRows * kStageK;  // 16 KB of codes
+constexpr int kTmemCols = 512;
+constexpr int kTmemA = 256;                         // first column of the widened codes
+constexpr int kASlots = 4;                          // of kStageK / 2 = 64 columns each
+constexpr int kAhead = 3;                           // stages widened before a finished sum is taken out
+constexpr int kPeakBlocks = (1 << 24) / kStageK;    // n = kPeakBlocks / peak
+
+// Tokens per tile (NMAX at most): the ring depths that fill shared memory,
+// and the accumulators that fit beside the widened codes.
+template <int NMAX>
+struct Tile {
+    static constexpr int kTokenStageBytes = NMAX / 2 * kStageK * 2;  // this CTA's half of the tokens
+    static constexpr int kTokenStages = NMAX == 256 ? 3 : NMAX == 128 ? 4 : 6;
+    static constexpr int kTableStages = (208 * 1024 - kTokenStages * kTokenStageBytes) / kTableStageBytes;
+    static constexpr int kAccs = NMAX == 256 ? 1 : 2;
+};
+
+template <int NMAX>
+struct Smem {
+    uint8_t table[Tile<NMAX>::kTableStages][kTableStageBytes];
+    uint8_t token[Tile<NMAX>::kTokenStages][Tile<NMAX>::kTokenStageBytes];
+    uint64_t table_full[Tile<NMAX>::kTableStages], table_empty[Tile<NMAX>::kTableStages];
+    uint64_t token_full[Tile<NMAX>::kTokenStages], token_empty[Tile<NMAX>::kTokenStages];
+    uint64_t a_full[kASlots], a_empty[kASlots];
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct Params {
+    const uint8_t *w_scales;
+    int64_t w_scale_stride;
+    int64_t channels, tokens;
+    int n;         // tokens per tile, a multiple of 32
+    int blocks;    // of tokens
+    int nk;        // stages per tile
+    int64_t items; // channel tiles x token blocks
+    const float *scales;
+    const int32_t *peaks;
+    void *out;
+    int64_t out_stride;
+    int out_dtype;
+    int32_t *err;
+};
+
+__device__ __forceinline__ uint32_t cluster_ctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t smem_addr, uint32_t cta) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr), "r"(cta));
+    return r;
+}
+// TMA load into this CTA's shared memory, counted on a barrier of either CTA.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar_cluster,
+                                                 int32_t c0, int32_t c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+__device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
+// 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+// A in TMEM (the widened codes of both CTAs, same columns), B in shared memory.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit_both(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(0x3))
+        : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// 16 consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+        "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 32 consecutive columns of this thread's TMEM lane, written.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+// Four signed codes as f16, in order: code + 128 under the exponent byte 0x64
+// is 1024 + code + 128; less 1152 it is the code, exactly.
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    const uint32_t x = codes ^ 0x80808080u;
+    const uint32_t bias = 0x64806480u;  // 1152, 1152
+    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+    const __half2 c = *reinterpret_cast<const __half2 *>(&bias);
+    const __half2 p = __hsub2(*reinterpret_cast<const __half2 *>(&a), c);
+    const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&b), c);
+    lo = *reinterpret_cast<const uint32_t *>(&p);
+    hi = *reinterpret_cast<const uint32_t *>(&q);
+}
+
+// Bounded wait that gives up at once when the CTA has already aborted.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, int *abort_flag, int32_t *err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<const volatile int *>(abort_flag)) return false;
+    if (mbar_wait(bar, parity, kWaitTimeoutNs)) return true;
+    set_err(err, LHS_ERRBIT_TIMEOUT);
+    *reinterpret_cast<volatile int *>(abort_flag) = 1;
+    return false;
+}
+
+__device__ __forceinline__ void store_out(void *out, int dtype, int64_t i, float v) {
+    if (dtype == LHS_F32) reinterpret_cast<float *>(out)[i] = v;
+    else if (dtype == LHS_F16) reinterpret_cast<__half *>(out)[i] = __float2half_rn(v);
     else reinterpret_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(v);
 }
 
-// Tiles of 64 channels x 32 tokens, 64 codes at a time in shared memory; a
-// thread sums one channel against eight tokens with four-way dot products.
-constexpr int kTC = 64, kTT = 32, kTK = 64;
-template <int OD>
-__global__ void __launch_bounds__(256)
-    i8_matmul_kernel(const lhs_i8 w, const int8_t *codes, const float *scales, int64_t tokens, int kpad, void *out,
-                     int64_t out_stride) {
-    __shared__ int ws[kTC][kTK / 4 + 1];
-    __shared__ int as[kTT][kTK / 4];
-    const int c = threadIdx.x & (kTC - 1), g = threadIdx.x / kTC;
-    pdl_trigger();
-    pdl_wait();
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kTC;
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * kTT; t0 < tokens;
-         t0 += static_cast<int64_t>(gridDim.y) * kTT) {
-        int acc[8] = {};
-        for (int k0 = 0; k0 < kpad; k0 += kTK) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < kTC * kTK / 4; i += 256) {
-                const int r = i / (kTK / 4), q = i % (kTK / 4);
-                uint32_t v = 0;
-                const int k = k0 + q * 4;
-                if (c0 + r < w.rows && k < w.hidden) {  // rows are 16-byte aligned, so the word lies inside the row's stride
-                    v = __ldg(reinterpret_cast<const uint32_t *>(w.codes + (c0 + r) * w.stride + k));
-                    if (w.hidden - k < 4) v &= (1u << (8 * (w.hidden - k))) - 1u;
-                }
-                ws[r][q] = static_cast<int>(v);
-            }
-            for (int i = threadIdx.x; i < kTT * kTK / 4; i += 256) {
-                const int r = i / (kTK / 4), q = i % (kTK / 4);
-                as[r][q] = t0 + r < tokens
-                               ? __ldcg(reinterpret_cast<const int *>(codes + (t0 + r) * kpad + k0) + q)
-                               : 0;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int q = 0; q < kTK / 4; ++q) {
-                const int wv = ws[c][q];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = __dp4a(wv, as[g * 8 + i][q], acc[i]);
-            }
+template <int NMAX>
+__global__ void __launch_bounds__(kThreads, 1)
+    i8_matmul_kernel(const __grid_constant__ CUtensorMap tm_table, const __grid_constant__ CUtensorMap tm_token,
+                     const Params p) {
+    constexpr int SW = Tile<NMAX>::kTableStages, SX = Tile<NMAX>::kTokenStages, ACCS = Tile<NMAX>::kAccs;
+    extern __shared__ uint8_t dyn_smem[];
+    Smem<NMAX> &sm = *reinterpret_cast<Smem<NMAX> *>(smem_align<1024>(dyn_smem));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int64_t cl = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+    const int64_t mine = cl < p.items ? (p.items - cl + clusters - 1) / clusters : 0;  // tiles of this pair
+    const int64_t total = mine * p.nk;                                                 // stages
+
+    if (tid == 0) {
+        for (int s = 0; s < SW; ++s) {
+            mbar_init(&sm.table_full[s], 1);
+            mbar_init(&sm.table_empty[s], kConvWarps);
         }
-        if (c0 + c < w.rows) {
-            const float wsc = __ldg(reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(w.scales) +
-                                                                    (c0 + c) * w.scale_stride));
+        for (int s = 0; s < SX; ++s) {
+            mbar_init(&sm.token_full[s], 1);   // leader: both CTAs' bytes
+            mbar_init(&sm.token_empty[s], 1);  // the leader's commit, to both
+        }
+        for (int s = 0; s < kASlots; ++s) {
+            mbar_init(&sm.a_full[s], 2 * kConvWarps);  // leader: both CTAs' warps
+            mbar_init(&sm.a_empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sm.acc_full[s], 1);
+            mbar_init(&sm.acc_empty[s], 2 * kConvWarps);
+        }
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kConvWarps + 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sm.tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync_all();  // the peer's barriers exist
+    const uint32_t tmem = sm.tmem_base;
+    pdl_trigger();
+
+    if (warp == kConvWarps) {
+        // ---------------- table producer (does not wait for the tokens) ----------------
+        if (lane == 0) {
+            tma_prefetch_map(&tm_table);
+            int64_t j = 0;
+            bool ok = true;
+            for (int64_t it = cl; it < p.items && ok; it += clusters) {
+                const int32_t row = static_cast<int32_t>(it / p.blocks) * kPairRows + static_cast<int32_t>(rank) * kCtaRows;
+                for (int kc = 0; kc < p.nk; ++kc, ++j) {
+                    const int s = static_cast<int>(j % SW);
+                    if (!wait_or_abort(&sm.table_empty[s], ((j / SW) & 1) ^ 1, &sm.abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&sm.table_full[s], kTableStageBytes);
+                    tma_load_2d(sm.table[s], &tm_table, &sm.table_full[s], kc * kStageK, row);
+                }
+            }
+            // the copies have landed, and the commits on the widened codes' slots have arrived
+            for (int64_t i = j > SW ? j - SW : 0; i < j; ++i) mbar_wait(&sm.table_full[i % SW], (i / SW) & 1, kWaitTimeoutNs);
+            for (int64_t i = total > kASlots ? total - kASlots : 0; i < total; ++i)
+                if (!wait_or_abort(&sm.a_empty[i % kASlots], (i / kASlots) & 1, &sm.abort_flag, p.err)) break;
+        }
+    } else if (warp == kConvWarps + 1) {
+        // ---------------- token producer ----------------
+        if (lane == 0) {
+            tma_prefetch_map(&tm_token);
+            pdl_wait();
+            const int half = p.n / 2;
+            int64_t j = 0;
+            bool ok = true;
+            for (int64_t it = cl; it < p.items && ok; it += clusters) {
+                const int32_t row = static_cast<int32_t>(it % p.blocks) * p.n + static_cast<int32_t>(rank) * half;
+                for (int kc = 0; kc < p.nk; ++kc, ++j) {
+                    const int s = static_cast<int>(j % SX);
+                    if (!wait_or_abort(&sm.token_empty[s], ((j / SX) & 1) ^ 1, &sm.abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.token_full[s], 2 * half * kStageK * 2);
+                    const uint32_t bar = cluster_addr(smem_u32(&sm.token_full[s]), 0);
+                    tma_load_2d_pair(sm.token[s], &tm_token, bar, kc * kStageK, row);
+                    tma_load_2d_pair(sm.token[s] + half * 128, &tm_token, bar, kc * kStageK + 64, row);
+                }
+            }
+            for (int64_t i = j > SX ? j - SX : 0; i < j; ++i)
+                if (!wait_or_abort(&sm.token_empty[i % SX], (i / SX) & 1, &sm.abort_flag, p.err)) break;
+        }
+    } else {
+        // blocks of 128 that may be summed in f32
+        pdl_wait();
+        int peak = 0;
+        for (int64_t t = lane; t < p.tokens; t += 32) peak = max(peak, ld_dep(p.peaks + t));
+        peak = __reduce_max_sync(0xFFFFFFFFu, peak);
+        const int chunk = peak ? kPeakBlocks / peak : p.nk;
+
+        if (warp == kConvWarps + 2) {
+            // ---------------- MMA issuer (the leader CTA only) ----------------
+            if (lane == 0 && rank == 0) {
+                const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.n >> 3) << 17) |
+                                       (static_cast<uint32_t>(kPairRows >> 4) << 24);  // f16 x f16 -> f32
+                const uint32_t half_bytes = static_cast<uint32_t>(p.n / 2) * 128;
+                int64_t j = 0, c = 0;  // stage, sum
+                bool ok = true;
+                for (int64_t it = 0; it < mine && ok; ++it) {
+                    int in = 0;  // stages of the current sum
+                    for (int kc = 0; kc < p.nk; ++kc, ++j) {
+                        const int buf = static_cast<int>(c % ACCS);
+                        const int sa = static_cast<int>(j % kASlots), sx = static_cast<int>(j % SX);
+                        if ((in == 0 && !wait_or_abort(&sm.acc_empty[buf], ((c / ACCS) & 1) ^ 1, &sm.abort_flag, p.err)) ||
+                            !wait_or_abort(&sm.token_full[sx], (j / SX) & 1, &sm.abort_flag, p.err) ||
+                            !wait_or_abort(&sm.a_full[sa], (j / kASlots) & 1, &sm.abort_flag, p.err)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_acquire_cluster();  // the peer's warps arrived on these barriers too
+                        tc_fence_after();
+                        const uint32_t d = tmem + buf * NMAX, a = tmem + kTmemA + sa * (kStageK / 2);
+                        const uint32_t b = smem_u32(sm.token[sx]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t t = t0 + g * 8 + i;
-                if (t < tokens)
-                    store_out<OD>(out, t * out_stride + c0 + c,
-                                  __fmul_rn(__fmul_rn(static_cast<float>(acc[i]), __ldcg(scales + t)), wsc));
+                        for (int ks = 0; ks < kStageK / 16; ++ks)
+                            umma_f16_ts(d, a + ks * 8, desc_sw128(b + (ks >> 2) * half_bytes + (ks & 3) * 32), idesc,
+                                        (in | ks) != 0);
+                        umma_commit_both(&sm.token_empty[sx]);
+                        umma_commit_both(&sm.a_empty[sa]);
+                        ++in;
+                        if (in == chunk || kc + 1 == p.nk) {
+                            umma_commit_both(&sm.acc_full[buf]);
+                            in = 0;
+                            ++c;
+                        }
+                    }
+                }
+            }
+        } else {
+            // ---------------- widen the codes, take the sums out ----------------
+            const int q = warp & 3, h = warp >> 2;  // TMEM lane quarter; half of the k, then of the tokens
+            const int row = q * 32 + lane;
+            const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+            const int half = p.n / 2;
+            int acc[NMAX / 2];  // sums of this channel against its half of the tile's tokens
+            int64_t c = 0, it = cl;
+            int kd = 0, in = 0;  // stage of the tile, of the sum, that the sums have got to
+            for (int64_t j = 0; j < total + kAhead; ++j) {
+                if (j < total) {
+                    const int s = static_cast<int>(j % SW), sa = static_cast<int>(j % kASlots);
+                    bool ok = wait_or_abort(&sm.table_full[s], (j / SW) & 1, &sm.abort_flag, p.err);
+                    uint4 w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)  // 16-byte piece 4h + i of this row, swizzled
+                        w[i] = *reinterpret_cast<const uint4 *>(sm.table[s] + row * kStageK + (((4 * h + i) ^ (row & 7)) << 4));
+                    uint32_t f[32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        widen4(w[i].x, f[8 * i], f[8 * i + 1]);
+                        widen4(w[i].y, f[8 * i + 2], f[8 * i + 3]);
+                        widen4(w[i].z, f[8 * i + 4], f[8 * i + 5]);
+                        widen4(w[i].w, f[8 * i + 6], f[8 * i + 7]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.table_empty[s]);
+                    ok = ok && wait_or_abort(&sm.a_empty[sa], ((j / kASlots) & 1) ^ 1, &sm.abort_flag, p.err);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) break;  // the tcgen05 instructions are warp-collective
+                    tc_fence_after();
+                    tmem_st32(tmem + lanes + kTmemA + sa * (kStageK / 2) + h * 32, f);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&sm.a_full[sa]), 0));
+                }
+                if (j < kAhead) continue;
+                // stage j - kAhead: does a sum end with it?
+                ++in;
+                ++kd;
+                const bool tile_done = kd == p.nk;
+                if (in < chunk && !tile_done) continue;
+                const int buf = static_cast<int>(c % ACCS);
+                const bool ok = wait_or_abort(&sm.acc_full[buf], (c / ACCS) & 1, &sm.abort_flag, p.err);
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                tc_fence_after();
+                const bool first = kd == in;
+#pragma unroll
+                for (int g = 0; g < NMAX / 32; ++g) {
+                    if (g * 16 >= half) break;
+                    float v[16];
+                    tmem_ld16(tmem + lanes + buf * NMAX + h * half + g * 16, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int s = __float2int_rn(v[i]);
+                        acc[g * 16 + i] = first ? s : acc[g * 16 + i] + s;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&sm.acc_empty[buf]), 0));
+                ++c;
+                in = 0;
+                if (!tile_done) continue;
+                kd = 0;
+                const int64_t ch = it / p.blocks * kPairRows + static_cast<int64_t>(rank) * kCtaRows + row;
+                const int64_t t0 = it % p.blocks * p.n + h * half;
+                it += clusters;
+                const bool valid = ch < p.channels;
+                const float ws = valid ? ld_dep(reinterpret_cast<const float *>(p.w_scales + ch * p.w_scale_stride)) : 0.0f;
+#pragma unroll
+                for (int g = 0; g < NMAX / 32; ++g) {
+                    if (g * 16 >= half || t0 + g * 16 >= p.tokens) break;
+                    const int64_t ts = t0 + g * 16 + (lane & 15);
+                    const float as = ts < p.tokens ? ld_dep(p.scales + ts) : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float sc = __shfl_sync(0xFFFFFFFFu, as, i);
+                        const int64_t t = t0 + g * 16 + i;
+                        if (valid && t < p.tokens)
+                            store_out(p.out, p.out_dtype, t * p.out_stride + ch,
+                                      __fmul_rn(__fmul_rn(static_cast<float>(acc[g * 16 + i]), sc), ws));
+                    }
+                }
             }
         }
     }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // the pair is done with its accumulators and barriers
+    if (warp == kConvWarps + 2) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+    cluster_sync_all();  // neither CTA leaves while its peer may still address it
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+bool make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols, uint64_t rows,
+              uint64_t pitch, uint32_t box_cols, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {pitch};
+    const cuuint32_t box[2] = {box_cols, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NMAX>
+cudaError_t launch_product(const CUtensorMap &tm_table, const CUtensorMap &tm_token, const Params &p,
+                           const DeviceInfo &dev, cudaStream_t stream) {
+    constexpr int smem = 1024 + static_cast<int>(sizeof(Smem<NMAX>));
+    auto kern = i8_matmul_kernel<NMAX>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    static std::mutex mu;
+    static int pairs[64] = {};  // resident at once
+    int fit;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!pairs[dev.device]) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            int n = dev.num_sms / 2, active = 0;
+            cfg.gridDim = dim3(2 * n);
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&active, kern, &cfg) == cudaSuccess && active > 0 && active < n) n = active;
+            (void)cudaGetLastError();
+            pairs[dev.device] = n < 1 ? 1 : n;
+        }
+        fit = pairs[dev.device];
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (p.items < fit ? p.items : fit)));
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, tm_table, tm_token, p);
 }
 
 template <int DT>
-cudaError_t prep_wide(const I8Tokens &a, int hidden, int kpad, int8_t *codes, float *scales, int32_t *err,
-                      unsigned grid, cudaStream_t stream) {
+cudaError_t prep_wide(const I8Tokens &a, int hidden, const Layout &l, uint8_t *ws, int32_t *err, unsigned grid,
+                      cudaStream_t stream) {
+    constexpr int64_t size = DT == LHS_F32 ? 4 : 2;
+    const bool vec = reinterpret_cast<uintptr_t>(a.x) % (4 * size) == 0 && a.x_stride % 4 == 0;
     return launch_pdl(i8_prep_wide_kernel<DT>, dim3(grid), dim3(kPrepThreads), 0, stream,
-                      static_cast<const typename Elem<DT>::T *>(a.x), a.x_stride, a.rows, hidden, kpad, codes,
-                      scales, err);
+                      static_cast<const typename Elem<DT>::T *>(a.x), a.x_stride, vec, a.rows, hidden, l.kpad,
+                      reinterpret_cast<__half *>(ws), reinterpret_cast<float *>(ws + l.scales),
+                      reinterpret_cast<int32_t *>(ws + l.peaks), err);
 }
 
 }  // namespace
 
 size_t i8_matmul_workspace(const lhs_i8 &table, int64_t tokens) {
-    return static_cast<size_t>(scales_offset(table.hidden, tokens) + align_up(tokens * 4, 256));
+    return static_cast<size_t>(layout_of(table.hidden, tokens).bytes);
 }
 
 cudaError_t launch_i8_matmul(const I8Tokens &a, const lhs_i8 &table, void *out, int32_t out_dtype,
-                             int64_t out_stride, void *ws, int32_t *err, cudaStream_t stream) {
-    const int kpad = static_cast<int>(kpad_of(table.hidden));
-    int8_t *codes = static_cast<int8_t *>(ws);
-    float *scales = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + scales_offset(table.hidden, a.rows));
-    const unsigned pg = static_cast<unsigned>(a.rows < (1 << 20) ? a.rows : (1 << 20));
-    cudaError_t e;
-    if (!a.x) e = launch_pdl(i8_prep_coded_kernel, dim3(pg), dim3(kPrepThreads), 0, stream, a.coded, kpad, codes,
-                             scales, err);
-    else if (a.x_dtype == LHS_F32) e = prep_wide<LHS_F32>(a, table.hidden, kpad, codes, scales, err, pg, stream);
-    else if (a.x_dtype == LHS_F16) e = prep_wide<LHS_F16>(a, table.hidden, kpad, codes, scales, err, pg, stream);
-    else e = prep_wide<LHS_BF16>(a, table.hidden, kpad, codes, scales, err, pg, stream);
+                             int64_t out_stride, void *ws_, int32_t *err, cudaStream_t stream) {
+    DeviceInfo dev;
+    cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return e;
-    const int64_t ty = (a.rows + kTT - 1) / kTT;
-    const dim3 grid(static_cast<unsigned>((table.rows + kTC - 1) / kTC), static_cast<unsigned>(ty < 65535 ? ty : 65535));
-    if (out_dtype == LHS_F32)
-        return launch_pdl(i8_matmul_kernel<LHS_F32>, grid, dim3(256), 0, stream, table, codes, scales, a.rows, kpad,
-                          out, out_stride);
-    if (out_dtype == LHS_F16)
-        return launch_pdl(i8_matmul_kernel<LHS_F16>, grid, dim3(256), 0, stream, table, codes, scales, a.rows, kpad,
-                          out, out_stride);
-    return launch_pdl(i8_matmul_kernel<LHS_BF16>, grid, dim3(256), 0, stream, table, codes, scales, a.rows, kpad,
-                      out, out_stride);
+    uint8_t *ws = static_cast<uint8_t *>(ws_);
+    const Layout l = layout_of(table.hidden, a.rows);
+
+    Params p = {};
+    p.w_scales = reinterpret_cast<const uint8_t *>(table.scales);
+    p.w_scale_stride = table.scale_stride;
+    p.channels = table.rows;
+    p.tokens = a.rows;
+    // token blocks of equal size, at most 256 tokens each
+    p.blocks = static_cast<int>((a.rows + 255) / 256);
+    p.n = static_cast<int>(align_up((a.rows + p.blocks - 1) / p.blocks, 32));
+    p.nk = l.kpad / kStageK;
+    p.items = (table.rows + kPairRows - 1) / kPairRows * p.blocks;
+    p.scales = reinterpret_cast<const float *>(ws + l.scales);
+    p.peaks = reinterpret_cast<const int32_t *>(ws + l.peaks);
+    p.out = out;
+    p.out_stride = out_stride;
+    p.out_dtype = out_dtype;
+    p.err = err;
+    CUtensorMap tm_table, tm_token;
+    if (!make_map(&tm_table, CU_TENSOR_MAP_DATA_TYPE_UINT8, table.codes, table.hidden, table.rows, table.stride,
+                  kStageK, kCtaRows) ||
+        !make_map(&tm_token, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws, l.kpad, a.rows, static_cast<uint64_t>(l.kpad) * 2, 64,
+                  p.n / 2))
+        return cudaErrorInvalidValue;
+
+    const unsigned pg = static_cast<unsigned>(a.rows < (1 << 20) ? a.rows : (1 << 20));
+    if (!a.x) {
+        const bool words = reinterpret_cast<uintptr_t>(a.coded.codes) % 4 == 0 && a.coded.stride % 4 == 0;
+        e = launch_pdl(i8_prep_coded_kernel, dim3(pg), dim3(kPrepThreads), 0, stream, a.coded, words, l.kpad,
+                       reinterpret_cast<__half *>(ws), reinterpret_cast<float *>(ws + l.scales),
+                       reinterpret_cast<int32_t *>(ws + l.peaks), err);
+    } else if (a.x_dtype == LHS_F32) {
+        e = prep_wide<LHS_F32>(a, table.hidden, l, ws, err, pg, stream);
+    } else if (a.x_dtype == LHS_F16) {
+        e = prep_wide<LHS_F16>(a, table.hidden, l, ws, err, pg, stream);
+    } else {
+        e = prep_wide<LHS_BF16>(a, table.hidden, l, ws, err, pg, stream);
+    }
+    if (e != cudaSuccess) return e;
+    if (p.n <= 32) return launch_product<32>(tm_table, tm_token, p, dev, stream);
+    if (p.n <= 64) return launch_product<64>(tm_table, tm_token, p, dev, stream);
+    if (p.n <= 128) return launch_product<128>(tm_table, tm_token, p, dev, stream);
+    return launch_product<256>(tm_table, tm_token, p, dev, stream);
 }
 
 }  // namespace lhs
