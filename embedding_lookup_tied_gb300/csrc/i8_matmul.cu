@@ -213,32 +213,35 @@ __global__ void __launch_bounds__(kPrepThreads)
 // ---------------------------------------------------------------------------
 constexpr int kCtaRows = 128;                       // channels per CTA: TMEM lanes
 constexpr int kPairRows = 2 * kCtaRows;
-constexpr int kConvWarps = 8;                       // widen the codes, take the sums out
-constexpr int kThreads = 32 * (kConvWarps + 3);     // + table producer, token producer, MMA issuer
 constexpr int kTableStageBytes = kCtaRows * kStageK;  // 16 KB of codes
 constexpr int kTmemCols = 512;
-constexpr int kTmemA = 256;                         // first column of the widened codes
-constexpr int kASlots = 4;                          // of kStageK / 2 = 64 columns each
-constexpr int kAhead = 3;                           // stages widened before a finished sum is taken out
+constexpr int kSlotCols = kStageK / 2;              // of one stage's widened codes
 constexpr int kPeakBlocks = (1 << 24) / kStageK;    // n = kPeakBlocks / peak
 
-// Tokens per tile (NMAX at most): the ring depths that fill shared memory,
-// and the accumulators that fit beside the widened codes.
+// By the most tokens of a tile: the groups of four warps that widen codes (a
+// group takes every kGroups-th stage, and an equal part of the sums), the
+// ring depths that fill shared memory, and how tensor memory is split.
 template <int NMAX>
 struct Tile {
-    static constexpr int kTokenStageBytes = NMAX / 2 * kStageK * 2;  // this CTA's half of the tokens
-    static constexpr int kTokenStages = NMAX == 256 ? 3 : NMAX == 128 ? 4 : 6;
-    static constexpr int kTableStages = (208 * 1024 - kTokenStages * kTokenStageBytes) / kTableStageBytes;
+    static constexpr int kGroups = NMAX == 256 ? 2 : 4;
+    static constexpr int kConvWarps = 4 * kGroups;
+    static constexpr int kThreads = 32 * (kConvWarps + 4);  // + table producer, token producer, MMA issuer, idle
     static constexpr int kAccs = NMAX == 256 ? 1 : 2;
+    static constexpr int kColA = kAccs * NMAX;               // first column of the widened codes
+    static constexpr int kSlots = (kTmemCols - kColA) / kSlotCols;  // stages the MMAs may hold
+    static constexpr int kTokenStageBytes = NMAX / 2 * kStageK * 2;  // this CTA's half of the tokens
+    static constexpr int kTableStages = (208 * 1024 - kSlots * kTokenStageBytes) / kTableStageBytes;
+    static constexpr int kAhead = kSlots - 1;                // stages widened before a finished sum is taken out
+    static constexpr int kPart = NMAX / kGroups;             // tokens whose sums a warp takes out
 };
 
 template <int NMAX>
 struct Smem {
-    uint8_t table[Tile<NMAX>::kTableStages][kTableStageBytes];
-    uint8_t token[Tile<NMAX>::kTokenStages][Tile<NMAX>::kTokenStageBytes];
-    uint64_t table_full[Tile<NMAX>::kTableStages], table_empty[Tile<NMAX>::kTableStages];
-    uint64_t token_full[Tile<NMAX>::kTokenStages], token_empty[Tile<NMAX>::kTokenStages];
-    uint64_t a_full[kASlots], a_empty[kASlots];
+    using T = Tile<NMAX>;
+    uint8_t table[T::kTableStages][kTableStageBytes];
+    uint8_t token[T::kSlots][T::kTokenStageBytes];
+    uint64_t table_full[T::kTableStages], table_empty[T::kTableStages];
+    uint64_t full[T::kSlots], empty[T::kSlots];  // a stage's operands, widened codes and tokens
     uint64_t acc_full[2], acc_empty[2];
     uint32_t tmem_base;
     int abort_flag;
@@ -283,10 +286,12 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1)
         : "memory");
 }
+// Arrive on a barrier of either CTA.  What it orders is tensor memory, by the
+// tcgen05 waits and fences around it; a release at cluster scope would add a
+// fence of all memory, which held every stage up by about 0.5 us.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
-__device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
 // 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
@@ -316,25 +321,23 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// 16 consecutive columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
+// 8 consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float *v) {
+    uint32_t r[8];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
-        "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
         : "r"(taddr)
         : "memory");
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 // 32 consecutive columns of this thread's TMEM lane, written.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
         "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
@@ -354,27 +357,77 @@ __device__ __forceinline__ void widen4(uint32_t codes, uint32_t &lo, uint32_t &h
     hi = *reinterpret_cast<const uint32_t *>(&q);
 }
 
+// A place in a ring of N slots and the parity of its phase.
+template <int N>
+struct Ring {
+    int i = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+// Whether the phase is over, acquiring what both CTAs of the pair released.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// The same look without a wait.
+__device__ __forceinline__ bool mbar_test_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // Bounded wait that gives up at once when the CTA has already aborted.
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, int *abort_flag, int32_t *err) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_cluster(bar, parity)) return true;
     if (*reinterpret_cast<const volatile int *>(abort_flag)) return false;
-    if (mbar_wait(bar, parity, kWaitTimeoutNs)) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (global_ns() - t0 > kWaitTimeoutNs) break;
+    }
     set_err(err, LHS_ERRBIT_TIMEOUT);
     *reinterpret_cast<volatile int *>(abort_flag) = 1;
     return false;
 }
 
-__device__ __forceinline__ void store_out(void *out, int dtype, int64_t i, float v) {
-    if (dtype == LHS_F32) reinterpret_cast<float *>(out)[i] = v;
-    else if (dtype == LHS_F16) reinterpret_cast<__half *>(out)[i] = __float2half_rn(v);
-    else reinterpret_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(v);
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Blocks of 128 codes that may be summed in f32.  Warp-collective.
+__device__ __forceinline__ int blocks_per_sum(const Params &p, int lane) {
+    int peak = 0;
+    for (int64_t t = lane; t < p.tokens; t += 32) peak = max(peak, ld_dep(p.peaks + t));
+    peak = __reduce_max_sync(0xFFFFFFFFu, peak);
+    return peak ? kPeakBlocks / peak : p.nk;
 }
 
 template <int NMAX>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
     i8_matmul_kernel(const __grid_constant__ CUtensorMap tm_table, const __grid_constant__ CUtensorMap tm_token,
                      const Params p) {
-    constexpr int SW = Tile<NMAX>::kTableStages, SX = Tile<NMAX>::kTokenStages, ACCS = Tile<NMAX>::kAccs;
+    using T = Tile<NMAX>;
+    constexpr int SW = T::kTableStages, SX = T::kSlots, ACCS = T::kAccs, kConvWarps = T::kConvWarps;
     extern __shared__ uint8_t dyn_smem[];
     Smem<NMAX> &sm = *reinterpret_cast<Smem<NMAX> *>(smem_align<1024>(dyn_smem));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -386,15 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < SW; ++s) {
             mbar_init(&sm.table_full[s], 1);
-            mbar_init(&sm.table_empty[s], kConvWarps);
+            mbar_init(&sm.table_empty[s], 4);
         }
         for (int s = 0; s < SX; ++s) {
-            mbar_init(&sm.token_full[s], 1);   // leader: both CTAs' bytes
-            mbar_init(&sm.token_empty[s], 1);  // the leader's commit, to both
-        }
-        for (int s = 0; s < kASlots; ++s) {
-            mbar_init(&sm.a_full[s], 2 * kConvWarps);  // leader: both CTAs' warps
-            mbar_init(&sm.a_empty[s], 1);
+            mbar_init(&sm.full[s], 1 + 2 * 4);  // leader: both CTAs' bytes, and a group of warps of each
+            mbar_init(&sm.empty[s], 1);         // the leader's commit, to both
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.acc_full[s], 1);
@@ -417,181 +466,247 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sm.tmem_base;
     pdl_trigger();
 
-    if (warp == kConvWarps) {
-        // ---------------- table producer (does not wait for the tokens) ----------------
-        if (lane == 0) {
-            tma_prefetch_map(&tm_table);
-            int64_t j = 0;
-            bool ok = true;
-            for (int64_t it = cl; it < p.items && ok; it += clusters) {
-                const int32_t row = static_cast<int32_t>(it / p.blocks) * kPairRows + static_cast<int32_t>(rank) * kCtaRows;
-                for (int kc = 0; kc < p.nk; ++kc, ++j) {
-                    const int s = static_cast<int>(j % SW);
-                    if (!wait_or_abort(&sm.table_empty[s], ((j / SW) & 1) ^ 1, &sm.abort_flag, p.err)) {
-                        ok = false;
-                        break;
+    // The warps that hold sums take registers from the others: 8 x 216 + 4 x
+    // 72 a lane are what 12 warps are launched with at 168, 16 x 104 + 4 x 64
+    // what 20 are at 96.
+    if (warp < kConvWarps) {
+        if constexpr (NMAX == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        pdl_wait();
+        const int chunk = blocks_per_sum(p, lane);
+        // ---------------- widen the codes, take the sums out ----------------
+        const int q = warp & 3, g = warp >> 2;  // TMEM lane quarter; group
+        const int row = q * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+        const int part = p.n / T::kGroups;
+        // the sums of this channel against the group's part of the tile's tokens: f32 while they
+        // are exact in it, 32-bit integers (whole) once they are not
+        float acc[T::kPart];
+        bool whole = false;
+#pragma unroll
+        for (int c = 0; c < T::kPart; ++c) acc[c] = 0.0f;
+        Ring<SW> sw;
+        Ring<T::kSlots> sa;
+        Ring<ACCS> sc;
+        Ring<T::kGroups> turn;
+        int64_t it = cl;
+        int kd = 0, in = 0;  // stage of the tile, of the sum, that the sums have got to
+        for (int64_t j = 0; j < total + T::kAhead; ++j) {
+            if (j < total && turn.i == g) {
+                bool ok = wait_or_abort(&sm.table_full[sw.i], sw.parity, &sm.abort_flag, p.err);
+                ok = wait_or_abort(&sm.empty[sa.i], sa.parity ^ 1u, &sm.abort_flag, p.err) && ok;
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;  // the tcgen05 instructions are warp-collective
+                tc_fence_after();
+                const uint8_t *src = sm.table[sw.i] + row * kStageK;
+                const uint32_t dst = tmem + lanes + T::kColA + sa.i * kSlotCols;
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    uint32_t f[32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // 16-byte piece 4o + i of this row, swizzled
+                        const uint4 u = *reinterpret_cast<const uint4 *>(src + (((4 * o + i) ^ (row & 7)) << 4));
+                        widen4(u.x, f[8 * i], f[8 * i + 1]);
+                        widen4(u.y, f[8 * i + 2], f[8 * i + 3]);
+                        widen4(u.z, f[8 * i + 4], f[8 * i + 5]);
+                        widen4(u.w, f[8 * i + 6], f[8 * i + 7]);
                     }
-                    mbar_arrive_expect_tx(&sm.table_full[s], kTableStageBytes);
-                    tma_load_2d(sm.table[s], &tm_table, &sm.table_full[s], kc * kStageK, row);
+                    tmem_st32(dst + o * 32, f);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.table_empty[sw.i]);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&sm.full[sa.i]), 0));
+            }
+            sw.next();
+            sa.next();
+            turn.next();
+            if (j < T::kAhead) continue;
+            // stage j - kAhead: does a sum end with it?
+            ++in;
+            ++kd;
+            const bool tile_done = kd == p.nk;
+            if (in < chunk && !tile_done) continue;
+            // the scales of what is about to be written, on their way while the sum is waited for
+            const int64_t ch = it / p.blocks * kPairRows + static_cast<int64_t>(rank) * kCtaRows + row;
+            const int64_t t0 = it % p.blocks * p.n + g * part;
+            const bool valid = ch < p.channels;
+            float ws = 0.0f, as[(T::kPart + 31) / 32];
+            if (tile_done) {
+                if (valid) ws = ld_dep(reinterpret_cast<const float *>(p.w_scales + ch * p.w_scale_stride));
+#pragma unroll
+                for (int i = 0; i < (T::kPart + 31) / 32; ++i)
+                    as[i] = t0 + i * 32 + lane < p.tokens ? ld_dep(p.scales + t0 + i * 32 + lane) : 0.0f;
+            }
+            const bool ok = wait_or_abort(&sm.acc_full[sc.i], sc.parity, &sm.abort_flag, p.err);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc_fence_after();
+            const uint32_t src = tmem + lanes + sc.i * NMAX + g * part;
+            if (kd == in) {  // the tile's first sum
+                whole = false;
+#pragma unroll
+                for (int c = 0; c < T::kPart; c += 8) {
+                    if (c >= part) break;
+                    tmem_ld8(src + c, &acc[c]);
+                }
+            } else {
+                // f32 still holds the new sums exactly where all of them stay below 2^24 (a
+                // larger one would round to 2^24 at least)
+                float big = 0.0f;
+                if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < T::kPart; c += 8) {
+                        if (c >= part) break;
+                        float v[8];
+                        tmem_ld8(src + c, v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(acc[c + i] + v[i]));
+                    }
+                    if (__any_sync(0xFFFFFFFFu, big >= 16777216.0f)) {
+                        whole = true;
+#pragma unroll
+                        for (int c = 0; c < T::kPart; ++c) acc[c] = __int_as_float(__float2int_rn(acc[c]));
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < T::kPart; c += 8) {
+                        if (c >= part) break;
+                        float v[8];
+                        tmem_ld8(src + c, v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[c + i] += v[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < T::kPart; c += 8) {
+                        if (c >= part) break;
+                        float v[8];
+                        tmem_ld8(src + c, v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            acc[c + i] = __int_as_float(__float_as_int(acc[c + i]) + __float2int_rn(v[i]));
+                    }
                 }
             }
-            // the copies have landed, and the commits on the widened codes' slots have arrived
-            for (int64_t i = j > SW ? j - SW : 0; i < j; ++i) mbar_wait(&sm.table_full[i % SW], (i / SW) & 1, kWaitTimeoutNs);
-            for (int64_t i = total > kASlots ? total - kASlots : 0; i < total; ++i)
-                if (!wait_or_abort(&sm.a_empty[i % kASlots], (i / kASlots) & 1, &sm.abort_flag, p.err)) break;
-        }
-    } else if (warp == kConvWarps + 1) {
-        // ---------------- token producer ----------------
-        if (lane == 0) {
-            tma_prefetch_map(&tm_token);
-            pdl_wait();
-            const int half = p.n / 2;
-            int64_t j = 0;
-            bool ok = true;
-            for (int64_t it = cl; it < p.items && ok; it += clusters) {
-                const int32_t row = static_cast<int32_t>(it % p.blocks) * p.n + static_cast<int32_t>(rank) * half;
-                for (int kc = 0; kc < p.nk; ++kc, ++j) {
-                    const int s = static_cast<int>(j % SX);
-                    if (!wait_or_abort(&sm.token_empty[s], ((j / SX) & 1) ^ 1, &sm.abort_flag, p.err)) {
-                        ok = false;
-                        break;
-                    }
-                    if (rank == 0) mbar_arrive_expect_tx(&sm.token_full[s], 2 * half * kStageK * 2);
-                    const uint32_t bar = cluster_addr(smem_u32(&sm.token_full[s]), 0);
-                    tma_load_2d_pair(sm.token[s], &tm_token, bar, kc * kStageK, row);
-                    tma_load_2d_pair(sm.token[s] + half * 128, &tm_token, bar, kc * kStageK + 64, row);
-                }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&sm.acc_empty[sc.i]), 0));
+            sc.next();
+            in = 0;
+            if (!tile_done) continue;
+            kd = 0;
+            it += clusters;
+            const int64_t left = p.tokens - t0;
+            const int cols = static_cast<int>(left < part ? left : part);
+            if (whole) {
+#pragma unroll
+                for (int c = 0; c < T::kPart; ++c) acc[c] = static_cast<float>(__float_as_int(acc[c]));
             }
-            for (int64_t i = j > SX ? j - SX : 0; i < j; ++i)
-                if (!wait_or_abort(&sm.token_empty[i % SX], (i / SX) & 1, &sm.abort_flag, p.err)) break;
+            auto emit = [&](auto *out) {
+                out += t0 * p.out_stride + ch;
+#pragma unroll
+                for (int c = 0; c < T::kPart; ++c) {
+                    if (c % 8 == 0 && c >= cols) break;
+                    const float v = __fmul_rn(
+                        __fmul_rn(acc[c], __shfl_sync(0xFFFFFFFFu, as[c / 32], c % 32)), ws);
+                    if (valid && c < cols) put(out, v);
+                    out += p.out_stride;
+                }
+            };
+            if (p.out_dtype == LHS_F32) emit(static_cast<float *>(p.out));
+            else if (p.out_dtype == LHS_F16) emit(static_cast<__half *>(p.out));
+            else emit(static_cast<__nv_bfloat16 *>(p.out));
         }
     } else {
-        // blocks of 128 that may be summed in f32
-        pdl_wait();
-        int peak = 0;
-        for (int64_t t = lane; t < p.tokens; t += 32) peak = max(peak, ld_dep(p.peaks + t));
-        peak = __reduce_max_sync(0xFFFFFFFFu, peak);
-        const int chunk = peak ? kPeakBlocks / peak : p.nk;
-
-        if (warp == kConvWarps + 2) {
+        if constexpr (NMAX == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == kConvWarps) {
+            // ---------------- table producer (does not wait for the tokens) ----------------
+            if (lane == 0) {
+                tma_prefetch_map(&tm_table);
+                int64_t j = 0;
+                Ring<SW> st;
+                bool ok = true;
+                for (int64_t it = cl; it < p.items && ok; it += clusters) {
+                    const int32_t row = static_cast<int32_t>(it / p.blocks) * kPairRows + static_cast<int32_t>(rank) * kCtaRows;
+                    for (int kc = 0; kc < p.nk; ++kc, ++j, st.next()) {
+                        if (!wait_or_abort(&sm.table_empty[st.i], st.parity ^ 1u, &sm.abort_flag, p.err)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&sm.table_full[st.i], kTableStageBytes);
+                        tma_load_2d(sm.table[st.i], &tm_table, &sm.table_full[st.i], kc * kStageK, row);
+                    }
+                }
+                // the copies have landed
+                for (int64_t i = j > SW ? j - SW : 0; i < j; ++i) mbar_wait(&sm.table_full[i % SW], (i / SW) & 1, kWaitTimeoutNs);
+            }
+        } else if (warp == kConvWarps + 1) {
+            // ---------------- token producer ----------------
+            if (lane == 0) {
+                tma_prefetch_map(&tm_token);
+                pdl_wait();
+                const int half = p.n / 2;
+                int64_t j = 0;
+                Ring<SX> st;
+                bool ok = true;
+                for (int64_t it = cl; it < p.items && ok; it += clusters) {
+                    const int32_t row = static_cast<int32_t>(it % p.blocks) * p.n + static_cast<int32_t>(rank) * half;
+                    for (int kc = 0; kc < p.nk; ++kc, ++j, st.next()) {
+                        const int s = st.i;
+                        if (!wait_or_abort(&sm.empty[s], st.parity ^ 1u, &sm.abort_flag, p.err)) {
+                            ok = false;
+                            break;
+                        }
+                        if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * half * kStageK * 2);
+                        const uint32_t bar = cluster_addr(smem_u32(&sm.full[s]), 0);
+                        tma_load_2d_pair(sm.token[s], &tm_token, bar, kc * kStageK, row);
+                        tma_load_2d_pair(sm.token[s] + half * 128, &tm_token, bar, kc * kStageK + 64, row);
+                    }
+                }
+                // the copies have landed and the last commits have arrived
+                for (int64_t i = j > SX ? j - SX : 0; i < j; ++i)
+                    if (!wait_or_abort(&sm.empty[i % SX], (i / SX) & 1, &sm.abort_flag, p.err)) break;
+            }
+        } else if (warp == kConvWarps + 2) {
             // ---------------- MMA issuer (the leader CTA only) ----------------
+            pdl_wait();
+            const int chunk = blocks_per_sum(p, lane);
             if (lane == 0 && rank == 0) {
                 const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.n >> 3) << 17) |
                                        (static_cast<uint32_t>(kPairRows >> 4) << 24);  // f16 x f16 -> f32
                 const uint32_t half_bytes = static_cast<uint32_t>(p.n / 2) * 128;
-                int64_t j = 0, c = 0;  // stage, sum
-                bool ok = true;
+                Ring<SX> sx;
+                Ring<ACCS> sc;
+                bool ok = true, ready = false;
                 for (int64_t it = 0; it < mine && ok; ++it) {
                     int in = 0;  // stages of the current sum
-                    for (int kc = 0; kc < p.nk; ++kc, ++j) {
-                        const int buf = static_cast<int>(c % ACCS);
-                        const int sa = static_cast<int>(j % kASlots), sx = static_cast<int>(j % SX);
-                        if ((in == 0 && !wait_or_abort(&sm.acc_empty[buf], ((c / ACCS) & 1) ^ 1, &sm.abort_flag, p.err)) ||
-                            !wait_or_abort(&sm.token_full[sx], (j / SX) & 1, &sm.abort_flag, p.err) ||
-                            !wait_or_abort(&sm.a_full[sa], (j / kASlots) & 1, &sm.abort_flag, p.err)) {
+                    for (int kc = 0; kc < p.nk; ++kc) {
+                        if ((in == 0 && !wait_or_abort(&sm.acc_empty[sc.i], sc.parity ^ 1u, &sm.abort_flag, p.err)) ||
+                            (!ready && !wait_or_abort(&sm.full[sx.i], sx.parity, &sm.abort_flag, p.err))) {
                             ok = false;
                             break;
                         }
-                        fence_acquire_cluster();  // the peer's warps arrived on these barriers too
                         tc_fence_after();
-                        const uint32_t d = tmem + buf * NMAX, a = tmem + kTmemA + sa * (kStageK / 2);
-                        const uint32_t b = smem_u32(sm.token[sx]);
-#pragma unroll
+                        const uint32_t d = tmem + sc.i * NMAX, a = tmem + T::kColA + sx.i * kSlotCols;
+                        const uint32_t b = smem_u32(sm.token[sx.i]);
+                        uint64_t *done = &sm.empty[sx.i];
+                        sx.next();
+                        // a look at the next stage, whose answer the MMAs' issue hides
+                        ready = mbar_test_cluster(&sm.full[sx.i], sx.parity);
+    #pragma unroll
                         for (int ks = 0; ks < kStageK / 16; ++ks)
                             umma_f16_ts(d, a + ks * 8, desc_sw128(b + (ks >> 2) * half_bytes + (ks & 3) * 32), idesc,
                                         (in | ks) != 0);
-                        umma_commit_both(&sm.token_empty[sx]);
-                        umma_commit_both(&sm.a_empty[sa]);
+                        umma_commit_both(done);
                         ++in;
                         if (in == chunk || kc + 1 == p.nk) {
-                            umma_commit_both(&sm.acc_full[buf]);
+                            umma_commit_both(&sm.acc_full[sc.i]);
                             in = 0;
-                            ++c;
+                            sc.next();
                         }
-                    }
-                }
-            }
-        } else {
-            // ---------------- widen the codes, take the sums out ----------------
-            const int q = warp & 3, h = warp >> 2;  // TMEM lane quarter; half of the k, then of the tokens
-            const int row = q * 32 + lane;
-            const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
-            const int half = p.n / 2;
-            int acc[NMAX / 2];  // sums of this channel against its half of the tile's tokens
-            int64_t c = 0, it = cl;
-            int kd = 0, in = 0;  // stage of the tile, of the sum, that the sums have got to
-            for (int64_t j = 0; j < total + kAhead; ++j) {
-                if (j < total) {
-                    const int s = static_cast<int>(j % SW), sa = static_cast<int>(j % kASlots);
-                    bool ok = wait_or_abort(&sm.table_full[s], (j / SW) & 1, &sm.abort_flag, p.err);
-                    uint4 w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)  // 16-byte piece 4h + i of this row, swizzled
-                        w[i] = *reinterpret_cast<const uint4 *>(sm.table[s] + row * kStageK + (((4 * h + i) ^ (row & 7)) << 4));
-                    uint32_t f[32];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        widen4(w[i].x, f[8 * i], f[8 * i + 1]);
-                        widen4(w[i].y, f[8 * i + 2], f[8 * i + 3]);
-                        widen4(w[i].z, f[8 * i + 4], f[8 * i + 5]);
-                        widen4(w[i].w, f[8 * i + 6], f[8 * i + 7]);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.table_empty[s]);
-                    ok = ok && wait_or_abort(&sm.a_empty[sa], ((j / kASlots) & 1) ^ 1, &sm.abort_flag, p.err);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) break;  // the tcgen05 instructions are warp-collective
-                    tc_fence_after();
-                    tmem_st32(tmem + lanes + kTmemA + sa * (kStageK / 2) + h * 32, f);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&sm.a_full[sa]), 0));
-                }
-                if (j < kAhead) continue;
-                // stage j - kAhead: does a sum end with it?
-                ++in;
-                ++kd;
-                const bool tile_done = kd == p.nk;
-                if (in < chunk && !tile_done) continue;
-                const int buf = static_cast<int>(c % ACCS);
-                const bool ok = wait_or_abort(&sm.acc_full[buf], (c / ACCS) & 1, &sm.abort_flag, p.err);
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
-                tc_fence_after();
-                const bool first = kd == in;
-#pragma unroll
-                for (int g = 0; g < NMAX / 32; ++g) {
-                    if (g * 16 >= half) break;
-                    float v[16];
-                    tmem_ld16(tmem + lanes + buf * NMAX + h * half + g * 16, v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int s = __float2int_rn(v[i]);
-                        acc[g * 16 + i] = first ? s : acc[g * 16 + i] + s;
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&sm.acc_empty[buf]), 0));
-                ++c;
-                in = 0;
-                if (!tile_done) continue;
-                kd = 0;
-                const int64_t ch = it / p.blocks * kPairRows + static_cast<int64_t>(rank) * kCtaRows + row;
-                const int64_t t0 = it % p.blocks * p.n + h * half;
-                it += clusters;
-                const bool valid = ch < p.channels;
-                const float ws = valid ? ld_dep(reinterpret_cast<const float *>(p.w_scales + ch * p.w_scale_stride)) : 0.0f;
-#pragma unroll
-                for (int g = 0; g < NMAX / 32; ++g) {
-                    if (g * 16 >= half || t0 + g * 16 >= p.tokens) break;
-                    const int64_t ts = t0 + g * 16 + (lane & 15);
-                    const float as = ts < p.tokens ? ld_dep(p.scales + ts) : 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float sc = __shfl_sync(0xFFFFFFFFu, as, i);
-                        const int64_t t = t0 + g * 16 + i;
-                        if (valid && t < p.tokens)
-                            store_out(p.out, p.out_dtype, t * p.out_stride + ch,
-                                      __fmul_rn(__fmul_rn(static_cast<float>(acc[g * 16 + i]), sc), ws));
                     }
                 }
             }
@@ -630,7 +745,7 @@ cudaError_t launch_product(const CUtensorMap &tm_table, const CUtensorMap &tm_to
     constexpr int smem = 1024 + static_cast<int>(sizeof(Smem<NMAX>));
     auto kern = i8_matmul_kernel<NMAX>;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Tile<NMAX>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
