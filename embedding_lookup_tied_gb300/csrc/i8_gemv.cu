@@ -1,0 +1,357 @@
+// i8_gemv.cu — the 8-bit lm_head product of up to eight tokens: the table
+// streams through shared memory once and is multiplied as it is, in integers.
+//
+// With m tokens a table byte carries 2 m operations, far below the ridge, so
+// the floor is the table's bytes at the HBM rate: 23.5 bytes a clock and SM.
+// mma.sync.m16n8k32 in s8 takes the codes straight from shared memory (no
+// widening), sums them exactly in 32 bits, and does 260 products a clock and
+// SM here, as many as four-way dot products do; with its eight columns that
+// is a 16 KB stage in 504 clocks, where HBM needs 697 to bring it.  (The
+// tcgen05 kernel of i8_matmul.cu, whose operand has to pass through tensor
+// memory, needs about 1,100 for a stage of so few tokens.)
+//
+// One CTA per SM: eight warps, each with 16 of a tile's 128 rows, and a
+// producer that keeps the ring of TMA boxes full.  The CTAs take the 128-row
+// tiles in turn; the rows that do not fill a round of them are split evenly,
+// in units of 16 rows with boxes of that size.  The tokens are quantised by
+// every CTA for itself while its ring fills, so a call is one launch.
+#include <mutex>
+
+#include "i8_common.cuh"
+
+namespace lhs {
+namespace {
+
+constexpr int kMaxTokens = 8;
+constexpr int kWarps = 8;
+constexpr int kConsumers = 32 * kWarps;
+constexpr int kThreads = kConsumers + 32;  // + producer
+constexpr int kUnitRows = 16;
+constexpr int kUnitBytes = kUnitRows * kStageK;
+constexpr int kMaxStages = 13;
+constexpr int kMaxHidden = 12288;  // tokens' codes: at most 98 KB beside seven stages
+constexpr int kSmemBytes = 224 * 1024;
+
+__host__ __device__ constexpr int round_up(int v, int a) { return (v + a - 1) / a * a; }
+// Token rows 16 bytes past a multiple of 128: eight rows' 16-byte pieces lie
+// in different banks.
+__host__ __device__ constexpr int token_pitch(int hidden) { return round_up(hidden, kStageK) + 16; }
+
+struct Head {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    float scale[kMaxTokens];
+    float part[kWarps][kMaxTokens];
+    int bad[kWarps];
+    int abort_flag;
+};
+
+struct Params {
+    I8Tokens a;
+    bool vec;           // four wide values (or codes) of a token may be loaded at once
+    const uint8_t *w_scales;
+    int64_t w_scale_stride;
+    int64_t channels;
+    int hidden, nst;
+    void *out;
+    int64_t out_stride;
+    int out_dtype;
+    int32_t *err;
+};
+
+// The tiles of one CTA: `rounds` full ones, then `units` units of 16 rows.
+struct Share {
+    int64_t rounds, tail;
+    int units;
+    __device__ __forceinline__ Share(int64_t channels) {
+        const int64_t round_rows = static_cast<int64_t>(gridDim.x) * kCtaRows;
+        rounds = channels / round_rows;
+        const int64_t u = (channels - rounds * round_rows + kUnitRows - 1) / kUnitRows;
+        const int64_t u0 = u * blockIdx.x / gridDim.x, u1 = u * (blockIdx.x + 1) / gridDim.x;
+        tail = rounds * round_rows + u0 * kUnitRows;
+        units = static_cast<int>(u1 - u0);
+    }
+    __device__ __forceinline__ int64_t tiles() const { return rounds + (units > 0 ? 1 : 0); }
+    __device__ __forceinline__ int64_t row(int64_t i) const {
+        return i < rounds ? (i * gridDim.x + blockIdx.x) * kCtaRows : tail;
+    }
+};
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_s8(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// DT: the tokens' type, or -1 for codes.
+template <int DT>
+__device__ __forceinline__ void stage_tokens(const Params &p, uint8_t *tok, Head &sm, int tid) {
+    const int warp = tid >> 5, lane = tid & 31;
+    const int pitch = token_pitch(p.hidden), groups = (pitch - 16) / 4, m = static_cast<int>(p.a.rows);
+    if constexpr (DT < 0) {
+        for (int i = tid; i < kMaxTokens * groups; i += kConsumers) {
+            const int t = i / groups, j = (i - t * groups) * 4;
+            uint32_t w = 0;
+            if (t < m) {
+                const int8_t *row = p.a.coded.codes + t * p.a.coded.stride;
+                if (p.vec && j + 4 <= p.hidden) w = ld_dep(reinterpret_cast<const uint32_t *>(row + j));
+                else
+                    for (int e = 0; e < 4; ++e)
+                        if (j + e < p.hidden) w |= static_cast<uint32_t>(static_cast<uint8_t>(ld_dep(row + j + e))) << (8 * e);
+            }
+            *reinterpret_cast<uint32_t *>(tok + t * pitch + j) = w;
+        }
+        if (tid < kMaxTokens) sm.scale[tid] = tid < m ? coded_scale(p.a.coded, tid, blockIdx.x == 0 ? p.err : nullptr) : 0.0f;
+        named_bar_sync(1, kConsumers);
+    } else {
+        using E = typename Elem<DT>::T;
+        const E *x = static_cast<const E *>(p.a.x);
+        // max|x| of every token (whether all are finite in bad), then scales and codes; the
+        // second reading comes from L2
+        float mx[kMaxTokens];
+        uint32_t bad = 0;
+#pragma unroll
+        for (int t = 0; t < kMaxTokens; ++t) {
+            mx[t] = 0.0f;
+            if (t >= m) continue;
+#pragma unroll 4
+            for (int g = tid; g < groups; g += kConsumers) {
+                float v[4];
+                load4<DT>(x + t * p.a.x_stride, 4 * g, p.hidden, p.vec, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (isfinite(v[i])) mx[t] = fmaxf(mx[t], fabsf(v[i]));
+                    else bad |= 1u << t;
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < kMaxTokens; ++t) {
+            if (t >= m) continue;
+            const uint32_t u = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mx[t]));
+            if (lane == 0) sm.part[warp][t] = __uint_as_float(u);
+        }
+        bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+        if (lane == 0) sm.bad[warp] = static_cast<int>(bad);
+        named_bar_sync(1, kConsumers);
+        for (int w = 0; w < kWarps; ++w) bad |= static_cast<uint32_t>(sm.bad[w]);
+        if (tid == 0 && blockIdx.x == 0 && bad) set_err(p.err, LHS_ERRBIT_NONFINITE);
+        for (int t = 0; t < kMaxTokens; ++t) {
+            float top = 0.0f;
+            if (t < m)
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.part[w][t]);
+            const float scale = (bad >> t) & 1u ? 0.0f : __fdiv_rn(top, 127.0f);
+            const float rcp = __frcp_rn(scale);
+            if (tid == 0) sm.scale[t] = scale;
+#pragma unroll 4
+            for (int g = tid; g < groups; g += kConsumers) {
+                uint32_t w = 0;
+                if (t < m) {
+                    float v[4];
+                    load4<DT>(x + t * p.a.x_stride, 4 * g, p.hidden, p.vec, v);
+                    w = i8_code4(v, scale, rcp);
+                }
+                *reinterpret_cast<uint32_t *>(tok + t * pitch + 4 * g) = w;
+            }
+        }
+        named_bar_sync(1, kConsumers);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    i8_gemv_kernel(const __grid_constant__ CUtensorMap tm_tile, const __grid_constant__ CUtensorMap tm_unit,
+                   const Params p) {
+    extern __shared__ uint8_t dyn_smem[];
+    uint8_t *ring = smem_align<1024>(dyn_smem);
+    const int pitch = token_pitch(p.hidden);
+    uint8_t *tok = ring + p.nst * kTableStageBytes;
+    Head &sm = *reinterpret_cast<Head *>(tok + kMaxTokens * pitch);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Share share(p.channels);
+    const int nk = (p.hidden + kStageK - 1) / kStageK;
+
+    if (tid == 0) {
+        for (int s = 0; s < p.nst; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], kWarps);
+        }
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_trigger();
+    pdl_wait();  // the table may have been quantised, the tokens written, by the kernel before
+
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int *>(&sm.abort_flag)) return false;
+        if (mbar_wait(bar, parity, kWaitTimeoutNs)) return true;
+        set_err(p.err, LHS_ERRBIT_TIMEOUT);
+        *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
+        return false;
+    };
+
+    if (warp == kWarps) {
+        if (lane == 0) {
+            tma_prefetch_map(&tm_tile);
+            int s = 0, issued = 0;
+            uint32_t parity = 1;
+            bool ok = true;
+            for (int64_t i = 0; i < share.tiles() && ok; ++i) {
+                const int32_t row = static_cast<int32_t>(share.row(i));
+                for (int kc = 0; kc < nk; ++kc) {
+                    if (!wait(&sm.empty[s], parity)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *dst = ring + s * kTableStageBytes;
+                    if (i < share.rounds) {
+                        mbar_arrive_expect_tx(&sm.full[s], kTableStageBytes);
+                        tma_load_2d(dst, &tm_tile, &sm.full[s], kc * kStageK, row);
+                    } else {
+                        mbar_arrive_expect_tx(&sm.full[s], share.units * kUnitBytes);
+                        for (int u = 0; u < share.units; ++u)
+                            tma_load_2d(dst + u * kUnitBytes, &tm_unit, &sm.full[s], kc * kStageK, row + u * kUnitRows);
+                    }
+                    if (issued < p.nst) ++issued;
+                    if (++s == p.nst) {
+                        s = 0;
+                        parity ^= 1u;
+                    }
+                }
+            }
+            // every stage that was issued has been taken, so no copy is still on its way
+            for (int i = 0; i < issued; ++i) {
+                if (--s < 0) {
+                    s = p.nst - 1;
+                    parity ^= 1u;
+                }
+                // parity is the one its filling waited for; the next phase ends when it is taken
+                if (!wait(&sm.empty[s], parity ^ 1u)) {
+                    mbar_wait(&sm.full[s], parity ^ 1u, kWaitTimeoutNs);
+                }
+            }
+        }
+        return;
+    }
+
+    if (!p.a.x) stage_tokens<-1>(p, tok, sm, tid);
+    else if (p.a.x_dtype == LHS_F32) stage_tokens<LHS_F32>(p, tok, sm, tid);
+    else if (p.a.x_dtype == LHS_F16) stage_tokens<LHS_F16>(p, tok, sm, tid);
+    else stage_tokens<LHS_BF16>(p, tok, sm, tid);
+
+    // ldmatrix addresses: lanes 8 i .. 8 i + 7 name the rows of matrix i.  A:
+    // rows 0-7 and 8-15 of the warp's 16, then the same 16 bytes further on; B:
+    // the eight tokens at four 16-byte steps.
+    const int arow = warp * 16 + (lane & 15), apiece = lane >> 4;
+    const uint32_t a_addr = smem_u32(ring) + arow * kStageK;
+    const uint32_t b_addr = smem_u32(tok) + (lane & 7) * pitch + (lane >> 3) * 16;
+    const int g = lane >> 2, t2 = (lane & 3) * 2;  // this thread's rows g, g + 8 and tokens t2, t2 + 1
+    const int m = static_cast<int>(p.a.rows);
+    const float as[2] = {sm.scale[t2], sm.scale[t2 + 1]};
+    int s = 0;
+    uint32_t parity = 0;
+    for (int64_t i = 0; i < share.tiles(); ++i) {
+        const bool mine = i < share.rounds || warp < share.units;  // the last tile may be short
+        const int64_t ch = share.row(i) + warp * 16 + g;
+        float ws[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            ws[h] = mine && ch + 8 * h < p.channels
+                        ? ld_dep(reinterpret_cast<const float *>(p.w_scales + (ch + 8 * h) * p.w_scale_stride))
+                        : 0.0f;
+        int c[2][4] = {};
+        for (int kc = 0; kc < nk; ++kc) {
+            if (!__all_sync(0xFFFFFFFFu, wait(&sm.full[s], parity))) return;
+            if (mine) {
+                const uint32_t base = a_addr + s * kTableStageBytes;
+                uint32_t a[4][4], b[2][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) ldmatrix_x4(base + (((2 * q + apiece) ^ (arow & 7)) << 4), a[q]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) ldmatrix_x4(b_addr + kc * kStageK + q * 64, b[q]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mma_s8(c[q & 1], a[q], b[q >> 1][2 * (q & 1)], b[q >> 1][2 * (q & 1) + 1]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[s]);
+            if (++s == p.nst) {
+                s = 0;
+                parity ^= 1u;
+            }
+        }
+        if (!mine) continue;
+        auto emit = [&](auto *out) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float v = __fmul_rn(
+                        __fmul_rn(static_cast<float>(c[0][2 * h + e] + c[1][2 * h + e]), as[e]), ws[h]);
+                    if (t2 + e < m && ch + 8 * h < p.channels) put(out + (t2 + e) * p.out_stride + ch + 8 * h, v);
+                }
+        };
+        if (p.out_dtype == LHS_F32) emit(static_cast<float *>(p.out));
+        else if (p.out_dtype == LHS_F16) emit(static_cast<__half *>(p.out));
+        else emit(static_cast<__nv_bfloat16 *>(p.out));
+    }
+}
+
+}  // namespace
+
+// The tokens' codes stay in shared memory, so hidden is bounded.
+bool i8_gemv_serves(const lhs_i8 &table, int64_t tokens) {
+    return tokens <= kMaxTokens && table.hidden <= kMaxHidden;
+}
+
+cudaError_t launch_i8_gemv(const I8Tokens &a, const lhs_i8 &table, void *out, int32_t out_dtype,
+                           int64_t out_stride, int32_t *err, const DeviceInfo &dev, cudaStream_t stream) {
+    Params p = {};
+    p.a = a;
+    if (a.x) {
+        const int64_t size = a.x_dtype == LHS_F32 ? 4 : 2;
+        p.vec = reinterpret_cast<uintptr_t>(a.x) % (4 * size) == 0 && a.x_stride % 4 == 0;
+    } else {
+        p.vec = reinterpret_cast<uintptr_t>(a.coded.codes) % 4 == 0 && a.coded.stride % 4 == 0;
+    }
+    p.w_scales = reinterpret_cast<const uint8_t *>(table.scales);
+    p.w_scale_stride = table.scale_stride;
+    p.channels = table.rows;
+    p.hidden = table.hidden;
+    p.out = out;
+    p.out_stride = out_stride;
+    p.out_dtype = out_dtype;
+    p.err = err;
+    const int fixed = 1024 + kMaxTokens * token_pitch(table.hidden) + static_cast<int>(sizeof(Head));
+    p.nst = (kSmemBytes - fixed) / kTableStageBytes;
+    if (p.nst > kMaxStages) p.nst = kMaxStages;
+    CUtensorMap tm_tile, tm_unit;
+    if (!make_map(&tm_tile, CU_TENSOR_MAP_DATA_TYPE_UINT8, table.codes, table.hidden, table.rows, table.stride, kStageK,
+                  kCtaRows) ||
+        !make_map(&tm_unit, CU_TENSOR_MAP_DATA_TYPE_UINT8, table.codes, table.hidden, table.rows, table.stride, kStageK,
+                  kUnitRows))
+        return cudaErrorInvalidValue;
+    {
+        static std::mutex mu;
+        static bool done[64] = {};
+        std::lock_guard<std::mutex> lock(mu);
+        if (!done[dev.device]) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(i8_gemv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+            if (e != cudaSuccess) return e;
+            done[dev.device] = true;
+        }
+    }
+    const int64_t units = (table.rows + kUnitRows - 1) / kUnitRows;
+    const unsigned grid = static_cast<unsigned>(units < dev.num_sms ? units : dev.num_sms);
+    return launch_pdl(i8_gemv_kernel, dim3(grid), dim3(kThreads), fixed + p.nst * kTableStageBytes, stream, tm_tile,
+                      tm_unit, p);
+}
+
+}  // namespace lhs

@@ -18,22 +18,15 @@
 // for each token, the largest sum|a| over 128 codes, b, so n = floor(2^24 /
 // (128 b)) blocks of 128 (at least 8) may be summed in the tensor cores.  Longer
 // sums are taken out every n blocks and added up as 32-bit integers.
-#include <cudaTypedefs.h>
-#include <cuda_bf16.h>
-
 #include <mutex>
 
-#include "decode.cuh"
+#include "i8_common.cuh"
 
 namespace lhs {
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // lm_head.cu
 
 namespace {
 
 __host__ __device__ constexpr int64_t align_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
-
-constexpr int kStageK = 128;  // codes per ring stage
 
 // Workspace: the tokens as f16 [tokens][kpad] (zeros past hidden), their
 // scales, and each one's largest sum|a| over a block of 128 codes.
@@ -57,24 +50,6 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepWarps = kPrepThreads / 32;
 constexpr int kPrepSteps = 6;  // blocks of 128 a warp keeps in registers: rows up to 6,144 values
 
-// Where a coded token set is a message, whether its header names another
-// seq_len (the words lie before the first position).
-__device__ __forceinline__ bool message_mismatch(const lhs_i8 &a) {
-    const uint8_t *buf = reinterpret_cast<const uint8_t *>(a.scales) - a.header;
-    return ld_dep(reinterpret_cast<const uint32_t *>(buf) + 1) != static_cast<uint32_t>(a.rows);
-}
-// The scale of coded token r; NaN (and MALFORMED) where its message is not
-// one the product can take.  Called by one thread.
-__device__ __forceinline__ float coded_scale(const lhs_i8 &a, int64_t r, int32_t *err) {
-    const uint8_t *p = reinterpret_cast<const uint8_t *>(a.scales) + r * a.scale_stride;
-    float s = ld_dep(reinterpret_cast<const float *>(p));
-    if (a.header && (message_mismatch(a) || ld_dep(reinterpret_cast<const float *>(p) + 1) != 0.0f)) {
-        set_err(err, LHS_ERRBIT_MALFORMED);
-        s = __int_as_float(0x7FC00000);
-    }
-    return s;
-}
-
 // Four codes (small integers) as f16, and the warp's sum of their magnitudes.
 __device__ __forceinline__ int store_codes(__half *dst, const int (&q)[4]) {
     const __half2 a = __floats2half2_rn(static_cast<float>(q[0]), static_cast<float>(q[1]));
@@ -82,26 +57,6 @@ __device__ __forceinline__ int store_codes(__half *dst, const int (&q)[4]) {
     *reinterpret_cast<uint2 *>(dst) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
     return __reduce_add_sync(0xFFFFFFFFu, abs(q[0]) + abs(q[1]) + abs(q[2]) + abs(q[3]));
-}
-
-// Values j .. j+3 of a row (zeros past hidden).
-template <int DT>
-__device__ __forceinline__ void load4(const typename Elem<DT>::T *row, int j, int hidden, bool vec,
-                                      float (&v)[4]) {
-    using E = Elem<DT>;
-    if (vec && j + 4 <= hidden) {
-        if (DT == LHS_F32) {
-            const float4 w = ld_dep(reinterpret_cast<const float4 *>(row + j));
-            v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-        } else {
-            const ushort4 w = ld_dep(reinterpret_cast<const ushort4 *>(row + j));
-            v[0] = E::widen(static_cast<typename E::T>(w.x)); v[1] = E::widen(static_cast<typename E::T>(w.y));
-            v[2] = E::widen(static_cast<typename E::T>(w.z)); v[3] = E::widen(static_cast<typename E::T>(w.w));
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = j + i < hidden ? E::widen(ld_dep(row + j + i)) : 0.0f;
-    }
 }
 
 // One CTA per wide token; a warp takes blocks of 128 values, four to a lane,
@@ -211,9 +166,7 @@ __global__ void __launch_bounds__(kPrepThreads)
 // ---------------------------------------------------------------------------
 // product
 // ---------------------------------------------------------------------------
-constexpr int kCtaRows = 128;                       // channels per CTA: TMEM lanes
-constexpr int kPairRows = 2 * kCtaRows;
-constexpr int kTableStageBytes = kCtaRows * kStageK;  // 16 KB of codes
+constexpr int kPairRows = 2 * kCtaRows;             // a CTA's are its TMEM lanes
 constexpr int kTmemCols = 512;
 constexpr int kSlotCols = kStageK / 2;              // of one stage's widened codes
 constexpr int kPeakBlocks = (1 << 24) / kStageK;    // n = kPeakBlocks / peak
@@ -409,10 +362,6 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, in
     *reinterpret_cast<volatile int *>(abort_flag) = 1;
     return false;
 }
-
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // Blocks of 128 codes that may be summed in f32.  Warp-collective.
 __device__ __forceinline__ int blocks_per_sum(const Params &p, int lane) {
@@ -726,19 +675,6 @@ __global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-bool make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols, uint64_t rows,
-              uint64_t pitch, uint32_t box_cols, uint32_t box_rows) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {pitch};
-    const cuuint32_t box[2] = {box_cols, box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(map, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int NMAX>
 cudaError_t launch_product(const CUtensorMap &tm_table, const CUtensorMap &tm_token, const Params &p,
                            const DeviceInfo &dev, cudaStream_t stream) {
@@ -800,6 +736,7 @@ cudaError_t launch_i8_matmul(const I8Tokens &a, const lhs_i8 &table, void *out, 
     DeviceInfo dev;
     cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return e;
+    if (i8_gemv_serves(table, a.rows)) return launch_i8_gemv(a, table, out, out_dtype, out_stride, err, dev, stream);
     uint8_t *ws = static_cast<uint8_t *>(ws_);
     const Layout l = layout_of(table.hidden, a.rows);
 
