@@ -55,6 +55,19 @@ __device__ __forceinline__ void load4(const typename Elem<DT>::T *row, int j, in
     }
 }
 
+// Four codes, their sign bits flipped (code + 128), as f16 in order: under the
+// exponent byte 0x64 code + 128 is 1024 + code + 128; less 1152 it is the code,
+// exactly.
+__device__ __forceinline__ void widen4(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    const uint32_t bias = 0x64806480u;  // 1152, 1152
+    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+    const __half2 c = *reinterpret_cast<const __half2 *>(&bias);
+    const __half2 p = __hsub2(*reinterpret_cast<const __half2 *>(&a), c);
+    const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&b), c);
+    lo = *reinterpret_cast<const uint32_t *>(&p);
+    hi = *reinterpret_cast<const uint32_t *>(&q);
+}
+
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }

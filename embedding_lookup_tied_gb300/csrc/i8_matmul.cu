@@ -297,19 +297,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-// Four signed codes as f16, in order: code + 128 under the exponent byte 0x64
-// is 1024 + code + 128; less 1152 it is the code, exactly.
-__device__ __forceinline__ void widen4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
-    const uint32_t x = codes ^ 0x80808080u;
-    const uint32_t bias = 0x64806480u;  // 1152, 1152
-    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
-    const __half2 c = *reinterpret_cast<const __half2 *>(&bias);
-    const __half2 p = __hsub2(*reinterpret_cast<const __half2 *>(&a), c);
-    const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&b), c);
-    lo = *reinterpret_cast<const uint32_t *>(&p);
-    hi = *reinterpret_cast<const uint32_t *>(&q);
-}
-
 // A place in a ring of N slots and the parity of its phase.
 template <int N>
 struct Ring {
@@ -454,10 +441,10 @@ __global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {  // 16-byte piece 4o + i of this row, swizzled
                         const uint4 u = *reinterpret_cast<const uint4 *>(src + (((4 * o + i) ^ (row & 7)) << 4));
-                        widen4(u.x, f[8 * i], f[8 * i + 1]);
-                        widen4(u.y, f[8 * i + 2], f[8 * i + 3]);
-                        widen4(u.z, f[8 * i + 4], f[8 * i + 5]);
-                        widen4(u.w, f[8 * i + 6], f[8 * i + 7]);
+                        widen4(u.x ^ 0x80808080u, f[8 * i], f[8 * i + 1]);
+                        widen4(u.y ^ 0x80808080u, f[8 * i + 2], f[8 * i + 3]);
+                        widen4(u.z ^ 0x80808080u, f[8 * i + 4], f[8 * i + 5]);
+                        widen4(u.w ^ 0x80808080u, f[8 * i + 6], f[8 * i + 7]);
                     }
                     tmem_st32(dst + o * 32, f);
                 }

@@ -190,7 +190,7 @@ def test_quantize_special_values():
     assert np.array_equal(t.scales.cpu().numpy(), s) and np.array_equal(t.codes.cpu().numpy(), q)
 
 
-SIZES = [(1, 1, 1), (1, 128, 64), (1, 129, 65), (2, 127, 16), (1, 1000, 896), (3, 257, 15), (8, 300, 17),
+SIZES = [(1, 1, 1), (1, 128, 64), (1, 129, 65), (2, 127, 16), (1, 1000, 896), (3, 257, 15), (8, 300, 17), (4, 5000, 300), (5, 40001, 130), (11, 21000, 256),
          (9, 640, 63), (16, 255, 127), (17, 513, 128), (31, 100, 129), (33, 1001, 1001), (64, 320, 768),
          (65, 130, 192), (128, 256, 1024), (129, 383, 1025), (200, 70, 333), (256, 512, 2048), (257, 200, 2100),
          (300, 129, 64), (513, 777, 100), (640, 2000, 320)]
@@ -212,7 +212,7 @@ def test_matmul_sizes(m, n, k):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("m", [1, 20, 140, 260])
+@pytest.mark.parametrize("m", [1, 2, 3, 7, 14, 20, 140, 260])
 @pytest.mark.parametrize("k", [1023, 1024, 1025, 2047, 3000, 9000, 40000, 131071])
 def test_matmul_sums_are_exact(m, k):
     # codes at the ends of the range with few signs: sums far beyond 2^24, up to 2^31
