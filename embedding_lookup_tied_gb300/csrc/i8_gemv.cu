@@ -9,17 +9,20 @@
 //  * Up to four tokens: four-way dot products on the codes as they are, about
 //    64 clocks a token and stage.
 //  * Up to sixteen: mma.sync.m16n8k16 in f16 (1,040 products a clock and SM
-//    here; the integer form, m16n8k32 in s8, does 260 and took 504 clocks a
-//    stage of eight tokens: 247 us for 8 x 262,144 x 5,376 against PLACEHOLDER).  The
-//    codes are widened in registers: a word of four consecutive codes becomes
+//    here; the integer form, m16n8k32 in s8, does 260, 504 clocks for a stage of
+//    eight tokens).  The codes are widened in registers: a word of four consecutive codes becomes
 //    two f16 pairs that serve as the k positions 2t, 2t+1, 2t+8 and 2t+9 of the
 //    fragment, for both operands alike, so no code moves between lanes.  f32
 //    sums of up to 1,024 products are exact; they are added up as integers.
 // (The tcgen05 kernel of i8_matmul.cu, whose operand has to pass through tensor
 // memory, needs about 1,100 clocks for a stage of so few tokens.)
 //
-// One CTA per SM: eight warps, each with 16 of a tile's 128 rows, and a
-// producer that keeps the ring of TMA boxes full.  The CTAs take the 128-row
+// One CTA per SM: two groups of eight warps, each warp with 16 of its group's
+// tile of 128 rows, and a producer that keeps a ring of TMA boxes full for each,
+// the two tiles' stages in turn.  (One ring for both would let a group that is
+// ahead mistake the barrier of a slot whose earlier copy, the other group's, is
+// still on its way for its own: a wait tells two phases apart, not three.  A stage's wait, loads, widening and products are
+// one chain of latencies; two groups have two under way.)  The CTAs take the 128-row
 // tiles in turn; the rows that do not fill a round of them are split evenly,
 // in units of 16 rows with boxes of that size.  The tokens are quantised by
 // every CTA for itself while its ring fills, so a call is one launch.
@@ -31,12 +34,14 @@ namespace lhs {
 namespace {
 
 constexpr int kMaxTokens = 16;
-constexpr int kWarps = 8;
+constexpr int kGroups = 2;                 // of warps, each with a tile of its own
+constexpr int kGroupWarps = 8;
+constexpr int kWarps = kGroups * kGroupWarps;
 constexpr int kConsumers = 32 * kWarps;
 constexpr int kThreads = kConsumers + 32;  // + producer
 constexpr int kUnitRows = 16;
 constexpr int kUnitBytes = kUnitRows * kStageK;
-constexpr int kMaxStages = 13;
+constexpr int kMaxStages = 12;            // of both groups' rings
 constexpr int kTokenBytes = 98 * 1024;     // tokens' codes at most, beside seven stages
 constexpr int kSmemBytes = 224 * 1024;
 
@@ -59,7 +64,7 @@ struct Params {
     const uint8_t *w_scales;
     int64_t w_scale_stride;
     int64_t channels;
-    int hidden, nst;
+    int hidden, nst;    // stages of each group's ring
     void *out;
     int64_t out_stride;
     int out_dtype;
@@ -185,16 +190,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t dyn_smem[];
     uint8_t *ring = smem_align<1024>(dyn_smem);
     const int pitch = token_pitch(p.hidden);
-    uint8_t *tok = ring + p.nst * kTableStageBytes;
+    uint8_t *tok = ring + kGroups * p.nst * kTableStageBytes;
     Head &sm = *reinterpret_cast<Head *>(tok + R * pitch);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Share share(p.channels);
     const int nk = (p.hidden + kStageK - 1) / kStageK;
 
     if (tid == 0) {
-        for (int s = 0; s < p.nst; ++s) {
+        for (int s = 0; s < kGroups * p.nst; ++s) {
             mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], kWarps);
+            mbar_init(&sm.empty[s], kGroupWarps);
         }
         sm.abort_flag = 0;
         fence_mbar_init();
@@ -215,43 +220,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarps) {
         if (lane == 0) {
             tma_prefetch_map(&tm_tile);
-            int s = 0, issued = 0;
-            uint32_t parity = 1;
+            int s[kGroups] = {}, issued[kGroups] = {};
+            uint32_t parity[kGroups];
+#pragma unroll
+            for (int w = 0; w < kGroups; ++w) parity[w] = 1;
             bool ok = true;
-            for (int64_t i = 0; i < share.tiles() && ok; ++i) {
-                const int32_t row = static_cast<int32_t>(share.row(i));
-                for (int kc = 0; kc < nk; ++kc) {
-                    if (!wait(&sm.empty[s], parity)) {
-                        ok = false;
-                        break;
+            // the groups' stages in turn
+            for (int64_t i0 = 0; i0 < share.tiles() && ok; i0 += kGroups)
+                for (int kc = 0; kc < nk && ok; ++kc)
+#pragma unroll
+                    for (int w = 0; w < kGroups; ++w) {
+                        const int64_t i = i0 + w;
+                        if (i >= share.tiles() || !ok) break;
+                        const int slot = w * p.nst + s[w];
+                        if (!wait(&sm.empty[slot], parity[w])) {
+                            ok = false;
+                            break;
+                        }
+                        const int32_t row = static_cast<int32_t>(share.row(i));
+                        uint8_t *dst = ring + slot * kTableStageBytes;
+                        if (i < share.rounds) {
+                            mbar_arrive_expect_tx(&sm.full[slot], kTableStageBytes);
+                            tma_load_2d(dst, &tm_tile, &sm.full[slot], kc * kStageK, row);
+                        } else {
+                            mbar_arrive_expect_tx(&sm.full[slot], share.units * kUnitBytes);
+                            for (int u = 0; u < share.units; ++u)
+                                tma_load_2d(dst + u * kUnitBytes, &tm_unit, &sm.full[slot], kc * kStageK,
+                                            row + u * kUnitRows);
+                        }
+                        if (issued[w] < p.nst) ++issued[w];
+                        if (++s[w] == p.nst) {
+                            s[w] = 0;
+                            parity[w] ^= 1u;
+                        }
                     }
-                    uint8_t *dst = ring + s * kTableStageBytes;
-                    if (i < share.rounds) {
-                        mbar_arrive_expect_tx(&sm.full[s], kTableStageBytes);
-                        tma_load_2d(dst, &tm_tile, &sm.full[s], kc * kStageK, row);
-                    } else {
-                        mbar_arrive_expect_tx(&sm.full[s], share.units * kUnitBytes);
-                        for (int u = 0; u < share.units; ++u)
-                            tma_load_2d(dst + u * kUnitBytes, &tm_unit, &sm.full[s], kc * kStageK, row + u * kUnitRows);
+            // every copy that was issued has landed
+#pragma unroll
+            for (int w = 0; w < kGroups; ++w)
+                for (int i = 0; i < issued[w]; ++i) {
+                    if (--s[w] < 0) {
+                        s[w] = p.nst - 1;
+                        parity[w] ^= 1u;
                     }
-                    if (issued < p.nst) ++issued;
-                    if (++s == p.nst) {
-                        s = 0;
-                        parity ^= 1u;
-                    }
+                    mbar_wait(&sm.full[w * p.nst + s[w]], parity[w] ^ 1u, kWaitTimeoutNs);
                 }
-            }
-            // every stage that was issued has been taken, so no copy is still on its way
-            for (int i = 0; i < issued; ++i) {
-                if (--s < 0) {
-                    s = p.nst - 1;
-                    parity ^= 1u;
-                }
-                // parity is the one its filling waited for; the next phase ends when it is taken
-                if (!wait(&sm.empty[s], parity ^ 1u)) {
-                    mbar_wait(&sm.full[s], parity ^ 1u, kWaitTimeoutNs);
-                }
-            }
         }
         return;
     }
@@ -266,14 +278,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the dot products: quarter q of both rows' codes.  The f16 products: ldmatrix addresses, lanes
     // 8 i .. 8 i + 7 naming the rows of matrix i (A: rows 0-7 and 8-15 of the warp's, then the same
     // 16 bytes further on; B: eight tokens at four 16-byte steps)
-    const int arow = warp * 16 + (lane & 15), apiece = lane >> 4;
+    const int group = warp / kGroupWarps, wrow = warp % kGroupWarps * 16;  // the warp's rows of the group's tile
+    const int arow = wrow + (lane & 15), apiece = lane >> 4;
     const uint32_t a_addr = smem_u32(ring) + arow * kStageK;
     const uint32_t b_addr = smem_u32(tok) + (lane & 7) * pitch + (lane >> 3) * 16;
-    int s = 0;
+    const int first = group * p.nst;  // the group's own ring
+    int s = first;
     uint32_t parity = 0;
-    for (int64_t i = 0; i < share.tiles(); ++i) {
-        const bool mine = i < share.rounds || warp < share.units;  // the last tile may be short
-        const int64_t ch = share.row(i) + warp * 16 + g;
+    for (int64_t i = group; i < share.tiles(); i += kGroups) {
+        const bool mine = i < share.rounds || wrow < share.units * kUnitRows;  // the last tile may be short
+        const int64_t ch = share.row(i) + wrow + g;
         float ws[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -289,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__all_sync(0xFFFFFFFFu, wait(&sm.full[s], parity))) return;
             if (mine) {
                 if constexpr (R <= 4) {
-                    const uint8_t *w = ring + s * kTableStageBytes + (warp * 16 + g) * kStageK;
+                    const uint8_t *w = ring + s * kTableStageBytes + (wrow + g) * kStageK;
                     const uint8_t *x = tok + kc * kStageK + q * 32;
                     uint4 u[2][2];
 #pragma unroll
@@ -337,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.empty[s]);
-            if (++s == p.nst) {
-                s = 0;
+            if (++s == first + p.nst) {
+                s = first;
                 parity ^= 1u;
             }
             if constexpr (R > 4) {
@@ -387,7 +401,7 @@ cudaError_t launch(const CUtensorMap &tm_tile, const CUtensorMap &tm_unit, Param
                    const DeviceInfo &dev, cudaStream_t stream) {
     const int fixed = 1024 + R * token_pitch(p.hidden) + static_cast<int>(sizeof(Head));
     p.nst = (kSmemBytes - fixed) / kTableStageBytes;
-    if (p.nst > kMaxStages) p.nst = kMaxStages;
+    p.nst = (p.nst < kMaxStages ? p.nst : kMaxStages) / kGroups;
     {
         static std::mutex mu;
         static bool done[64] = {};
@@ -399,7 +413,7 @@ cudaError_t launch(const CUtensorMap &tm_tile, const CUtensorMap &tm_unit, Param
             done[dev.device] = true;
         }
     }
-    return launch_pdl(i8_gemv_kernel<R>, dim3(grid), dim3(kThreads), fixed + p.nst * kTableStageBytes, stream, tm_tile,
+    return launch_pdl(i8_gemv_kernel<R>, dim3(grid), dim3(kThreads), fixed + kGroups * p.nst * kTableStageBytes, stream, tm_tile,
                       tm_unit, p);
 }
 

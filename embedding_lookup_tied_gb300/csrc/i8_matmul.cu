@@ -181,7 +181,7 @@ struct Tile {
     static constexpr int kThreads = 32 * (kConvWarps + 4);  // + table producer, token producer, MMA issuer, idle
     static constexpr int kAccs = NMAX == 256 ? 1 : 2;
     static constexpr int kColA = kAccs * NMAX;               // first column of the widened codes
-    static constexpr int kSlots = (kTmemCols - kColA) / kSlotCols;  // stages the MMAs may hold
+    static constexpr int kSlots = 4;                         // stages the MMAs may hold, a multiple of the groups
     static constexpr int kTokenStageBytes = NMAX / 2 * kStageK * 2;  // this CTA's half of the tokens
     static constexpr int kTableStages = (208 * 1024 - kSlots * kTokenStageBytes) / kTableStageBytes;
     static constexpr int kAhead = kSlots - 1;                // stages widened before a finished sum is taken out
@@ -191,6 +191,8 @@ struct Tile {
 template <int NMAX>
 struct Smem {
     using T = Tile<NMAX>;
+    static_assert(T::kSlots % T::kGroups == 0 && T::kTableStages >= T::kSlots && T::kColA + T::kSlots * kSlotCols <= kTmemCols,
+                  "see the waits of the widening warps");
     uint8_t table[T::kTableStages][kTableStageBytes];
     uint8_t token[T::kSlots][T::kTokenStageBytes];
     uint64_t table_full[T::kTableStages], table_empty[T::kTableStages];
@@ -429,8 +431,12 @@ __global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
         int kd = 0, in = 0;  // stage of the tile, of the sum, that the sums have got to
         for (int64_t j = 0; j < total + T::kAhead; ++j) {
             if (j < total && turn.i == g) {
-                bool ok = wait_or_abort(&sm.table_full[sw.i], sw.parity, &sm.abort_flag, p.err);
-                ok = wait_or_abort(&sm.empty[sa.i], sa.parity ^ 1u, &sm.abort_flag, p.err) && ok;
+                // in this order: once the slot is free, every stage up to kSlots before this one has been
+                // widened, so the copy before this one in the same place of the table's ring (at least
+                // kSlots back, and perhaps another group's) has landed, and the wait for this one cannot
+                // take that one's phase for its own
+                bool ok = wait_or_abort(&sm.empty[sa.i], sa.parity ^ 1u, &sm.abort_flag, p.err);
+                ok = ok && wait_or_abort(&sm.table_full[sw.i], sw.parity, &sm.abort_flag, p.err);
                 if (!__all_sync(0xFFFFFFFFu, ok)) break;  // the tcgen05 instructions are warp-collective
                 tc_fence_after();
                 const uint8_t *src = sm.table[sw.i] + row * kStageK;
