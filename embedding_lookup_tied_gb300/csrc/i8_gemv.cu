@@ -9,23 +9,25 @@
 //  * Up to four tokens: four-way dot products on the codes as they are, about
 //    64 clocks a token and stage.
 //  * Up to sixteen: mma.sync.m16n8k16 in f16 (1,040 products a clock and SM
-//    here; the integer form, m16n8k32 in s8, does 260, 504 clocks for a stage of
-//    eight tokens).  The codes are widened in registers: a word of four consecutive codes becomes
-//    two f16 pairs that serve as the k positions 2t, 2t+1, 2t+8 and 2t+9 of the
-//    fragment, for both operands alike, so no code moves between lanes.  f32
-//    sums of up to 1,024 products are exact; they are added up as integers.
+//    here; the integer form, m16n8k32 in s8, does 260, 504 clocks for a stage
+//    of eight tokens).  The codes are widened in registers: a word of four
+//    consecutive codes becomes two f16 pairs that serve as the k positions 2t,
+//    2t+1, 2t+8 and 2t+9 of the fragment, for both operands alike, so no code
+//    moves between lanes.  f32 sums of up to 1,024 products are exact; they
+//    are added up as integers.
 // (The tcgen05 kernel of i8_matmul.cu, whose operand has to pass through tensor
 // memory, needs about 1,100 clocks for a stage of so few tokens.)
 //
 // One CTA per SM: two groups of eight warps, each warp with 16 of its group's
-// tile of 128 rows, and a producer that keeps a ring of TMA boxes full for each,
-// the two tiles' stages in turn.  (One ring for both would let a group that is
-// ahead mistake the barrier of a slot whose earlier copy, the other group's, is
-// still on its way for its own: a wait tells two phases apart, not three.  A stage's wait, loads, widening and products are
-// one chain of latencies; two groups have two under way.)  The CTAs take the 128-row
-// tiles in turn; the rows that do not fill a round of them are split evenly,
-// in units of 16 rows with boxes of that size.  The tokens are quantised by
-// every CTA for itself while its ring fills, so a call is one launch.
+// tile of 128 rows, and a producer that keeps a ring of TMA boxes full for
+// each, the two tiles' stages in turn.  A stage's wait, loads, widening and
+// products are one chain of latencies, and two groups have two under way.
+// (One ring for both would let a group that is ahead mistake the barrier of a
+// slot whose earlier copy, the other group's, is still on its way for its own:
+// a wait tells two phases apart, not three.)  The CTAs take the 128-row tiles
+// in turn; the rows that do not fill a round of them are split evenly, in units
+// of 16 rows with boxes of that size.  The tokens are quantised by every CTA
+// for itself while its ring fills, so a call is one launch.
 #include <mutex>
 
 #include "i8_common.cuh"

@@ -247,27 +247,37 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(2) << 61);
+// Low word of the shared-memory matrix descriptor; the high word is constant:
+// K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | (1u << 16); }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// One lane of the warp, for the instructions below: the whole warp runs the
+// loop around them, so that their operands stay in uniform registers (in a
+// branch of one lane every operand of every MMA was moved there first, about
+// 85 clocks an MMA).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p)::"memory");
+    return p;
 }
 // A in TMEM (the widened codes of both CTAs, same columns), B in shared memory.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+__device__ __forceinline__ void umma_f16_ts(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                            uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(elected), "n"(kDescHi)
         : "memory");
 }
-__device__ __forceinline__ void umma_commit_both(uint64_t *bar) {
+__device__ __forceinline__ void umma_commit_both(uint32_t elected, uint64_t *bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(smem_u32(bar)),
-        "h"(static_cast<uint16_t>(0x3))
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::
+            "r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(0x3)), "r"(elected)
         : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() {
@@ -616,36 +626,40 @@ __global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
             // ---------------- MMA issuer (the leader CTA only) ----------------
             pdl_wait();
             const int chunk = blocks_per_sum(p, lane);
-            if (lane == 0 && rank == 0) {
+            if (rank == 0) {
                 const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.n >> 3) << 17) |
                                        (static_cast<uint32_t>(kPairRows >> 4) << 24);  // f16 x f16 -> f32
-                const uint32_t half_bytes = static_cast<uint32_t>(p.n / 2) * 128;
+                const uint32_t half16 = static_cast<uint32_t>(p.n / 2) * 128 >> 4;  // half a stage, in descriptor units
+                const uint32_t tm = __reduce_or_sync(0xFFFFFFFFu, tmem);
+                const uint32_t elected = elect_one();
                 Ring<SX> sx;
                 Ring<ACCS> sc;
                 bool ok = true, ready = false;
                 for (int64_t it = 0; it < mine && ok; ++it) {
                     int in = 0;  // stages of the current sum
                     for (int kc = 0; kc < p.nk; ++kc) {
-                        if ((in == 0 && !wait_or_abort(&sm.acc_empty[sc.i], sc.parity ^ 1u, &sm.abort_flag, p.err)) ||
-                            (!ready && !wait_or_abort(&sm.full[sx.i], sx.parity, &sm.abort_flag, p.err))) {
+                        bool go = true;
+                        if (in == 0) go = wait_or_abort(&sm.acc_empty[sc.i], sc.parity ^ 1u, &sm.abort_flag, p.err);
+                        if (!ready) go = go && wait_or_abort(&sm.full[sx.i], sx.parity, &sm.abort_flag, p.err);
+                        if (!__all_sync(0xFFFFFFFFu, go)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t d = tmem + sc.i * NMAX, a = tmem + T::kColA + sx.i * kSlotCols;
-                        const uint32_t b = smem_u32(sm.token[sx.i]);
+                        const uint32_t d = tm + sc.i * NMAX, a = tm + T::kColA + sx.i * kSlotCols;
+                        const uint32_t b = desc_lo(smem_u32(sm.token[sx.i]));
                         uint64_t *done = &sm.empty[sx.i];
                         sx.next();
                         // a look at the next stage, whose answer the MMAs' issue hides
                         ready = mbar_test_cluster(&sm.full[sx.i], sx.parity);
-    #pragma unroll
+#pragma unroll
                         for (int ks = 0; ks < kStageK / 16; ++ks)
-                            umma_f16_ts(d, a + ks * 8, desc_sw128(b + (ks >> 2) * half_bytes + (ks & 3) * 32), idesc,
-                                        (in | ks) != 0);
-                        umma_commit_both(done);
+                            umma_f16_ts(elected, d, a + ks * 8, b + (ks >> 2) * half16 + (ks & 3) * 2, idesc, (in | ks) != 0);
+                        umma_commit_both(elected, done);
+                        ready = __all_sync(0xFFFFFFFFu, ready);
                         ++in;
                         if (in == chunk || kc + 1 == p.nk) {
-                            umma_commit_both(&sm.acc_full[sc.i]);
+                            umma_commit_both(elected, &sm.acc_full[sc.i]);
                             in = 0;
                             sc.next();
                         }
