@@ -4,18 +4,31 @@
 // sampling").
 //
 // Mathematics.  All three filters keep a head of the row in the order (logit
-// descending, id ascending), so together they keep the ids whose (order key,
-// inverted id) is at least a threshold; top-k finds it by counts, top-p by
-// sums of weights.  The draw inverts the running sum of the kept weights in id
-// order.  Weights are 2^S exp((logit - max) / T) as 64-bit integers (see
-// Weight), so every sum is exact, whatever the order in which warps, CTAs and
-// atomics form it, and two passes over a row agree to the last bit.
+// descending, id ascending), so together they keep the entries whose 64-bit
+// (order key, inverted id) is at least a threshold; top-k finds it by counts,
+// top-p by sums of weights.  The draw inverts the running sum of the kept
+// weights in id order.  Weights are 2^S exp((logit - max) / T) as 64-bit
+// integers (see Weight), so every sum is exact, whatever the order in which
+// warps, CTAs and atomics form it, and two passes over a row agree to the last
+// bit.
 //
-// A cluster of CTAs owns a row; each warp owns one contiguous piece of it.
-// The threshold is found digit by digit (11, 11 and 10 bits of the 32-bit
-// order key) from histograms of counts or weights in shared memory, which the
-// cluster's CTAs read from one another.
+// A cluster of CTAs owns a row and holds it in its shared memory: HBM is read
+// once, and every later pass is a lane's own 16-byte words from shared memory.
+//  * top-k: at least k entries lie in or above the bin that holds the k-th
+//    largest of the threads' maxima, and few more do, so that bound gathers a
+//    short list; one CTA sorts it and does the rest (k, p, min-p, the draw).
+//  * top-p alone: one pass sums all weights and counts the entries by
+//    bins of 1/64 octave; the counts bracket the bin in which the weights
+//    reach p of their sum, a pass over the bracket sums its bins exactly, and
+//    the entries of the one bin left are sorted.
+//  * Where a list does not fit (equal logits by the thousand, a large k), the
+//    threshold is found digit by digit (11, 11 and 10 bits of the order key)
+//    from histograms of counts or weights.
+//  * The draw: each warp's sum over its piece of the row, the pieces in id
+//    order; the warp whose piece holds the answer walks it.
 #include <cooperative_groups.h>
+
+#include <mutex>
 
 #include "decode.cuh"
 
@@ -27,8 +40,11 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 2048;
-constexpr int kBinsPerThread = kBins / kThreads;
+constexpr int kList = 2048;                   // entries one CTA sorts
+constexpr int kDigits = 2048;                 // bins of a digit of the order key
+constexpr int kBins = 1024;                   // of 1/64 octave of weight; the last takes all that is below
+constexpr float kBinsPerOctave = 64.0f;
+constexpr int kMaxSmem = 224 * 1024;
 constexpr uint32_t kKeyInf = 0xFF800000u;     // order key of +inf; NaN lies above
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // order key of -inf
 
@@ -91,33 +107,190 @@ struct Weight {
 };
 
 struct Shared {
-    uint64_t hist[kBins];
+    uint64_t list[kList];           // entries; the digit histograms where no list fits
+    uint64_t mass[kBins];
+    uint32_t count[kBins];
     uint64_t slot[2][kMaxCluster];  // one value from each CTA of the cluster, two exchanges
     uint64_t warp_sum[kWarps];
-    uint64_t cross_above, cross_in;
+    uint64_t above, in;
     uint64_t pow16[16];
-    int32_t cross_bin;
+    int32_t bin;
     int32_t found;
+    int32_t gathered;
 };
+static_assert(kList == kDigits, "the digit histograms take the list's place");
+static_assert(sizeof(Shared) % 16 == 0, "the row's words follow it");
 
 __device__ __forceinline__ uint64_t warp_add(uint64_t v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
+__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t up = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += up;
+    }
+    return v;
+}
 
-// One row, as one CTA of its cluster sees it.
-template <int DT>
+// Sum over the CTA, leaving the warps' sums in warp_sum until the next use.
+__device__ __forceinline__ uint64_t cta_sum(Shared &sm, uint64_t v) {
+    v = warp_add(v);
+    if ((threadIdx.x & 31) == 0) sm.warp_sum[threadIdx.x >> 5] = v;
+    __syncthreads();
+    uint64_t s = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) s += sm.warp_sum[i];
+    return s;
+}
+// Exclusive scan over the CTA's threads; the caller syncs before the next use.
+__device__ __forceinline__ uint64_t cta_scan(Shared &sm, uint64_t v) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint64_t incl = warp_scan(v, lane);
+    if (lane == 31) sm.warp_sum[warp] = incl;
+    __syncthreads();
+    uint64_t before = incl - v;
+    for (int w = 0; w < warp; ++w) before += sm.warp_sum[w];
+    return before;
+}
+
+// Descending sort of the 512 E (or fewer, a power of two) entries of buf: thread
+// t holds entries t E .. t E + E - 1 in registers; partners within a warp meet
+// by shuffles, others through buf.
+template <int E>
+__device__ __forceinline__ void sort_entries(uint64_t *buf, int size_all) {
+    const int tid = threadIdx.x;
+    uint64_t v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = tid * E + e < size_all ? buf[tid * E + e] : 0ull;
+    for (int size = 2; size <= size_all; size <<= 1) {
+        for (int d = size >> 1; d > 0; d >>= 1) {
+            if (d >= 32 * E) {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < E; ++e) buf[tid * E + e] = v[e];
+                __syncthreads();
+            }
+            uint64_t other[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (d >= 32 * E) other[e] = buf[(tid * E + e) ^ d];
+                else if (d >= E) other[e] = __shfl_xor_sync(0xFFFFFFFFu, v[e], d / E);
+                else other[e] = d == 1 ? v[e ^ (1 % E)] : v[e ^ (2 % E)];
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int i = tid * E + e;
+                const bool larger = ((i & d) == 0) == ((i & size) == 0);
+                v[e] = (v[e] > other[e]) == larger ? v[e] : other[e];
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) buf[tid * E + e] = v[e];
+    __syncthreads();
+}
+// The first n entries of the list, sorted descending; the rest of the list
+// becomes zeros.  CTA-collective.
+__device__ __forceinline__ void sort_list(Shared &sm, int n) {
+    for (int i = n + threadIdx.x; i < kList; i += kThreads) sm.list[i] = 0ull;
+    __syncthreads();
+    int size = 32;
+    while (size < n) size <<= 1;
+    if (size <= kThreads) sort_entries<1>(sm.list, size);
+    else if (size <= 2 * kThreads) sort_entries<2>(sm.list, size);
+    else sort_entries<4>(sm.list, size);
+}
+
+// What stays: entries with a key of at least `edge`.
+struct Edge {
+    float value;  // logits above it stay, those equal to it up to id `last`
+    int last;
+    __device__ __forceinline__ bool stays(float l, int id) const { return l > value || (l == value && id <= last); }
+    __device__ __forceinline__ void set(uint64_t key) {
+        value = key_value(key);
+        last = key_id(key);
+    }
+};
+
+// One row, as one CTA of its cluster sees it.  The row's 16-byte words (as
+// addresses fall, so the first and last may be partly another row's: those
+// elements read as -inf) are dealt out to warps in contiguous pieces.
+template <int DT, bool RESIDENT>
 struct RowView {
     using E = Elem<DT>;
+    using T = typename E::T;
+    static constexpr int VE = 16 / static_cast<int>(sizeof(T));
     Shared &sm;
     cg::cluster_group cl;
     int rank, ranks;
-    const typename E::T *row;
-    int lo, hi;  // this warp's piece
-    int flip;    // which exchange slots come next
+    uint4 *hold;      // this lane's words in shared memory, kThreads... 32 apart
+    int steps;        // words per lane
+    int word0;        // this lane's first word; the next are 32 further on
+    int vocab;
+    const uint4 *base;  // the word that holds the row's first element
+    int skip;           // elements of that word before it
+    int flip;           // which exchange slots come next
 
-    __device__ __forceinline__ float at(int i) const { return E::widen(ld_dep(row + i)); }
+    __device__ __forceinline__ uint4 fetch(int w) const {
+        const int64_t first = static_cast<int64_t>(w) * VE - skip;  // id of the word's first element
+        if (first >= vocab || first + VE <= 0) return outside();
+        uint4 u = ld_dep(base + w);
+        if (first < 0 || first + VE > vocab) {
+            T *e = reinterpret_cast<T *>(&u);
+            const uint4 o = outside();
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                if (first + i < 0 || first + i >= vocab) e[i] = reinterpret_cast<const T *>(&o)[i];
+        }
+        return u;
+    }
+    static __device__ __forceinline__ uint4 outside() {  // -inf
+        const uint32_t w = DT == LHS_F32 ? 0xFF800000u : DT == LHS_F16 ? 0xFC00FC00u : 0xFF80FF80u;
+        return make_uint4(w, w, w, w);
+    }
+    static __device__ __forceinline__ void widen(const uint4 &u, float (&v)[VE]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        if (DT == LHS_F32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) v[i] = E::widen(static_cast<T>(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu));
+        }
+    }
+    // f(values, id of the first) for each of this lane's words, in id order.
+    template <typename F>
+    __device__ __forceinline__ void each(const F &f) const {
+#pragma unroll 2
+        for (int s = 0; s < steps; ++s) {
+            float v[VE];
+            widen(RESIDENT ? hold[s * 32] : fetch(word0 + s * 32), v);
+            f(v, (word0 + s * 32) * VE - skip);
+        }
+    }
+    // The row's first reading: this lane's largest order key.
+    __device__ __forceinline__ uint32_t read() {
+        uint32_t top = 0;
+        constexpr int kBatch = 8;
+        for (int s = 0; s < steps; s += kBatch) {
+            uint4 u[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) u[i] = s + i < steps ? fetch(word0 + (s + i) * 32) : outside();
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (RESIDENT && s + i < steps) hold[(s + i) * 32] = u[i];
+                float v[VE];
+                widen(u[i], v);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) top = max(top, order_key32(v[e]));
+            }
+        }
+        return top;
+    }
 
     // Every CTA's v, in this CTA's shared memory.
     __device__ __forceinline__ const uint64_t *exchange(uint64_t v) {
@@ -127,84 +300,163 @@ struct RowView {
         cl.sync();
         return slots;
     }
-    // Sum over the CTA of per-warp sums; leaves them in warp_sum.
-    __device__ __forceinline__ uint64_t cta_sum(uint64_t lane_sum) {
-        const uint64_t w = warp_add(lane_sum);
-        if ((threadIdx.x & 31) == 0) sm.warp_sum[threadIdx.x >> 5] = w;
-        __syncthreads();
-        uint64_t s = 0;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) s += sm.warp_sum[i];
-        return s;
-    }
-    template <typename F>
-    __device__ __forceinline__ uint64_t row_sum(const F &value) {
-        uint64_t s = 0;
-        for (int i = lo + (threadIdx.x & 31); i < hi; i += 32) s += value(at(i), i);
-        const uint64_t mine = cta_sum(s);
-        const uint64_t *all = exchange(mine);
+    __device__ __forceinline__ uint64_t row_sum(uint64_t lane_sum) {
+        const uint64_t *all = exchange(cta_sum(sm, lane_sum));
         uint64_t t = 0;
         for (int i = 0; i < ranks; ++i) t += all[i];
         __syncthreads();
         return t;
     }
 
-    // The largest order key at which the sum of value over the keys from it
-    // upwards reaches `need` (>= 1, at most the row's sum).  need: what is
-    // left of it for that key's own elements; in: their sum.
+    // The bin in which the cluster's sums over bins 0, 1, .. reach need (>= 1):
+    // its number, and in sm.above / sm.in the sums before and of it.  A bin's
+    // sum in one CTA is value(CTA, bin).  kBins where they do not.
     template <typename F>
-    __device__ __forceinline__ uint32_t threshold(const F &value, uint64_t &need, uint64_t &in) {
+    __device__ __forceinline__ int crossing(const F &value, uint64_t need) {
+        if (threadIdx.x == 0) sm.bin = kBins;
+        cl.sync();
+        constexpr int B = kBins / kThreads;
+        uint64_t h[B], mine = 0;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            h[b] = 0;
+            for (int r = 0; r < ranks; ++r) h[b] += value(r, static_cast<int>(threadIdx.x) * B + b);
+            mine += h[b];
+        }
+        uint64_t above = cta_scan(sm, mine);
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (above < need && above + h[b] >= need) {
+                sm.bin = static_cast<int>(threadIdx.x) * B + b;
+                sm.above = above;
+                sm.in = h[b];
+            }
+            above += h[b];
+        }
+        __syncthreads();
+        return sm.bin;
+    }
+
+    // Entries that `take` takes, as keys: into this CTA's list, its number (of
+    // which kList at most are held) into sm.gathered; their number over the
+    // cluster.
+    template <typename F>
+    __device__ __forceinline__ int64_t gather(const F &take) {
+        if (threadIdx.x == 0) sm.gathered = 0;
+        __syncthreads();
+        each([&](const float (&v)[VE], int id) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                if (take(v[e], id + e)) {
+                    const int at = atomicAdd(&sm.gathered, 1);
+                    if (at < kList) sm.list[at] = topk_key(v[e], id + e);
+                }
+            }
+        });
+        __syncthreads();
+        const uint64_t *all = exchange(static_cast<uint64_t>(sm.gathered));
+        int64_t n = 0;
+        for (int i = 0; i < ranks; ++i) n += static_cast<int64_t>(all[i]);
+        return n;
+    }
+    // CTA 0: the other CTAs' entries (gathered, kList in all at most) behind its own.
+    __device__ __forceinline__ void pull(const uint64_t *counts) {
+        int at = static_cast<int>(counts[0]);
+        for (int r = 1; r < ranks; ++r) {
+            const int n = static_cast<int>(counts[r]);
+            const uint64_t *src = cl.map_shared_rank(sm.list, r);
+            for (int i = threadIdx.x; i < n; i += kThreads) sm.list[at + i] = src[i];
+            at += n;
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ const uint64_t *last_exchange() const { return sm.slot[flip ^ 1]; }
+
+    // The key at which the sums of value over the entries that `take` takes, in
+    // descending order of keys, reach need (>= 1, at most their sum).
+    template <typename F, typename G>
+    __device__ __forceinline__ uint64_t cut(const F &take, const G &value, uint64_t need) {
+        const int64_t n = gather(take);
+        if (n <= kList) {
+            uint64_t key = 0;
+            if (rank == 0) {
+                pull(last_exchange());
+                sort_list(sm, static_cast<int>(n));
+                constexpr int P = kList / kThreads;
+                uint64_t w[P], mine = 0;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const uint64_t k = sm.list[threadIdx.x * P + i];
+                    w[i] = k ? value(key_value(k)) : 0ull;
+                    mine += w[i];
+                }
+                uint64_t above = cta_scan(sm, mine);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    if (above < need && above + w[i] >= need) sm.above = sm.list[threadIdx.x * P + i];
+                    above += w[i];
+                }
+                __syncthreads();
+                key = sm.above;
+            }
+            return exchange(key)[0];
+        }
+        __syncthreads();
+        // digit by digit, then the id among equal logits
         uint32_t prefix = 0, mask = 0;
+        uint64_t in = 0;
         const int shifts[3] = {21, 10, 0};
         for (int level = 0; level < 3; ++level) {
             const int sh = shifts[level];
             const uint32_t digit = level < 2 ? 0x7FFu : 0x3FFu;
-            for (int i = threadIdx.x; i < kBins; i += kThreads) sm.hist[i] = 0;
+            for (int i = threadIdx.x; i < kDigits; i += kThreads) sm.list[i] = 0;
             __syncthreads();
-            for (int i = lo + (threadIdx.x & 31); i < hi; i += 32) {
-                const float l = at(i);
-                const uint32_t k = order_key32(l);
-                if ((k & mask) != prefix) continue;
-                const uint64_t v = value(l, i);
-                if (v) atomicAdd(reinterpret_cast<unsigned long long *>(&sm.hist[(k >> sh) & digit]), v);
-            }
-            cl.sync();
-            // bins from the top: thread t holds bins kBins - 1 - t * kBinsPerThread - (0 ..)
-            uint64_t h[kBinsPerThread], mine = 0;
+            each([&](const float (&v)[VE], int id) {
 #pragma unroll
-            for (int b = 0; b < kBinsPerThread; ++b) {
-                const int bin = kBins - 1 - (threadIdx.x * kBinsPerThread + b);
+                for (int e = 0; e < VE; ++e) {
+                    if (!take(v[e], id + e)) continue;
+                    const uint32_t k = order_key32(v[e]);
+                    if ((k & mask) == prefix)
+                        atomicAdd(reinterpret_cast<unsigned long long *>(&sm.list[(k >> sh) & digit]), value(v[e]));
+                }
+            });
+            cl.sync();
+            // bins from the top: thread t holds kDigits - 1 - t P - (0 .. P - 1)
+            constexpr int P = kDigits / kThreads;
+            uint64_t h[P], mine = 0;
+#pragma unroll
+            for (int b = 0; b < P; ++b) {
                 h[b] = 0;
-                for (int r = 0; r < ranks; ++r) h[b] += cl.map_shared_rank(sm.hist, r)[bin];
+                for (int r = 0; r < ranks; ++r)
+                    h[b] += cl.map_shared_rank(sm.list, r)[kDigits - 1 - (threadIdx.x * P + b)];
                 mine += h[b];
             }
-            uint64_t incl = mine;
+            uint64_t above = cta_scan(sm, mine);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if (static_cast<int>(threadIdx.x & 31) >= o) incl += up;
-            }
-            if ((threadIdx.x & 31) == 31) sm.warp_sum[threadIdx.x >> 5] = incl;
-            __syncthreads();
-            uint64_t above = incl - mine;
-            for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) above += sm.warp_sum[w];
-#pragma unroll
-            for (int b = 0; b < kBinsPerThread; ++b) {
+            for (int b = 0; b < P; ++b) {
                 if (above < need && above + h[b] >= need) {
-                    sm.cross_bin = kBins - 1 - (threadIdx.x * kBinsPerThread + b);
-                    sm.cross_above = above;
-                    sm.cross_in = h[b];
+                    sm.bin = kDigits - 1 - static_cast<int>(threadIdx.x * P + b);
+                    sm.above = above;
+                    sm.in = h[b];
                 }
                 above += h[b];
             }
             cl.sync();  // also: every CTA has read this one's histogram
-            prefix |= static_cast<uint32_t>(sm.cross_bin) << sh;
+            prefix |= static_cast<uint32_t>(sm.bin) << sh;
             mask |= digit << sh;
-            need -= sm.cross_above;
-            in = sm.cross_in;
+            need -= sm.above;
+            in = sm.in;
             __syncthreads();
         }
-        return prefix;
+        const float edge = key_value(static_cast<uint64_t>(prefix) << 32);
+        const uint64_t one = value(edge), m = (need + one - 1) / one;  // of in / one equal logits
+        int last = 0x7FFFFFFF;
+        if (m < in / one) {
+            uint64_t total;
+            last = locate([&](float l, int id) { return uint64_t(l == edge && take(l, id)); },
+                          [&](uint64_t) { return m - 1; }, total);
+        }
+        return topk_key(edge, last);
     }
 
     // The first id at which the running sum of value passes target(total).
@@ -212,9 +464,11 @@ struct RowView {
     __device__ __forceinline__ int locate(const F &value, const G &target, uint64_t &total) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         uint64_t s = 0;
-        for (int i = lo + lane; i < hi; i += 32) s += value(at(i), i);
-        const uint64_t mine = cta_sum(s);
-        const uint64_t *all = exchange(mine);
+        each([&](const float (&v)[VE], int id) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) s += value(v[e], id + e);
+        });
+        const uint64_t *all = exchange(cta_sum(sm, s));
         uint64_t before = 0;
         total = 0;
         for (int i = 0; i < ranks; ++i) {
@@ -224,17 +478,29 @@ struct RowView {
         const uint64_t t = target(total);
         for (int w = 0; w < warp; ++w) before += sm.warp_sum[w];
         if (t >= before && t < before + sm.warp_sum[warp]) {  // in this warp's piece
-            for (int i0 = lo; i0 < hi; i0 += 32) {
-                const int i = i0 + lane;
-                uint64_t incl = i < hi ? value(at(i), i) : 0;
+            for (int st = 0; st < steps; ++st) {
+                float v[VE];
+                widen(RESIDENT ? hold[st * 32] : fetch(word0 + st * 32), v);
+                const int id = (word0 + st * 32) * VE - skip;
+                uint64_t w[VE], mine = 0;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                    if (lane >= o) incl += up;
+                for (int e = 0; e < VE; ++e) {
+                    w[e] = value(v[e], id + e);
+                    mine += w[e];
                 }
+                const uint64_t incl = warp_scan(mine, lane);
                 const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > t);
                 if (hit) {
-                    if (lane < ranks) *cl.map_shared_rank(&sm.found, lane) = i0 + __ffs(hit) - 1;
+                    if (lane == __ffs(hit) - 1) {
+                        uint64_t at = before + incl - mine;
+                        int found = -1;
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            at += w[e];
+                            if (found < 0 && at > t) found = id + e;
+                        }
+                        for (int r = 0; r < ranks; ++r) *cl.map_shared_rank(&sm.found, r) = found;
+                    }
                     break;
                 }
                 before += __shfl_sync(0xFFFFFFFFu, incl, 31);
@@ -249,10 +515,69 @@ struct RowView {
 __device__ __forceinline__ uint64_t fraction64(float f) {
     return static_cast<uint64_t>(static_cast<double>(f) * 0x1p64);
 }
+// The least integer that is at least p of all (1 at least).
+__device__ __forceinline__ uint64_t share_of(float p, uint64_t all) {
+    const uint64_t P = fraction64(p);
+    const uint64_t need = __umul64hi(P, all) + (P * all != 0 ? 1 : 0);
+    return need ? need : 1;
+}
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, const int S) {
-    __shared__ Shared sm;
+// A row that the filters have narrowed to the n <= kList entries of the list, in
+// any order, in one CTA: top-k of them, top-p, min-p and the draw.
+__device__ void finish_list(Shared &sm, const Weight &weight, int n, int k, float top_p, uint64_t floor_w, uint64_t U,
+                            int32_t *id, float *prob) {
+    constexpr int P = kList / kThreads;
+    const int tid = threadIdx.x;
+    sort_list(sm, n);
+    if (k < n) n = k;
+    uint64_t w[P], mine = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        w[i] = tid * P + i < n ? weight(key_value(sm.list[tid * P + i])) : 0ull;
+        mine += w[i];
+    }
+    const uint64_t all = cta_sum(sm, mine);
+    __syncthreads();
+    const uint64_t need = top_p < 1.0f ? share_of(top_p, all) : ~0ull;
+    uint64_t above = cta_scan(sm, mine);
+    // those that stay, keyed by id (ascending: the inverted id descending) with the order key
+    // below, so that a second sort puts them into id order
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const bool stays = tid * P + i < n && above < need && w[i] >= floor_w && w[i] > 0;
+        above += w[i];
+        const uint64_t key = sm.list[tid * P + i];
+        sm.list[tid * P + i] = stays ? (key << 32) | (key >> 32) : 0ull;
+    }
+    __syncthreads();
+    sort_list(sm, n);
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const uint64_t key = sm.list[tid * P + i];
+        w[i] = key ? weight(key_value(key << 32)) : 0ull;
+        mine += w[i];
+    }
+    const uint64_t total = cta_sum(sm, mine);
+    __syncthreads();
+    const uint64_t t = __umul64hi(U, total);
+    above = cta_scan(sm, mine);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        if (above <= t && t < above + w[i]) {
+            *id = key_id(sm.list[tid * P + i] >> 32);
+            if (prob) *prob = static_cast<float>(static_cast<double>(w[i]) / static_cast<double>(total));
+        }
+        above += w[i];
+    }
+}
+
+template <int DT, bool RESIDENT>
+__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, const int S, const int steps) {
+    using View = RowView<DT, RESIDENT>;
+    constexpr int VE = View::VE;
+    extern __shared__ __align__(16) uint8_t dyn_smem[];
+    Shared &sm = *reinterpret_cast<Shared *>(dyn_smem);
     cg::cluster_group cl = cg::this_cluster();
     const int rank = static_cast<int>(cl.block_rank()), ranks = static_cast<int>(cl.num_blocks());
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -261,14 +586,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
     pdl_wait();
     cl.sync();  // the peers run: their shared memory may be written
 
-    const int seg = ((p.vocab + ranks * kWarps - 1) / (ranks * kWarps) + 31) & ~31;
-    const int64_t first = static_cast<int64_t>(rank * kWarps + warp) * seg;
-    const int lo = static_cast<int>(first < p.vocab ? first : p.vocab);
-    const int hi = static_cast<int>(first + seg < p.vocab ? first + seg : p.vocab);
-    RowView<DT> v{sm, cl, rank, ranks, nullptr, lo, hi, 0};
+    View v{sm, cl, rank, ranks, nullptr, steps, (rank * kWarps + warp) * steps * 32 + lane, p.vocab, nullptr, 0, 0};
+    v.hold = reinterpret_cast<uint4 *>(dyn_smem + sizeof(Shared)) + warp * steps * 32 + lane;
 
     for (int64_t r = blockIdx.x / ranks; r < p.rows; r += gridDim.x / ranks) {
-        v.row = static_cast<const typename Elem<DT>::T *>(p.logits) + r * p.stride;
+        const uintptr_t row = reinterpret_cast<uintptr_t>(static_cast<const typename View::T *>(p.logits) + r * p.stride);
+        v.base = reinterpret_cast<const uint4 *>(row & ~uintptr_t(15));
+        v.skip = static_cast<int>((row & 15) / sizeof(typename View::T));
         const float u = ld_dep(p.u + r);
         float T = p.temperature ? ld_dep(p.temperature + r) : 1.0f;
         const float top_p = p.top_p ? ld_dep(p.top_p + r) : 1.0f;
@@ -281,12 +605,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
             k = 1;
         }
         T = fminf(fmaxf(T, 0x1p-100f), 0x1p100f);
+        if (k <= 0 || k >= p.vocab) k = p.vocab;
 
         // the row's largest logit (as an order key: NaN lies above +inf)
-        uint32_t top = 0;
-        for (int i = lo + lane; i < hi; i += 32) top = max(top, order_key32(v.at(i)));
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        const uint32_t lane_top = v.read();
+        uint32_t top = __reduce_max_sync(0xFFFFFFFFu, lane_top);
         if (lane == 0) sm.warp_sum[warp] = top;
+        for (int i = tid; i < kBins; i += kThreads) sm.count[i] = 0;
         __syncthreads();
         for (int i = 0; i < kWarps; ++i) top = max(top, static_cast<uint32_t>(sm.warp_sum[i]));
         const uint64_t *tops = v.exchange(top);
@@ -304,72 +629,157 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
         }
         Weight weight;
         weight.init(key_value(static_cast<uint64_t>(top) << 32), T, S, sm.pow16);
+        const float per_bin = weight.c_hi * kBinsPerOctave;
+        // bins from the top of the row down; a larger logit never lies in a later bin
+        auto bin_of = [&](float l) { return static_cast<int>(fminf((weight.max - l) * per_bin, kBins - 1.0f)); };
+        auto counts = [&](int from, int b) { return uint64_t(cl.map_shared_rank(sm.count, from)[b]); };
+        const uint64_t floor_w = static_cast<uint64_t>(ceil(ldexp(static_cast<double>(min_p), S)));
+        const uint64_t U = fraction64(u);
 
-        // what stays: keys above `edge`, and those equal to it up to id `last`
-        uint32_t edge = 0;
-        int last = 0x7FFFFFFF;
-        auto stays = [&](uint32_t key, int i) { return key > edge || (key == edge && i <= last); };
-        if (k > 0 && k < p.vocab) {
-            uint64_t need = static_cast<uint64_t>(k), in = 0;
-            const uint32_t e = v.threshold([](float, int) { return uint64_t(1); }, need, in);
-            if (need < in) {
-                uint64_t total;
-                last = v.locate([&](float l, int) { return uint64_t(order_key32(l) == e); },
-                                [&](uint64_t) { return need - 1; }, total);
+        Edge edge = {-INFINITY, 0x7FFFFFFF};
+        if (k < p.vocab) {
+            // at least k entries lie in the bins up to the one in which the k-th of the lanes' maxima does
+            const float lane_max = key_value(static_cast<uint64_t>(lane_top) << 32);
+            if (lane_top > kKeyNegInf) atomicAdd(&sm.count[bin_of(lane_max)], 1u);
+            const int bound = v.crossing(counts, static_cast<uint64_t>(k));
+            if (bound < kBins - 1) {
+                const int64_t n = v.gather([&](float l, int) { return bin_of(l) <= bound; });
+                if (n <= kList) {
+                    if (rank == 0) {
+                        v.pull(v.last_exchange());
+                        finish_list(sm, weight, static_cast<int>(n), k, top_p, floor_w, U, p.ids + r,
+                                    p.probs ? p.probs + r : nullptr);
+                    }
+                    cl.sync();  // the lists have been read
+                    continue;
+                }
             }
-            edge = e;
+            cl.sync();
+            // the bin of the k-th entry, then the entry
+            for (int i = tid; i < kBins; i += kThreads) sm.count[i] = 0;
+            __syncthreads();
+            v.each([&](const float (&x)[VE], int id) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    if (x[e] > -INFINITY) atomicAdd(&sm.count[bin_of(x[e])], 1u);
+            });
+            const int b = v.crossing(counts, static_cast<uint64_t>(k));
+            const uint64_t need = static_cast<uint64_t>(k) - sm.above;
+            if (b < kBins)  // else fewer than k are not masked: all of them stay
+                edge.set(v.cut([&](float l, int) { return l > -INFINITY && bin_of(l) == b; },
+                               [](float) { return uint64_t(1); }, need));
+            cl.sync();
+            for (int i = tid; i < kBins; i += kThreads) sm.count[i] = 0;
+            __syncthreads();
         }
         if (top_p < 1.0f) {
-            auto kept = [&](float l, int i) { return stays(order_key32(l), i) ? weight(l) : uint64_t(0); };
-            const uint64_t all = v.row_sum(kept), P = fraction64(top_p);
-            uint64_t need = __umul64hi(P, all) + (P * all != 0 ? 1 : 0), in = 0;
-            if (need == 0) need = 1;
-            const uint32_t e = v.threshold(kept, need, in);
-            const uint64_t one = weight(key_value(static_cast<uint64_t>(e) << 32));
-            const uint64_t m = (need + one - 1) / one;  // of the in / one equal logits
-            if (m < in / one) {
-                uint64_t total;
-                last = v.locate([&](float l, int i) {
-                                    const uint32_t key = order_key32(l);
-                                    return uint64_t(key == e && stays(key, i));
-                                },
-                                [&](uint64_t) { return m - 1; }, total);
-            } else if (e != edge) {
-                last = 0x7FFFFFFF;
+            // all weights that stay, and how many of them lie in each bin
+            uint64_t sum = 0;
+            v.each([&](const float (&x)[VE], int id) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    if (!edge.stays(x[e], id + e)) continue;
+                    const uint64_t w = weight(x[e]);
+                    sum += w;
+                    if (w) atomicAdd(&sm.count[bin_of(x[e])], 1u);
+                }
+            });
+            for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0;
+            const uint64_t need = share_of(top_p, v.row_sum(sum));
+            // the bins that may be the one in which the sum of weights reaches need: a bin's weights lie
+            // between 2^(S - (b + 1) / 64) and 2^(S - b / 64), the last one's anywhere below that
+            constexpr int B = kBins / kThreads;
+            double low[B], high[B], l0 = 0.0, h0 = 0.0;
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int bin = tid * B + b;
+                uint64_t c = 0;
+                for (int from = 0; from < ranks; ++from) c += counts(from, bin);
+                const float x = static_cast<float>(c) * exp2f(static_cast<float>(S) - bin / kBinsPerOctave);
+                high[b] = x;
+                low[b] = bin < kBins - 1 ? x * 0.9892f : 0.0f;  // 2^(-1/64) = 0.98922...
+                h0 += high[b];
+                l0 += low[b];
             }
-            edge = e;
+            if (tid == 0) {
+                sm.bin = 0;
+                sm.found = kBins - 1;
+            }
+            // (bounds in whole units of weight: what rounding loses is within the margin below)
+            uint64_t hs = cta_scan(sm, static_cast<uint64_t>(h0));
+            __syncthreads();
+            uint64_t ls = cta_scan(sm, static_cast<uint64_t>(l0));
+            const double want = static_cast<double>(need);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const double hb = static_cast<double>(hs) + (b ? high[0] : 0.0), lb = static_cast<double>(ls) + (b ? low[0] : 0.0);
+                // first bins at which the upper bound may, and the lower bound must, have reached it
+                if (hb * 1.001 + 4096.0 < want && (hb + high[b]) * 1.001 + 4096.0 >= want) sm.bin = tid * B + b;
+                if (lb * 0.999 - 4096.0 < want && (lb + low[b]) * 0.999 - 4096.0 >= want) sm.found = tid * B + b;
+            }
+            __syncthreads();
+            const int ba = sm.bin, bb = sm.found;
+            // the bracket's bins, and what lies above it, exactly
+            sum = 0;
+            v.each([&](const float (&x)[VE], int id) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const int b = bin_of(x[e]);
+                    if (b > bb || !edge.stays(x[e], id + e)) continue;
+                    const uint64_t w = weight(x[e]);
+                    if (b < ba) sum += w;
+                    else if (w) atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[b]), w);
+                }
+            });
+            const uint64_t over = v.row_sum(sum);
+            const int b = v.crossing([&](int from, int i) { return cl.map_shared_rank(sm.mass, from)[i]; }, need - over);
+            const uint64_t rest = need - over - sm.above;
+            const Edge kept = edge;
+            edge.set(v.cut([&](float l, int id) { return bin_of(l) == b && kept.stays(l, id) && weight(l) > 0; }, weight,
+                           rest));
         }
-        const uint64_t floor_w = static_cast<uint64_t>(ceil(ldexp(static_cast<double>(min_p), S)));
         uint64_t total;
-        const uint64_t U = fraction64(u);
         const int id = v.locate(
             [&](float l, int i) {
-                if (!stays(order_key32(l), i)) return uint64_t(0);
+                if (!edge.stays(l, i)) return uint64_t(0);
                 const uint64_t w = weight(l);
                 return w >= floor_w ? w : uint64_t(0);
             },
             [&](uint64_t t) { return __umul64hi(U, t); }, total);
         if (rank == 0 && tid == 0) {
             p.ids[r] = id;
-            if (p.probs) p.probs[r] = static_cast<float>(static_cast<double>(weight(v.at(id))) /
-                                                         static_cast<double>(total));
+            if (p.probs) {
+                const float l = Elem<DT>::widen(ld_dep(static_cast<const typename View::T *>(p.logits) + r * p.stride + id));
+                p.probs[r] = static_cast<float>(static_cast<double>(weight(l)) / static_cast<double>(total));
+            }
         }
         __syncthreads();
     }
     cl.sync();  // no CTA leaves while a peer may address its shared memory
 }
 
-template <int DT>
-cudaError_t launch(const SampleParams &p, cudaStream_t stream) {
-    int bits = 0;
-    while ((1ll << bits) < p.vocab) ++bits;
-    const int S = 62 - bits < 45 ? 62 - bits : 45;  // a row's sum stays below 2^62
-    int ranks = 1;
-    while (ranks < kMaxCluster && static_cast<int64_t>(ranks) * 8192 < p.vocab) ranks *= 2;
+template <int DT, bool RESIDENT>
+cudaError_t launch_kernel(const SampleParams &p, int S, int steps, int ranks, cudaStream_t stream) {
+    const size_t smem = sizeof(Shared) + (RESIDENT ? static_cast<size_t>(steps) * kThreads * 16 : 0);
+    auto kern = sample_kernel<DT, RESIDENT>;
+    {
+        DeviceInfo dev;
+        cudaError_t e = device_info(&dev);
+        if (e != cudaSuccess) return e;
+        static std::mutex mu;
+        static bool done[64] = {};
+        std::lock_guard<std::mutex> lock(mu);
+        if (!done[dev.device]) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+            if (e != cudaSuccess) return e;
+            done[dev.device] = true;
+        }
+    }
     const int64_t clusters = p.rows < (1 << 20) ? p.rows : (1 << 20);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -380,7 +790,23 @@ cudaError_t launch(const SampleParams &p, cudaStream_t stream) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<DT>, p, S);
+    return cudaLaunchKernelEx(&cfg, kern, p, S, steps);
+}
+
+template <int DT>
+cudaError_t launch(const SampleParams &p, cudaStream_t stream) {
+    constexpr int VE = 16 / static_cast<int>(sizeof(typename Elem<DT>::T));
+    int bits = 0;
+    while ((1ll << bits) < p.vocab) ++bits;
+    const int S = 62 - bits < 45 ? 62 - bits : 45;  // a row's sum stays below 2^62
+    // words of a row, one more for a row that starts inside its first
+    const int64_t words = (static_cast<int64_t>(p.vocab) + VE - 1) / VE + 1;
+    int ranks = 1;
+    while (ranks < kMaxCluster && static_cast<int64_t>(ranks) * 4 * kThreads < words) ranks *= 2;
+    const int64_t steps = (words + ranks * kThreads - 1) / (ranks * kThreads);
+    if (sizeof(Shared) + steps * kThreads * 16 <= kMaxSmem)
+        return launch_kernel<DT, true>(p, S, static_cast<int>(steps), ranks, stream);
+    return launch_kernel<DT, false>(p, S, static_cast<int>(steps), ranks, stream);
 }
 
 }  // namespace
