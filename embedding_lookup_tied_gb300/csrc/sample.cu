@@ -17,10 +17,10 @@
 //  * top-k: at least k entries lie in or above the bin that holds the k-th
 //    largest of the threads' maxima, and few more do, so that bound gathers a
 //    short list; one CTA sorts it and does the rest (k, p, min-p, the draw).
-//  * top-p alone: one pass sums all weights and counts the entries by
-//    bins of 1/64 octave; the counts bracket the bin in which the weights
-//    reach p of their sum, a pass over the bracket sums its bins exactly, and
-//    the entries of the one bin left are sorted.
+//  * top-p alone: one pass counts the entries by bins of 1/32 octave; the
+//    counts bracket the bin in which the weights reach p of their sum, a pass
+//    sums all weights and the bracket's bins exactly, and the entries of the
+//    one bin left are sorted.
 //  * Where a list does not fit (equal logits by the thousand, a large k), the
 //    threshold is found digit by digit (11, 11 and 10 bits of the order key)
 //    from histograms of counts or weights.
@@ -42,8 +42,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 2048;                   // entries one CTA sorts
 constexpr int kDigits = 2048;                 // bins of a digit of the order key
-constexpr int kBins = 1024;                   // of 1/64 octave of weight; the last takes all that is below
-constexpr float kBinsPerOctave = 64.0f;
+constexpr int kBins = 1024;                   // of 1/32 octave of weight; the last takes all that is below
+constexpr float kBinsPerOctave = 32.0f;
 constexpr int kMaxSmem = 224 * 1024;
 constexpr uint32_t kKeyInf = 0xFF800000u;     // order key of +inf; NaN lies above
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // order key of -inf
@@ -70,15 +70,6 @@ struct Weight {
     int shift;  // 62 - S
     const uint64_t *pow16;  // kPow16 in shared memory: 16 pairs of words, one to a bank
 
-    __device__ __forceinline__ void init(float max_, float temperature, int S, const uint64_t *table) {
-        max = max_;
-        const double c = 1.4426950408889634 / static_cast<double>(temperature);
-        c_hi = static_cast<float>(c);
-        c_lo = static_cast<float>(c - static_cast<double>(c_hi));
-        far = static_cast<float>(S + 1) / c_hi;
-        shift = 62 - S;
-        pow16 = table;
-    }
     __device__ __forceinline__ uint64_t operator()(float l) const {
         const float s = __fsub_rn(max, l);
         if (!(s <= far)) return 0ull;  // also -inf
@@ -106,7 +97,17 @@ struct Weight {
     }
 };
 
-struct Shared {
+// What a row's parameters come to, worked out by one thread of each CTA (its
+// 64-bit floating point would take every thread's turn on a slow unit).
+struct RowScale {
+    float c_hi, c_lo;   // log2(e) / T
+    float far;          // differences from the largest logit beyond it weigh 0
+    float span;         // differences beyond it are below min-p for certain
+    uint64_t floor_w;   // min-p as a weight
+    uint64_t U, P;      // u and top-p in units of 2^-64
+};
+
+struct alignas(16) Shared {
     uint64_t list[kList];           // entries; the digit histograms where no list fits
     uint64_t mass[kBins];
     uint32_t count[kBins];
@@ -114,6 +115,8 @@ struct Shared {
     uint64_t warp_sum[kWarps];
     uint64_t above, in;
     uint64_t pow16[16];
+    uint64_t arrived[kWarps];       // each warp's piece of the row has
+    RowScale scale;
     int32_t bin;
     int32_t found;
     int32_t gathered;
@@ -145,14 +148,21 @@ __device__ __forceinline__ uint64_t cta_sum(Shared &sm, uint64_t v) {
     for (int i = 0; i < kWarps; ++i) s += sm.warp_sum[i];
     return s;
 }
-// Exclusive scan over the CTA's threads; the caller syncs before the next use.
-__device__ __forceinline__ uint64_t cta_scan(Shared &sm, uint64_t v) {
+// Exclusive scan over the CTA's threads, and the sum of all; the caller syncs
+// before the next use.
+__device__ __forceinline__ uint64_t cta_scan(Shared &sm, uint64_t v, uint64_t &all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint64_t incl = warp_scan(v, lane);
     if (lane == 31) sm.warp_sum[warp] = incl;
     __syncthreads();
     uint64_t before = incl - v;
-    for (int w = 0; w < warp; ++w) before += sm.warp_sum[w];
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const uint64_t x = sm.warp_sum[w];
+        if (w < warp) before += x;
+        all += x;
+    }
     return before;
 }
 
@@ -235,18 +245,28 @@ struct RowView {
     int skip;           // elements of that word before it
     int flip;           // which exchange slots come next
 
+    // Word w of the row, -inf where its elements are not the row's.
     __device__ __forceinline__ uint4 fetch(int w) const {
         const int64_t first = static_cast<int64_t>(w) * VE - skip;  // id of the word's first element
         if (first >= vocab || first + VE <= 0) return outside();
-        uint4 u = ld_dep(base + w);
-        if (first < 0 || first + VE > vocab) {
-            T *e = reinterpret_cast<T *>(&u);
-            const uint4 o = outside();
+        const uint4 u = ld_dep(base + w);
+        return first < 0 || first + VE > vocab ? trim(u, w) : u;
+    }
+    __device__ __forceinline__ uint4 trim(const uint4 &u, int w) const {
+        const int64_t first = static_cast<int64_t>(w) * VE - skip;
+        const uint32_t in[4] = {u.x, u.y, u.z, u.w}, o = outside().x;
+        uint32_t r[4];
 #pragma unroll
-            for (int i = 0; i < VE; ++i)
-                if (first + i < 0 || first + i >= vocab) e[i] = reinterpret_cast<const T *>(&o)[i];
+        for (int i = 0; i < 4; ++i) {
+            if (VE == 4) {
+                r[i] = first + i >= 0 && first + i < vocab ? in[i] : o;
+            } else {
+                const bool lo = first + 2 * i >= 0 && first + 2 * i < vocab;
+                const bool hi = first + 2 * i + 1 >= 0 && first + 2 * i + 1 < vocab;
+                r[i] = (lo ? in[i] & 0xFFFFu : o & 0xFFFFu) | (hi ? in[i] & 0xFFFF0000u : o & 0xFFFF0000u);
+            }
         }
-        return u;
+        return make_uint4(r[0], r[1], r[2], r[3]);
     }
     static __device__ __forceinline__ uint4 outside() {  // -inf
         const uint32_t w = DT == LHS_F32 ? 0xFF800000u : DT == LHS_F16 ? 0xFC00FC00u : 0xFF80FF80u;
@@ -272,24 +292,49 @@ struct RowView {
             f(v, (word0 + s * 32) * VE - skip);
         }
     }
-    // The row's first reading: this lane's largest order key.
-    __device__ __forceinline__ uint32_t read() {
-        uint32_t top = 0;
-        constexpr int kBatch = 8;
-        for (int s = 0; s < steps; s += kBatch) {
-            uint4 u[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) u[i] = s + i < steps ? fetch(word0 + (s + i) * 32) : outside();
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (RESIDENT && s + i < steps) hold[(s + i) * 32] = u[i];
-                float v[VE];
-                widen(u[i], v);
-#pragma unroll
-                for (int e = 0; e < VE; ++e) top = max(top, order_key32(v[e]));
+    // Starts the copy of this warp's piece of the row (the words that lie in it).
+    __device__ __forceinline__ void start() const {
+        if (!RESIDENT || (threadIdx.x & 31)) return;
+        const int n = piece();
+        uint64_t *bar = &sm.arrived[threadIdx.x >> 5];
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the last row's reads
+        mbar_arrive_expect_tx(bar, n * 16);
+        if (n > 0) bulk_load(hold, base + word0, n * 16, bar);
+    }
+    // Words of the warp's piece that hold elements of the row.
+    __device__ __forceinline__ int piece() const {
+        const int64_t words = (static_cast<int64_t>(skip) + vocab + VE - 1) / VE;
+        const int64_t n = words - (word0 - static_cast<int>(threadIdx.x & 31));
+        return static_cast<int>(n < 0 ? 0 : n < steps * 32 ? n : steps * 32);
+    }
+    // The row's first reading, once its piece has arrived: elements that are not
+    // the row's become -inf; this lane's largest logit as an order key.
+    __device__ __forceinline__ uint32_t read(uint32_t parity, int32_t *err) {
+        const int lane = threadIdx.x & 31;
+        float top = -INFINITY;
+        uint32_t magnitude = 0;  // above the bits of inf: a NaN
+        if (RESIDENT) {
+            const int n = piece();
+            if (!mbar_wait(&sm.arrived[threadIdx.x >> 5], parity, kWaitTimeoutNs)) set_err(err, LHS_ERRBIT_TIMEOUT);
+            for (int w = n + ((lane - n) & 31); w < steps * 32; w += 32) hold[w - lane] = outside();  // words lane, lane + 32, ..
+            const int w0 = word0 - lane;
+            if (n > 0 && ((w0 == 0 && skip) || n < steps * 32 || static_cast<int64_t>(w0 + n) * VE - skip > vocab)) {
+                // the row's first and last words
+                if (lane == 0 && w0 == 0) hold[0] = trim(hold[0], 0);
+                if (lane == (n - 1) % 32) hold[n - 1 - lane] = trim(hold[n - 1 - lane], w0 + n - 1);
             }
         }
-        return top;
+#pragma unroll 4
+        for (int s = 0; s < steps; ++s) {
+            float v[VE];
+            widen(RESIDENT ? hold[s * 32] : fetch(word0 + s * 32), v);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                top = fmaxf(top, v[e]);
+                magnitude = max(magnitude, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+            }
+        }
+        return magnitude > 0x7F800000u ? 0xFFFFFFFFu : order_key32(top);
     }
 
     // Every CTA's v, in this CTA's shared memory.
@@ -320,10 +365,12 @@ struct RowView {
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             h[b] = 0;
-            for (int r = 0; r < ranks; ++r) h[b] += value(r, static_cast<int>(threadIdx.x) * B + b);
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                if (r < ranks) h[b] += value(r, static_cast<int>(threadIdx.x) * B + b);
             mine += h[b];
         }
-        uint64_t above = cta_scan(sm, mine);
+        uint64_t all, above = cta_scan(sm, mine, all);
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             if (above < need && above + h[b] >= need) {
@@ -390,7 +437,7 @@ struct RowView {
                     w[i] = k ? value(key_value(k)) : 0ull;
                     mine += w[i];
                 }
-                uint64_t above = cta_scan(sm, mine);
+                uint64_t all, above = cta_scan(sm, mine, all);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     if (above < need && above + w[i] >= need) sm.above = sm.list[threadIdx.x * P + i];
@@ -427,11 +474,12 @@ struct RowView {
 #pragma unroll
             for (int b = 0; b < P; ++b) {
                 h[b] = 0;
-                for (int r = 0; r < ranks; ++r)
-                    h[b] += cl.map_shared_rank(sm.list, r)[kDigits - 1 - (threadIdx.x * P + b)];
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r)
+                    if (r < ranks) h[b] += cl.map_shared_rank(sm.list, r)[kDigits - 1 - (threadIdx.x * P + b)];
                 mine += h[b];
             }
-            uint64_t above = cta_scan(sm, mine);
+            uint64_t all, above = cta_scan(sm, mine, all);
 #pragma unroll
             for (int b = 0; b < P; ++b) {
                 if (above < need && above + h[b] >= need) {
@@ -476,34 +524,42 @@ struct RowView {
             total += all[i];
         }
         const uint64_t t = target(total);
-        for (int w = 0; w < warp; ++w) before += sm.warp_sum[w];
-        if (t >= before && t < before + sm.warp_sum[warp]) {  // in this warp's piece
-            for (int st = 0; st < steps; ++st) {
+        // the warp whose piece holds the answer; the whole CTA walks that piece
+        int at = -1;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const uint64_t x = sm.warp_sum[w];
+            if (at < 0 && t >= before && t < before + x) at = w;
+            if (at < 0) before += x;
+        }
+        __syncthreads();
+        if (at >= 0) {
+            const int words = steps * 32;
+            const int w0 = word0 - lane + (at - warp) * words;  // the piece's first word
+            const uint4 *src = hold - lane + (at - warp) * words;
+            for (int i0 = 0; i0 < words; i0 += kThreads) {
+                const int i = i0 + threadIdx.x;
                 float v[VE];
-                widen(RESIDENT ? hold[st * 32] : fetch(word0 + st * 32), v);
-                const int id = (word0 + st * 32) * VE - skip;
-                uint64_t w[VE], mine = 0;
+                widen(i < words ? (RESIDENT ? src[i] : fetch(w0 + i)) : outside(), v);
+                const int id = (w0 + i) * VE - skip;
+                uint64_t x[VE], mine_i = 0;
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    w[e] = value(v[e], id + e);
-                    mine += w[e];
+                    x[e] = value(v[e], id + e);
+                    mine_i += x[e];
                 }
-                const uint64_t incl = warp_scan(mine, lane);
-                const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > t);
-                if (hit) {
-                    if (lane == __ffs(hit) - 1) {
-                        uint64_t at = before + incl - mine;
-                        int found = -1;
+                uint64_t all_i, run = before + cta_scan(sm, mine_i, all_i);
+                if (t >= run && t < run + mine_i) {
+                    int found = -1;
 #pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            at += w[e];
-                            if (found < 0 && at > t) found = id + e;
-                        }
-                        for (int r = 0; r < ranks; ++r) *cl.map_shared_rank(&sm.found, r) = found;
+                    for (int e = 0; e < VE; ++e) {
+                        run += x[e];
+                        if (found < 0 && run > t) found = id + e;
                     }
-                    break;
+                    for (int r = 0; r < ranks; ++r) *cl.map_shared_rank(&sm.found, r) = found;
                 }
-                before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+                before += all_i;
+                __syncthreads();
             }
         }
         cl.sync();
@@ -515,65 +571,59 @@ struct RowView {
 __device__ __forceinline__ uint64_t fraction64(float f) {
     return static_cast<uint64_t>(static_cast<double>(f) * 0x1p64);
 }
-// The least integer that is at least p of all (1 at least).
-__device__ __forceinline__ uint64_t share_of(float p, uint64_t all) {
-    const uint64_t P = fraction64(p);
+// The least integer that is at least P 2^-64 of all (1 at least).
+__device__ __forceinline__ uint64_t share_of(uint64_t P, uint64_t all) {
     const uint64_t need = __umul64hi(P, all) + (P * all != 0 ? 1 : 0);
     return need ? need : 1;
 }
 
-// A row that the filters have narrowed to the n <= kList entries of the list, in
+// A row that the filters have narrowed to the n <= 512 E entries of the list, in
 // any order, in one CTA: top-k of them, top-p, min-p and the draw.
-__device__ void finish_list(Shared &sm, const Weight &weight, int n, int k, float top_p, uint64_t floor_w, uint64_t U,
-                            int32_t *id, float *prob) {
-    constexpr int P = kList / kThreads;
+template <int E>
+__device__ void finish_list(Shared &sm, const Weight &weight, int n, int k, float top_p, int32_t *id, float *prob) {
     const int tid = threadIdx.x;
     sort_list(sm, n);
-    if (k < n) n = k;
-    uint64_t w[P], mine = 0;
+    const int most = k < n ? k : n;
+    uint64_t key[E], w[E], mine = 0, all;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        w[i] = tid * P + i < n ? weight(key_value(sm.list[tid * P + i])) : 0ull;
+    for (int i = 0; i < E; ++i) {
+        key[i] = sm.list[tid * E + i];
+        w[i] = tid * E + i < most ? weight(key_value(key[i])) : 0ull;
         mine += w[i];
     }
-    const uint64_t all = cta_sum(sm, mine);
-    __syncthreads();
-    const uint64_t need = top_p < 1.0f ? share_of(top_p, all) : ~0ull;
-    uint64_t above = cta_scan(sm, mine);
+    uint64_t above = cta_scan(sm, mine, all);
+    const uint64_t need = top_p < 1.0f ? share_of(sm.scale.P, all) : ~0ull;
     // those that stay, keyed by id (ascending: the inverted id descending) with the order key
     // below, so that a second sort puts them into id order
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const bool stays = tid * P + i < n && above < need && w[i] >= floor_w && w[i] > 0;
+    for (int i = 0; i < E; ++i) {
+        const bool stays = above < need && w[i] >= sm.scale.floor_w && w[i] > 0;
         above += w[i];
-        const uint64_t key = sm.list[tid * P + i];
-        sm.list[tid * P + i] = stays ? (key << 32) | (key >> 32) : 0ull;
+        sm.list[tid * E + i] = stays ? (key[i] << 32) | (key[i] >> 32) : 0ull;
     }
     __syncthreads();
-    sort_list(sm, n);
+    sort_list(sm, most);
     mine = 0;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const uint64_t key = sm.list[tid * P + i];
-        w[i] = key ? weight(key_value(key << 32)) : 0ull;
+    for (int i = 0; i < E; ++i) {
+        key[i] = sm.list[tid * E + i];
+        w[i] = key[i] ? weight(key_value(key[i] << 32)) : 0ull;
         mine += w[i];
     }
-    const uint64_t total = cta_sum(sm, mine);
-    __syncthreads();
-    const uint64_t t = __umul64hi(U, total);
-    above = cta_scan(sm, mine);
+    above = cta_scan(sm, mine, all);
+    const uint64_t t = __umul64hi(sm.scale.U, all);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
+    for (int i = 0; i < E; ++i) {
         if (above <= t && t < above + w[i]) {
-            *id = key_id(sm.list[tid * P + i] >> 32);
-            if (prob) *prob = static_cast<float>(static_cast<double>(w[i]) / static_cast<double>(total));
+            *id = key_id(key[i] >> 32);
+            if (prob) *prob = static_cast<float>(static_cast<double>(w[i]) / static_cast<double>(all));
         }
         above += w[i];
     }
 }
 
 template <int DT, bool RESIDENT>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, const int S, const int steps) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p, const int S, const int steps) {
     using View = RowView<DT, RESIDENT>;
     constexpr int VE = View::VE;
     extern __shared__ __align__(16) uint8_t dyn_smem[];
@@ -582,6 +632,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
     const int rank = static_cast<int>(cl.block_rank()), ranks = static_cast<int>(cl.num_blocks());
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid < 16) sm.pow16[tid] = kPow16[tid];
+    if (lane == 0) {
+        mbar_init(&sm.arrived[warp], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
     pdl_trigger();
     pdl_wait();
     cl.sync();  // the peers run: their shared memory may be written
@@ -589,10 +644,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
     View v{sm, cl, rank, ranks, nullptr, steps, (rank * kWarps + warp) * steps * 32 + lane, p.vocab, nullptr, 0, 0};
     v.hold = reinterpret_cast<uint4 *>(dyn_smem + sizeof(Shared)) + warp * steps * 32 + lane;
 
-    for (int64_t r = blockIdx.x / ranks; r < p.rows; r += gridDim.x / ranks) {
+    uint32_t parity = 0;
+    for (int64_t r = blockIdx.x / ranks; r < p.rows; r += gridDim.x / ranks, parity ^= 1u) {
         const uintptr_t row = reinterpret_cast<uintptr_t>(static_cast<const typename View::T *>(p.logits) + r * p.stride);
         v.base = reinterpret_cast<const uint4 *>(row & ~uintptr_t(15));
         v.skip = static_cast<int>((row & 15) / sizeof(typename View::T));
+        v.start();
         const float u = ld_dep(p.u + r);
         float T = p.temperature ? ld_dep(p.temperature + r) : 1.0f;
         const float top_p = p.top_p ? ld_dep(p.top_p + r) : 1.0f;
@@ -607,8 +664,20 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
         T = fminf(fmaxf(T, 0x1p-100f), 0x1p100f);
         if (k <= 0 || k >= p.vocab) k = p.vocab;
 
+        if (tid == 0) {
+            const double c = 1.4426950408889634 / static_cast<double>(T);
+            const float c_hi = static_cast<float>(c);
+            RowScale &x = sm.scale;
+            x.c_hi = c_hi;
+            x.c_lo = static_cast<float>(c - static_cast<double>(c_hi));
+            x.far = static_cast<float>(S + 1) / c_hi;
+            x.span = min_p > 0.0f ? (0.001f - log2f(min_p)) / c_hi : INFINITY;
+            x.floor_w = static_cast<uint64_t>(ceil(ldexp(static_cast<double>(min_p), S)));
+            x.U = fraction64(u);
+            x.P = fraction64(top_p);
+        }
         // the row's largest logit (as an order key: NaN lies above +inf)
-        const uint32_t lane_top = v.read();
+        const uint32_t lane_top = v.read(parity, p.err);
         uint32_t top = __reduce_max_sync(0xFFFFFFFFu, lane_top);
         if (lane == 0) sm.warp_sum[warp] = top;
         for (int i = tid; i < kBins; i += kThreads) sm.count[i] = 0;
@@ -627,15 +696,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
             __syncthreads();
             continue;
         }
-        Weight weight;
-        weight.init(key_value(static_cast<uint64_t>(top) << 32), T, S, sm.pow16);
+        const Weight weight = {key_value(static_cast<uint64_t>(top) << 32), sm.scale.c_hi, sm.scale.c_lo, sm.scale.far,
+                               62 - S, sm.pow16};
         const float per_bin = weight.c_hi * kBinsPerOctave;
         // bins from the top of the row down; a larger logit never lies in a later bin
         auto bin_of = [&](float l) { return static_cast<int>(fminf((weight.max - l) * per_bin, kBins - 1.0f)); };
         auto counts = [&](int from, int b) { return uint64_t(cl.map_shared_rank(sm.count, from)[b]); };
-        const uint64_t floor_w = static_cast<uint64_t>(ceil(ldexp(static_cast<double>(min_p), S)));
-        const uint64_t U = fraction64(u);
-
         Edge edge = {-INFINITY, 0x7FFFFFFF};
         if (k < p.vocab) {
             // at least k entries lie in the bins up to the one in which the k-th of the lanes' maxima does
@@ -647,8 +713,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
                 if (n <= kList) {
                     if (rank == 0) {
                         v.pull(v.last_exchange());
-                        finish_list(sm, weight, static_cast<int>(n), k, top_p, floor_w, U, p.ids + r,
-                                    p.probs ? p.probs + r : nullptr);
+                        float *prob = p.probs ? p.probs + r : nullptr;
+                        if (n <= kThreads) finish_list<1>(sm, weight, static_cast<int>(n), k, top_p, p.ids + r, prob);
+                        else finish_list<kList / kThreads>(sm, weight, static_cast<int>(n), k, top_p, p.ids + r, prob);
                     }
                     cl.sync();  // the lists have been read
                     continue;
@@ -673,65 +740,64 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
             __syncthreads();
         }
         if (top_p < 1.0f) {
-            // all weights that stay, and how many of them lie in each bin
-            uint64_t sum = 0;
+            // how many of those that stay lie in each bin
             v.each([&](const float (&x)[VE], int id) {
 #pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    if (!edge.stays(x[e], id + e)) continue;
-                    const uint64_t w = weight(x[e]);
-                    sum += w;
-                    if (w) atomicAdd(&sm.count[bin_of(x[e])], 1u);
-                }
+                for (int e = 0; e < VE; ++e)
+                    if (x[e] > -INFINITY && edge.stays(x[e], id + e)) atomicAdd(&sm.count[bin_of(x[e])], 1u);
             });
             for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0;
-            const uint64_t need = share_of(top_p, v.row_sum(sum));
-            // the bins that may be the one in which the sum of weights reaches need: a bin's weights lie
-            // between 2^(S - (b + 1) / 64) and 2^(S - b / 64), the last one's anywhere below that
-            constexpr int B = kBins / kThreads;
-            double low[B], high[B], l0 = 0.0, h0 = 0.0;
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int bin = tid * B + b;
-                uint64_t c = 0;
-                for (int from = 0; from < ranks; ++from) c += counts(from, bin);
-                const float x = static_cast<float>(c) * exp2f(static_cast<float>(S) - bin / kBinsPerOctave);
-                high[b] = x;
-                low[b] = bin < kBins - 1 ? x * 0.9892f : 0.0f;  // 2^(-1/64) = 0.98922...
-                h0 += high[b];
-                l0 += low[b];
-            }
             if (tid == 0) {
                 sm.bin = 0;
                 sm.found = kBins - 1;
             }
-            // (bounds in whole units of weight: what rounding loses is within the margin below)
-            uint64_t hs = cta_scan(sm, static_cast<uint64_t>(h0));
-            __syncthreads();
-            uint64_t ls = cta_scan(sm, static_cast<uint64_t>(l0));
-            const double want = static_cast<double>(need);
+            cl.sync();
+            // The bins that may be the one in which the sum of weights reaches p of all.  A bin's
+            // weights lie between 2^(S - (b + 1) / 32) and 2^(S - b / 32), the last one's anywhere
+            // below that: bounds for the sums up to each bin and for all.
+            constexpr int B = kBins / kThreads;
+            uint64_t high[B], low[B], h0 = 0, l0 = 0, h_all, l_all;
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                const double hb = static_cast<double>(hs) + (b ? high[0] : 0.0), lb = static_cast<double>(ls) + (b ? low[0] : 0.0);
-                // first bins at which the upper bound may, and the lower bound must, have reached it
-                if (hb * 1.001 + 4096.0 < want && (hb + high[b]) * 1.001 + 4096.0 >= want) sm.bin = tid * B + b;
-                if (lb * 0.999 - 4096.0 < want && (lb + low[b]) * 0.999 - 4096.0 >= want) sm.found = tid * B + b;
+                const int bin = tid * B + b;
+                uint32_t c = 0;
+#pragma unroll
+                for (int from = 0; from < kMaxCluster; ++from)
+                    if (from < ranks) c += static_cast<uint32_t>(counts(from, bin));
+                const float x = static_cast<float>(c) * exp2f(static_cast<float>(S) - bin / kBinsPerOctave);
+                high[b] = static_cast<uint64_t>(x * 1.0001f) + c;
+                low[b] = bin < kBins - 1 ? static_cast<uint64_t>(x * 0.9784f) : 0ull;  // 2^(-1/32) = 0.97857..
+                h0 += high[b];
+                l0 += low[b];
+            }
+            uint64_t hs = cta_scan(sm, h0, h_all);
+            __syncthreads();
+            uint64_t ls = cta_scan(sm, l0, l_all);
+            const uint64_t least = share_of(sm.scale.P, l_all), most = share_of(sm.scale.P, h_all);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (hs < least && hs + high[b] >= least) sm.bin = tid * B + b;
+                if (ls < most && ls + low[b] >= most) sm.found = tid * B + b;
+                hs += high[b];
+                ls += low[b];
             }
             __syncthreads();
             const int ba = sm.bin, bb = sm.found;
-            // the bracket's bins, and what lies above it, exactly
-            sum = 0;
+            // all weights, those above the bracket, and its bins one by one, exactly
+            uint64_t sum = 0, over = 0;
             v.each([&](const float (&x)[VE], int id) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
+                    if (!edge.stays(x[e], id + e)) continue;
                     const int b = bin_of(x[e]);
-                    if (b > bb || !edge.stays(x[e], id + e)) continue;
                     const uint64_t w = weight(x[e]);
-                    if (b < ba) sum += w;
-                    else if (w) atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[b]), w);
+                    sum += w;
+                    if (b < ba) over += w;
+                    else if (b <= bb && w) atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[b]), w);
                 }
             });
-            const uint64_t over = v.row_sum(sum);
+            const uint64_t need = share_of(sm.scale.P, v.row_sum(sum));
+            over = v.row_sum(over);
             const int b = v.crossing([&](int from, int i) { return cl.map_shared_rank(sm.mass, from)[i]; }, need - over);
             const uint64_t rest = need - over - sm.above;
             const Edge kept = edge;
@@ -741,11 +807,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
         uint64_t total;
         const int id = v.locate(
             [&](float l, int i) {
-                if (!edge.stays(l, i)) return uint64_t(0);
+                if (!edge.stays(l, i) || weight.max - l > sm.scale.span) return uint64_t(0);
                 const uint64_t w = weight(l);
-                return w >= floor_w ? w : uint64_t(0);
+                return w >= sm.scale.floor_w ? w : uint64_t(0);
             },
-            [&](uint64_t t) { return __umul64hi(U, t); }, total);
+            [&](uint64_t t) { return __umul64hi(sm.scale.U, t); }, total);
         if (rank == 0 && tid == 0) {
             p.ids[r] = id;
             if (p.probs) {
@@ -802,7 +868,7 @@ cudaError_t launch(const SampleParams &p, cudaStream_t stream) {
     // words of a row, one more for a row that starts inside its first
     const int64_t words = (static_cast<int64_t>(p.vocab) + VE - 1) / VE + 1;
     int ranks = 1;
-    while (ranks < kMaxCluster && static_cast<int64_t>(ranks) * 4 * kThreads < words) ranks *= 2;
+    while (ranks < kMaxCluster && static_cast<int64_t>(ranks) * 5 * kThreads < words) ranks *= 2;
     const int64_t steps = (words + ranks * kThreads - 1) / (ranks * kThreads);
     if (sizeof(Shared) + steps * kThreads * 16 <= kMaxSmem)
         return launch_kernel<DT, true>(p, S, static_cast<int>(steps), ranks, stream);

@@ -152,6 +152,27 @@ def test_many_rows(v):
 
 
 @pytest.mark.gpu
+def test_more_rows_than_one_grid():
+    # more rows than CTAs: each works through several, at changing alignments
+    n, v = (1 << 20) + 4321, 7
+    x, u, _ = draw_rows(4, n, v)
+    xd, ud = x.cuda(), u.cuda()
+    k = torch.full((n,), 3, dtype=torch.int32, device="cuda")
+    for args in (dict(), dict(top_k=k)):
+        ids, probs, err = lhs.lhs_sample(xd, ud, **args)
+        assert int(err.item()) == 0
+        w = torch.exp(x.double() - x.double().amax(1, keepdim=True))
+        if args:
+            w = torch.where(x >= x.topk(3, dim=1).values[:, -1:], w, 0.0)
+        c = w.cumsum(1)
+        share = c / c[:, -1:]
+        far = (share - u.double()[:, None]).abs().amin(1) > NEAR
+        want = (share <= u.double()[:, None]).sum(1)
+        assert int(far.sum()) > 0.99 * n
+        assert torch.equal(ids.cpu()[far].long(), want[far])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("v", [10, 4096, 30000, 262144])
 def test_equal_logits(v):
     # ties: lower ids first.  Powers of two make every share exact.
