@@ -17,7 +17,7 @@
 //  * top-k: at least k entries lie in or above the bin that holds the k-th
 //    largest of the threads' maxima, and few more do, so that bound gathers a
 //    short list; one CTA sorts it and does the rest (k, p, min-p, the draw).
-//  * top-p alone: one pass counts the entries by bins of 1/32 octave; the
+//  * top-p alone: one pass counts the entries by bins of 1/16 octave; the
 //    counts bracket the bin in which the weights reach p of their sum, a pass
 //    sums all weights and the bracket's bins exactly, and the entries of the
 //    one bin left are sorted.
@@ -37,13 +37,13 @@ namespace cg = cooperative_groups;
 namespace lhs {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
-constexpr int kList = 2048;                   // entries one CTA sorts
-constexpr int kDigits = 2048;                 // bins of a digit of the order key
-constexpr int kBins = 1024;                   // of 1/32 octave of weight; the last takes all that is below
-constexpr float kBinsPerOctave = 32.0f;
+constexpr int kMaxCluster = 16;
+constexpr int kList = 1024;                   // entries one CTA sorts
+constexpr int kDigits = 256;                  // bins of a digit of the order key
+constexpr int kBins = 512;                    // of 1/16 octave of weight; the last takes all that is below
+constexpr float kBinsPerOctave = 16.0f;
 constexpr int kMaxSmem = 224 * 1024;
 constexpr uint32_t kKeyInf = 0xFF800000u;     // order key of +inf; NaN lies above
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // order key of -inf
@@ -70,9 +70,12 @@ struct Weight {
     int shift;  // 62 - S
     const uint64_t *pow16;  // kPow16 in shared memory: 16 pairs of words, one to a bank
 
+    // (No branch, so that the weights of a word's logits are worked out side by side.)
     __device__ __forceinline__ uint64_t operator()(float l) const {
-        const float s = __fsub_rn(max, l);
-        if (!(s <= far)) return 0ull;  // also -inf
+        const float d = __fsub_rn(max, l);
+        const bool none = !(d <= far);  // also -inf
+        l = none ? max : l;
+        const float s = none ? 0.0f : d;
         const float bv = __fsub_rn(s, max), av = __fsub_rn(s, bv);
         const float e = __fsub_rn(__fsub_rn(max, av), __fadd_rn(l, bv));
         const float th = __fmul_rn(s, c_hi);
@@ -93,12 +96,12 @@ struct Weight {
         const uint64_t f = pow16[n & 15];
         const uint64_t w = f + static_cast<uint64_t>(
             (static_cast<int64_t>(static_cast<int>(f >> 32)) * delta) >> 4);
-        return w >> min(shift + (n >> 4), 63);
+        return none ? 0ull : w >> min(shift + (n >> 4), 63);
     }
 };
 
-// What a row's parameters come to, worked out by one thread of each CTA (its
-// 64-bit floating point would take every thread's turn on a slow unit).
+// What a row's parameters come to, worked out by one thread of each CTA while
+// the row is on its way.  No 64-bit floating point: its unit here is slow.
 struct RowScale {
     float c_hi, c_lo;   // log2(e) / T
     float far;          // differences from the largest logit beyond it weigh 0
@@ -121,7 +124,7 @@ struct alignas(16) Shared {
     int32_t found;
     int32_t gathered;
 };
-static_assert(kList == kDigits, "the digit histograms take the list's place");
+static_assert(kDigits <= kList, "the digit histograms take the list's place");
 static_assert(sizeof(Shared) % 16 == 0, "the row's words follow it");
 
 __device__ __forceinline__ uint64_t warp_add(uint64_t v) {
@@ -166,15 +169,16 @@ __device__ __forceinline__ uint64_t cta_scan(Shared &sm, uint64_t v, uint64_t &a
     return before;
 }
 
-// Descending sort of the 512 E (or fewer, a power of two) entries of buf: thread
-// t holds entries t E .. t E + E - 1 in registers; partners within a warp meet
-// by shuffles, others through buf.
+// Descending sort of the first size_all (a power of two, kThreads E at most)
+// entries of buf: thread t holds entries t E .. t E + E - 1 in registers;
+// partners within a warp meet by shuffles, others through buf.
 template <int E>
 __device__ __forceinline__ void sort_entries(uint64_t *buf, int size_all) {
     const int tid = threadIdx.x;
+    const bool active = (tid & ~31) * E < size_all;  // a warp's
     uint64_t v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = tid * E + e < size_all ? buf[tid * E + e] : 0ull;
+    for (int e = 0; e < E; ++e) v[e] = buf[tid * E + e];
     for (int size = 2; size <= size_all; size <<= 1) {
         for (int d = size >> 1; d > 0; d >>= 1) {
             if (d >= 32 * E) {
@@ -183,6 +187,7 @@ __device__ __forceinline__ void sort_entries(uint64_t *buf, int size_all) {
                 for (int e = 0; e < E; ++e) buf[tid * E + e] = v[e];
                 __syncthreads();
             }
+            if (!active) continue;
             uint64_t other[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -203,16 +208,15 @@ __device__ __forceinline__ void sort_entries(uint64_t *buf, int size_all) {
     for (int e = 0; e < E; ++e) buf[tid * E + e] = v[e];
     __syncthreads();
 }
-// The first n entries of the list, sorted descending; the rest of the list
-// becomes zeros.  CTA-collective.
+// The first n entries of the list, sorted descending, zeros after them up to
+// kThreads E.  CTA-collective.
+template <int E>
 __device__ __forceinline__ void sort_list(Shared &sm, int n) {
-    for (int i = n + threadIdx.x; i < kList; i += kThreads) sm.list[i] = 0ull;
+    for (int i = n + threadIdx.x; i < kThreads * E; i += kThreads) sm.list[i] = 0ull;
     __syncthreads();
-    int size = 32;
+    int size = 32 * E;
     while (size < n) size <<= 1;
-    if (size <= kThreads) sort_entries<1>(sm.list, size);
-    else if (size <= 2 * kThreads) sort_entries<2>(sm.list, size);
-    else sort_entries<4>(sm.list, size);
+    sort_entries<E>(sm.list, size);
 }
 
 // What stays: entries with a key of at least `edge`.
@@ -348,7 +352,9 @@ struct RowView {
     __device__ __forceinline__ uint64_t row_sum(uint64_t lane_sum) {
         const uint64_t *all = exchange(cta_sum(sm, lane_sum));
         uint64_t t = 0;
-        for (int i = 0; i < ranks; ++i) t += all[i];
+#pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i)
+            if (i < ranks) t += all[i];
         __syncthreads();
         return t;
     }
@@ -386,33 +392,42 @@ struct RowView {
 
     // Entries that `take` takes, as keys: into this CTA's list, its number (of
     // which kList at most are held) into sm.gathered; their number over the
-    // cluster.
+    // cluster.  take(values, id): a bit for each of a word's logits.
     template <typename F>
     __device__ __forceinline__ int64_t gather(const F &take) {
         if (threadIdx.x == 0) sm.gathered = 0;
         __syncthreads();
         each([&](const float (&v)[VE], int id) {
+            uint32_t mask = take(v, id);
+            if (mask == 0) return;
+            const int n = __popc(mask);
+            int at = atomicAdd(&sm.gathered, n);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                if (take(v[e], id + e)) {
-                    const int at = atomicAdd(&sm.gathered, 1);
+            for (int e = 0; e < VE; ++e)
+                if ((mask >> e) & 1u) {
                     if (at < kList) sm.list[at] = topk_key(v[e], id + e);
+                    ++at;
                 }
-            }
         });
         __syncthreads();
         const uint64_t *all = exchange(static_cast<uint64_t>(sm.gathered));
         int64_t n = 0;
-        for (int i = 0; i < ranks; ++i) n += static_cast<int64_t>(all[i]);
+#pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i)
+            if (i < ranks) n += static_cast<int64_t>(all[i]);
         return n;
     }
     // CTA 0: the other CTAs' entries (gathered, kList in all at most) behind its own.
     __device__ __forceinline__ void pull(const uint64_t *counts) {
+        // a warp takes every kWarps-th CTA's list
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         int at = static_cast<int>(counts[0]);
         for (int r = 1; r < ranks; ++r) {
             const int n = static_cast<int>(counts[r]);
-            const uint64_t *src = cl.map_shared_rank(sm.list, r);
-            for (int i = threadIdx.x; i < n; i += kThreads) sm.list[at + i] = src[i];
+            if (r % kWarps == warp) {
+                const uint64_t *src = cl.map_shared_rank(sm.list, r);
+                for (int i = lane; i < n; i += 32) sm.list[at + i] = src[i];
+            }
             at += n;
         }
         __syncthreads();
@@ -428,8 +443,8 @@ struct RowView {
             uint64_t key = 0;
             if (rank == 0) {
                 pull(last_exchange());
-                sort_list(sm, static_cast<int>(n));
                 constexpr int P = kList / kThreads;
+                sort_list<P>(sm, static_cast<int>(n));
                 uint64_t w[P], mine = 0;
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
@@ -452,46 +467,34 @@ struct RowView {
         // digit by digit, then the id among equal logits
         uint32_t prefix = 0, mask = 0;
         uint64_t in = 0;
-        const int shifts[3] = {21, 10, 0};
-        for (int level = 0; level < 3; ++level) {
-            const int sh = shifts[level];
-            const uint32_t digit = level < 2 ? 0x7FFu : 0x3FFu;
-            for (int i = threadIdx.x; i < kDigits; i += kThreads) sm.list[i] = 0;
+        for (int sh = 24; sh >= 0; sh -= 8) {
+            sm.list[threadIdx.x] = 0;
             __syncthreads();
             each([&](const float (&v)[VE], int id) {
+                const uint32_t taken = take(v, id);
+                if (taken == 0) return;
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    if (!take(v[e], id + e)) continue;
                     const uint32_t k = order_key32(v[e]);
-                    if ((k & mask) == prefix)
-                        atomicAdd(reinterpret_cast<unsigned long long *>(&sm.list[(k >> sh) & digit]), value(v[e]));
+                    if (((taken >> e) & 1u) && (k & mask) == prefix)
+                        atomicAdd(reinterpret_cast<unsigned long long *>(&sm.list[(k >> sh) & 0xFFu]), value(v[e]));
                 }
             });
             cl.sync();
-            // bins from the top: thread t holds kDigits - 1 - t P - (0 .. P - 1)
-            constexpr int P = kDigits / kThreads;
-            uint64_t h[P], mine = 0;
+            // bins from the top, one to a thread
+            uint64_t h = 0;
 #pragma unroll
-            for (int b = 0; b < P; ++b) {
-                h[b] = 0;
-#pragma unroll
-                for (int r = 0; r < kMaxCluster; ++r)
-                    if (r < ranks) h[b] += cl.map_shared_rank(sm.list, r)[kDigits - 1 - (threadIdx.x * P + b)];
-                mine += h[b];
-            }
-            uint64_t all, above = cta_scan(sm, mine, all);
-#pragma unroll
-            for (int b = 0; b < P; ++b) {
-                if (above < need && above + h[b] >= need) {
-                    sm.bin = kDigits - 1 - static_cast<int>(threadIdx.x * P + b);
-                    sm.above = above;
-                    sm.in = h[b];
-                }
-                above += h[b];
+            for (int r = 0; r < kMaxCluster; ++r)
+                if (r < ranks) h += cl.map_shared_rank(sm.list, r)[kDigits - 1 - threadIdx.x];
+            uint64_t all, above = cta_scan(sm, h, all);
+            if (above < need && above + h >= need) {
+                sm.bin = kDigits - 1 - static_cast<int>(threadIdx.x);
+                sm.above = above;
+                sm.in = h;
             }
             cl.sync();  // also: every CTA has read this one's histogram
             prefix |= static_cast<uint32_t>(sm.bin) << sh;
-            mask |= digit << sh;
+            mask |= 0xFFu << sh;
             need -= sm.above;
             in = sm.in;
             __syncthreads();
@@ -501,27 +504,37 @@ struct RowView {
         int last = 0x7FFFFFFF;
         if (m < in / one) {
             uint64_t total;
-            last = locate([&](float l, int id) { return uint64_t(l == edge && take(l, id)); },
-                          [&](uint64_t) { return m - 1; }, total);
+            last = locate(
+                [&](const float (&v)[VE], int id, uint64_t (&w)[VE]) {
+                    const uint32_t taken = take(v, id);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) w[e] = v[e] == edge ? (taken >> e) & 1u : 0u;
+                    return taken != 0;
+                },
+                [&](uint64_t) { return m - 1; }, total);
         }
         return topk_key(edge, last);
     }
 
-    // The first id at which the running sum of value passes target(total).
+    // The first id at which the running sum of weights passes target(total).
+    // value(values, id, weights): false where all of a word's weights are 0.
     template <typename F, typename G>
     __device__ __forceinline__ int locate(const F &value, const G &target, uint64_t &total) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         uint64_t s = 0;
         each([&](const float (&v)[VE], int id) {
+            uint64_t x[VE];
+            if (!value(v, id, x)) return;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) s += value(v[e], id + e);
+            for (int e = 0; e < VE; ++e) s += x[e];
         });
         const uint64_t *all = exchange(cta_sum(sm, s));
         uint64_t before = 0;
         total = 0;
-        for (int i = 0; i < ranks; ++i) {
+#pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i) {
             if (i < rank) before += all[i];
-            total += all[i];
+            if (i < ranks) total += all[i];
         }
         const uint64_t t = target(total);
         // the warp whose piece holds the answer; the whole CTA walks that piece
@@ -543,9 +556,10 @@ struct RowView {
                 widen(i < words ? (RESIDENT ? src[i] : fetch(w0 + i)) : outside(), v);
                 const int id = (w0 + i) * VE - skip;
                 uint64_t x[VE], mine_i = 0;
+                const bool some = value(v, id, x);
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    x[e] = value(v[e], id + e);
+                    if (!some) x[e] = 0;
                     mine_i += x[e];
                 }
                 uint64_t all_i, run = before + cta_scan(sm, mine_i, all_i);
@@ -567,9 +581,16 @@ struct RowView {
     }
 };
 
-// A fraction of 0 <= f < 1 in units of 2^-64 (exact above 2^-40).
-__device__ __forceinline__ uint64_t fraction64(float f) {
-    return static_cast<uint64_t>(static_cast<double>(f) * 0x1p64);
+// A fraction 0 <= f < 1 in units of 2^-64 (exact above 2^-40).
+__device__ __forceinline__ uint64_t fraction64(float f) { return __float2ull_rz(f * 0x1p64f); }
+// a / b to about 2^-24 of itself, 0 < a <= b, in two floats a number.
+__device__ __forceinline__ float quotient(uint64_t a, uint64_t b) {
+    const float ah = __ull2float_rn(a), bh = __ull2float_rn(b);
+    const float al = __ll2float_rn(static_cast<int64_t>(a - __float2ull_rn(ah)));
+    const float bl = __ll2float_rn(static_cast<int64_t>(b - __float2ull_rn(bh)));
+    const float q = __fdiv_rn(ah, bh);
+    const float rest = __fmaf_rn(-q, bh, ah) + __fmaf_rn(-q, bl, al);
+    return q + __fdiv_rn(rest, bh);
 }
 // The least integer that is at least P 2^-64 of all (1 at least).
 __device__ __forceinline__ uint64_t share_of(uint64_t P, uint64_t all) {
@@ -577,12 +598,12 @@ __device__ __forceinline__ uint64_t share_of(uint64_t P, uint64_t all) {
     return need ? need : 1;
 }
 
-// A row that the filters have narrowed to the n <= 512 E entries of the list, in
+// A row that the filters have narrowed to the n <= kThreads E entries of the list, in
 // any order, in one CTA: top-k of them, top-p, min-p and the draw.
 template <int E>
 __device__ void finish_list(Shared &sm, const Weight &weight, int n, int k, float top_p, int32_t *id, float *prob) {
     const int tid = threadIdx.x;
-    sort_list(sm, n);
+    sort_list<E>(sm, n);
     const int most = k < n ? k : n;
     uint64_t key[E], w[E], mine = 0, all;
 #pragma unroll
@@ -602,7 +623,7 @@ __device__ void finish_list(Shared &sm, const Weight &weight, int n, int k, floa
         sm.list[tid * E + i] = stays ? (key[i] << 32) | (key[i] >> 32) : 0ull;
     }
     __syncthreads();
-    sort_list(sm, most);
+    sort_list<E>(sm, most);
     mine = 0;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -616,7 +637,7 @@ __device__ void finish_list(Shared &sm, const Weight &weight, int n, int k, floa
     for (int i = 0; i < E; ++i) {
         if (above <= t && t < above + w[i]) {
             *id = key_id(key[i] >> 32);
-            if (prob) *prob = static_cast<float>(static_cast<double>(w[i]) / static_cast<double>(all));
+            if (prob) *prob = quotient(w[i], all);
         }
         above += w[i];
     }
@@ -665,14 +686,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         if (k <= 0 || k >= p.vocab) k = p.vocab;
 
         if (tid == 0) {
-            const double c = 1.4426950408889634 / static_cast<double>(T);
-            const float c_hi = static_cast<float>(c);
+            constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.925963033500e-8f;
+            const float c_hi = __fdiv_rn(kLog2eHi, T);
             RowScale &x = sm.scale;
             x.c_hi = c_hi;
-            x.c_lo = static_cast<float>(c - static_cast<double>(c_hi));
+            x.c_lo = __fdiv_rn(__fmaf_rn(-c_hi, T, kLog2eHi) + kLog2eLo, T);
             x.far = static_cast<float>(S + 1) / c_hi;
             x.span = min_p > 0.0f ? (0.001f - log2f(min_p)) / c_hi : INFINITY;
-            x.floor_w = static_cast<uint64_t>(ceil(ldexp(static_cast<double>(min_p), S)));
+            x.floor_w = __float2ull_ru(ldexpf(min_p, S));
             x.U = fraction64(u);
             x.P = fraction64(top_p);
         }
@@ -700,16 +721,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                                62 - S, sm.pow16};
         const float per_bin = weight.c_hi * kBinsPerOctave;
         // bins from the top of the row down; a larger logit never lies in a later bin
-        auto bin_of = [&](float l) { return static_cast<int>(fminf((weight.max - l) * per_bin, kBins - 1.0f)); };
+        auto place = [&](float l) { return fminf((weight.max - l) * per_bin, kBins - 1.0f); };
+        auto bin_at = [](float x) {  // truncated by the addition
+            return static_cast<int>(__float_as_uint(__fadd_rz(x, 8388608.0f)) - 0x4B000000u);
+        };
         auto counts = [&](int from, int b) { return uint64_t(cl.map_shared_rank(sm.count, from)[b]); };
+        // The weights of a word's logits that stay and are at least `least`; false where all are 0
+        // (those below every possible limit are not worked out).
+        auto weigh = [&](const float (&x)[VE], int id, const Edge &in, uint64_t least, uint64_t (&w)[VE]) {
+            float most = x[0];
+#pragma unroll
+            for (int e = 1; e < VE; ++e) most = fmaxf(most, x[e]);
+            if (most < in.value || weight.max - most > (least ? sm.scale.span : weight.far)) return false;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const uint64_t y = weight(x[e]);
+                w[e] = in.stays(x[e], id + e) && y >= least ? y : 0ull;
+            }
+            return true;
+        };
+
         Edge edge = {-INFINITY, 0x7FFFFFFF};
         if (k < p.vocab) {
             // at least k entries lie in the bins up to the one in which the k-th of the lanes' maxima does
             const float lane_max = key_value(static_cast<uint64_t>(lane_top) << 32);
-            if (lane_top > kKeyNegInf) atomicAdd(&sm.count[bin_of(lane_max)], 1u);
+            if (lane_top > kKeyNegInf) atomicAdd(&sm.count[bin_at(place(lane_max))], 1u);
             const int bound = v.crossing(counts, static_cast<uint64_t>(k));
             if (bound < kBins - 1) {
-                const int64_t n = v.gather([&](float l, int) { return bin_of(l) <= bound; });
+                const float past = static_cast<float>(bound + 1);
+                const int64_t n = v.gather([&](const float (&x)[VE], int) {
+                    uint32_t mask = 0;
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) mask |= place(x[e]) < past ? 1u << e : 0u;
+                    return mask;
+                });
                 if (n <= kList) {
                     if (rank == 0) {
                         v.pull(v.last_exchange());
@@ -728,13 +773,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             v.each([&](const float (&x)[VE], int id) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
-                    if (x[e] > -INFINITY) atomicAdd(&sm.count[bin_of(x[e])], 1u);
+                    if (x[e] > -INFINITY) atomicAdd(&sm.count[bin_at(place(x[e]))], 1u);
             });
             const int b = v.crossing(counts, static_cast<uint64_t>(k));
             const uint64_t need = static_cast<uint64_t>(k) - sm.above;
             if (b < kBins)  // else fewer than k are not masked: all of them stay
-                edge.set(v.cut([&](float l, int) { return l > -INFINITY && bin_of(l) == b; },
-                               [](float) { return uint64_t(1); }, need));
+                edge.set(v.cut(
+                    [&](const float (&x)[VE], int) {
+                        uint32_t mask = 0;
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) mask |= x[e] > -INFINITY && bin_at(place(x[e])) == b ? 1u << e : 0u;
+                        return mask;
+                    },
+                    [](float) { return uint64_t(1); }, need));
             cl.sync();
             for (int i = tid; i < kBins; i += kThreads) sm.count[i] = 0;
             __syncthreads();
@@ -744,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             v.each([&](const float (&x)[VE], int id) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
-                    if (x[e] > -INFINITY && edge.stays(x[e], id + e)) atomicAdd(&sm.count[bin_of(x[e])], 1u);
+                    if (x[e] > -INFINITY && edge.stays(x[e], id + e)) atomicAdd(&sm.count[bin_at(place(x[e]))], 1u);
             });
             for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0;
             if (tid == 0) {
@@ -753,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             }
             cl.sync();
             // The bins that may be the one in which the sum of weights reaches p of all.  A bin's
-            // weights lie between 2^(S - (b + 1) / 32) and 2^(S - b / 32), the last one's anywhere
+            // weights lie between 2^(S - (b + 1) / 16) and 2^(S - b / 16), the last one's anywhere
             // below that: bounds for the sums up to each bin and for all.
             constexpr int B = kBins / kThreads;
             uint64_t high[B], low[B], h0 = 0, l0 = 0, h_all, l_all;
@@ -766,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     if (from < ranks) c += static_cast<uint32_t>(counts(from, bin));
                 const float x = static_cast<float>(c) * exp2f(static_cast<float>(S) - bin / kBinsPerOctave);
                 high[b] = static_cast<uint64_t>(x * 1.0001f) + c;
-                low[b] = bin < kBins - 1 ? static_cast<uint64_t>(x * 0.9784f) : 0ull;  // 2^(-1/32) = 0.97857..
+                low[b] = bin < kBins - 1 ? static_cast<uint64_t>(x * 0.9575f) : 0ull;  // 2^(-1/16) = 0.95760..
                 h0 += high[b];
                 l0 += low[b];
             }
@@ -785,15 +836,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const int ba = sm.bin, bb = sm.found;
             // all weights, those above the bracket, and its bins one by one, exactly
             uint64_t sum = 0, over = 0;
+            const float from = static_cast<float>(ba), past = bb < kBins - 1 ? static_cast<float>(bb + 1) : INFINITY;
             v.each([&](const float (&x)[VE], int id) {
+                uint64_t w[VE];
+                if (!weigh(x, id, edge, 0, w)) return;
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    if (!edge.stays(x[e], id + e)) continue;
-                    const int b = bin_of(x[e]);
-                    const uint64_t w = weight(x[e]);
-                    sum += w;
-                    if (b < ba) over += w;
-                    else if (b <= bb && w) atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[b]), w);
+                    const float at = place(x[e]);
+                    sum += w[e];
+                    over += at < from ? w[e] : 0ull;
+                    if (at >= from && at < past && w[e])
+                        atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[bin_at(at)]), w[e]);
                 }
             });
             const uint64_t need = share_of(sm.scale.P, v.row_sum(sum));
@@ -801,22 +854,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const int b = v.crossing([&](int from, int i) { return cl.map_shared_rank(sm.mass, from)[i]; }, need - over);
             const uint64_t rest = need - over - sm.above;
             const Edge kept = edge;
-            edge.set(v.cut([&](float l, int id) { return bin_of(l) == b && kept.stays(l, id) && weight(l) > 0; }, weight,
-                           rest));
+            edge.set(v.cut(
+                [&](const float (&x)[VE], int id) {
+                    uint32_t mask = 0;
+#pragma unroll
+                    for (int e = 0; e < VE; ++e)
+                        mask |= x[e] > -INFINITY && kept.stays(x[e], id + e) && bin_at(place(x[e])) == b ? 1u << e : 0u;
+                    return mask;
+                },
+                weight, rest));
         }
         uint64_t total;
         const int id = v.locate(
-            [&](float l, int i) {
-                if (!edge.stays(l, i) || weight.max - l > sm.scale.span) return uint64_t(0);
-                const uint64_t w = weight(l);
-                return w >= sm.scale.floor_w ? w : uint64_t(0);
-            },
+            [&](const float (&x)[VE], int i, uint64_t (&w)[VE]) { return weigh(x, i, edge, sm.scale.floor_w, w); },
             [&](uint64_t t) { return __umul64hi(sm.scale.U, t); }, total);
         if (rank == 0 && tid == 0) {
             p.ids[r] = id;
             if (p.probs) {
                 const float l = Elem<DT>::widen(ld_dep(static_cast<const typename View::T *>(p.logits) + r * p.stride + id));
-                p.probs[r] = static_cast<float>(static_cast<double>(weight(l)) / static_cast<double>(total));
+                p.probs[r] = quotient(weight(l), total);
             }
         }
         __syncthreads();
@@ -837,6 +893,8 @@ cudaError_t launch_kernel(const SampleParams &p, int S, int steps, int ranks, cu
         std::lock_guard<std::mutex> lock(mu);
         if (!done[dev.device]) {
             e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+            if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e != cudaSuccess) return e;
             done[dev.device] = true;
         }
