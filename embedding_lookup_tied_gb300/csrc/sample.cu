@@ -40,7 +40,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kList = 1024;                   // entries one CTA sorts
+constexpr int kList = 2 * kThreads;           // entries one CTA ranks
 constexpr int kDigits = 256;                  // bins of a digit of the order key
 constexpr int kBins = 512;                    // of 1/16 octave of weight; the last takes all that is below
 constexpr float kBinsPerOctave = 16.0f;
@@ -48,55 +48,65 @@ constexpr int kMaxSmem = 224 * 1024;
 constexpr uint32_t kKeyInf = 0xFF800000u;     // order key of +inf; NaN lies above
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // order key of -inf
 
-// round(2^62 * 2^(-j/16))
+// round(2^61 * 2^(j/16))
 __constant__ const uint64_t kPow16[16] = {
-    0x4000000000000000ull, 0x3D495F454921B30Bull, 0x3AB031B9F7490E4Cull, 0x383337BB0AA53844ull,
-    0x35D13F32B5A75ABDull, 0x3389230547E12039ull, 0x3159CA845541B6B7ull, 0x2F4228E7D6030DB0ull,
-    0x2D413CCCFE779921ull, 0x2B560FBA90A852B2ull, 0x297FB5AA6C544E3Bull, 0x27BD4C982468446Bull,
-    0x260DFC14636E2A5Cull, 0x2470F4DCEAC470CEull, 0x22E57078FAA2F5BAull, 0x216AB0D9F3121EC5ull};
+    0x2000000000000000ull, 0x216AB0D9F3121EC5ull, 0x22E57078FAA2F5BAull, 0x2470F4DCEAC470CEull,
+    0x260DFC14636E2A5Cull, 0x27BD4C982468446Bull, 0x297FB5AA6C544E3Bull, 0x2B560FBA90A852B2ull,
+    0x2D413CCCFE779921ull, 0x2F4228E7D6030DB0ull, 0x3159CA845541B6B7ull, 0x3389230547E12039ull,
+    0x35D13F32B5A75ABDull, 0x383337BB0AA53844ull, 0x3AB031B9F7490E4Cull, 0x3D495F454921B30Bull};
 
-// The weight 2^S * 2^(-(max - l) * c), c = log2(e) / T, as an integer.
+// A logit's weight exp(l / T) over its row's scale, as an integer: 2^(S - G) *
+// 2^(l c), c = log2(e) / T, G the integer next above c times the largest logit.
 //
-// d = max - l is held as the rounded difference and its error, t = d * c as
-// two floats, so an argument is good to about 2^-46 of itself.  With n the
-// nearest integer to 16 t and x = t - n/16 (|x| <= 1/32),
-//   2^-t = 2^-(n div 16) * 2^(-(n mod 16)/16) * 2^-x,
-// the middle factor from a table in 62 bits and 2^-x = 1 - x ln2 + x^2 q(x)
+// c is two floats, l c = p + z with p = RN(l c_hi) and z the rest.  With K the
+// nearest integer to 16 p, x = l c - K/16 is small (|x| <= 1/32 and a little),
+// p - K/16 is exact, and
+//   2^(l c) = 2^(K div 16) * 2^((K mod 16)/16) * 2^x,
+// the middle factor from a table in 62 bits and 2^x = 1 + x ln2 + x^2 q(x)
 // from its Taylor series: x ln2 in two floats, the rest (below 2^-12) in one.
 // The factor's distance from 1 is below 2^-5.5 and is held as a 32-bit
 // integer in units of 2^-36.  Together about 2^-36 of the weight, unbiased.
+// Where c times the largest logit passes 2^10 the rounding of l c_lo would
+// show; there logits are first taken relative to the largest, and those that
+// weigh anything are so near to it that the difference is exact.
+// (No branch, so that the weights of a word's logits are worked out side by
+// side; 16 and 8 warps an SM: 70 and 105 issue slots a weight.)
 struct Weight {
-    float max, c_hi, c_lo, far;
-    int shift;  // 62 - S
+    float ref, low;    // what logits are relative to; below `low` they weigh 0
+    float c_hi, c_lo;
+    int shift;         // 61 - S + G
     const uint64_t *pow16;  // kPow16 in shared memory: 16 pairs of words, one to a bank
 
-    // (No branch, so that the weights of a word's logits are worked out side by side.)
-    __device__ __forceinline__ uint64_t operator()(float l) const {
-        const float d = __fsub_rn(max, l);
-        const bool none = !(d <= far);  // also -inf
-        l = none ? max : l;
-        const float s = none ? 0.0f : d;
-        const float bv = __fsub_rn(s, max), av = __fsub_rn(s, bv);
-        const float e = __fsub_rn(__fsub_rn(max, av), __fadd_rn(l, bv));
-        const float th = __fmul_rn(s, c_hi);
-        const float tl = __fmaf_rn(s, c_hi, -th) + __fmaf_rn(s, c_lo, e * c_hi);
+    __device__ __forceinline__ void init(float max, float c_hi_, float c_lo_, int S, const uint64_t *table) {
+        c_hi = c_hi_;
+        c_lo = c_lo_;
+        ref = fabsf(max * c_hi) < 1024.0f ? 0.0f : max;
+        low = max - static_cast<float>(S) / c_hi;
+        const float top = (max - ref) * c_hi;
+        shift = 61 - S + (__float2int_rn(top * 16.0f) >> 4) + 1;
+        pow16 = table;
+    }
+    __device__ __forceinline__ uint64_t operator()(float logit) const {
+        const float l = __fsub_rn(logit, ref);
+        const float p = __fmul_rn(l, c_hi);
+        const float z = __fmaf_rn(l, c_lo, __fmaf_rn(l, c_hi, -p));
         const float magic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
-        const float y = __fmaf_rn(th, 16.0f, magic);
-        const int n = static_cast<int>(__float_as_uint(y) - 0x4B400000u);
-        const float r = __fmaf_rn(__fsub_rn(y, magic), -0.0625f, th);  // exact
-        const float x = __fadd_rn(r, tl), xl = __fadd_rn(__fsub_rn(r, x), tl);
-        constexpr float kLn2Hi = 0.6931471824645996f, kLn2Lo = -1.9046542e-9f;
-        const float p = __fmul_rn(x, kLn2Hi);
-        const float pl = __fmaf_rn(x, kLn2Hi, -p) + __fmaf_rn(x, kLn2Lo, xl * kLn2Hi);
-        float q = __fmaf_rn(x, -0.0013333558f, 0.009618129f);
-        q = __fmaf_rn(x, q, -0.05550411f);
-        q = __fmaf_rn(x, q, 0.24022651f);
-        const float z = __fmaf_rn(x * x, q, -pl);
-        const int delta = __float2int_rn(z * 0x1p36f) - __float2int_rn(p * 0x1p36f);  // 2^-x - 1
-        const uint64_t f = pow16[n & 15];
-        const uint64_t w = f + static_cast<uint64_t>(
-            (static_cast<int64_t>(static_cast<int>(f >> 32)) * delta) >> 4);
-        return none ? 0ull : w >> min(shift + (n >> 4), 63);
+        const float y = __fmaf_rn(p, 16.0f, magic);
+        const int K = static_cast<int>(__float_as_uint(y) - 0x4B400000u);
+        const float r = __fmaf_rn(__fsub_rn(y, magic), -0.0625f, p);  // exact
+        const float x = __fadd_rn(r, z), xl = __fadd_rn(__fsub_rn(r, x), z);
+        constexpr float kLn2Hi = 0.6931471824645996f * 0x1p36f, kLn2Lo = -1.9046542e-9f * 0x1p36f;
+        const float a = __fmul_rn(x, kLn2Hi);
+        const float al = __fmaf_rn(x, kLn2Hi, -a) + __fmaf_rn(x, kLn2Lo, xl * kLn2Hi);
+        float q = __fmaf_rn(x, 0.0013333558f * 0x1p36f, 0.009618129f * 0x1p36f);
+        q = __fmaf_rn(x, q, 0.05550411f * 0x1p36f);
+        q = __fmaf_rn(x, q, 0.24022651f * 0x1p36f);
+        const int delta = __float2int_rn(a) + __float2int_rn(__fmaf_rn(x * x, q, al));  // (2^x - 1) 2^36
+        const uint64_t f = pow16[K & 15];
+        const uint64_t w =
+            f + static_cast<uint64_t>((static_cast<int64_t>(static_cast<int>(f >> 32)) * delta) >> 4);
+        // (below `low`, also at -inf, the rest may be anything, but w stays below 2^63)
+        return w >> (logit < low ? 63 : min(shift - (K >> 4), 63));
     }
 };
 
@@ -104,10 +114,8 @@ struct Weight {
 // the row is on its way.  No 64-bit floating point: its unit here is slow.
 struct RowScale {
     float c_hi, c_lo;   // log2(e) / T
-    float far;          // differences from the largest logit beyond it weigh 0
-    float span;         // differences beyond it are below min-p for certain
-    uint64_t floor_w;   // min-p as a weight
-    uint64_t U, P;      // u and top-p in units of 2^-64
+    float span;         // differences from the largest logit beyond it are below min-p for certain
+    uint64_t U, P, M;   // u, top-p and min-p in units of 2^-64
 };
 
 struct alignas(16) Shared {
@@ -169,54 +177,29 @@ __device__ __forceinline__ uint64_t cta_scan(Shared &sm, uint64_t v, uint64_t &a
     return before;
 }
 
-// Descending sort of the first size_all (a power of two, kThreads E at most)
-// entries of buf: thread t holds entries t E .. t E + E - 1 in registers;
-// partners within a warp meet by shuffles, others through buf.
+// The n entries of the list, weighed into mass: for each of this thread's
+// entries (threadIdx.x and kThreads further on) the number and the weights of
+// those with larger keys.  Every pair is compared: no rounds of a sort to wait
+// for, and short lists are the rule.
 template <int E>
-__device__ __forceinline__ void sort_entries(uint64_t *buf, int size_all) {
-    const int tid = threadIdx.x;
-    const bool active = (tid & ~31) * E < size_all;  // a warp's
-    uint64_t v[E];
+__device__ __forceinline__ void rank_list(const Shared &sm, int n, const uint64_t (&key)[E], int (&rank)[E],
+                                          uint64_t (&above)[E]) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = buf[tid * E + e];
-    for (int size = 2; size <= size_all; size <<= 1) {
-        for (int d = size >> 1; d > 0; d >>= 1) {
-            if (d >= 32 * E) {
-                __syncthreads();
-#pragma unroll
-                for (int e = 0; e < E; ++e) buf[tid * E + e] = v[e];
-                __syncthreads();
-            }
-            if (!active) continue;
-            uint64_t other[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (d >= 32 * E) other[e] = buf[(tid * E + e) ^ d];
-                else if (d >= E) other[e] = __shfl_xor_sync(0xFFFFFFFFu, v[e], d / E);
-                else other[e] = d == 1 ? v[e ^ (1 % E)] : v[e ^ (2 % E)];
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int i = tid * E + e;
-                const bool larger = ((i & d) == 0) == ((i & size) == 0);
-                v[e] = (v[e] > other[e]) == larger ? v[e] : other[e];
-            }
-        }
+    for (int e = 0; e < E; ++e) {
+        rank[e] = 0;
+        above[e] = 0;
     }
-    __syncthreads();
+    if ((threadIdx.x & ~31u) >= static_cast<unsigned>(n)) return;  // none of the warp's
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+        const uint64_t k = sm.list[j], w = sm.mass[j];
 #pragma unroll
-    for (int e = 0; e < E; ++e) buf[tid * E + e] = v[e];
-    __syncthreads();
-}
-// The first n entries of the list, sorted descending, zeros after them up to
-// kThreads E.  CTA-collective.
-template <int E>
-__device__ __forceinline__ void sort_list(Shared &sm, int n) {
-    for (int i = n + threadIdx.x; i < kThreads * E; i += kThreads) sm.list[i] = 0ull;
-    __syncthreads();
-    int size = 32 * E;
-    while (size < n) size <<= 1;
-    sort_entries<E>(sm.list, size);
+        for (int e = 0; e < E; ++e)
+            if (k > key[e]) {
+                ++rank[e];
+                above[e] += w;
+            }
+    }
 }
 
 // What stays: entries with a key of at least `edge`.
@@ -228,6 +211,43 @@ struct Edge {
         value = key_value(key);
         last = key_id(key);
     }
+};
+
+// Bins from the top of a row down; a larger logit never lies in a later bin.
+struct Bins {
+    float largest, per_bin;
+    __device__ __forceinline__ float place(float l) const { return fminf((largest - l) * per_bin, kBins - 1.0f); }
+    static __device__ __forceinline__ int at(float place) {  // truncated by the addition
+        return static_cast<int>(__float_as_uint(__fadd_rz(place, 8388608.0f)) - 0x4B000000u);
+    }
+};
+
+// The weights of a word's logits that stay (EDGED) and are at least min-p's
+// (FLOORED); false where all are 0 for certain.
+template <bool EDGED, bool FLOORED, int VE>
+struct Weigh {
+    const Weight &weight;
+    const Edge &edge;
+    float largest, span;
+    uint64_t floor_w;
+    __device__ __forceinline__ bool operator()(const float (&x)[VE], int id, uint64_t (&w)[VE]) const {
+        if (EDGED || FLOORED) {
+            float most = x[0];
+#pragma unroll
+            for (int e = 1; e < VE; ++e) most = fmaxf(most, x[e]);
+            if ((EDGED && most < edge.value) || (FLOORED && largest - most > span)) return false;
+        }
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            w[e] = weight(x[e]);
+            if (EDGED && !edge.stays(x[e], id + e)) w[e] = 0;
+            if (FLOORED && w[e] < floor_w) w[e] = 0;
+        }
+        return true;
+    }
+};
+struct One {
+    __device__ __forceinline__ uint64_t operator()(float) const { return 1; }
 };
 
 // One row, as one CTA of its cluster sees it.  The row's 16-byte words (as
@@ -361,12 +381,12 @@ struct RowView {
 
     // The bin in which the cluster's sums over bins 0, 1, .. reach need (>= 1):
     // its number, and in sm.above / sm.in the sums before and of it.  A bin's
-    // sum in one CTA is value(CTA, bin).  kBins where they do not.
-    template <typename F>
+    // sum in one CTA is value(CTA, bin).  BINS where they do not.
+    template <int BINS, typename F>
     __device__ __forceinline__ int crossing(const F &value, uint64_t need) {
-        if (threadIdx.x == 0) sm.bin = kBins;
+        if (threadIdx.x == 0) sm.bin = BINS;
         cl.sync();
-        constexpr int B = kBins / kThreads;
+        constexpr int B = BINS / kThreads;
         uint64_t h[B], mine = 0;
 #pragma unroll
         for (int b = 0; b < B; ++b) {
@@ -388,6 +408,15 @@ struct RowView {
         }
         __syncthreads();
         return sm.bin;
+    }
+
+    template <int BINS>
+    __device__ __forceinline__ int count_crossing(uint64_t need) {
+        return crossing<BINS>([&](int from, int b) { return uint64_t(cl.map_shared_rank(sm.count, from)[b]); }, need);
+    }
+    template <int BINS>
+    __device__ __forceinline__ int mass_crossing(uint64_t need) {
+        return crossing<BINS>([&](int from, int b) { return cl.map_shared_rank(sm.mass, from)[b]; }, need);
     }
 
     // Entries that `take` takes, as keys: into this CTA's list, its number (of
@@ -443,20 +472,21 @@ struct RowView {
             uint64_t key = 0;
             if (rank == 0) {
                 pull(last_exchange());
-                constexpr int P = kList / kThreads;
-                sort_list<P>(sm, static_cast<int>(n));
-                uint64_t w[P], mine = 0;
+                const int m = static_cast<int>(n);
+                uint64_t mine[2], above[2];
+                int before[2];
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const uint64_t k = sm.list[threadIdx.x * P + i];
-                    w[i] = k ? value(key_value(k)) : 0ull;
-                    mine += w[i];
+                for (int e = 0; e < 2; ++e) {
+                    const int i = threadIdx.x + e * kThreads;
+                    mine[e] = i < m ? sm.list[i] : ~0ull;
+                    if (i < m) sm.mass[i] = value(key_value(mine[e]));
                 }
-                uint64_t all, above = cta_scan(sm, mine, all);
+                __syncthreads();
+                rank_list<2>(sm, m, mine, before, above);
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    if (above < need && above + w[i] >= need) sm.above = sm.list[threadIdx.x * P + i];
-                    above += w[i];
+                for (int e = 0; e < 2; ++e) {
+                    const int i = threadIdx.x + e * kThreads;
+                    if (i < m && above[e] < need && above[e] + sm.mass[i] >= need) sm.above = mine[e];
                 }
                 __syncthreads();
                 key = sm.above;
@@ -514,6 +544,78 @@ struct RowView {
                 [&](uint64_t) { return m - 1; }, total);
         }
         return topk_key(edge, last);
+    }
+
+    // The key at which the sums of value over bin b's entries (that stay by
+    // `in`) reach need: the bin in 256 parts, then the entries of the part.
+    template <typename G>
+    __device__ __forceinline__ uint64_t narrow(const Bins &bins, int b, uint64_t need, const Edge &in, const G &value) {
+        const float first = static_cast<float>(b);
+        auto within = [&](const float (&x)[VE], int id) {
+            uint32_t mask = 0;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const float at = bins.place(x[e]) - first;
+                mask |= at >= 0.0f && at < 1.0f && x[e] > -INFINITY && in.stays(x[e], id + e) ? 1u << e : 0u;
+            }
+            return mask;
+        };
+        __syncthreads();
+        sm.mass[threadIdx.x] = 0;
+        __syncthreads();
+        each([&](const float (&x)[VE], int id) {
+            const uint32_t mask = within(x, id);
+            if (mask == 0) return;
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                if ((mask >> e) & 1u)
+                    atomicAdd(reinterpret_cast<unsigned long long *>(
+                                  &sm.mass[Bins::at((bins.place(x[e]) - first) * static_cast<float>(kThreads))]),
+                              value(x[e]));
+        });
+        const int part = mass_crossing<kThreads>(need);
+        const float from = static_cast<float>(part), past = from + 1.0f;
+        const uint64_t rest = need - sm.above;
+        return cut(
+            [&](const float (&x)[VE], int id) {
+                uint32_t mask = within(x, id);
+                if (mask == 0) return mask;
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const float at = (bins.place(x[e]) - first) * static_cast<float>(kThreads);
+                    if (!(at >= from && at < past)) mask &= ~(1u << e);
+                }
+                return mask;
+            },
+            value, rest);
+    }
+
+    // All weights that stay, those in bins before ba, and bins ba .. bb one by
+    // one into mass.
+    template <bool EDGED>
+    __device__ __forceinline__ void bracket(const Bins &bins, const Weigh<EDGED, false, VE> &weigh, int ba, int bb,
+                                            uint64_t &sum, uint64_t &over) {
+        const float from = static_cast<float>(ba), past = bb < kBins - 1 ? static_cast<float>(bb + 1) : INFINITY;
+        uint64_t a = 0, o = 0;
+        each([&](const float (&x)[VE], int id) {
+            uint64_t w[VE];
+            if (!weigh(x, id, w)) return;
+            uint32_t inside = 0;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const float at = bins.place(x[e]);
+                a += w[e];
+                o += at < from ? w[e] : 0ull;
+                inside |= at >= from && at < past && w[e] ? 1u << e : 0u;
+            }
+            if (inside == 0) return;
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                if ((inside >> e) & 1u)
+                    atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[Bins::at(bins.place(x[e]))]), w[e]);
+        });
+        sum = a;
+        over = o;
     }
 
     // The first id at which the running sum of weights passes target(total).
@@ -598,48 +700,62 @@ __device__ __forceinline__ uint64_t share_of(uint64_t P, uint64_t all) {
     return need ? need : 1;
 }
 
-// A row that the filters have narrowed to the n <= kThreads E entries of the list, in
+// A row that the filters have narrowed to the n <= kList entries of the list, in
 // any order, in one CTA: top-k of them, top-p, min-p and the draw.
-template <int E>
-__device__ void finish_list(Shared &sm, const Weight &weight, int n, int k, float top_p, int32_t *id, float *prob) {
-    const int tid = threadIdx.x;
-    sort_list<E>(sm, n);
-    const int most = k < n ? k : n;
-    uint64_t key[E], w[E], mine = 0, all;
+__device__ __forceinline__ void finish_list(Shared &sm, const Weight &weight, int n, int k, float top_p, uint64_t floor_w,
+                                            int32_t *id, float *prob) {
+    uint64_t key[2], w[2], above[2], mine = 0, all;
+    int before[2];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        key[i] = sm.list[tid * E + i];
-        w[i] = tid * E + i < most ? weight(key_value(key[i])) : 0ull;
-        mine += w[i];
-    }
-    uint64_t above = cta_scan(sm, mine, all);
-    const uint64_t need = top_p < 1.0f ? share_of(sm.scale.P, all) : ~0ull;
-    // those that stay, keyed by id (ascending: the inverted id descending) with the order key
-    // below, so that a second sort puts them into id order
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const bool stays = above < need && w[i] >= sm.scale.floor_w && w[i] > 0;
-        above += w[i];
-        sm.list[tid * E + i] = stays ? (key[i] << 32) | (key[i] >> 32) : 0ull;
+    for (int e = 0; e < 2; ++e) {
+        const int i = threadIdx.x + e * kThreads;
+        key[e] = i < n ? sm.list[i] : ~0ull;
+        w[e] = i < n ? weight(key_value(key[e])) : 0ull;
+        if (i < n) sm.mass[i] = w[e];
     }
     __syncthreads();
-    sort_list<E>(sm, most);
+    if (n <= kThreads) {
+        const uint64_t key1[1] = {key[0]};
+        int before1[1];
+        uint64_t above1[1];
+        rank_list<1>(sm, n, key1, before1, above1);
+        before[0] = before1[0];
+        above[0] = above1[0];
+        before[1] = 0;
+        above[1] = 0;
+    } else {
+        rank_list<2>(sm, n, key, before, above);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (before[e] >= k) w[e] = 0;
+        mine += w[e];
+    }
+    all = cta_sum(sm, mine);  // also: every pair has been compared
+    __syncthreads();
+    const uint64_t need = top_p < 1.0f ? share_of(sm.scale.P, all) : ~0ull;
+    // those that stay, keyed by id (ascending: the inverted id descending), the others by 0
     mine = 0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        key[i] = sm.list[tid * E + i];
-        w[i] = key[i] ? weight(key_value(key[i] << 32)) : 0ull;
-        mine += w[i];
-    }
-    above = cta_scan(sm, mine, all);
-    const uint64_t t = __umul64hi(sm.scale.U, all);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        if (above <= t && t < above + w[i]) {
-            *id = key_id(key[i] >> 32);
-            if (prob) *prob = quotient(w[i], all);
+    for (int e = 0; e < 2; ++e) {
+        const int i = threadIdx.x + e * kThreads;
+        if (above[e] >= need || w[e] < floor_w) w[e] = 0;
+        key[e] = w[e] ? (key[e] << 32) | 1u : 0ull;
+        if (i < n) {
+            sm.list[i] = key[e];
+            sm.mass[i] = w[e];
         }
-        above += w[i];
+        mine += w[e];
+    }
+    const uint64_t total = cta_sum(sm, mine);
+    const uint64_t t = __umul64hi(sm.scale.U, total);
+    rank_list<2>(sm, n, key, before, above);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (w[e] && above[e] <= t && t < above[e] + w[e]) {
+            *id = key_id(key[e] >> 32);
+            if (prob) *prob = quotient(w[e], total);
+        }
     }
 }
 
@@ -691,11 +807,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             RowScale &x = sm.scale;
             x.c_hi = c_hi;
             x.c_lo = __fdiv_rn(__fmaf_rn(-c_hi, T, kLog2eHi) + kLog2eLo, T);
-            x.far = static_cast<float>(S + 1) / c_hi;
             x.span = min_p > 0.0f ? (0.001f - log2f(min_p)) / c_hi : INFINITY;
-            x.floor_w = __float2ull_ru(ldexpf(min_p, S));
             x.U = fraction64(u);
             x.P = fraction64(top_p);
+            x.M = fraction64(min_p);
         }
         // the row's largest logit (as an order key: NaN lies above +inf)
         const uint32_t lane_top = v.read(parity, p.err);
@@ -717,50 +832,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             __syncthreads();
             continue;
         }
-        const Weight weight = {key_value(static_cast<uint64_t>(top) << 32), sm.scale.c_hi, sm.scale.c_lo, sm.scale.far,
-                               62 - S, sm.pow16};
-        const float per_bin = weight.c_hi * kBinsPerOctave;
-        // bins from the top of the row down; a larger logit never lies in a later bin
-        auto place = [&](float l) { return fminf((weight.max - l) * per_bin, kBins - 1.0f); };
-        auto bin_at = [](float x) {  // truncated by the addition
-            return static_cast<int>(__float_as_uint(__fadd_rz(x, 8388608.0f)) - 0x4B000000u);
-        };
-        auto counts = [&](int from, int b) { return uint64_t(cl.map_shared_rank(sm.count, from)[b]); };
-        // The weights of a word's logits that stay and are at least `least`; false where all are 0
-        // (those below every possible limit are not worked out).
-        auto weigh = [&](const float (&x)[VE], int id, const Edge &in, uint64_t least, uint64_t (&w)[VE]) {
-            float most = x[0];
-#pragma unroll
-            for (int e = 1; e < VE; ++e) most = fmaxf(most, x[e]);
-            if (most < in.value || weight.max - most > (least ? sm.scale.span : weight.far)) return false;
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const uint64_t y = weight(x[e]);
-                w[e] = in.stays(x[e], id + e) && y >= least ? y : 0ull;
-            }
-            return true;
-        };
+        const float largest = key_value(static_cast<uint64_t>(top) << 32);
+        Weight weight;
+        weight.init(largest, sm.scale.c_hi, sm.scale.c_lo, S, sm.pow16);
+        const uint64_t heaviest = weight(largest);
+        const uint64_t floor_w = min_p >= 1.0f ? heaviest : min_p > 0.0f ? share_of(sm.scale.M, heaviest) : 0ull;
+        const Bins bins = {largest, weight.c_hi * kBinsPerOctave};
 
         Edge edge = {-INFINITY, 0x7FFFFFFF};
+        bool edged = false;
         if (k < p.vocab) {
             // at least k entries lie in the bins up to the one in which the k-th of the lanes' maxima does
             const float lane_max = key_value(static_cast<uint64_t>(lane_top) << 32);
-            if (lane_top > kKeyNegInf) atomicAdd(&sm.count[bin_at(place(lane_max))], 1u);
-            const int bound = v.crossing(counts, static_cast<uint64_t>(k));
-            if (bound < kBins - 1) {
-                const float past = static_cast<float>(bound + 1);
+            constexpr int kHalf = kBins / 2;  // bins twice as wide
+            if (lane_top > kKeyNegInf) atomicAdd(&sm.count[Bins::at(bins.place(lane_max) * 0.5f)], 1u);
+            const int bound = v.template count_crossing<kHalf>(static_cast<uint64_t>(k));
+            if (bound < kHalf - 1) {
+                const float past = static_cast<float>(2 * (bound + 1));
                 const int64_t n = v.gather([&](const float (&x)[VE], int) {
                     uint32_t mask = 0;
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) mask |= place(x[e]) < past ? 1u << e : 0u;
+                    for (int e = 0; e < VE; ++e) mask |= bins.place(x[e]) < past ? 1u << e : 0u;
                     return mask;
                 });
                 if (n <= kList) {
                     if (rank == 0) {
                         v.pull(v.last_exchange());
-                        float *prob = p.probs ? p.probs + r : nullptr;
-                        if (n <= kThreads) finish_list<1>(sm, weight, static_cast<int>(n), k, top_p, p.ids + r, prob);
-                        else finish_list<kList / kThreads>(sm, weight, static_cast<int>(n), k, top_p, p.ids + r, prob);
+                        finish_list(sm, weight, static_cast<int>(n), k, top_p, floor_w, p.ids + r,
+                                    p.probs ? p.probs + r : nullptr);
                     }
                     cl.sync();  // the lists have been read
                     continue;
@@ -773,19 +872,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             v.each([&](const float (&x)[VE], int id) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
-                    if (x[e] > -INFINITY) atomicAdd(&sm.count[bin_at(place(x[e]))], 1u);
+                    if (x[e] > -INFINITY) atomicAdd(&sm.count[Bins::at(bins.place(x[e]))], 1u);
             });
-            const int b = v.crossing(counts, static_cast<uint64_t>(k));
-            const uint64_t need = static_cast<uint64_t>(k) - sm.above;
+            const int b = v.template count_crossing<kBins>(static_cast<uint64_t>(k));
             if (b < kBins)  // else fewer than k are not masked: all of them stay
-                edge.set(v.cut(
-                    [&](const float (&x)[VE], int) {
-                        uint32_t mask = 0;
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) mask |= x[e] > -INFINITY && bin_at(place(x[e])) == b ? 1u << e : 0u;
-                        return mask;
-                    },
-                    [](float) { return uint64_t(1); }, need));
+                edge.set(v.narrow(bins, b, static_cast<uint64_t>(k) - sm.above, Edge{-INFINITY, 0x7FFFFFFF}, One()));
+            edged = true;
             cl.sync();
             for (int i = tid; i < kBins; i += kThreads) sm.count[i] = 0;
             __syncthreads();
@@ -795,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             v.each([&](const float (&x)[VE], int id) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
-                    if (x[e] > -INFINITY && edge.stays(x[e], id + e)) atomicAdd(&sm.count[bin_at(place(x[e]))], 1u);
+                    if (x[e] > -INFINITY && edge.stays(x[e], id + e)) atomicAdd(&sm.count[Bins::at(bins.place(x[e]))], 1u);
             });
             for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0;
             if (tid == 0) {
@@ -814,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 uint32_t c = 0;
 #pragma unroll
                 for (int from = 0; from < kMaxCluster; ++from)
-                    if (from < ranks) c += static_cast<uint32_t>(counts(from, bin));
+                    if (from < ranks) c += cl.map_shared_rank(sm.count, from)[bin];
                 const float x = static_cast<float>(c) * exp2f(static_cast<float>(S) - bin / kBinsPerOctave);
                 high[b] = static_cast<uint64_t>(x * 1.0001f) + c;
                 low[b] = bin < kBins - 1 ? static_cast<uint64_t>(x * 0.9575f) : 0ull;  // 2^(-1/16) = 0.95760..
@@ -835,39 +927,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             __syncthreads();
             const int ba = sm.bin, bb = sm.found;
             // all weights, those above the bracket, and its bins one by one, exactly
-            uint64_t sum = 0, over = 0;
-            const float from = static_cast<float>(ba), past = bb < kBins - 1 ? static_cast<float>(bb + 1) : INFINITY;
-            v.each([&](const float (&x)[VE], int id) {
-                uint64_t w[VE];
-                if (!weigh(x, id, edge, 0, w)) return;
-#pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    const float at = place(x[e]);
-                    sum += w[e];
-                    over += at < from ? w[e] : 0ull;
-                    if (at >= from && at < past && w[e])
-                        atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[bin_at(at)]), w[e]);
-                }
-            });
+            uint64_t sum, over;
+            if (edged) v.bracket(bins, Weigh<true, false, VE>{weight, edge, largest, 0.0f, 0}, ba, bb, sum, over);
+            else v.bracket(bins, Weigh<false, false, VE>{weight, edge, largest, 0.0f, 0}, ba, bb, sum, over);
             const uint64_t need = share_of(sm.scale.P, v.row_sum(sum));
             over = v.row_sum(over);
-            const int b = v.crossing([&](int from, int i) { return cl.map_shared_rank(sm.mass, from)[i]; }, need - over);
+            const int b = v.template mass_crossing<kBins>(need - over);
             const uint64_t rest = need - over - sm.above;
+            cl.sync();  // the sums have been read
             const Edge kept = edge;
-            edge.set(v.cut(
-                [&](const float (&x)[VE], int id) {
-                    uint32_t mask = 0;
-#pragma unroll
-                    for (int e = 0; e < VE; ++e)
-                        mask |= x[e] > -INFINITY && kept.stays(x[e], id + e) && bin_at(place(x[e])) == b ? 1u << e : 0u;
-                    return mask;
-                },
-                weight, rest));
+            edge.set(v.narrow(bins, b, rest, kept, weight));
+            edged = true;
         }
         uint64_t total;
-        const int id = v.locate(
-            [&](const float (&x)[VE], int i, uint64_t (&w)[VE]) { return weigh(x, i, edge, sm.scale.floor_w, w); },
-            [&](uint64_t t) { return __umul64hi(sm.scale.U, t); }, total);
+        const float span = sm.scale.span;
+        const uint64_t U = sm.scale.U;
+        auto target = [&](uint64_t t) { return __umul64hi(U, t); };
+        int id;
+        if (edged) id = v.locate(Weigh<true, true, VE>{weight, edge, largest, span, floor_w}, target, total);
+        else if (floor_w) id = v.locate(Weigh<false, true, VE>{weight, edge, largest, span, floor_w}, target, total);
+        else id = v.locate(Weigh<false, false, VE>{weight, edge, largest, span, floor_w}, target, total);
         if (rank == 0 && tid == 0) {
             p.ids[r] = id;
             if (p.probs) {
