@@ -121,6 +121,7 @@ struct RowScale {
 struct alignas(16) Shared {
     uint64_t list[kList];           // entries; the digit histograms where no list fits
     uint64_t mass[kBins];
+    uint64_t sums[kBins];           // a histogram's sums over the cluster
     uint32_t count[kBins];
     uint64_t slot[2][kMaxCluster];  // one value from each CTA of the cluster, two exchanges
     uint64_t warp_sum[kWarps];
@@ -177,29 +178,43 @@ __device__ __forceinline__ uint64_t cta_scan(Shared &sm, uint64_t v, uint64_t &a
     return before;
 }
 
-// The n entries of the list, weighed into mass: for each of this thread's
-// entries (threadIdx.x and kThreads further on) the number and the weights of
-// those with larger keys.  Every pair is compared: no rounds of a sort to wait
-// for, and short lists are the rule.
-template <int E>
-__device__ __forceinline__ void rank_list(const Shared &sm, int n, const uint64_t (&key)[E], int (&rank)[E],
-                                          uint64_t (&above)[E]) {
+// The n entries of the list in descending order.  An entry's place is the number
+// of larger ones: every pair is compared, two keys to a load (no rounds of a
+// sort to wait for, and short lists are the rule).  CTA-collective.
+__device__ __forceinline__ void sort_list(Shared &sm, int n) {
+    const int tid = threadIdx.x;
+    constexpr int E = kList / kThreads;
+    if (tid == 0 && n < kList) sm.list[n] = 0;  // the last pair's other half
+    __syncthreads();
+    uint64_t key[E];
+    int place[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        rank[e] = 0;
-        above[e] = 0;
+        key[e] = tid + e * kThreads < n ? sm.list[tid + e * kThreads] : ~0ull;
+        place[e] = 0;
     }
-    if ((threadIdx.x & ~31u) >= static_cast<unsigned>(n)) return;  // none of the warp's
+    if ((tid & ~31) < n) {  // else none of the warp's
+        const ulonglong2 *pairs = reinterpret_cast<const ulonglong2 *>(sm.list);
+        if (n <= kThreads) {
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-        const uint64_t k = sm.list[j], w = sm.mass[j];
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (k > key[e]) {
-                ++rank[e];
-                above[e] += w;
+            for (int j = 0; j < (n + 1) / 2; ++j) {
+                const ulonglong2 k = pairs[j];
+                place[0] += (k.x > key[0] ? 1 : 0) + (k.y > key[0] ? 1 : 0);
             }
+        } else {
+#pragma unroll 4
+            for (int j = 0; j < (n + 1) / 2; ++j) {
+                const ulonglong2 k = pairs[j];
+#pragma unroll
+                for (int e = 0; e < E; ++e) place[e] += (k.x > key[e] ? 1 : 0) + (k.y > key[e] ? 1 : 0);
+            }
+        }
     }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (tid + e * kThreads < n) sm.list[place[e]] = key[e];
+    __syncthreads();
 }
 
 // What stays: entries with a key of at least `edge`.
@@ -369,31 +384,54 @@ struct RowView {
         cl.sync();
         return slots;
     }
-    __device__ __forceinline__ uint64_t row_sum(uint64_t lane_sum) {
-        const uint64_t *all = exchange(cta_sum(sm, lane_sum));
-        uint64_t t = 0;
+    // The row's sums of two values.
+    __device__ __forceinline__ void row_sums(uint64_t &a, uint64_t &b) {
+        a = cta_sum(sm, a);
+        __syncthreads();
+        b = cta_sum(sm, b);
+        uint64_t *sa = sm.slot[flip], *sb = sm.slot[flip ^ 1];
+        if (static_cast<int>(threadIdx.x) < ranks) {
+            cl.map_shared_rank(sa, threadIdx.x)[rank] = a;
+            cl.map_shared_rank(sb, threadIdx.x)[rank] = b;
+        }
+        cl.sync();
+        a = b = 0;
 #pragma unroll
         for (int i = 0; i < kMaxCluster; ++i)
-            if (i < ranks) t += all[i];
-        __syncthreads();
-        return t;
+            if (i < ranks) {
+                a += sa[i];
+                b += sb[i];
+            }
+        cl.sync();  // both slots are free again
     }
 
-    // The bin in which the cluster's sums over bins 0, 1, .. reach need (>= 1):
-    // its number, and in sm.above / sm.in the sums before and of it.  A bin's
-    // sum in one CTA is value(CTA, bin).  BINS where they do not.
-    template <int BINS, typename F>
-    __device__ __forceinline__ int crossing(const F &value, uint64_t need) {
-        if (threadIdx.x == 0) sm.bin = BINS;
+    // A histogram's (BINS of count or mass) sums over the cluster, into sums:
+    // each CTA adds up its share of the bins, one source to a lane, and
+    // hands the sums to all.
+    template <int BINS, typename H>
+    __device__ __forceinline__ void add_up(H *hist) {
         cl.sync();
+#pragma unroll
+        for (int i0 = 0; i0 < BINS; i0 += kThreads) {
+            const int i = i0 + threadIdx.x, from = i & (ranks - 1);  // ranks: a power of two
+            const int bin = (i & ~(ranks - 1)) / ranks + rank * (BINS / ranks);
+            uint64_t x = cl.map_shared_rank(hist, from)[bin];
+            for (int o = 1; o < ranks; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+            cl.map_shared_rank(sm.sums, from)[bin] = x;
+        }
+        cl.sync();
+    }
+    // The bin in which the sums up to it reach need (>= 1): its number, and in
+    // sm.above / sm.in the sums before and of it.  BINS where they do not.
+    template <int BINS, typename H>
+    __device__ __forceinline__ int crossing(H *hist, uint64_t need) {
+        if (threadIdx.x == 0) sm.bin = BINS;
+        add_up<BINS>(hist);
         constexpr int B = BINS / kThreads;
         uint64_t h[B], mine = 0;
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-            h[b] = 0;
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                if (r < ranks) h[b] += value(r, static_cast<int>(threadIdx.x) * B + b);
+            h[b] = sm.sums[threadIdx.x * B + b];
             mine += h[b];
         }
         uint64_t all, above = cta_scan(sm, mine, all);
@@ -408,15 +446,6 @@ struct RowView {
         }
         __syncthreads();
         return sm.bin;
-    }
-
-    template <int BINS>
-    __device__ __forceinline__ int count_crossing(uint64_t need) {
-        return crossing<BINS>([&](int from, int b) { return uint64_t(cl.map_shared_rank(sm.count, from)[b]); }, need);
-    }
-    template <int BINS>
-    __device__ __forceinline__ int mass_crossing(uint64_t need) {
-        return crossing<BINS>([&](int from, int b) { return cl.map_shared_rank(sm.mass, from)[b]; }, need);
     }
 
     // Entries that `take` takes, as keys: into this CTA's list, its number (of
@@ -473,20 +502,20 @@ struct RowView {
             if (rank == 0) {
                 pull(last_exchange());
                 const int m = static_cast<int>(n);
-                uint64_t mine[2], above[2];
-                int before[2];
+                sort_list(sm, m);
+                constexpr int P = kList / kThreads;
+                uint64_t w[P], mine = 0;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = threadIdx.x + e * kThreads;
-                    mine[e] = i < m ? sm.list[i] : ~0ull;
-                    if (i < m) sm.mass[i] = value(key_value(mine[e]));
+                for (int i = 0; i < P; ++i) {
+                    const int at = threadIdx.x * P + i;
+                    w[i] = at < m ? value(key_value(sm.list[at])) : 0ull;
+                    mine += w[i];
                 }
-                __syncthreads();
-                rank_list<2>(sm, m, mine, before, above);
+                uint64_t all, above = cta_scan(sm, mine, all);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = threadIdx.x + e * kThreads;
-                    if (i < m && above[e] < need && above[e] + sm.mass[i] >= need) sm.above = mine[e];
+                for (int i = 0; i < P; ++i) {
+                    if (above < need && above + w[i] >= need) sm.above = sm.list[threadIdx.x * P + i];
+                    above += w[i];
                 }
                 __syncthreads();
                 key = sm.above;
@@ -510,19 +539,16 @@ struct RowView {
                         atomicAdd(reinterpret_cast<unsigned long long *>(&sm.list[(k >> sh) & 0xFFu]), value(v[e]));
                 }
             });
-            cl.sync();
             // bins from the top, one to a thread
-            uint64_t h = 0;
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                if (r < ranks) h += cl.map_shared_rank(sm.list, r)[kDigits - 1 - threadIdx.x];
+            add_up<kDigits>(sm.list);
+            const uint64_t h = sm.sums[kDigits - 1 - threadIdx.x];
             uint64_t all, above = cta_scan(sm, h, all);
             if (above < need && above + h >= need) {
                 sm.bin = kDigits - 1 - static_cast<int>(threadIdx.x);
                 sm.above = above;
                 sm.in = h;
             }
-            cl.sync();  // also: every CTA has read this one's histogram
+            __syncthreads();
             prefix |= static_cast<uint32_t>(sm.bin) << sh;
             mask |= 0xFFu << sh;
             need -= sm.above;
@@ -573,7 +599,7 @@ struct RowView {
                                   &sm.mass[Bins::at((bins.place(x[e]) - first) * static_cast<float>(kThreads))]),
                               value(x[e]));
         });
-        const int part = mass_crossing<kThreads>(need);
+        const int part = crossing<kThreads>(sm.mass, need);
         const float from = static_cast<float>(part), past = from + 1.0f;
         const uint64_t rest = need - sm.above;
         return cut(
@@ -704,58 +730,68 @@ __device__ __forceinline__ uint64_t share_of(uint64_t P, uint64_t all) {
 // any order, in one CTA: top-k of them, top-p, min-p and the draw.
 __device__ __forceinline__ void finish_list(Shared &sm, const Weight &weight, int n, int k, float top_p, uint64_t floor_w,
                                             int32_t *id, float *prob) {
-    uint64_t key[2], w[2], above[2], mine = 0, all;
-    int before[2];
+    constexpr int E = kList / kThreads;
+    const int first = threadIdx.x * E, most = k < n ? k : n;
+    sort_list(sm, n);
+    uint64_t w[E], mine = 0, all;
+    uint32_t id_key[E];  // inverted ids, 0 for none
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int i = threadIdx.x + e * kThreads;
-        key[e] = i < n ? sm.list[i] : ~0ull;
-        w[e] = i < n ? weight(key_value(key[e])) : 0ull;
-        if (i < n) sm.mass[i] = w[e];
-    }
-    __syncthreads();
-    if (n <= kThreads) {
-        const uint64_t key1[1] = {key[0]};
-        int before1[1];
-        uint64_t above1[1];
-        rank_list<1>(sm, n, key1, before1, above1);
-        before[0] = before1[0];
-        above[0] = above1[0];
-        before[1] = 0;
-        above[1] = 0;
-    } else {
-        rank_list<2>(sm, n, key, before, above);
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (before[e] >= k) w[e] = 0;
+    for (int e = 0; e < E; ++e) {
+        const uint64_t key = first + e < most ? sm.list[first + e] : 0ull;
+        w[e] = key ? weight(key_value(key)) : 0ull;
+        id_key[e] = static_cast<uint32_t>(key);
         mine += w[e];
     }
-    all = cta_sum(sm, mine);  // also: every pair has been compared
-    __syncthreads();
+    uint64_t above = cta_scan(sm, mine, all);
     const uint64_t need = top_p < 1.0f ? share_of(sm.scale.P, all) : ~0ull;
-    // those that stay, keyed by id (ascending: the inverted id descending), the others by 0
+    // those that stay (a head of the list), then their places in ascending order of ids
+    int kept = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const bool stays = above < need && w[e] >= floor_w && w[e] > 0;
+        above += w[e];
+        if (!stays) id_key[e] = 0;
+        kept += stays;
+        sm.count[first + e] = id_key[e];
+    }
+    __syncthreads();
+    int place[E] = {};
+    if (__any_sync(0xFFFFFFFFu, kept > 0)) {
+        const uint4 *four = reinterpret_cast<const uint4 *>(sm.count);
+#pragma unroll 4
+        for (int j = 0; j < (most + 3) / 4; ++j) {
+            const uint4 k4 = four[j];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                place[e] += (k4.x > id_key[e] ? 1 : 0) + (k4.y > id_key[e] ? 1 : 0) + (k4.z > id_key[e] ? 1 : 0) +
+                            (k4.w > id_key[e] ? 1 : 0);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sm.mass[first + e] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (id_key[e]) {
+            sm.mass[place[e]] = w[e];
+            sm.list[place[e]] = id_key[e];
+        }
+    __syncthreads();
     mine = 0;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int i = threadIdx.x + e * kThreads;
-        if (above[e] >= need || w[e] < floor_w) w[e] = 0;
-        key[e] = w[e] ? (key[e] << 32) | 1u : 0ull;
-        if (i < n) {
-            sm.list[i] = key[e];
-            sm.mass[i] = w[e];
-        }
+    for (int e = 0; e < E; ++e) {
+        w[e] = sm.mass[first + e];
         mine += w[e];
     }
-    const uint64_t total = cta_sum(sm, mine);
-    const uint64_t t = __umul64hi(sm.scale.U, total);
-    rank_list<2>(sm, n, key, before, above);
+    above = cta_scan(sm, mine, all);
+    const uint64_t t = __umul64hi(sm.scale.U, all);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (w[e] && above[e] <= t && t < above[e] + w[e]) {
-            *id = key_id(key[e] >> 32);
-            if (prob) *prob = quotient(w[e], total);
+    for (int e = 0; e < E; ++e) {
+        if (above <= t && t < above + w[e]) {
+            *id = key_id(sm.list[first + e]);
+            if (prob) *prob = quotient(w[e], all);
         }
+        above += w[e];
     }
 }
 
@@ -846,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const float lane_max = key_value(static_cast<uint64_t>(lane_top) << 32);
             constexpr int kHalf = kBins / 2;  // bins twice as wide
             if (lane_top > kKeyNegInf) atomicAdd(&sm.count[Bins::at(bins.place(lane_max) * 0.5f)], 1u);
-            const int bound = v.template count_crossing<kHalf>(static_cast<uint64_t>(k));
+            const int bound = v.template crossing<kHalf>(sm.count, static_cast<uint64_t>(k));
             if (bound < kHalf - 1) {
                 const float past = static_cast<float>(2 * (bound + 1));
                 const int64_t n = v.gather([&](const float (&x)[VE], int) {
@@ -861,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                         finish_list(sm, weight, static_cast<int>(n), k, top_p, floor_w, p.ids + r,
                                     p.probs ? p.probs + r : nullptr);
                     }
-                    cl.sync();  // the lists have been read
+                    if (r + gridDim.x / ranks < p.rows) cl.sync();  // the lists have been read
                     continue;
                 }
             }
@@ -874,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 for (int e = 0; e < VE; ++e)
                     if (x[e] > -INFINITY) atomicAdd(&sm.count[Bins::at(bins.place(x[e]))], 1u);
             });
-            const int b = v.template count_crossing<kBins>(static_cast<uint64_t>(k));
+            const int b = v.template crossing<kBins>(sm.count, static_cast<uint64_t>(k));
             if (b < kBins)  // else fewer than k are not masked: all of them stay
                 edge.set(v.narrow(bins, b, static_cast<uint64_t>(k) - sm.above, Edge{-INFINITY, 0x7FFFFFFF}, One()));
             edged = true;
@@ -894,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 sm.bin = 0;
                 sm.found = kBins - 1;
             }
-            cl.sync();
+            v.template add_up<kBins>(sm.count);
             // The bins that may be the one in which the sum of weights reaches p of all.  A bin's
             // weights lie between 2^(S - (b + 1) / 16) and 2^(S - b / 16), the last one's anywhere
             // below that: bounds for the sums up to each bin and for all.
@@ -903,10 +939,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 const int bin = tid * B + b;
-                uint32_t c = 0;
-#pragma unroll
-                for (int from = 0; from < kMaxCluster; ++from)
-                    if (from < ranks) c += cl.map_shared_rank(sm.count, from)[bin];
+                const uint64_t c = sm.sums[bin];
                 const float x = static_cast<float>(c) * exp2f(static_cast<float>(S) - bin / kBinsPerOctave);
                 high[b] = static_cast<uint64_t>(x * 1.0001f) + c;
                 low[b] = bin < kBins - 1 ? static_cast<uint64_t>(x * 0.9575f) : 0ull;  // 2^(-1/16) = 0.95760..
@@ -930,11 +963,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             uint64_t sum, over;
             if (edged) v.bracket(bins, Weigh<true, false, VE>{weight, edge, largest, 0.0f, 0}, ba, bb, sum, over);
             else v.bracket(bins, Weigh<false, false, VE>{weight, edge, largest, 0.0f, 0}, ba, bb, sum, over);
-            const uint64_t need = share_of(sm.scale.P, v.row_sum(sum));
-            over = v.row_sum(over);
-            const int b = v.template mass_crossing<kBins>(need - over);
+            v.row_sums(sum, over);
+            const uint64_t need = share_of(sm.scale.P, sum);
+            const int b = v.template crossing<kBins>(sm.mass, need - over);
             const uint64_t rest = need - over - sm.above;
-            cl.sync();  // the sums have been read
             const Edge kept = edge;
             edge.set(v.narrow(bins, b, rest, kept, weight));
             edged = true;
@@ -1004,9 +1036,18 @@ cudaError_t launch(const SampleParams &p, cudaStream_t stream) {
     const int S = 62 - bits < 45 ? 62 - bits : 45;  // a row's sum stays below 2^62
     // words of a row, one more for a row that starts inside its first
     const int64_t words = (static_cast<int64_t>(p.vocab) + VE - 1) / VE + 1;
+    // The smallest cluster that leaves room for two CTAs on an SM; a larger one while SMs would be
+    // idle and a lane still has work (256 rows of 151,936 in bf16: PLACEHOLDER us in clusters of 4, of 16 PLACEHOLDER)
+    DeviceInfo dev;
+    const cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return e;
+    auto steps_of = [&](int ranks) { return (words + ranks * kThreads - 1) / (ranks * kThreads); };
     int ranks = 1;
-    while (ranks < kMaxCluster && static_cast<int64_t>(ranks) * 5 * kThreads < words) ranks *= 2;
-    const int64_t steps = (words + ranks * kThreads - 1) / (ranks * kThreads);
+    while (ranks < kMaxCluster &&
+           (static_cast<int64_t>(sizeof(Shared)) + steps_of(ranks) * kThreads * 16 > kMaxSmem / 2 ||
+            (p.rows * ranks < dev.num_sms && steps_of(ranks) > 5)))
+        ranks *= 2;
+    const int64_t steps = steps_of(ranks);
     if (sizeof(Shared) + steps * kThreads * 16 <= kMaxSmem)
         return launch_kernel<DT, true>(p, S, static_cast<int>(steps), ranks, stream);
     return launch_kernel<DT, false>(p, S, static_cast<int>(steps), ranks, stream);
