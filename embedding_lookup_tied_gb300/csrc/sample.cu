@@ -384,27 +384,6 @@ struct RowView {
         cl.sync();
         return slots;
     }
-    // The row's sums of two values.
-    __device__ __forceinline__ void row_sums(uint64_t &a, uint64_t &b) {
-        a = cta_sum(sm, a);
-        __syncthreads();
-        b = cta_sum(sm, b);
-        uint64_t *sa = sm.slot[flip], *sb = sm.slot[flip ^ 1];
-        if (static_cast<int>(threadIdx.x) < ranks) {
-            cl.map_shared_rank(sa, threadIdx.x)[rank] = a;
-            cl.map_shared_rank(sb, threadIdx.x)[rank] = b;
-        }
-        cl.sync();
-        a = b = 0;
-#pragma unroll
-        for (int i = 0; i < kMaxCluster; ++i)
-            if (i < ranks) {
-                a += sa[i];
-                b += sb[i];
-            }
-        cl.sync();  // both slots are free again
-    }
-
     // A histogram's (BINS of count or mass) sums over the cluster, into sums:
     // each CTA adds up its share of the bins, one source to a lane, and
     // hands the sums to all.
@@ -421,10 +400,11 @@ struct RowView {
         }
         cl.sync();
     }
-    // The bin in which the sums up to it reach need (>= 1): its number, and in
-    // sm.above / sm.in the sums before and of it.  BINS where they do not.
-    template <int BINS, typename H>
-    __device__ __forceinline__ int crossing(H *hist, uint64_t need) {
+    // The bin in which the sums up to it reach need = need_of(all of them) (>= 1):
+    // its number, and in sm.above / sm.in the sums before and of it.  BINS where
+    // they do not.
+    template <int BINS, typename H, typename F>
+    __device__ __forceinline__ int crossing(H *hist, uint64_t &need, const F &need_of) {
         if (threadIdx.x == 0) sm.bin = BINS;
         add_up<BINS>(hist);
         constexpr int B = BINS / kThreads;
@@ -435,6 +415,7 @@ struct RowView {
             mine += h[b];
         }
         uint64_t all, above = cta_scan(sm, mine, all);
+        need = need_of(all);
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             if (above < need && above + h[b] >= need) {
@@ -446,6 +427,11 @@ struct RowView {
         }
         __syncthreads();
         return sm.bin;
+    }
+
+    template <int BINS, typename H>
+    __device__ __forceinline__ int crossing(H *hist, uint64_t need) {
+        return crossing<BINS>(hist, need, [&](uint64_t) { return need; });
     }
 
     // Entries that `take` takes, as keys: into this CTA's list, its number (of
@@ -559,23 +545,29 @@ struct RowView {
         const uint64_t one = value(edge), m = (need + one - 1) / one;  // of in / one equal logits
         int last = 0x7FFFFFFF;
         if (m < in / one) {
-            uint64_t total;
-            last = locate(
+            locate(
                 [&](const float (&v)[VE], int id, uint64_t (&w)[VE]) {
                     const uint32_t taken = take(v, id);
 #pragma unroll
                     for (int e = 0; e < VE; ++e) w[e] = v[e] == edge ? (taken >> e) & 1u : 0u;
                     return taken != 0;
                 },
-                [&](uint64_t) { return m - 1; }, total);
+                [&](uint64_t) { return m - 1; },
+                [&](int id, uint64_t, uint64_t) {
+                    for (int r = 0; r < ranks; ++r) *cl.map_shared_rank(&sm.found, r) = id;
+                });
+            cl.sync();
+            last = sm.found;
         }
         return topk_key(edge, last);
     }
 
-    // The key at which the sums of value over bin b's entries (that stay by
-    // `in`) reach need: the bin in 256 parts, then the entries of the part.
+    // The key at which the sums of value over bin b's entries (n of them stay by
+    // `in`) reach need: where they are many, the bin in 256 parts and the
+    // entries of the part.
     template <typename G>
-    __device__ __forceinline__ uint64_t narrow(const Bins &bins, int b, uint64_t need, const Edge &in, const G &value) {
+    __device__ __forceinline__ uint64_t narrow(const Bins &bins, int b, uint64_t n, uint64_t need, const Edge &in,
+                                               const G &value) {
         const float first = static_cast<float>(b);
         auto within = [&](const float (&x)[VE], int id) {
             uint32_t mask = 0;
@@ -586,6 +578,7 @@ struct RowView {
             }
             return mask;
         };
+        if (n <= kList) return cut(within, value, need);
         __syncthreads();
         sm.mass[threadIdx.x] = 0;
         __syncthreads();
@@ -616,13 +609,13 @@ struct RowView {
             value, rest);
     }
 
-    // All weights that stay, those in bins before ba, and bins ba .. bb one by
-    // one into mass.
+    // All weights that stay into mass: bins ba .. bb one by one, those above
+    // them in bin 0 and those below in the last (which leaves the sums up to
+    // each bin of the bracket, and of all, as they are).
     template <bool EDGED>
-    __device__ __forceinline__ void bracket(const Bins &bins, const Weigh<EDGED, false, VE> &weigh, int ba, int bb,
-                                            uint64_t &sum, uint64_t &over) {
+    __device__ __forceinline__ void bracket(const Bins &bins, const Weigh<EDGED, false, VE> &weigh, int ba, int bb) {
         const float from = static_cast<float>(ba), past = bb < kBins - 1 ? static_cast<float>(bb + 1) : INFINITY;
-        uint64_t a = 0, o = 0;
+        uint64_t over = 0, under = 0;
         each([&](const float (&x)[VE], int id) {
             uint64_t w[VE];
             if (!weigh(x, id, w)) return;
@@ -630,8 +623,8 @@ struct RowView {
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 const float at = bins.place(x[e]);
-                a += w[e];
-                o += at < from ? w[e] : 0ull;
+                over += at < from ? w[e] : 0ull;
+                under += at >= past ? w[e] : 0ull;
                 inside |= at >= from && at < past && w[e] ? 1u << e : 0u;
             }
             if (inside == 0) return;
@@ -640,14 +633,19 @@ struct RowView {
                 if ((inside >> e) & 1u)
                     atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[Bins::at(bins.place(x[e]))]), w[e]);
         });
-        sum = a;
-        over = o;
+        over = warp_add(over);
+        under = warp_add(under);
+        if ((threadIdx.x & 31) == 0) {
+            if (over) atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[0]), over);
+            if (under) atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[kBins - 1]), under);
+        }
     }
 
-    // The first id at which the running sum of weights passes target(total).
+    // The first id at which the running sum of weights passes target(total):
+    // the one thread that finds it calls found(id, weight, total).
     // value(values, id, weights): false where all of a word's weights are 0.
-    template <typename F, typename G>
-    __device__ __forceinline__ int locate(const F &value, const G &target, uint64_t &total) {
+    template <typename F, typename G, typename H>
+    __device__ __forceinline__ void locate(const F &value, const G &target, const H &found) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         uint64_t s = 0;
         each([&](const float (&v)[VE], int id) {
@@ -657,8 +655,7 @@ struct RowView {
             for (int e = 0; e < VE; ++e) s += x[e];
         });
         const uint64_t *all = exchange(cta_sum(sm, s));
-        uint64_t before = 0;
-        total = 0;
+        uint64_t before = 0, total = 0;
 #pragma unroll
         for (int i = 0; i < kMaxCluster; ++i) {
             if (i < rank) before += all[i];
@@ -692,20 +689,22 @@ struct RowView {
                 }
                 uint64_t all_i, run = before + cta_scan(sm, mine_i, all_i);
                 if (t >= run && t < run + mine_i) {
-                    int found = -1;
+                    int at_id = -1;
+                    uint64_t at_w = 0;
 #pragma unroll
                     for (int e = 0; e < VE; ++e) {
                         run += x[e];
-                        if (found < 0 && run > t) found = id + e;
+                        if (at_id < 0 && run > t) {
+                            at_id = id + e;
+                            at_w = x[e];
+                        }
                     }
-                    for (int r = 0; r < ranks; ++r) *cl.map_shared_rank(&sm.found, r) = found;
+                    found(at_id, at_w, total);
                 }
                 before += all_i;
                 __syncthreads();
             }
         }
-        cl.sync();
-        return sm.found;
     }
 };
 
@@ -912,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             });
             const int b = v.template crossing<kBins>(sm.count, static_cast<uint64_t>(k));
             if (b < kBins)  // else fewer than k are not masked: all of them stay
-                edge.set(v.narrow(bins, b, static_cast<uint64_t>(k) - sm.above, Edge{-INFINITY, 0x7FFFFFFF}, One()));
+                edge.set(v.narrow(bins, b, sm.in, static_cast<uint64_t>(k) - sm.above, Edge{-INFINITY, 0x7FFFFFFF}, One()));
             edged = true;
             cl.sync();
             for (int i = tid; i < kBins; i += kThreads) sm.count[i] = 0;
@@ -933,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             v.template add_up<kBins>(sm.count);
             // The bins that may be the one in which the sum of weights reaches p of all.  A bin's
             // weights lie between 2^(S - (b + 1) / 16) and 2^(S - b / 16), the last one's anywhere
-            // below that: bounds for the sums up to each bin and for all.
+            // below that, the largest taken as 2^S: bounds for the sums up to each bin and for all.
             constexpr int B = kBins / kThreads;
             uint64_t high[B], low[B], h0 = 0, l0 = 0, h_all, l_all;
 #pragma unroll
@@ -959,33 +958,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             }
             __syncthreads();
             const int ba = sm.bin, bb = sm.found;
-            // all weights, those above the bracket, and its bins one by one, exactly
-            uint64_t sum, over;
-            if (edged) v.bracket(bins, Weigh<true, false, VE>{weight, edge, largest, 0.0f, 0}, ba, bb, sum, over);
-            else v.bracket(bins, Weigh<false, false, VE>{weight, edge, largest, 0.0f, 0}, ba, bb, sum, over);
-            v.row_sums(sum, over);
-            const uint64_t need = share_of(sm.scale.P, sum);
-            const int b = v.template crossing<kBins>(sm.mass, need - over);
-            const uint64_t rest = need - over - sm.above;
+            // (how many entries each has, for below)
+            for (int i = tid; i < kBins; i += kThreads) sm.count[i] = static_cast<uint32_t>(sm.sums[i]);
+            if (edged) v.bracket(bins, Weigh<true, false, VE>{weight, edge, largest, 0.0f, 0}, ba, bb);
+            else v.bracket(bins, Weigh<false, false, VE>{weight, edge, largest, 0.0f, 0}, ba, bb);
+            const uint64_t P = sm.scale.P;
+            uint64_t need;
+            const int b = v.template crossing<kBins>(sm.mass, need, [&](uint64_t all) { return share_of(P, all); });
+            const uint64_t rest = need - sm.above;
             const Edge kept = edge;
-            edge.set(v.narrow(bins, b, rest, kept, weight));
+            edge.set(v.narrow(bins, b, b < kBins ? sm.count[b] : 0, rest, kept, weight));
             edged = true;
         }
-        uint64_t total;
         const float span = sm.scale.span;
         const uint64_t U = sm.scale.U;
-        auto target = [&](uint64_t t) { return __umul64hi(U, t); };
-        int id;
-        if (edged) id = v.locate(Weigh<true, true, VE>{weight, edge, largest, span, floor_w}, target, total);
-        else if (floor_w) id = v.locate(Weigh<false, true, VE>{weight, edge, largest, span, floor_w}, target, total);
-        else id = v.locate(Weigh<false, false, VE>{weight, edge, largest, span, floor_w}, target, total);
-        if (rank == 0 && tid == 0) {
+        auto target = [&](uint64_t total) { return __umul64hi(U, total); };
+        auto drawn = [&](int id, uint64_t w, uint64_t total) {
             p.ids[r] = id;
-            if (p.probs) {
-                const float l = Elem<DT>::widen(ld_dep(static_cast<const typename View::T *>(p.logits) + r * p.stride + id));
-                p.probs[r] = quotient(weight(l), total);
-            }
-        }
+            if (p.probs) p.probs[r] = quotient(w, total);
+        };
+        if (edged) v.locate(Weigh<true, true, VE>{weight, edge, largest, span, floor_w}, target, drawn);
+        else if (floor_w) v.locate(Weigh<false, true, VE>{weight, edge, largest, span, floor_w}, target, drawn);
+        else v.locate(Weigh<false, false, VE>{weight, edge, largest, span, floor_w}, target, drawn);
         __syncthreads();
     }
     cl.sync();  // no CTA leaves while a peer may address its shared memory
@@ -1045,7 +1039,7 @@ cudaError_t launch(const SampleParams &p, cudaStream_t stream) {
     int ranks = 1;
     while (ranks < kMaxCluster &&
            (static_cast<int64_t>(sizeof(Shared)) + steps_of(ranks) * kThreads * 16 > kMaxSmem / 2 ||
-            (p.rows * ranks < dev.num_sms && steps_of(ranks) > 5)))
+            (p.rows * ranks < dev.num_sms && steps_of(ranks) > 2)))
         ranks *= 2;
     const int64_t steps = steps_of(ranks);
     if (sizeof(Shared) + steps * kThreads * 16 <= kMaxSmem)
