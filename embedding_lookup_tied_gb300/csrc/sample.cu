@@ -40,10 +40,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kList = 2 * kThreads;           // entries one CTA ranks
+constexpr int kList = 512;                    // entries one CTA ranks
 constexpr int kDigits = 256;                  // bins of a digit of the order key
 constexpr int kBins = 512;                    // of 1/16 octave of weight; the last takes all that is below
 constexpr float kBinsPerOctave = 16.0f;
+constexpr int kParts = 256;                   // of a bin that holds too many entries
 constexpr int kMaxSmem = 224 * 1024;
 constexpr uint32_t kKeyInf = 0xFF800000u;     // order key of +inf; NaN lies above
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // order key of -inf
@@ -393,6 +394,7 @@ struct RowView {
 #pragma unroll
         for (int i0 = 0; i0 < BINS; i0 += kThreads) {
             const int i = i0 + threadIdx.x, from = i & (ranks - 1);  // ranks: a power of two
+            if (i >= BINS) break;                                    // whole warps
             const int bin = (i & ~(ranks - 1)) / ranks + rank * (BINS / ranks);
             uint64_t x = cl.map_shared_rank(hist, from)[bin];
             for (int o = 1; o < ranks; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
@@ -407,11 +409,12 @@ struct RowView {
     __device__ __forceinline__ int crossing(H *hist, uint64_t &need, const F &need_of) {
         if (threadIdx.x == 0) sm.bin = BINS;
         add_up<BINS>(hist);
-        constexpr int B = BINS / kThreads;
+        constexpr int B = (BINS + kThreads - 1) / kThreads;
         uint64_t h[B], mine = 0;
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-            h[b] = sm.sums[threadIdx.x * B + b];
+            const int bin = threadIdx.x * B + b;
+            h[b] = bin < BINS ? sm.sums[bin] : 0ull;
             mine += h[b];
         }
         uint64_t all, above = cta_scan(sm, mine, all);
@@ -510,10 +513,11 @@ struct RowView {
         }
         __syncthreads();
         // digit by digit, then the id among equal logits
+        static_assert(kDigits <= kThreads, "one digit to a thread");
         uint32_t prefix = 0, mask = 0;
         uint64_t in = 0;
         for (int sh = 24; sh >= 0; sh -= 8) {
-            sm.list[threadIdx.x] = 0;
+            if (threadIdx.x < kDigits) sm.list[threadIdx.x] = 0;
             __syncthreads();
             each([&](const float (&v)[VE], int id) {
                 const uint32_t taken = take(v, id);
@@ -527,7 +531,7 @@ struct RowView {
             });
             // bins from the top, one to a thread
             add_up<kDigits>(sm.list);
-            const uint64_t h = sm.sums[kDigits - 1 - threadIdx.x];
+            const uint64_t h = threadIdx.x < kDigits ? sm.sums[kDigits - 1 - threadIdx.x] : 0ull;
             uint64_t all, above = cta_scan(sm, h, all);
             if (above < need && above + h >= need) {
                 sm.bin = kDigits - 1 - static_cast<int>(threadIdx.x);
@@ -580,7 +584,7 @@ struct RowView {
         };
         if (n <= kList) return cut(within, value, need);
         __syncthreads();
-        sm.mass[threadIdx.x] = 0;
+        if (threadIdx.x < kParts) sm.mass[threadIdx.x] = 0;
         __syncthreads();
         each([&](const float (&x)[VE], int id) {
             const uint32_t mask = within(x, id);
@@ -589,10 +593,10 @@ struct RowView {
             for (int e = 0; e < VE; ++e)
                 if ((mask >> e) & 1u)
                     atomicAdd(reinterpret_cast<unsigned long long *>(
-                                  &sm.mass[Bins::at((bins.place(x[e]) - first) * static_cast<float>(kThreads))]),
+                                  &sm.mass[Bins::at((bins.place(x[e]) - first) * static_cast<float>(kParts))]),
                               value(x[e]));
         });
-        const int part = crossing<kThreads>(sm.mass, need);
+        const int part = crossing<kParts>(sm.mass, need);
         const float from = static_cast<float>(part), past = from + 1.0f;
         const uint64_t rest = need - sm.above;
         return cut(
@@ -601,7 +605,7 @@ struct RowView {
                 if (mask == 0) return mask;
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    const float at = (bins.place(x[e]) - first) * static_cast<float>(kThreads);
+                    const float at = (bins.place(x[e]) - first) * static_cast<float>(kParts);
                     if (!(at >= from && at < past)) mask &= ~(1u << e);
                 }
                 return mask;
@@ -934,6 +938,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             // weights lie between 2^(S - (b + 1) / 16) and 2^(S - b / 16), the last one's anywhere
             // below that, the largest taken as 2^S: bounds for the sums up to each bin and for all.
             constexpr int B = kBins / kThreads;
+            static_assert(B * kThreads == kBins, "whole bins to a thread");
             uint64_t high[B], low[B], h0 = 0, l0 = 0, h_all, l_all;
 #pragma unroll
             for (int b = 0; b < B; ++b) {
@@ -1028,8 +1033,9 @@ cudaError_t launch(const SampleParams &p, cudaStream_t stream) {
     int bits = 0;
     while ((1ll << bits) < p.vocab) ++bits;
     const int S = 62 - bits < 45 ? 62 - bits : 45;  // a row's sum stays below 2^62
-    // words of a row, one more for a row that starts inside its first
-    const int64_t words = (static_cast<int64_t>(p.vocab) + VE - 1) / VE + 1;
+    // words of a row, one more where a row may start inside its first
+    const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && (p.stride % VE == 0 || p.rows == 1);
+    const int64_t words = (static_cast<int64_t>(p.vocab) + VE - 1) / VE + (aligned ? 0 : 1);
     // The smallest cluster that leaves room for two CTAs on an SM; a larger one while SMs would be
     // idle and a lane still has work (256 rows of 151,936 in bf16: PLACEHOLDER us in clusters of 4, of 16 PLACEHOLDER)
     DeviceInfo dev;
