@@ -120,9 +120,15 @@ struct RowScale {
 };
 
 struct alignas(16) Shared {
-    uint64_t list[kList];           // entries; the digit histograms where no list fits
+    union {
+        struct {
+            uint64_t list[kList];   // entries; the digit histograms where no list fits
+            uint64_t sums[kBins];   // a histogram's sums over the cluster
+        };
+        uint32_t copies[kBins][4];  // counts in the making: a lane's copy is lane mod 4
+        uint32_t limbs[kBins][4];   // weights in the making: 15 bits to a limb, three used
+    };
     uint64_t mass[kBins];
-    uint64_t sums[kBins];           // a histogram's sums over the cluster
     uint32_t count[kBins];
     uint64_t slot[2][kMaxCluster];  // one value from each CTA of the cluster, two exchanges
     uint64_t warp_sum[kWarps];
@@ -566,6 +572,53 @@ struct RowView {
         return topk_key(edge, last);
     }
 
+    // How many of this CTA's entries that stay lie in each bin, into count.  Four
+    // copies of the counts: a warp's 32 logits meet in few bins.
+    __device__ __forceinline__ void count_bins(const Bins &bins, const Edge &edge) {
+        uint32_t *copies = &sm.copies[0][0];
+        for (int i = threadIdx.x; i < 4 * kBins; i += kThreads) copies[i] = 0;
+        __syncthreads();
+        each([&](const float (&x)[VE], int id) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                if (x[e] > -INFINITY && edge.stays(x[e], id + e))
+                    atomicAdd(copies + 4 * Bins::at(bins.place(x[e])) + (threadIdx.x & 3), 1u);
+        });
+        __syncthreads();
+        for (int i = threadIdx.x; i < kBins; i += kThreads) {
+            const uint4 c = *reinterpret_cast<const uint4 *>(sm.copies[i]);
+            sm.count[i] = c.x + c.y + c.z + c.w;
+        }
+    }
+    // Sums of weights by bins, into mass: start, add from any thread, finish.
+    // 64-bit additions to shared memory are loops of compare and swap; where
+    // a CTA's share of the row is resident (below 2^17 entries) a weight's three
+    // limbs of 15 bits are added without waiting for an answer.
+    __device__ __forceinline__ void mass_start(int bins) {
+        for (int i = threadIdx.x; i < bins; i += kThreads) {
+            sm.mass[i] = 0;
+            if (RESIDENT) *reinterpret_cast<uint4 *>(sm.limbs[i]) = make_uint4(0, 0, 0, 0);
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void mass_add(int bin, uint64_t w) {
+        if constexpr (RESIDENT) {
+            atomicAdd(&sm.limbs[bin][0], static_cast<uint32_t>(w) & 0x7FFFu);
+            atomicAdd(&sm.limbs[bin][1], static_cast<uint32_t>(w >> 15) & 0x7FFFu);
+            atomicAdd(&sm.limbs[bin][2], static_cast<uint32_t>(w >> 30));
+        } else {
+            atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[bin]), w);
+        }
+    }
+    __device__ __forceinline__ void mass_finish(int bins) {
+        __syncthreads();
+        if constexpr (RESIDENT) {
+            for (int i = threadIdx.x; i < bins; i += kThreads)
+                sm.mass[i] += sm.limbs[i][0] + (static_cast<uint64_t>(sm.limbs[i][1]) << 15) +
+                              (static_cast<uint64_t>(sm.limbs[i][2]) << 30);
+        }
+    }
+
     // The key at which the sums of value over bin b's entries (n of them stay by
     // `in`) reach need: where they are many, the bin in 256 parts and the
     // entries of the part.
@@ -584,18 +637,16 @@ struct RowView {
         };
         if (n <= kList) return cut(within, value, need);
         __syncthreads();
-        if (threadIdx.x < kParts) sm.mass[threadIdx.x] = 0;
-        __syncthreads();
+        mass_start(kParts);
         each([&](const float (&x)[VE], int id) {
             const uint32_t mask = within(x, id);
             if (mask == 0) return;
 #pragma unroll
             for (int e = 0; e < VE; ++e)
                 if ((mask >> e) & 1u)
-                    atomicAdd(reinterpret_cast<unsigned long long *>(
-                                  &sm.mass[Bins::at((bins.place(x[e]) - first) * static_cast<float>(kParts))]),
-                              value(x[e]));
+                    mass_add(Bins::at((bins.place(x[e]) - first) * static_cast<float>(kParts)), value(x[e]));
         });
+        mass_finish(kParts);
         const int part = crossing<kParts>(sm.mass, need);
         const float from = static_cast<float>(part), past = from + 1.0f;
         const uint64_t rest = need - sm.above;
@@ -620,6 +671,7 @@ struct RowView {
     __device__ __forceinline__ void bracket(const Bins &bins, const Weigh<EDGED, false, VE> &weigh, int ba, int bb) {
         const float from = static_cast<float>(ba), past = bb < kBins - 1 ? static_cast<float>(bb + 1) : INFINITY;
         uint64_t over = 0, under = 0;
+        mass_start(kBins);
         each([&](const float (&x)[VE], int id) {
             uint64_t w[VE];
             if (!weigh(x, id, w)) return;
@@ -634,8 +686,7 @@ struct RowView {
             if (inside == 0) return;
 #pragma unroll
             for (int e = 0; e < VE; ++e)
-                if ((inside >> e) & 1u)
-                    atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[Bins::at(bins.place(x[e]))]), w[e]);
+                if ((inside >> e) & 1u) mass_add(Bins::at(bins.place(x[e])), w[e]);
         });
         over = warp_add(over);
         under = warp_add(under);
@@ -643,6 +694,7 @@ struct RowView {
             if (over) atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[0]), over);
             if (under) atomicAdd(reinterpret_cast<unsigned long long *>(&sm.mass[kBins - 1]), under);
         }
+        mass_finish(kBins);
     }
 
     // The first id at which the running sum of weights passes target(total):
@@ -906,29 +958,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             }
             cl.sync();
             // the bin of the k-th entry, then the entry
-            for (int i = tid; i < kBins; i += kThreads) sm.count[i] = 0;
-            __syncthreads();
-            v.each([&](const float (&x)[VE], int id) {
-#pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    if (x[e] > -INFINITY) atomicAdd(&sm.count[Bins::at(bins.place(x[e]))], 1u);
-            });
+            v.count_bins(bins, edge);
             const int b = v.template crossing<kBins>(sm.count, static_cast<uint64_t>(k));
             if (b < kBins)  // else fewer than k are not masked: all of them stay
                 edge.set(v.narrow(bins, b, sm.in, static_cast<uint64_t>(k) - sm.above, Edge{-INFINITY, 0x7FFFFFFF}, One()));
             edged = true;
             cl.sync();
-            for (int i = tid; i < kBins; i += kThreads) sm.count[i] = 0;
-            __syncthreads();
         }
         if (top_p < 1.0f) {
-            // how many of those that stay lie in each bin
-            v.each([&](const float (&x)[VE], int id) {
-#pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    if (x[e] > -INFINITY && edge.stays(x[e], id + e)) atomicAdd(&sm.count[Bins::at(bins.place(x[e]))], 1u);
-            });
-            for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0;
+            v.count_bins(bins, edge);
             if (tid == 0) {
                 sm.bin = 0;
                 sm.found = kBins - 1;
@@ -965,6 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const int ba = sm.bin, bb = sm.found;
             // (how many entries each has, for below)
             for (int i = tid; i < kBins; i += kThreads) sm.count[i] = static_cast<uint32_t>(sm.sums[i]);
+            __syncthreads();
             if (edged) v.bracket(bins, Weigh<true, false, VE>{weight, edge, largest, 0.0f, 0}, ba, bb);
             else v.bracket(bins, Weigh<false, false, VE>{weight, edge, largest, 0.0f, 0}, ba, bb);
             const uint64_t P = sm.scale.P;
