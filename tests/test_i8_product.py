@@ -150,7 +150,7 @@ def table_of(buf, scales, hidden):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", WIDE, ids=str)
 @pytest.mark.parametrize("rows,hidden", [(1, 1), (3, 2), (5, 17), (300, 31), (7, 128), (33, 896), (4, 1001),
-                                         (2, 1024), (2, 1030), (9, 5376), (2, 20003), (1100, 64), (0, 16)])
+                                         (2, 1024), (2, 1030), (9, 5376), (3, 8192), (2, 20003), (1100, 64), (0, 16)])
 def test_quantize(dtype, rows, hidden):
     g = torch.Generator().manual_seed(rows * 7 + hidden)
     x = torch.randn((rows, hidden + 3), generator=g) * 3
@@ -169,6 +169,11 @@ def test_quantize(dtype, rows, hidden):
     assert np.array_equal(t.codes.cpu().numpy(), q)
     assert canaries_intact(raw, pad)
     assert bool((codes[:, hidden:] == 0x5A).all())  # the gap between rows is not written
+    if rows:  # codes and values at any address
+        odd = torch.full((rows, hidden + 6), 90, dtype=torch.int8, device="cuda")
+        t, _ = lhs.lhs_i8_quantize(xd.contiguous(), codes=odd[:, 3:hidden + 3])
+        assert np.array_equal(t.codes.cpu().numpy(), q) and np.array_equal(t.scales.cpu().numpy(), s)
+        assert bool((odd[:, :3] == 90).all()) and bool((odd[:, hidden + 3:] == 90).all())
 
 
 @pytest.mark.gpu
