@@ -309,6 +309,29 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+// The tile a pair works on: channels from 256 tile, tokens from n block.  Items
+// (tile, block), blocks innermost, are dealt out to the pairs in turn; a step
+// is worked out once, so that no tile waits for a division.
+struct Item {
+    int64_t tile;
+    int block, blocks, step_block;
+    int64_t step_tile;
+    __device__ __forceinline__ Item(int64_t first, int64_t step, int blocks_) : blocks(blocks_) {
+        tile = first / blocks;
+        block = static_cast<int>(first - tile * blocks);
+        step_tile = step / blocks;
+        step_block = static_cast<int>(step - step_tile * blocks);
+    }
+    __device__ __forceinline__ void next() {
+        tile += step_tile;
+        block += step_block;
+        if (block >= blocks) {
+            block -= blocks;
+            ++tile;
+        }
+    }
+};
+
 // A place in a ring of N slots and the parity of its phase.
 template <int N>
 struct Ring {
@@ -437,8 +460,22 @@ __global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
         Ring<T::kSlots> sa;
         Ring<ACCS> sc;
         Ring<T::kGroups> turn;
-        int64_t it = cl;
+        Item it(cl, clusters, p.blocks);
         int kd = 0, in = 0;  // stage of the tile, of the sum, that the sums have got to
+        // the tile's scales, asked for one tile ahead
+        int64_t ch = 0, t0 = 0;
+        float ws = 0.0f, as[(T::kPart + 31) / 32];
+        auto ask = [&]() {
+            ch = it.tile * kPairRows + static_cast<int64_t>(rank) * kCtaRows + row;
+            t0 = static_cast<int64_t>(it.block) * p.n + g * part;
+            if (ch < p.channels) ws = ld_dep(reinterpret_cast<const float *>(p.w_scales + ch * p.w_scale_stride));
+#pragma unroll
+            for (int i = 0; i < (T::kPart + 31) / 32; ++i)
+                if (t0 + i * 32 + lane < p.tokens) as[i] = ld_dep(p.scales + t0 + i * 32 + lane);
+        };
+#pragma unroll
+        for (int i = 0; i < (T::kPart + 31) / 32; ++i) as[i] = 0.0f;
+        if (total > 0) ask();
         for (int64_t j = 0; j < total + T::kAhead; ++j) {
             if (j < total && turn.i == g) {
                 // in this order: once the slot is free, every stage up to kSlots before this one has been
@@ -480,17 +517,6 @@ __global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
             ++kd;
             const bool tile_done = kd == p.nk;
             if (in < chunk && !tile_done) continue;
-            // the scales of what is about to be written, on their way while the sum is waited for
-            const int64_t ch = it / p.blocks * kPairRows + static_cast<int64_t>(rank) * kCtaRows + row;
-            const int64_t t0 = it % p.blocks * p.n + g * part;
-            const bool valid = ch < p.channels;
-            float ws = 0.0f, as[(T::kPart + 31) / 32];
-            if (tile_done) {
-                if (valid) ws = ld_dep(reinterpret_cast<const float *>(p.w_scales + ch * p.w_scale_stride));
-#pragma unroll
-                for (int i = 0; i < (T::kPart + 31) / 32; ++i)
-                    as[i] = t0 + i * 32 + lane < p.tokens ? ld_dep(p.scales + t0 + i * 32 + lane) : 0.0f;
-            }
             const bool ok = wait_or_abort(&sm.acc_full[sc.i], sc.parity, &sm.abort_flag, p.err);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after();
@@ -549,7 +575,7 @@ __global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
             in = 0;
             if (!tile_done) continue;
             kd = 0;
-            it += clusters;
+            const bool valid = ch < p.channels;
             const int64_t left = p.tokens - t0;
             const int cols = static_cast<int>(left < part ? left : part);
             if (whole) {
@@ -570,6 +596,8 @@ __global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
             if (p.out_dtype == LHS_F32) emit(static_cast<float *>(p.out));
             else if (p.out_dtype == LHS_F16) emit(static_cast<__half *>(p.out));
             else emit(static_cast<__nv_bfloat16 *>(p.out));
+            it.next();
+            ask();
         }
     } else {
         if constexpr (NMAX == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -581,8 +609,9 @@ __global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
                 int64_t j = 0;
                 Ring<SW> st;
                 bool ok = true;
-                for (int64_t it = cl; it < p.items && ok; it += clusters) {
-                    const int32_t row = static_cast<int32_t>(it / p.blocks) * kPairRows + static_cast<int32_t>(rank) * kCtaRows;
+                Item it(cl, clusters, p.blocks);
+                for (int64_t i = 0; i < mine && ok; ++i, it.next()) {
+                    const int32_t row = static_cast<int32_t>(it.tile) * kPairRows + static_cast<int32_t>(rank) * kCtaRows;
                     for (int kc = 0; kc < p.nk; ++kc, ++j, st.next()) {
                         if (!wait_or_abort(&sm.table_empty[st.i], st.parity ^ 1u, &sm.abort_flag, p.err)) {
                             ok = false;
@@ -604,8 +633,9 @@ __global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
                 int64_t j = 0;
                 Ring<SX> st;
                 bool ok = true;
-                for (int64_t it = cl; it < p.items && ok; it += clusters) {
-                    const int32_t row = static_cast<int32_t>(it % p.blocks) * p.n + static_cast<int32_t>(rank) * half;
+                Item it(cl, clusters, p.blocks);
+                for (int64_t i = 0; i < mine && ok; ++i, it.next()) {
+                    const int32_t row = it.block * p.n + static_cast<int32_t>(rank) * half;
                     for (int kc = 0; kc < p.nk; ++kc, ++j, st.next()) {
                         const int s = st.i;
                         if (!wait_or_abort(&sm.empty[s], st.parity ^ 1u, &sm.abort_flag, p.err)) {
