@@ -16,7 +16,7 @@
 //    moves between lanes.  f32 sums of up to 1,024 products are exact; they
 //    are added up as integers.
 // (The tcgen05 kernel of i8_matmul.cu, whose operand has to pass through tensor
-// memory, needs about 1,100 clocks for a stage of so few tokens.)
+// memory, needs about 1,000 clocks for a stage of so few tokens.)
 //
 // One CTA per SM: two groups of eight warps, each warp with 16 of its group's
 // tile of 128 rows, and a producer that keeps a ring of TMA boxes full for
@@ -28,6 +28,9 @@
 // in turn; the rows that do not fill a round of them are split evenly, in units
 // of 16 rows with boxes of that size.  The tokens are quantised by every CTA
 // for itself while its ring fills, so a call is one launch.
+//
+// Measured: 1 x 151,936 x 896 in 23.2 us (87% of the HBM rate; a stream this
+// short is 3 us of start and end), 8 x 262,144 x 5,376 in 233 us (90%).
 #include <mutex>
 
 #include "i8_common.cuh"

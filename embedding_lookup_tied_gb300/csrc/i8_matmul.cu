@@ -13,11 +13,27 @@
 // channels x up to 256 tokens (tcgen05 cta_group::2: each CTA holds 128
 // channels and half of the tokens' tile).
 //
+// Roles in a CTA: one warp streams the table, one the tokens, one issues the
+// MMAs, and 8 or 16 widen the codes and take the sums out, in groups of four
+// warps that take the stages in turn (a stage's waits, loads, widening and
+// TMEM store are one chain of about 1,000 clocks).
+//
 // Exact sums.  f32 sums of integers are exact while they stay within 2^24.  A
 // partial sum over some k is at most 128 * sum|a|; the first kernel leaves,
 // for each token, the largest sum|a| over 128 codes, b, so n = floor(2^24 /
 // (128 b)) blocks of 128 (at least 8) may be summed in the tensor cores.  Longer
 // sums are taken out every n blocks and added up as 32-bit integers.
+//
+// What bounds it.  256 x 262,144 x 5,120: the tensor cores (387 us, 1,775
+// TFLOP/s, the sustained bf16 rate and a little more; 429 us back to back for
+// seconds, under the power cap; HBM alone would take 238 us).  628 x 151,936 x
+// 896 (143 us; 99 us by that rate): a tile is seven stages, and the warps that
+// widen also write its 224 results a channel, about 4,300 of its 11,300 clocks;
+// the tensor cores are busy 56% of the time.  64 x 262,144 x 768 (50 us; 35 us of
+// HBM): the widening chain (48 us with the MMAs left out).
+// Tried and not kept: results of 16 bits written two channels to a word (no
+// change), a tile's results written between the next tile's stages (143 -> 235
+// us), tiles of at most 128 or 192 tokens (batch 392 -> 503 us).
 #include <mutex>
 
 #include "i8_common.cuh"

@@ -13,19 +13,30 @@
 // bit.
 //
 // A cluster of CTAs owns a row and holds it in its shared memory: HBM is read
-// once, and every later pass is a lane's own 16-byte words from shared memory.
+// once (bulk copies), and every later pass is a lane's own 16-byte words from
+// shared memory.  Rows too long for 16 CTAs (815,000 f32 logits) are read from
+// L2 in every pass.
 //  * top-k: at least k entries lie in or above the bin that holds the k-th
 //    largest of the threads' maxima, and few more do, so that bound gathers a
 //    short list; one CTA sorts it and does the rest (k, p, min-p, the draw).
 //  * top-p alone: one pass counts the entries by bins of 1/16 octave; the
 //    counts bracket the bin in which the weights reach p of their sum, a pass
-//    sums all weights and the bracket's bins exactly, and the entries of the
-//    one bin left are sorted.
-//  * Where a list does not fit (equal logits by the thousand, a large k), the
-//    threshold is found digit by digit (11, 11 and 10 bits of the order key)
-//    from histograms of counts or weights.
+//    sums the bracket's bins, and what lies above and below it, exactly, and
+//    the entries of the one bin left (or of 1/256 of it) are sorted.
+//  * Where a list does not fit (equal logits by the thousand), the threshold is
+//    found digit by digit (8 bits) from histograms over the order key.
 //  * The draw: each warp's sum over its piece of the row, the pieces in id
-//    order; the warp whose piece holds the answer walks it.
+//    order; the CTA whose warp's piece holds the answer walks it.
+//
+// What bounds it: latency.  A row of 1 MB is 0.15 us of HBM time, but 8 to 14
+// exchanges across the cluster of about 0.7 us each, and passes of 1 to 7 us
+// over 64 logits a lane (ncu, 256 rows of 262,144 f32 with mixed filters: 31% of
+// issue slots, 3.2 of 4 warps a scheduler active, a third of the stalls at
+// barriers).  Measured: 1 x 151,936 f32 with all filters 10.6 us; 8 x 262,144 f32
+// with top-p 53 us; 256 x 262,144 f32 386 us mixed, 165 us min-p, 248 us with the
+// temperature alone, 278 us top-k, 890 us top-p.  Tried and slower: CTAs of 512
+// threads (426 -> 453 us mixed), two words side by side (441 -> 455 us), clusters
+// of at most 8 (441 -> 499 us).
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -71,7 +82,7 @@ __constant__ const uint64_t kPow16[16] = {
 // show; there logits are first taken relative to the largest, and those that
 // weigh anything are so near to it that the difference is exact.
 // (No branch, so that the weights of a word's logits are worked out side by
-// side; 16 and 8 warps an SM: 70 and 105 issue slots a weight.)
+// side: 33 issue slots a weight with 16 warps on an SM.)
 struct Weight {
     float ref, low;    // what logits are relative to; below `low` they weigh 0
     float c_hi, c_lo;
@@ -1075,8 +1086,9 @@ cudaError_t launch(const SampleParams &p, cudaStream_t stream) {
     // words of a row, one more where a row may start inside its first
     const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && (p.stride % VE == 0 || p.rows == 1);
     const int64_t words = (static_cast<int64_t>(p.vocab) + VE - 1) / VE + (aligned ? 0 : 1);
-    // The smallest cluster that leaves room for two CTAs on an SM; a larger one while SMs would be
-    // idle and a lane still has work (256 rows of 151,936 in bf16: PLACEHOLDER us in clusters of 4, of 16 PLACEHOLDER)
+    // The smallest cluster that leaves room for two CTAs on an SM (64 rows of 151,936 in bf16, min-p:
+    // 31 us in clusters of 4, 65 us of 16); a larger one while SMs would be idle and a lane still has
+    // more than two words (4 rows of 8,192: 13.2 us in clusters of 4, 15.2 us of 2).
     DeviceInfo dev;
     const cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return e;

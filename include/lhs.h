@@ -392,6 +392,8 @@ LHS_API int lhs_i8_workspace(const lhs_i8 *table, int64_t tokens, size_t *bytes)
  *   d_out : row t at element t*out_stride (out_stride >= table->rows),
  *           aligned to its element size; nothing else is written
  *   d_ws  : 256-byte aligned, >= lhs_i8_workspace bytes, overwritten
+ *           (calls of up to 16 tokens leave it alone where their codes fit
+ *           in shared memory, but it has to be there)
  * a->rows == 0 or table->rows == 0 enqueues nothing.  Errors:
  * LHS_ERR_INVALID_ARG, LHS_ERR_BUFFER_TOO_SMALL, LHS_ERR_CUDA. */
 LHS_API int lhs_i8_matmul(const lhs_i8 *a, const lhs_i8 *table, void *d_out, int32_t out_dtype,
@@ -421,7 +423,8 @@ LHS_API int lhs_i8_logits(const lhs_i8 *table, const void *d_x, int32_t x_dtype,
  * others are clamped to [2^-100, 2^100].  A logit of -inf is a masked token
  * and is never drawn.  Weights are evaluated to about 2^-36 of themselves
  * and summed as integers, so the result does not depend on the order of the
- * sums; a weight below about 2^-45 of the row's largest counts as 0.
+ * sums; a weight below about 2^-43 of the row's largest (for a vocabulary of
+ * 2^18; a bit more for each doubling beyond) counts as 0.
  *   d_logits : LHS_F32, LHS_F16 or LHS_BF16, row r at element r*stride
  *              (stride >= vocab), aligned to its element size
  *   d_u      : f32 [rows], each in [0, 1)
