@@ -483,12 +483,16 @@ def _wide_rows(t: torch.Tensor, name: str):
     apart."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _WIDE:
+    dt = _WIDE.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2:
         raise ValueError(f"{name} must be two-dimensional with contiguous rows")
-    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    return t.data_ptr(), _WIDE[t.dtype], stride
+    rows, cols = t.shape
+    stride, one = t.stride()
+    if cols > 1 and one != 1:
+        raise ValueError(f"{name} must be two-dimensional with contiguous rows")
+    return t.data_ptr(), dt, stride if rows > 1 else cols
 
 
 class I8Rows:
@@ -576,14 +580,15 @@ def lhs_i8_workspace(table: I8Rows, tokens: int) -> int:
 
 
 def _i8_out(table: I8Rows, tokens: int, out_dtype, out, ws):
+    rows, dev = table.c.rows, table.tensors[0].device
     if out is None:
-        out = torch.empty((tokens, table.rows), dtype=out_dtype or torch.float32, device=table.device)
+        out = torch.empty((tokens, rows), dtype=out_dtype or torch.float32, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError("out is not of out_dtype")
-    if tuple(out.shape) != (tokens, table.rows):
+    elif tuple(out.shape) != (tokens, rows):
         raise ValueError("out must be [tokens, table rows]")
     if ws is None:
-        ws = torch.empty(max(256, lhs_i8_workspace(table, tokens)), dtype=torch.uint8, device=table.device)
+        ws = torch.empty(max(256, lhs_i8_workspace(table, tokens)), dtype=torch.uint8, device=dev)
     return out, ws
 
 

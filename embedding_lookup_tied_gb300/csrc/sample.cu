@@ -294,7 +294,7 @@ struct RowView {
     Shared &sm;
     cg::cluster_group cl;
     int rank, ranks;
-    uint4 *hold;      // this lane's words in shared memory, kThreads... 32 apart
+    uint4 *hold;      // this lane's words in shared memory, 32 apart
     int steps;        // words per lane
     int word0;        // this lane's first word; the next are 32 further on
     int vocab;
@@ -342,7 +342,7 @@ struct RowView {
     // f(values, id of the first) for each of this lane's words, in id order.
     template <typename F>
     __device__ __forceinline__ void each(const F &f) const {
-#pragma unroll 2
+#pragma unroll 1
         for (int s = 0; s < steps; ++s) {
             float v[VE];
             widen(RESIDENT ? hold[s * 32] : fetch(word0 + s * 32), v);
@@ -373,7 +373,8 @@ struct RowView {
         if (RESIDENT) {
             const int n = piece();
             if (!mbar_wait(&sm.arrived[threadIdx.x >> 5], parity, kWaitTimeoutNs)) set_err(err, LHS_ERRBIT_TIMEOUT);
-            for (int w = n + ((lane - n) & 31); w < steps * 32; w += 32) hold[w - lane] = outside();  // words lane, lane + 32, ..
+            // of this lane's words, lane, lane + 32, ..
+            for (int w = n + ((lane - n) & 31); w < steps * 32; w += 32) hold[w - lane] = outside();
             const int w0 = word0 - lane;
             if (n > 0 && ((w0 == 0 && skip) || n < steps * 32 || static_cast<int64_t>(w0 + n) * VE - skip > vocab)) {
                 // the row's first and last words
@@ -794,8 +795,8 @@ __device__ __forceinline__ uint64_t share_of(uint64_t P, uint64_t all) {
 
 // A row that the filters have narrowed to the n <= kList entries of the list, in
 // any order, in one CTA: top-k of them, top-p, min-p and the draw.
-__device__ __forceinline__ void finish_list(Shared &sm, const Weight &weight, int n, int k, float top_p, uint64_t floor_w,
-                                            int32_t *id, float *prob) {
+__device__ __forceinline__ void finish_list(Shared &sm, const Weight &weight, int n, int k, float top_p,
+                                            uint64_t floor_w, int32_t *id, float *prob) {
     constexpr int E = kList / kThreads;
     const int first = threadIdx.x * E, most = k < n ? k : n;
     sort_list(sm, n);

@@ -124,7 +124,8 @@ def test_draws(dtype, mode, n, v):
 @pytest.mark.gpu
 @pytest.mark.parametrize("mode", ["none", "p", "all"])
 @pytest.mark.parametrize("v,dtype", [(151936, torch.float32), (262144, torch.bfloat16), (262145, torch.float32),
-                                     (600001, torch.float16), (1200003, torch.float32)])
+                                     (600001, torch.float16), (800001, torch.float32),
+                                     (1200003, torch.float32)])
 def test_long_rows(mode, v, dtype):
     x, u, g = draw_rows(v, 3, v, dtype)
     t, k, p, q = params(g, 3, v, mode)
