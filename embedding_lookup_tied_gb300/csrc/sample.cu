@@ -33,7 +33,7 @@
 // over 64 logits a lane (ncu, 256 rows of 262,144 f32 with mixed filters: 31% of
 // issue slots, 3.2 of 4 warps a scheduler active, a third of the stalls at
 // barriers).  Measured: 1 x 151,936 f32 with all filters 10.6 us; 8 x 262,144 f32
-// with top-p 53 us; 256 x 262,144 f32 386 us mixed, 165 us min-p, 248 us with the
+// with top-p 53 us; 256 x 262,144 f32 392 us mixed, 165 us min-p, 248 us with the
 // temperature alone, 278 us top-k, 890 us top-p.  Tried and slower: CTAs of 512
 // threads (426 -> 453 us mixed), two words side by side (441 -> 455 us), clusters
 // of at most 8 (441 -> 499 us).
