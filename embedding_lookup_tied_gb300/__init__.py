@@ -4,10 +4,16 @@ Argument marshalling only: every step runs in the library's CUDA kernels.
 The functions carry the C-ABI names (see ``include/lhs.h``) and take torch
 CUDA tensors, which supply device memory and the stream.  There is no CPU
 path: a missing library, a CPU tensor or a failed call raises.
+
+A call runs on the current stream, or on ``stream`` (a torch.cuda.Stream or a
+handle) where that is given.  What a call allocates itself is allocated on the
+stream that it runs on; the tensors that it is given are the caller's to keep
+until that stream has used them.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -156,6 +162,25 @@ def _err_word(err, device) -> torch.Tensor:
     return torch.zeros(1, dtype=torch.int32, device=device) if err is None else err
 
 
+def _on_its_stream(fn):
+    """What ``fn`` allocates or clears itself (default outputs, workspaces, error
+    words) is allocated and cleared on the stream that it is given: a clear is
+    then in order with the kernels, and a workspace dropped on return is not
+    handed to another stream while they still use it."""
+    at = fn.__code__.co_varnames.index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return fn(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
+
+
 class Table:
     """A device-resident table plus its ``lhs_table`` descriptor.  Keeps the
     tensor alive for as long as the descriptor is used."""
@@ -199,6 +224,7 @@ def lhs_table_info(table: Table) -> dict:
             "total_bytes": tb.value}
 
 
+@_on_its_stream
 def lhs_embed(table: Table, ids: torch.Tensor, scale: float, out=None, err=None,
               stream=None):
     """Gather rows ``ids`` (int32, CUDA) -> f32 [n, hidden] scaled by ``scale``.
@@ -215,6 +241,7 @@ def lhs_embed(table: Table, ids: torch.Tensor, scale: float, out=None, err=None,
     return out, err
 
 
+@_on_its_stream
 def lhs_embed_wire(table: Table, ids: torch.Tensor, scale: float, fmt: int, layer: int = 0,
                    flags: int = 0, top_k: int = 0, buf=None, err=None, stream=None):
     """Gather rows ``ids`` scaled by ``scale`` straight into a wire message of
@@ -233,6 +260,7 @@ def lhs_embed_wire(table: Table, ids: torch.Tensor, scale: float, fmt: int, laye
     return buf, err
 
 
+@_on_its_stream
 def lhs_embed_wire_response(table: Table, ids: torch.Tensor, scale: float, fmt: int, layer: int = 0,
                             latency_ms: float = 0.0, buf=None, err=None, stream=None):
     """Gather rows ``ids`` scaled by ``scale`` straight into a single-layer
@@ -255,6 +283,7 @@ def lhs_embed_wire_response(table: Table, ids: torch.Tensor, scale: float, fmt: 
     return buf, err
 
 
+@_on_its_stream
 def lhs_unique_ids(ids: torch.Tensor, vocab: int, ws=None, err=None, stream=None, unique=None,
                    inverse=None, count=None):
     """Distinct ids in [0, vocab), ascending, and each position's index into
@@ -283,6 +312,7 @@ def lhs_unique_ids(ids: torch.Tensor, vocab: int, ws=None, err=None, stream=None
     return unique, inverse[:n], count, err
 
 
+@_on_its_stream
 def lhs_embed_dedup(table: Table, ids: torch.Tensor, scale: float, out=None, ws=None, err=None,
                     stream=None):
     """lhs_embed through the distinct ids (each distinct row decoded once).
@@ -303,6 +333,7 @@ def lhs_embed_dedup(table: Table, ids: torch.Tensor, scale: float, out=None, ws=
     return out, err
 
 
+@_on_its_stream
 def lhs_embed_mixed(data: torch.Tensor, row_offset: torch.Tensor, row_dtype: torch.Tensor, vocab: int,
                     hidden: int, ids: torch.Tensor, scale: float, out=None, err=None, stream=None):
     """Gather from a table whose rows carry their own element type (uint8
@@ -342,6 +373,7 @@ def lhs_logits_topk_launches(table: Table, batch: int, k: int, resid_dtype: int)
     return n.value
 
 
+@_on_its_stream
 def lhs_logits_topk(table: Table, resid: torch.Tensor, k: int, temperature: float = 1.0,
                     want_probs: bool = True, ws=None, ids=None, logits=None, probs=None,
                     err=None, stream=None):
@@ -367,6 +399,7 @@ def lhs_logits_topk(table: Table, resid: torch.Tensor, k: int, temperature: floa
     return ids, logits, (probs if want_probs else None), err
 
 
+@_on_its_stream
 def lhs_logits(table: Table, resid: torch.Tensor, ws=None, out=None, err=None, stream=None):
     """Raw logits f32 [batch, vocab].  Returns (logits, err word)."""
     B = resid.shape[0]
@@ -384,6 +417,7 @@ def lhs_logits(table: Table, resid: torch.Tensor, ws=None, out=None, err=None, s
     return out, err
 
 
+@_on_its_stream
 def lhs_logits_topk_noalloc(table: Table, resid: torch.Tensor, k: int,
                             temperature: float = 1.0, want_probs: bool = True, ids=None,
                             logits=None, probs=None, err=None, stream=None):
@@ -410,6 +444,7 @@ def lhs_wire_bytes(fmt: int, seq_len: int, hidden: int) -> int:
     return int(lib().lhs_wire_bytes(fmt, seq_len, hidden))
 
 
+@_on_its_stream
 def lhs_wire_encode(fmt: int, x: torch.Tensor, layer: int = 0, flags: int = 0,
                     top_k: int = 0, buf=None, err=None, stream=None):
     """Encode residuals [seq_len, hidden] (f32 or bf16) into a uint8 message.
@@ -426,6 +461,7 @@ def lhs_wire_encode(fmt: int, x: torch.Tensor, layer: int = 0, flags: int = 0,
     return buf, err
 
 
+@_on_its_stream
 def lhs_wire_decode(fmt: int, buf: torch.Tensor, seq_len: int, hidden: int, out=None,
                     err=None, stream=None):
     """Decode a message into f32 [seq_len, hidden].  Returns (x, err word)."""
@@ -442,6 +478,7 @@ def lhs_wire_response_bytes(fmt: int, seq_len: int, hidden: int) -> int:
     return int(lib().lhs_wire_response_bytes(fmt, seq_len, hidden))
 
 
+@_on_its_stream
 def lhs_wire_encode_response(fmt: int, x: torch.Tensor, layer: int = 0, latency_ms: float = 0.0,
                              buf=None, err=None, stream=None):
     """Encode residuals [seq_len, hidden] (f32 or bf16) as a single-layer
@@ -461,6 +498,7 @@ def lhs_wire_encode_response(fmt: int, x: torch.Tensor, layer: int = 0, latency_
     return buf, err
 
 
+@_on_its_stream
 def lhs_wire_decode_response(fmt: int, buf: torch.Tensor, seq_len: int, hidden: int, out=None,
                              err=None, stream=None):
     """Decode a single-layer response message into f32 [seq_len, hidden].
@@ -554,6 +592,7 @@ def lhs_i8_message(buf: torch.Tensor, seq_len: int, hidden: int, response: bool 
     return I8Rows(c, buf)
 
 
+@_on_its_stream
 def lhs_i8_quantize(x: torch.Tensor, codes=None, scales=None, err=None, stream=None):
     """Quantise rows of ``x`` (f32, f16 or bf16 [rows, hidden]) to int8 with one
     scale each.  Without ``codes`` the rows lie on 16-byte boundaries, as a
@@ -592,6 +631,7 @@ def _i8_out(table: I8Rows, tokens: int, out_dtype, out, ws):
     return out, ws
 
 
+@_on_its_stream
 def lhs_i8_matmul(a: I8Rows, table: I8Rows, out_dtype=None, out=None, ws=None, err=None, stream=None):
     """Logits [a.rows, table.rows] of coded tokens against an i8 table, in
     ``out_dtype`` (float32 by default, float16 or bfloat16).  Returns (out,
@@ -605,6 +645,7 @@ def lhs_i8_matmul(a: I8Rows, table: I8Rows, out_dtype=None, out=None, ws=None, e
     return out, err
 
 
+@_on_its_stream
 def lhs_i8_logits(table: I8Rows, x: torch.Tensor, out_dtype=None, out=None, ws=None, err=None, stream=None):
     """Logits of wide residuals ``x`` (f32, f16 or bf16 [tokens, hidden]),
     quantised per token on the way.  Returns (out, err word)."""
@@ -628,6 +669,7 @@ def _per_row(t, n: int, dtype, name: str):
     return _dev(t, name)
 
 
+@_on_its_stream
 def lhs_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None,
                ids=None, probs=None, want_probs: bool = True, err=None, stream=None):
     """One token per row of ``logits`` (f32, f16 or bf16 [rows, vocab]), drawn
@@ -651,6 +693,7 @@ def lhs_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=No
     return ids, (probs if want_probs else None), err
 
 
+@_on_its_stream
 def lhs_selftest_bounded_wait(timeout_ns: int, err=None, device=None, stream=None):
     """Run the never-satisfied bounded wait; returns the err word (TIMEOUT set)."""
     err = _err_word(err, device or torch.device("cuda"))
