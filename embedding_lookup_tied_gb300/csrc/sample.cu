@@ -987,6 +987,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             // The bins that may be the one in which the sum of weights reaches p of all.  A bin's
             // weights lie between 2^(S - (b + 1) / 16) and 2^(S - b / 16), the last one's anywhere
             // below that, the largest taken as 2^S: bounds for the sums up to each bin and for all.
+            // The largest is 2^(S - 1) units at least and each weight less than a unit below its
+            // value, hence two of these less for each entry (which is what counts in rows of 2^28
+            // and more, where small weights are a unit or two).
             constexpr int B = kBins / kThreads;
             static_assert(B * kThreads == kBins, "whole bins to a thread");
             uint64_t high[B], low[B], h0 = 0, l0 = 0, h_all, l_all;
@@ -996,7 +999,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 const uint64_t c = sm.sums[bin];
                 const float x = static_cast<float>(c) * exp2f(static_cast<float>(S) - bin / kBinsPerOctave);
                 high[b] = static_cast<uint64_t>(x * 1.0001f) + c;
-                low[b] = bin < kBins - 1 ? static_cast<uint64_t>(x * 0.9575f) : 0ull;  // 2^(-1/16) = 0.95760..
+                const uint64_t l = static_cast<uint64_t>(x * 0.9575f);  // 2^(-1/16) = 0.95760..
+                low[b] = bin < kBins - 1 && l > 2 * c ? l - 2 * c : 0ull;
                 h0 += high[b];
                 l0 += low[b];
             }
