@@ -10,7 +10,9 @@
 // weights in id order.  Weights are 2^S exp((logit - max) / T) as 64-bit
 // integers (see Weight), so every sum is exact, whatever the order in which
 // warps, CTAs and atomics form it, and two passes over a row agree to the last
-// bit.
+// bit.  A weight is cut to whole units, of which the largest has 2^(S-1) at least, so
+// a sum is up to its number of entries in units below its value (2^-43 of the
+// largest weight an entry for a vocabulary of 2^18).
 //
 // A cluster of CTAs owns a row and holds it in its shared memory: HBM is read
 // once (bulk copies), and every later pass is a lane's own 16-byte words from
@@ -77,7 +79,12 @@ __constant__ const uint64_t kPow16[16] = {
 // the middle factor from a table in 62 bits and 2^x = 1 + x ln2 + x^2 q(x)
 // from its Taylor series: x ln2 in two floats, the rest (below 2^-12) in one.
 // The factor's distance from 1 is below 2^-5.5 and is held as a 32-bit
-// integer in units of 2^-36.  Together about 2^-36 of the weight, unbiased.
+// integer in units of 2^-36.  Together about 2^-36 of the weight, unbiased; then
+// it is cut down to whole units, which is the larger error for weights below 2^-7
+// of the largest (up to 2^-20 of a weight of 2^-23, S = 44).  Rounding would add
+// a 64-bit addition and a shift to each weight, for sums that are already
+// finer than u, a binary32 number (262,144 logits of N(0, 5) at temperature 0.8:
+// running shares off by up to 2^-28).
 // Where c times the largest logit passes 2^10 the rounding of l c_lo would
 // show; there logits are first taken relative to the largest, and those that
 // weigh anything are so near to it that the difference is exact.
@@ -98,7 +105,8 @@ struct Weight {
         shift = 61 - S + (__float2int_rn(top * 16.0f) >> 4) + 1;
         pow16 = table;
     }
-    __device__ __forceinline__ uint64_t operator()(float logit) const {
+    // 2^cut times the weight, before it is cut to whole units.
+    __device__ __forceinline__ uint64_t whole(float logit, int &cut) const {
         const float l = __fsub_rn(logit, ref);
         const float p = __fmul_rn(l, c_hi);
         const float z = __fmaf_rn(l, c_lo, __fmaf_rn(l, c_hi, -p));
@@ -118,7 +126,13 @@ struct Weight {
         const uint64_t w =
             f + static_cast<uint64_t>((static_cast<int64_t>(static_cast<int>(f >> 32)) * delta) >> 4);
         // (below `low`, also at -inf, the rest may be anything, but w stays below 2^63)
-        return w >> (logit < low ? 63 : min(shift - (K >> 4), 63));
+        cut = logit < low ? 63 : min(shift - (K >> 4), 63);
+        return w;
+    }
+    __device__ __forceinline__ uint64_t operator()(float logit) const {
+        int cut;
+        const uint64_t w = whole(logit, cut);
+        return w >> cut;
     }
 };
 
@@ -575,7 +589,7 @@ struct RowView {
                     return taken != 0;
                 },
                 [&](uint64_t) { return m - 1; },
-                [&](int id, uint64_t, uint64_t) {
+                [&](int id, float, uint64_t) {
                     for (int r = 0; r < ranks; ++r) *cl.map_shared_rank(&sm.found, r) = id;
                 });
             cl.sync();
@@ -710,7 +724,7 @@ struct RowView {
     }
 
     // The first id at which the running sum of weights passes target(total):
-    // the one thread that finds it calls found(id, weight, total).
+    // the one thread that finds it calls found(id, logit, total).
     // value(values, id, weights): false where all of a word's weights are 0.
     template <typename F, typename G, typename H>
     __device__ __forceinline__ void locate(const F &value, const G &target, const H &found) {
@@ -758,16 +772,16 @@ struct RowView {
                 uint64_t all_i, run = before + cta_scan(sm, mine_i, all_i);
                 if (t >= run && t < run + mine_i) {
                     int at_id = -1;
-                    uint64_t at_w = 0;
+                    float at_logit = 0.0f;
 #pragma unroll
                     for (int e = 0; e < VE; ++e) {
                         run += x[e];
                         if (at_id < 0 && run > t) {
                             at_id = id + e;
-                            at_w = x[e];
+                            at_logit = v[e];
                         }
                     }
-                    found(at_id, at_w, total);
+                    found(at_id, at_logit, total);
                 }
                 before += all_i;
                 __syncthreads();
@@ -778,7 +792,7 @@ struct RowView {
 
 // A fraction 0 <= f < 1 in units of 2^-64 (exact above 2^-40).
 __device__ __forceinline__ uint64_t fraction64(float f) { return __float2ull_rz(f * 0x1p64f); }
-// a / b to about 2^-24 of itself, 0 < a <= b, in two floats a number.
+// a / b to about 2^-24 of itself, a, b > 0, in two floats a number.
 __device__ __forceinline__ float quotient(uint64_t a, uint64_t b) {
     const float ah = __ull2float_rn(a), bh = __ull2float_rn(b);
     const float al = __ll2float_rn(static_cast<int64_t>(a - __float2ull_rn(ah)));
@@ -786,6 +800,13 @@ __device__ __forceinline__ float quotient(uint64_t a, uint64_t b) {
     const float q = __fdiv_rn(ah, bh);
     const float rest = __fmaf_rn(-q, bh, ah) + __fmaf_rn(-q, bl, al);
     return q + __fdiv_rn(rest, bh);
+}
+// The drawn token's weight over the total of those that stayed.  Its weight is
+// taken before it is cut to whole units: an unlikely token has few of them.
+__device__ __forceinline__ float probability(const Weight &weight, float logit, uint64_t total) {
+    int cut;
+    const uint64_t w = weight.whole(logit, cut);
+    return quotient(w, total) * __uint_as_float(static_cast<uint32_t>(127 - cut) << 23);
 }
 // The least integer that is at least P 2^-64 of all (1 at least).
 __device__ __forceinline__ uint64_t share_of(uint64_t P, uint64_t all) {
@@ -801,12 +822,13 @@ __device__ __forceinline__ void finish_list(Shared &sm, const Weight &weight, in
     const int first = threadIdx.x * E, most = k < n ? k : n;
     sort_list(sm, n);
     uint64_t w[E], mine = 0, all;
+    uint64_t entry[E];
     uint32_t id_key[E];  // inverted ids, 0 for none
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const uint64_t key = first + e < most ? sm.list[first + e] : 0ull;
-        w[e] = key ? weight(key_value(key)) : 0ull;
-        id_key[e] = static_cast<uint32_t>(key);
+        entry[e] = first + e < most ? sm.list[first + e] : 0ull;
+        w[e] = entry[e] ? weight(key_value(entry[e])) : 0ull;
+        id_key[e] = static_cast<uint32_t>(entry[e]);
         mine += w[e];
     }
     uint64_t above = cta_scan(sm, mine, all);
@@ -841,7 +863,7 @@ __device__ __forceinline__ void finish_list(Shared &sm, const Weight &weight, in
     for (int e = 0; e < E; ++e)
         if (id_key[e]) {
             sm.mass[place[e]] = w[e];
-            sm.list[place[e]] = id_key[e];
+            sm.list[place[e]] = entry[e];
         }
     __syncthreads();
     mine = 0;
@@ -855,8 +877,9 @@ __device__ __forceinline__ void finish_list(Shared &sm, const Weight &weight, in
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         if (above <= t && t < above + w[e]) {
-            *id = key_id(sm.list[first + e]);
-            if (prob) *prob = quotient(w[e], all);
+            const uint64_t drawn = sm.list[first + e];
+            *id = key_id(drawn);
+            if (prob) *prob = probability(weight, key_value(drawn), all);
         }
         above += w[e];
     }
@@ -1033,9 +1056,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const float span = sm.scale.span;
         const uint64_t U = sm.scale.U;
         auto target = [&](uint64_t total) { return __umul64hi(U, total); };
-        auto drawn = [&](int id, uint64_t w, uint64_t total) {
+        auto drawn = [&](int id, float logit, uint64_t total) {
             p.ids[r] = id;
-            if (p.probs) p.probs[r] = quotient(w, total);
+            if (p.probs) p.probs[r] = probability(weight, logit, total);
         };
         if (edged) v.locate(Weigh<true, true, VE>{weight, edge, largest, span, floor_w}, target, drawn);
         else if (floor_w) v.locate(Weigh<false, true, VE>{weight, edge, largest, span, floor_w}, target, drawn);

@@ -421,18 +421,22 @@ LHS_API int lhs_i8_logits(const lhs_i8 *table, const void *d_x, int32_t x_dtype,
  *   running sum of the weights that stayed passes u[r] times their total.
  * A temperature of 0 takes the largest logit (the lowest id of equal ones);
  * others are clamped to [2^-100, 2^100].  A logit of -inf is a masked token
- * and is never drawn.  Weights are evaluated to about 2^-36 of themselves
- * and summed as integers, so the result does not depend on the order of the
- * sums; a weight below about 2^-43 of the row's largest (for a vocabulary of
- * 2^18; a bit more for each doubling beyond) counts as 0.
+ * and is never drawn.  Weights are evaluated to about 2^-36 of themselves,
+ * cut down to whole units of at most 2^-(S-1) of the row's largest, S =
+ * min(45, 62 - ceil(log2 vocab)) (2^-43 for a vocabulary of 2^18), and summed
+ * as integers, so the result does not depend on the order of the sums.  A
+ * weight below one unit counts as 0, and a sum lies up to one unit an entry
+ * below its value (all in all 2^-25 of the largest weight at most for 2^18
+ * entries; 2^-13 for 2^24): a border (of top-p, min-p or the draw) nearer to its
+ * value than that may fall on either side.
  *   d_logits : LHS_F32, LHS_F16 or LHS_BF16, row r at element r*stride
  *              (stride >= vocab), aligned to its element size
  *   d_u      : f32 [rows], each in [0, 1)
  *   d_temperature, d_top_p, d_min_p : f32 [rows]; d_top_k : int32 [rows];
  *              each may be NULL: temperature 1, the filter off
  *   d_ids    : int32 [rows]
- *   d_probs  : f32 [rows] or NULL: the weight of the drawn token over the
- *              total of those that stayed
+ *   d_probs  : f32 [rows] or NULL: the weight of the drawn token (not cut)
+ *              over the total of those that stayed
  * A row without a logit above -inf gives id -1 and probability 0.  A row
  * holding NaN or +inf does too and sets LHS_ERRBIT_NONFINITE; a row with
  * temperature not finite or < 0, top_p outside (0, 1], min_p outside

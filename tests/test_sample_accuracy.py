@@ -1,5 +1,5 @@
-"""Sampling where the weights' accuracy shows: rows so long that a unit of
-weight is no longer small.
+"""Sampling where the weights' accuracy shows: unlikely tokens, running sums,
+and rows so long that a unit of weight is no longer small.
 
 A row's weights are whole multiples of a unit that is at most 2^-(S-1) of the
 largest, S = min(45, 62 - ceil(log2 vocab)), each up to one unit below
@@ -13,6 +13,7 @@ import pytest
 import torch
 
 import embedding_lookup_tied_gb300 as lhs
+from test_sample import reference
 
 pytestmark = pytest.mark.gpu
 
@@ -20,6 +21,65 @@ pytestmark = pytest.mark.gpu
 def unit_of(v):
     """The unit, in terms of the largest weight (an upper bound)."""
     return 2.0 ** -(min(45, 62 - math.ceil(math.log2(v))) - 1)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("mode", ["none", "k", "p", "q"])
+@pytest.mark.parametrize("v", [7, 300, 5000, 300001])
+def test_probability_of_unlikely_tokens(v, mode, dtype):
+    # u = 0 draws the first id that stays: one that weighs e^-8 .. e^-24 of the largest.  What weighs
+    # anything is a few tokens, so the total is good to a few units of 2^-42, and the probability
+    # to its own rounding, 2^-24.
+    ls = [-8.3, -11.7, -15.1, -18.45, -21.9, -24.3]
+    if mode == "p":
+        ls = ls[:3]  # weights above the 2^-24 that top-p leaves out
+    x = torch.full((len(ls), v), -200.0)
+    x[:, v // 2] = 0.4
+    x[:, v - 1] = -0.3
+    x[:, v - 2] = -30.0
+    for r, l in enumerate(ls):
+        x[r, 0] = l
+    x = x.to(dtype)
+    n = len(ls)
+    u = torch.zeros(n)
+    t = torch.full((n,), 0.97)
+    k = torch.full((n,), 3, dtype=torch.int32) if mode == "k" else None
+    p = torch.full((n,), 1 - 2.0 ** -24) if mode == "p" else None
+    q = torch.full((n,), 2.0 ** -38) if mode == "q" else None
+    up = lambda a: None if a is None else a.cuda()  # noqa: E731
+    ids, probs, err = lhs.lhs_sample(x.cuda(), u.cuda(), up(t), up(k), up(p), up(q))
+    assert int(err.item()) == 0
+    for r in range(n):
+        tok, pr, near = reference(x[r].double().numpy(), 0.0, float(t[r]), 3 if mode == "k" else 0,
+                                  float(p[r]) if p is not None else 1.0, float(q[r]) if q is not None else 0.0)
+        assert not near and tok == 0
+        assert int(ids[r]) == tok
+        assert abs(float(probs[r]) - pr) <= 2.0 ** -23 * pr, (r, float(probs[r]), pr)
+
+
+@pytest.mark.parametrize("v", [5000, 100003, 262144])
+def test_running_sums_are_within_their_units(v):
+    # rows of many small weights: the drawn token's stretch of the running sum holds u, up to the
+    # units that the sums may be below their values
+    g = torch.Generator().manual_seed(v)
+    x = torch.randn((3, v), generator=g) * 5
+    t = 0.8
+    us = torch.cat([torch.rand(60, generator=g), torch.rand(60, generator=g) * 2.0 ** -12,
+                    1 - torch.rand(20, generator=g) * 2.0 ** -12]).clamp(max=1 - 2.0 ** -24)
+    for r in range(3):
+        w = np.exp((x[r].double().numpy() - float(x[r].max())) / float(np.float32(t)))
+        c = np.cumsum(w)
+        share, slack = c / c[-1], (v + 1) * unit_of(v) / c[-1] + 2.0 ** -35
+        n = len(us)
+        ids, probs, err = lhs.lhs_sample(x[r].expand(n, v).contiguous().cuda(), us.cuda(),
+                                         torch.full((n,), t, device="cuda"))
+        assert int(err.item()) == 0
+        ids = ids.cpu().numpy()
+        uu = us.double().numpy()
+        before = np.where(ids > 0, share[np.maximum(ids - 1, 0)], 0.0)
+        assert (before <= uu + slack).all() and (uu <= share[ids] + slack).all()
+        pr = w[ids] / c[-1]
+        assert (np.abs(probs.cpu().numpy() - pr) <= (2.0 ** -23 + slack) * pr).all()
 
 
 def test_top_p_of_half_a_billion_logits():
