@@ -59,7 +59,9 @@ constexpr int kBins = 512;                    // of 1/16 octave of weight; the l
 constexpr float kBinsPerOctave = 16.0f;
 constexpr int kParts = 256;                   // of a bin that holds too many entries
 constexpr int kMaxSmem = 224 * 1024;
-constexpr uint32_t kKeyInf = 0xFF800000u;     // order key of +inf; NaN lies above
+constexpr uint32_t kKeyInf = 0xFF800000u;     // order key of +inf; these lie above:
+constexpr uint32_t kKeyNan = 0xFFFFFFFEu;     // a NaN
+constexpr uint32_t kKeyLate = 0xFFFFFFFFu;    // a piece of the row that has not arrived in time
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // order key of -inf
 
 // round(2^61 * 2^(j/16))
@@ -379,14 +381,18 @@ struct RowView {
         return static_cast<int>(n < 0 ? 0 : n < steps * 32 ? n : steps * 32);
     }
     // The row's first reading, once its piece has arrived: elements that are not
-    // the row's become -inf; this lane's largest logit as an order key.
+    // the row's become -inf; this lane's largest logit as an order key (kKeyNan where
+    // one is NaN, kKeyLate where the piece has not arrived).
     __device__ __forceinline__ uint32_t read(uint32_t parity, int32_t *err) {
         const int lane = threadIdx.x & 31;
         float top = -INFINITY;
         uint32_t magnitude = 0;  // above the bits of inf: a NaN
         if (RESIDENT) {
             const int n = piece();
-            if (!mbar_wait(&sm.arrived[threadIdx.x >> 5], parity, kWaitTimeoutNs)) set_err(err, LHS_ERRBIT_TIMEOUT);
+            if (!mbar_wait(&sm.arrived[threadIdx.x >> 5], parity, kWaitTimeoutNs)) {
+                set_err(err, LHS_ERRBIT_TIMEOUT);
+                return kKeyLate;
+            }
             // of this lane's words, lane, lane + 32, ..
             for (int w = n + ((lane - n) & 31); w < steps * 32; w += 32) hold[w - lane] = outside();
             const int w0 = word0 - lane;
@@ -406,7 +412,7 @@ struct RowView {
                 magnitude = max(magnitude, __float_as_uint(v[e]) & 0x7FFFFFFFu);
             }
         }
-        return magnitude > 0x7F800000u ? 0xFFFFFFFFu : order_key32(top);
+        return magnitude > 0x7F800000u ? kKeyNan : order_key32(top);
     }
 
     // Every CTA's v, in this CTA's shared memory.
@@ -938,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             x.P = fraction64(top_p);
             x.M = fraction64(min_p);
         }
-        // the row's largest logit (as an order key: NaN lies above +inf)
+        // the row's largest logit (as an order key: NaN lies above +inf, a late piece above that)
         const uint32_t lane_top = v.read(parity, p.err);
         uint32_t top = __reduce_max_sync(0xFFFFFFFFu, lane_top);
         if (lane == 0) sm.warp_sum[warp] = top;
@@ -947,6 +953,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         for (int i = 0; i < kWarps; ++i) top = max(top, static_cast<uint32_t>(sm.warp_sum[i]));
         const uint64_t *tops = v.exchange(top);
         for (int i = 0; i < ranks; ++i) top = max(top, static_cast<uint32_t>(tops[i]));
+        if (top == kKeyLate) {
+            // the whole cluster gives up, after one more wait for its copies: no id for this row and
+            // those that it would have come to
+            if (RESIDENT) mbar_wait(&sm.arrived[warp], parity, kWaitTimeoutNs);
+            if (rank == 0 && tid == 0)
+                for (; r < p.rows; r += gridDim.x / ranks) {
+                    p.ids[r] = -1;
+                    if (p.probs) p.probs[r] = 0.0f;
+                }
+            break;
+        }
         if (bad_param || top >= kKeyInf || top <= kKeyNegInf) {
             if (rank == 0 && tid == 0) {
                 p.ids[r] = -1;

@@ -441,6 +441,8 @@ LHS_API int lhs_i8_logits(const lhs_i8 *table, const void *d_x, int32_t x_dtype,
  * holding NaN or +inf does too and sets LHS_ERRBIT_NONFINITE; a row with
  * temperature not finite or < 0, top_p outside (0, 1], min_p outside
  * [0, 1] or u outside [0, 1) does too and sets LHS_ERRBIT_BAD_PARAM.
+ * Where a row does not reach the SM within 2 s, it and the rows that would
+ * have followed it there do too and set LHS_ERRBIT_TIMEOUT.
  * rows == 0 enqueues nothing; 1 <= vocab <= 2^31-1.  No workspace.
  * Errors: LHS_ERR_INVALID_ARG, LHS_ERR_CUDA. */
 LHS_API int lhs_sample(const void *d_logits, int32_t dtype, int64_t stride, int64_t rows,
