@@ -300,8 +300,8 @@ struct One {
 };
 
 // One row, as one CTA of its cluster sees it.  The row's 16-byte words (as
-// addresses fall, so the first and last may be partly another row's: those
-// elements read as -inf) are dealt out to warps in contiguous pieces.
+// addresses fall, so the first and last may be partly another's: those elements
+// are not read and count as -inf) are dealt out to warps in contiguous pieces.
 template <int DT, bool RESIDENT>
 struct RowView {
     using E = Elem<DT>;
@@ -322,24 +322,29 @@ struct RowView {
     __device__ __forceinline__ uint4 fetch(int w) const {
         const int64_t first = static_cast<int64_t>(w) * VE - skip;  // id of the word's first element
         if (first >= vocab || first + VE <= 0) return outside();
-        const uint4 u = ld_dep(base + w);
-        return first < 0 || first + VE > vocab ? trim(u, w) : u;
+        return first < 0 || first + VE > vocab ? part(w) : ld_dep(base + w);
     }
-    __device__ __forceinline__ uint4 trim(const uint4 &u, int w) const {
-        const int64_t first = static_cast<int64_t>(w) * VE - skip;
-        const uint32_t in[4] = {u.x, u.y, u.z, u.w}, o = outside().x;
-        uint32_t r[4];
+    // A word that is partly the row's: its elements one by one, nothing else is read.
+    __device__ __forceinline__ uint4 part(int w) const {
+        const int64_t at = static_cast<int64_t>(w) * VE;
+        const T *x = reinterpret_cast<const T *>(base) + at;
+        uint32_t r[4] = {outside().x, outside().x, outside().x, outside().x};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (VE == 4) {
-                r[i] = first + i >= 0 && first + i < vocab ? in[i] : o;
+        for (int e = 0; e < VE; ++e) {
+            if (at + e < skip || at + e - skip >= vocab) continue;
+            if constexpr (VE == 4) {
+                r[e] = __float_as_uint(ld_dep(x + e));
             } else {
-                const bool lo = first + 2 * i >= 0 && first + 2 * i < vocab;
-                const bool hi = first + 2 * i + 1 >= 0 && first + 2 * i + 1 < vocab;
-                r[i] = (lo ? in[i] & 0xFFFFu : o & 0xFFFFu) | (hi ? in[i] & 0xFFFF0000u : o & 0xFFFF0000u);
+                const uint32_t v = ld_dep(x + e);
+                r[e >> 1] = e & 1 ? (r[e >> 1] & 0xFFFFu) | v << 16 : (r[e >> 1] & 0xFFFF0000u) | v;
             }
         }
         return make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    // Whether the row starts (ends) inside this warp's first (last) word, of n.
+    __device__ __forceinline__ bool starts_inside(int w0) const { return w0 == 0 && skip > 0; }
+    __device__ __forceinline__ bool ends_inside(int w0, int n) const {
+        return n > 0 && static_cast<int64_t>(w0 + n) * VE - skip > vocab;
     }
     static __device__ __forceinline__ uint4 outside() {  // -inf
         const uint32_t w = DT == LHS_F32 ? 0xFF800000u : DT == LHS_F16 ? 0xFC00FC00u : 0xFF80FF80u;
@@ -365,14 +370,25 @@ struct RowView {
             f(v, (word0 + s * 32) * VE - skip);
         }
     }
-    // Starts the copy of this warp's piece of the row (the words that lie in it).
+    // Starts the copy of this warp's piece of the row (the words that are wholly the row's).
     __device__ __forceinline__ void start() const {
         if (!RESIDENT || (threadIdx.x & 31)) return;
         const int n = piece();
         uint64_t *bar = &sm.arrived[threadIdx.x >> 5];
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the last row's reads
-        mbar_arrive_expect_tx(bar, n * 16);
-        if (n > 0) bulk_load(hold, base + word0, n * 16, bar);
+        const int from = starts_inside(word0) ? 1 : 0, whole = n - from - (ends_inside(word0, n) ? 1 : 0);
+        mbar_arrive_expect_tx(bar, whole > 0 ? whole * 16 : 0);
+        if (whole > 0) bulk_load(hold + from, base + word0 + from, whole * 16, bar);
+    }
+    // What the copy leaves out, while it is on its way: the row's ends, and -inf for
+    // words of the piece beyond them.
+    __device__ __forceinline__ void ends() const {
+        if (!RESIDENT) return;
+        const int lane = threadIdx.x & 31, n = piece(), w0 = word0 - lane;
+        if (lane == 0 && n > 0 && starts_inside(w0)) hold[0] = part(0);
+        if (lane == ((n - 1) & 31) && ends_inside(w0, n)) hold[n - 1 - lane] = part(w0 + n - 1);
+        // of this lane's words, lane, lane + 32, ..
+        for (int w = n + ((lane - n) & 31); w < steps * 32; w += 32) hold[w - lane] = outside();
     }
     // Words of the warp's piece that hold elements of the row.
     __device__ __forceinline__ int piece() const {
@@ -380,26 +396,15 @@ struct RowView {
         const int64_t n = words - (word0 - static_cast<int>(threadIdx.x & 31));
         return static_cast<int>(n < 0 ? 0 : n < steps * 32 ? n : steps * 32);
     }
-    // The row's first reading, once its piece has arrived: elements that are not
-    // the row's become -inf; this lane's largest logit as an order key (kKeyNan where
-    // one is NaN, kKeyLate where the piece has not arrived).
+    // The row's first reading, once its piece has arrived: this lane's largest logit as
+    // an order key (kKeyNan where one is NaN, kKeyLate where the piece has not arrived).
     __device__ __forceinline__ uint32_t read(uint32_t parity, int32_t *err) {
-        const int lane = threadIdx.x & 31;
         float top = -INFINITY;
         uint32_t magnitude = 0;  // above the bits of inf: a NaN
         if (RESIDENT) {
-            const int n = piece();
             if (!mbar_wait(&sm.arrived[threadIdx.x >> 5], parity, kWaitTimeoutNs)) {
                 set_err(err, LHS_ERRBIT_TIMEOUT);
                 return kKeyLate;
-            }
-            // of this lane's words, lane, lane + 32, ..
-            for (int w = n + ((lane - n) & 31); w < steps * 32; w += 32) hold[w - lane] = outside();
-            const int w0 = word0 - lane;
-            if (n > 0 && ((w0 == 0 && skip) || n < steps * 32 || static_cast<int64_t>(w0 + n) * VE - skip > vocab)) {
-                // the row's first and last words
-                if (lane == 0 && w0 == 0) hold[0] = trim(hold[0], 0);
-                if (lane == (n - 1) % 32) hold[n - 1 - lane] = trim(hold[n - 1 - lane], w0 + n - 1);
             }
         }
 #pragma unroll 4
@@ -924,6 +929,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const float top_p = p.top_p ? ld_dep(p.top_p + r) : 1.0f;
         const float min_p = p.min_p ? ld_dep(p.min_p + r) : 0.0f;
         int k = p.top_k ? ld_dep(p.top_k + r) : 0;
+        v.ends();
         const bool bad_param = !(T >= 0.0f && T <= 3.4028234663852886e38f) || !(top_p > 0.0f && top_p <= 1.0f) ||
                                !(min_p >= 0.0f && min_p <= 1.0f) || !(u >= 0.0f && u < 1.0f);
         if (T == 0.0f) {  // greedy
