@@ -576,9 +576,10 @@ def lhs_i8_init(codes: torch.Tensor, scales: torch.Tensor, hidden: int) -> I8Row
     rows = codes.shape[0]
     if scales.dim() != 1 or scales.shape[0] != rows:
         raise ValueError("one scale for each row")
+    # no second row: any distance will do, and a table's is a multiple of 16
+    stride = codes.stride(0) if rows > 1 else (codes.shape[1] + 15) // 16 * 16
     c = lhs_i8()
-    _check(lib().lhs_i8_init(ctypes.byref(c), codes.data_ptr(),
-                             codes.stride(0) if rows > 1 else codes.shape[1], scales.data_ptr(),
+    _check(lib().lhs_i8_init(ctypes.byref(c), codes.data_ptr(), stride, scales.data_ptr(),
                              4 * (scales.stride(0) if rows > 1 else 1), rows, hidden), "lhs_i8_init")
     return I8Rows(c, codes, scales)
 
