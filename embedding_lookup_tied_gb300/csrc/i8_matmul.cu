@@ -664,9 +664,13 @@ __global__ void __launch_bounds__(Tile<NMAX>::kThreads, 1)
                         tma_load_2d_pair(sm.token[s] + half * 128, &tm_token, bar, kc * kStageK + 64, row);
                     }
                 }
-                // the copies have landed and the last commits have arrived
+                // the copies have landed and the last commits have arrived; after an abort, when some
+                // never will, what is still under way has one more limit's time to land
                 for (int64_t i = j > SX ? j - SX : 0; i < j; ++i)
-                    if (!wait_or_abort(&sm.empty[i % SX], (i / SX) & 1, &sm.abort_flag, p.err)) break;
+                    if (!mbar_wait(&sm.empty[i % SX], (i / SX) & 1, kWaitTimeoutNs)) {
+                        if (!*reinterpret_cast<volatile int *>(&sm.abort_flag)) set_err(p.err, LHS_ERRBIT_TIMEOUT);
+                        break;
+                    }
             }
         } else if (warp == kConvWarps + 2) {
             // ---------------- MMA issuer (the leader CTA only) ----------------
