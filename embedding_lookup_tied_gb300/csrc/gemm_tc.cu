@@ -448,9 +448,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 issue(it, true, true);
             }
             // drain: the pair has consumed every issued stage, so no copy,
-            // completion or commit is still headed for either CTA
+            // completion or commit is still headed for either CTA (after an
+            // abort, when some never come, one more limit's time to land)
             for (uint32_t j = (it > static_cast<uint32_t>(S) ? it - S : 0); j < it; ++j)
-                if (!wait_or_abort(&sm.empty[j % S], (j / S) & 1, &sm.abort_flag, p.err)) break;
+                if (!mbar_wait(&sm.empty[j % S], (j / S) & 1, kWaitTimeoutNs)) {
+                    if (!ld_vol(&sm.abort_flag)) set_err(p.err, LHS_ERRBIT_TIMEOUT);
+                    break;
+                }
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer (the leader CTA only) ----------------
