@@ -385,10 +385,20 @@ struct RowView {
     __device__ __forceinline__ void ends() const {
         if (!RESIDENT) return;
         const int lane = threadIdx.x & 31, n = piece(), w0 = word0 - lane;
-        if (lane == 0 && n > 0 && starts_inside(w0)) hold[0] = part(0);
-        if (lane == ((n - 1) & 31) && ends_inside(w0, n)) hold[n - 1 - lane] = part(w0 + n - 1);
+        // an element to a lane: the first VE have the piece's first word, the next its last
+        const bool first = lane < VE, cut = first ? starts_inside(w0) : ends_inside(w0, n);
+        if (n > 0 && lane < 2 * VE && cut) {
+            const int w = first ? 0 : n - 1, e = lane % VE;
+            const int64_t at = static_cast<int64_t>(w0 + w) * VE + e;
+            T x;
+            if constexpr (DT == LHS_F32) x = -INFINITY;
+            else x = static_cast<T>(outside().x);
+            if (at >= skip && at - skip < vocab) x = ld_dep(reinterpret_cast<const T *>(base) + at);
+            reinterpret_cast<T *>(hold - lane + w)[e] = x;
+        }
         // of this lane's words, lane, lane + 32, ..
         for (int w = n + ((lane - n) & 31); w < steps * 32; w += 32) hold[w - lane] = outside();
+        __syncwarp();
     }
     // Words of the warp's piece that hold elements of the row.
     __device__ __forceinline__ int piece() const {
