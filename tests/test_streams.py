@@ -113,6 +113,19 @@ def test_a_stream_may_be_given_by_position(data):
     assert all(equal(a, b) for a, b in zip(got, want))
 
 
+def test_default_stream_from_another(data):
+    # the default stream's handle is 0
+    want = [t.clone() for t in parts(data["i8_logits_bad"]())]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for st in (0, torch.cuda.default_stream()):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+            got = parts(data["i8_logits_bad"](stream=st))
+        torch.cuda.synchronize()
+        assert all(equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("name", ["lhs_i8_logits", "lhs_i8_matmul", "lhs_logits_topk", "lhs_embed_dedup"])
 def test_workspace_is_not_handed_out_again(name, monkeypatch):
     # the call's own workspace may be in use on its stream after the call has returned: an
