@@ -1,5 +1,6 @@
 // decode.cuh — launcher prototypes of the 8-bit lm_head product and of token
-// sampling (i8_rows.cu, i8_matmul.cu, sample.cu; checked in decode_abi.cu).
+// sampling (i8_rows.cu, i8_gemv.cu, i8_matmul.cu, sample.cu; checked in
+// decode_abi.cu).
 #pragma once
 
 #include "lhs_internal.cuh"

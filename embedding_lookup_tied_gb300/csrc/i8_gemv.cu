@@ -47,7 +47,7 @@ constexpr int kThreads = kConsumers + 32;  // + producer
 constexpr int kUnitRows = 16;
 constexpr int kUnitBytes = kUnitRows * kStageK;
 constexpr int kMaxStages = 12;            // of both groups' rings
-constexpr int kTokenBytes = 98 * 1024;     // tokens' codes at most, beside seven stages
+constexpr int kTokenBytes = 98 * 1024;     // tokens' codes at most, beside six stages
 constexpr int kSmemBytes = 224 * 1024;
 
 __host__ __device__ constexpr int round_up(int v, int a) { return (v + a - 1) / a * a; }

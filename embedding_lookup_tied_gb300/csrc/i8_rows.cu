@@ -3,13 +3,19 @@
 // Evolution", Wire Layout): scale = f32(max|x| / 127), code = clamp(rne(f32(x
 // / scale)), -127, 127).
 //
-// Bound by HBM: a value is read once (2 or 4 bytes) and its code written (1).
-// A row belongs to a warp (up to 1,024 values) or to a CTA of eight, whose lanes
-// take four values at a time and keep them in registers between the maximum
-// and the codes: up to eight fours a lane; what is beyond, in rows of more than
-// 8,192 values, is read again from L2.  151,936 x 896: 133 us from f32 (76% of
-// the HBM rate), 125 us from bf16 (48%, issue-bound by the exact quotients);
-// 262,144 x 5,376 from f16 1.53 ms (41%).
+// A value is read once (2 or 4 bytes) and its code written (1), so HBM is the
+// floor.  A row belongs to a warp (up to 1,024 values) or to a CTA of eight, whose
+// lanes take four values at a time and keep them in registers between the
+// maximum and the codes: up to eight fours a lane; what is beyond, in rows of more
+// than 8,192 values, is read again from L2.
+//
+// What bounds it: issue slots.  151,936 x 896, a warp to a row: 133 us from f32
+// (76% of the HBM rate) and 128 us from bf16 (48%), where 28.6 instructions a value
+// take 79% of the slots (about 11 of them the quotient, the tests for its borders
+// and the packing; the rest is widening, the maximum, predicates and the loop in
+// fours).  A CTA to a row adds two barriers without a load under way: 262,144 x
+// 5,376 from f16 1.53 ms (41%), 65,536 x 5,376 from f32 445 us, for which the wire
+// format's bulk encoder, the same rule in eights out of a ring of rows, takes 285.
 #include "i8_common.cuh"
 
 namespace lhs {

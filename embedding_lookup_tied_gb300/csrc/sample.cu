@@ -16,8 +16,8 @@
 //
 // A cluster of CTAs owns a row and holds it in its shared memory: HBM is read
 // once (bulk copies), and every later pass is a lane's own 16-byte words from
-// shared memory.  Rows too long for 16 CTAs (815,000 f32 logits) are read from
-// L2 in every pass.
+// shared memory.  Rows too long for 16 CTAs (more than 52 words a thread, 851,968
+// f32 logits) are read from L2 or HBM in every pass.
 //  * top-k: at least k entries lie in or above the bin that holds the k-th
 //    largest of the threads' maxima, and few more do, so that bound gathers a
 //    short list; one CTA sorts it and does the rest (k, p, min-p, the draw).
@@ -32,11 +32,12 @@
 //
 // What bounds it: latency.  A row of 1 MB is 0.15 us of HBM time, but 8 to 14
 // exchanges across the cluster of about 0.7 us each, and passes of 1 to 7 us
-// over 64 logits a lane (ncu, 256 rows of 262,144 f32 with mixed filters: 31% of
+// over 64 logits a lane (ncu, 256 rows of 262,144 f32 with mixed filters: 29% of
 // issue slots, 3.2 of 4 warps a scheduler active, a third of the stalls at
 // barriers).  Measured: 1 x 151,936 f32 with all filters 10.6 us; 8 x 262,144 f32
-// with top-p 53 us; 256 x 262,144 f32 392 us mixed, 165 us min-p, 248 us with the
-// temperature alone, 278 us top-k, 890 us top-p.  Tried and slower: CTAs of 512
+// with top-p 53 us; 256 x 262,144 f32 393 us mixed, 171 us min-p, 249 us with the
+// temperature alone, 279 us top-k, 895 us top-p; a row that is not resident, 1 x
+// 1,200,000 f32, 61 us with the temperature alone, 44 us top-k, 214 us top-p.  Tried and slower: CTAs of 512
 // threads (426 -> 453 us mixed), two words side by side (441 -> 455 us), clusters
 // of at most 8 (441 -> 499 us).
 #include <cooperative_groups.h>
