@@ -47,6 +47,8 @@ ABI_SYMBOLS = (
     "lhs_wire_decode", "lhs_wire_response_bytes", "lhs_wire_encode_response", "lhs_wire_decode_response",
     "lhs_i8_init", "lhs_i8_message", "lhs_i8_quantize", "lhs_i8_workspace", "lhs_i8_matmul", "lhs_i8_logits",
     "lhs_sample",
+    "lhs_loss_workspace", "lhs_loss", "lhs_loss_grad_workspace", "lhs_loss_grad", "lhs_embed_grad_workspace",
+    "lhs_embed_grad",
     "lhs_selftest_bounded_wait", "lhs_strerror",
     "lhs_last_cuda_error", "lhs_version",
 )
@@ -123,6 +125,14 @@ def lib() -> ctypes.CDLL:
         "lhs_i8_matmul": (ctypes.c_int, [Q, Q, P, i32, i64, P, sz, P, P]),
         "lhs_i8_logits": (ctypes.c_int, [Q, P, i32, i64, i64, P, i32, i64, P, sz, P, P]),
         "lhs_sample": (ctypes.c_int, [P, i32, i64, i64, i64, P, P, P, P, P, P, P, P, P]),
+        "lhs_loss_workspace": (ctypes.c_int, [T, i64, P]),
+        "lhs_loss": (ctypes.c_int, [T, P, i32, i64, i64, P, i32, ctypes.c_float, P, P, P, sz, P, P]),
+        "lhs_loss_grad_workspace": (ctypes.c_int, [T, i64, P]),
+        "lhs_loss_grad": (ctypes.c_int, [T, P, i32, i64, i64, P, i32, ctypes.c_float, P, P, P, i32, i64, P, i32,
+                                         i32, P, sz, P, P]),
+        "lhs_embed_grad_workspace": (i64, [i64, i32, i64]),
+        "lhs_embed_grad": (ctypes.c_int, [i64, i32, P, i64, i32, ctypes.c_float, P, i32, i64, P, i32, i32, P, sz,
+                                          P, P]),
         "lhs_selftest_bounded_wait": (ctypes.c_int, [P, i64, P]),
         "lhs_strerror": (ctypes.c_char_p, [ctypes.c_int]),
         "lhs_last_cuda_error": (ctypes.c_int, []),
@@ -692,6 +702,145 @@ def lhs_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=No
                             _per_row(probs, n, f, "probs") if want_probs else None, _dev(err, "err"),
                             _stream(stream)), "lhs_sample")
     return ids, (probs if want_probs else None), err
+
+
+IGNORE = -100  # the id or target that takes no part, by default
+
+
+def _one_device(device, **tensors):
+    """Tensors of one call lie on one device, and that is the current one (the
+    stream and the workspace belong to it)."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+
+
+def _loss_args(table: Table, x: torch.Tensor, targets: torch.Tensor):
+    xp, xdt, stride = _wide_rows(x, "x")
+    if x.shape[1] != table.hidden:
+        raise ValueError("x and the table differ in hidden")
+    if xdt != table.dtype:
+        raise ValueError("x must be of the table's type")
+    return xp, xdt, stride, x.shape[0], _per_row(targets, x.shape[0], torch.int32, "targets")
+
+
+def _workspace(fn, table: Table, tokens: int) -> int:
+    b = ctypes.c_size_t()
+    _check(getattr(lib(), fn)(ctypes.byref(table.c), tokens, ctypes.byref(b)), fn)
+    return b.value
+
+
+def lhs_loss_workspace(table: Table, tokens: int) -> int:
+    return _workspace("lhs_loss_workspace", table, tokens)
+
+
+def lhs_loss_grad_workspace(table: Table, tokens: int) -> int:
+    return _workspace("lhs_loss_grad_workspace", table, tokens)
+
+
+@_on_its_stream
+def lhs_loss(table: Table, x: torch.Tensor, targets: torch.Tensor, ignore: int = IGNORE, temperature: float = 1.0,
+             loss=None, lse=None, ws=None, err=None, stream=None):
+    """Cross entropy (f32 [tokens]) of ``targets`` (int32 [tokens]) under the
+    softmax over the whole vocabulary of residuals ``x`` ([tokens, hidden] of
+    the table's type, f16 or bf16), and the logarithm of its normaliser; 0 where
+    the target is ``ignore``.  Returns (loss, lse, err word)."""
+    xp, xdt, stride, n, tp = _loss_args(table, x, targets)
+    dev = x.device
+    loss = torch.empty(n, dtype=torch.float32, device=dev) if loss is None else loss
+    lse = torch.empty(n, dtype=torch.float32, device=dev) if lse is None else lse
+    if ws is None:
+        ws = torch.empty(lhs_loss_workspace(table, n), dtype=torch.uint8, device=dev)
+    err = _err_word(err, dev)
+    _one_device(dev, table=table, targets=targets, loss=loss, lse=lse, ws=ws, err=err)
+    f = torch.float32
+    _check(lib().lhs_loss(ctypes.byref(table.c), xp, xdt, stride, n, tp, ignore, float(temperature),
+                          _per_row(loss, n, f, "loss"), _per_row(lse, n, f, "lse"), _dev(ws, "ws"),
+                          ws.numel() * ws.element_size(), _dev(err, "err"), _stream(stream)), "lhs_loss")
+    return loss, lse, err
+
+
+def _table_grad(dtable, vocab: int, hidden: int, dtype, device, accumulate: bool):
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dtable")
+        dtable = torch.empty((vocab, hidden), dtype=dtype, device=device)
+    elif tuple(dtable.shape) != (vocab, hidden):
+        raise ValueError("dtable must be [vocab, hidden]")
+    elif dtype is not None and dtable.dtype != dtype:
+        raise ValueError("dtable is not of the type asked for")
+    if dtable.dtype not in _WIDE:
+        raise ValueError("dtable must be float32, float16 or bfloat16")
+    return dtable
+
+
+@_on_its_stream
+def lhs_loss_grad(table: Table, x: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, dloss: torch.Tensor,
+                  ignore: int = IGNORE, temperature: float = 1.0, dx=None, dtable=None, want_dx: bool = True,
+                  want_dtable: bool = True, accumulate: bool = False, ws=None, err=None, stream=None):
+    """Gradients of ``sum(dloss * loss)`` for the residuals ([tokens, hidden])
+    and for the table ([vocab, hidden]), given :func:`lhs_loss`'s ``lse``.
+    ``dx`` and ``dtable`` are of the table's type, or f32 where such a tensor is
+    given; ``accumulate`` adds to ``dtable``.  Returns (dx|None, dtable|None, err
+    word)."""
+    xp, xdt, stride, n, tp = _loss_args(table, x, targets)
+    dev, f = x.device, torch.float32
+    if want_dx:
+        dx = torch.empty((n, table.hidden), dtype=x.dtype, device=dev) if dx is None else dx
+        if tuple(dx.shape) != (n, table.hidden):
+            raise ValueError("dx must be [tokens, hidden]")
+        dxp, dxdt, dxs = _wide_rows(dx, "dx")
+    else:
+        dx, dxp, dxdt, dxs = None, None, xdt, table.hidden
+    dtp, dtdt = None, xdt
+    if want_dtable:
+        dtable = _table_grad(dtable, table.vocab, table.hidden, x.dtype if dtable is None else None, dev, accumulate)
+        dtp, dtdt = _dev(dtable, "dtable"), _WIDE[dtable.dtype]
+    else:
+        dtable = None
+    if ws is None:
+        ws = torch.empty(lhs_loss_grad_workspace(table, n), dtype=torch.uint8, device=dev)
+    err = _err_word(err, dev)
+    _one_device(dev, table=table, targets=targets, lse=lse, dloss=dloss, dx=dx, dtable=dtable, ws=ws, err=err)
+    _check(lib().lhs_loss_grad(ctypes.byref(table.c), xp, xdt, stride, n, tp, ignore, float(temperature),
+                               _per_row(lse, n, f, "lse"), _per_row(dloss, n, f, "dloss"), dxp, dxdt, dxs,
+                               dtp, dtdt, int(accumulate), _dev(ws, "ws"), ws.numel() * ws.element_size(),
+                               _dev(err, "err"), _stream(stream)), "lhs_loss_grad")
+    return dx, dtable, err
+
+
+def lhs_embed_grad_workspace(vocab: int, hidden: int, n: int) -> int:
+    b = int(lib().lhs_embed_grad_workspace(vocab, hidden, n))
+    if b < 0:
+        raise ValueError("vocab, hidden or the number of ids is out of range")
+    return b
+
+
+@_on_its_stream
+def lhs_embed_grad(ids: torch.Tensor, dout: torch.Tensor, vocab: int, scale: float, dtype=None, dtable=None,
+                   accumulate: bool = False, ignore: int = IGNORE, ws=None, err=None, stream=None):
+    """Gradient of :func:`lhs_embed` for its table: rows of ``dout`` ([n,
+    hidden] f32, f16 or bf16) added up by ``ids`` (int32 [n]) into [vocab,
+    hidden], scaled by ``scale``; of ``dtype`` (float32 by default, float16 or
+    bfloat16), or added to ``dtable`` with ``accumulate``.  Ids equal to
+    ``ignore`` take no part.  Returns (dtable, err word)."""
+    dp, ddt, stride = _wide_rows(dout, "dout")
+    n, h = dout.shape
+    dev = dout.device
+    ip = _per_row(ids, n, torch.int32, "ids")
+    if dtable is None and dtype is None:
+        dtype = torch.float32
+    dtable = _table_grad(dtable, vocab, h, dtype, dev, accumulate)
+    if ws is None:
+        ws = torch.empty(max(256, lhs_embed_grad_workspace(vocab, h, n)), dtype=torch.uint8, device=dev)
+    err = _err_word(err, dev)
+    _one_device(dev, ids=ids, dtable=dtable, ws=ws, err=err)
+    _check(lib().lhs_embed_grad(vocab, h, ip, n, ignore, float(scale), dp, ddt, stride, _dev(dtable, "dtable"),
+                                _WIDE[dtable.dtype], int(accumulate), _dev(ws, "ws"), ws.numel() * ws.element_size(),
+                                _dev(err, "err"), _stream(stream)), "lhs_embed_grad")
+    return dtable, err
 
 
 @_on_its_stream

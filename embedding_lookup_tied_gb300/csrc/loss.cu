@@ -1,0 +1,364 @@
+// loss.cu — softmax cross entropy over the tied table, and its gradient: what
+// stands before and after the products (loss_gemm.cu).
+//
+// ADR-0008 "Remote Embeddings and lm_head Service", POST /v1/logits, gives the
+// softmax over the whole vocabulary for the largest logits; here it is asked
+// for given tokens, and differentiated.
+//
+// The first kernel of a call numbers the positions that take part and copies
+// their residuals, packed, into the workspace.  Positions without a target
+// (prompts, padding) then cost nothing, whatever their residuals hold reaches
+// nothing (0 * NaN would, in the sums over positions of the table's gradient),
+// and rows of any stride and length become rows that TMA takes.
+#include "train.cuh"
+
+namespace lhs {
+namespace {
+
+constexpr int kPackThreads = 256;
+constexpr int kPackWarps = kPackThreads / 32;
+constexpr float kLog2e = 1.4426950408889634f;
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct PackParams {
+    const uint16_t *x;
+    int64_t x_stride, T;
+    bool vec;                // rows of x start on 16-byte boundaries
+    int32_t H, Hp, ignore;
+    int64_t V;
+    const int32_t *targets;
+    float *loss, *lse;       // loss: zeroed where a position takes no part
+    const float *lse_in, *dloss;
+    float inv_temperature;
+    bool f16;
+    LossMeta *meta;
+    int32_t *act, *tgt, *pos;
+    float *lse2, *gs;
+    uint16_t *xc;
+    int32_t *err;
+};
+
+__device__ __forceinline__ bool takes_part(const PackParams &p, int32_t y) {
+    return y >= 0 && static_cast<int64_t>(y) < p.V && y != p.ignore;
+}
+
+// Exclusive prefix of `flag` over the CTA's threads, and the total.
+__device__ __forceinline__ int block_rank(bool flag, int &total, int *warp_n) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, flag);
+    if (lane == 0) warp_n[warp] = __popc(m);
+    __syncthreads();
+    int before = 0;
+    total = 0;
+    for (int w = 0; w < kPackWarps; ++w) {
+        if (w < warp) before += warp_n[w];
+        total += warp_n[w];
+    }
+    __syncthreads();
+    return before + __popc(m & ((1u << lane) - 1u));
+}
+
+// Copies one residual (or zeros, src null) into a compact row.  Warp-collective.
+__device__ __forceinline__ void pack_row(const uint16_t *src, uint16_t *dst, int H, int Hp, bool vec, int lane) {
+    uint4 *d4 = reinterpret_cast<uint4 *>(dst);
+    for (int j = lane; j < Hp / 8; j += 32) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (src) {
+            if (vec && 8 * j + 8 <= H) {
+                w = ld_dep(reinterpret_cast<const uint4 *>(src) + j);
+            } else {
+                uint32_t u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = 8 * j + i < H ? ld_dep(src + 8 * j + i) : 0u;
+                w = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+            }
+        }
+        d4[j] = w;
+    }
+}
+
+// Each CTA takes an equal range of positions.  It counts the ones before it
+// (and all of them) itself: reading every target in every CTA is less than a
+// launch that would count first (8,192 targets: 32 KB from L2).
+template <bool GRAD>
+__global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParams p) {
+    __shared__ int warp_n[kPackWarps];
+    __shared__ int sum_before, sum_all;
+    __shared__ int rank_of[kPackThreads];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t per = (p.T + gridDim.x - 1) / gridDim.x;
+    const int64_t r0 = per * blockIdx.x < p.T ? per * blockIdx.x : p.T;
+    const int64_t r1 = r0 + per < p.T ? r0 + per : p.T;
+    if (tid == 0) sum_before = sum_all = 0;
+    pdl_wait();
+    pdl_trigger();  // after the wait, so that whoever follows has everything earlier behind it
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int64_t i = tid; i < p.T; i += kPackThreads) {
+        const int on = takes_part(p, ld_dep(p.targets + i)) ? 1 : 0;
+        all += on;
+        before += i < r0 ? on : 0;
+    }
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    all = __reduce_add_sync(0xFFFFFFFFu, all);
+    if (lane == 0) {
+        atomicAdd(&sum_before, before);
+        atomicAdd(&sum_all, all);
+    }
+    __syncthreads();
+    const int count = sum_all;
+    int base = sum_before;
+    bool bad = false, nonfinite = false;
+    for (int64_t b = r0; b < r1; b += kPackThreads) {
+        const int64_t r = b + tid;
+        const int32_t y = r < r1 ? ld_dep(p.targets + r) : p.ignore;
+        const bool on = r < r1 && takes_part(p, y);
+        if (r < r1 && !on && y != p.ignore) bad = true;
+        int total;
+        const int c = base + block_rank(on, total, warp_n);
+        rank_of[tid] = on ? c : -1;
+        if (on) {
+            p.act[c] = static_cast<int32_t>(r);
+            p.tgt[c] = y;
+        }
+        if (r < r1) {
+            if (GRAD) {
+                p.pos[r] = on ? c : -1;
+                if (on) {
+                    const float l = ld_dep(p.lse_in + r), d = ld_dep(p.dloss + r);
+                    if (!isfinite(l) || !isfinite(d)) nonfinite = true;
+                    p.lse2[c] = l * kLog2e;
+                    p.gs[c] = d * p.inv_temperature;
+                }
+            } else if (!on) {
+                p.loss[r] = 0.0f;
+                p.lse[r] = 0.0f;
+            }
+        }
+        __syncthreads();
+        const int n = static_cast<int>(r1 - b < kPackThreads ? r1 - b : kPackThreads);
+        for (int i = warp; i < n; i += kPackWarps) {
+            const int k = rank_of[i];
+            if (k >= 0) pack_row(p.x + (b + i) * p.x_stride, p.xc + static_cast<int64_t>(k) * p.Hp, p.H, p.Hp, p.vec, lane);
+        }
+        __syncthreads();
+        base += total;
+    }
+    // rows past the last one, to the end of its tile: zeros, no target, no gradient
+    const int64_t end = count > 0 ? (static_cast<int64_t>(count) + kLossTile - 1) / kLossTile * kLossTile : kLossTile;
+    for (int64_t r = count + blockIdx.x * kPackWarps + warp; r < end; r += static_cast<int64_t>(gridDim.x) * kPackWarps) {
+        pack_row(nullptr, p.xc + r * p.Hp, p.H, p.Hp, p.vec, lane);
+        if (lane == 0) {
+            p.act[r] = -1;
+            p.tgt[r] = -1;
+            if (GRAD) {
+                p.lse2[r] = INFINITY;
+                p.gs[r] = 0.0f;
+            }
+        }
+    }
+    if (bad) set_err(p.err, LHS_ERRBIT_BAD_TOKEN);
+    if (nonfinite) set_err(p.err, LHS_ERRBIT_NONFINITE);
+    if (blockIdx.x == 0) {
+        // The power of two that brings the largest |g| into (1/4, 1] (bf16: its range needs no
+        // more, and larger terms could overflow sums that fit) or up to 2^15 (f16: what lies
+        // 2^-29 below it is still normal, 2^-39 below it the last subnormal).
+        float top = 0.0f;
+        if (GRAD) {
+            for (int64_t i = tid; i < p.T; i += kPackThreads)
+                if (takes_part(p, ld_dep(p.targets + i))) {
+                    const float d = fabsf(ld_dep(p.dloss + i) * p.inv_temperature);
+                    if (isfinite(d)) top = fmaxf(top, d);
+                }
+            __shared__ float warp_top[kPackWarps];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            if (lane == 0) warp_top[warp] = top;
+            __syncthreads();
+            for (int w = 0; w < kPackWarps; ++w) top = fmaxf(top, warp_top[w]);
+        }
+        if (tid == 0) {
+            int e = top > 0.0f ? ilogbf(top) + 1 : 0;  // top < 2^e
+            e = e < -100 ? -100 : e > 100 ? 100 : e;
+            e -= p.f16 ? 15 : 0;
+            p.meta->count = count;
+            p.meta->scale = exp2f(static_cast<float>(-e));
+            p.meta->unscale = exp2f(static_cast<float>(e));
+        }
+    }
+}
+
+// Joins a token's tiles: 32 tokens to a CTA, whose warps share the tiles.  The
+// maximum is exact, and the sums of the warps are joined in their order.
+constexpr int kMergeWarps = 32;
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    loss_merge_kernel(const LossMeta *meta, const int32_t *act, const float2 *stats, const float *zt, int64_t vt,
+                      int64_t Tpad, float inv_temperature, float *loss, float *lse, int32_t *err) {
+    __shared__ float2 part[kMergeWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    const int count = ld_dep(&meta->count);
+    if (static_cast<int64_t>(blockIdx.x) * 32 >= count) return;
+    const float l2 = kLog2e * inv_temperature;
+    float m = -INFINITY, s = 0.0f;
+    auto join = [&](float om, float os) {
+        const float n = fmaxf(m, om);
+        // an empty side adds nothing; a sum that is NaN stays NaN
+        const float a = m == -INFINITY ? s : s * exp2f((m - n) * l2);
+        const float b = om == -INFINITY ? os : os * exp2f((om - n) * l2);
+        s = a + b;
+        m = n;
+    };
+    if (i < count)
+#pragma unroll 4
+        for (int64_t v = warp; v < vt; v += kMergeWarps) {
+            const float2 t = ld_dep(stats + v * Tpad + i);
+            join(t.x, t.y);
+        }
+    part[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    if (warp == 0 && i < count) {
+        for (int w = 1; w < kMergeWarps; ++w) join(part[w][lane].x, part[w][lane].y);
+        const float ls = logf(s);
+        float l = m * inv_temperature + ls;
+        float c = (m - ld_dep(zt + i)) * inv_temperature + ls;
+        if (!isfinite(l)) {
+            l = c = __int_as_float(0x7FC00000);
+            set_err(err, LHS_ERRBIT_NONFINITE);
+        }
+        const int32_t r = ld_dep(act + i);
+        loss[r] = c;
+        lse[r] = l;
+    }
+}
+
+// dx of every position: its compact row of sums times the inverse of g's scale,
+// or zeros.  A warp to a position.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    loss_dx_kernel(const LossMeta *meta, const int32_t *pos, const float *part, int64_t n, int32_t H, T *dx,
+                   int64_t dx_stride) {
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    const float u = ld_dep(&meta->unscale);
+    for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < n;
+         r += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5) {
+        const int32_t c = ld_dep(pos + r);
+        const float *src = part + static_cast<int64_t>(c) * H;
+        T *d = dx + r * dx_stride;
+        for (int j = lane; j < H; j += 32) put_rn(d + j, c < 0 ? 0.0f : ld_dep(src + j) * u);
+    }
+}
+
+cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &dev, cudaStream_t stream) {
+    PackParams k = {};
+    k.x = static_cast<const uint16_t *>(a.x);
+    k.x_stride = a.x_stride;
+    k.T = p.T;
+    k.vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_stride % 8 == 0;
+    k.H = p.H;
+    k.Hp = p.Hp;
+    k.ignore = a.ignore;
+    k.V = p.V;
+    k.targets = a.targets;
+    k.loss = a.loss;
+    k.lse = a.lse;
+    k.lse_in = a.lse_in;
+    k.dloss = a.dloss;
+    k.inv_temperature = a.inv_temperature;
+    k.f16 = !p.bf16;
+    k.meta = reinterpret_cast<LossMeta *>(a.ws + p.off_meta);
+    k.act = reinterpret_cast<int32_t *>(a.ws + p.off_act);
+    k.tgt = reinterpret_cast<int32_t *>(a.ws + p.off_tgt);
+    k.pos = reinterpret_cast<int32_t *>(a.ws + p.off_pos);
+    k.lse2 = reinterpret_cast<float *>(a.ws + p.off_lse2);
+    k.gs = reinterpret_cast<float *>(a.ws + p.off_gs);
+    k.xc = reinterpret_cast<uint16_t *>(a.ws + p.off_x);
+    k.err = a.err;
+    const int64_t want = (p.T + kPackWarps - 1) / kPackWarps;
+    const unsigned grid = static_cast<unsigned>(want < 4 * dev.num_sms ? want : 4 * dev.num_sms);
+    return launch_pdl(p.grad ? loss_pack_kernel<true> : loss_pack_kernel<false>, dim3(grid), dim3(kPackThreads), 0,
+                      stream, k);
+}
+
+}  // namespace
+
+LossPlan plan_loss(const lhs_table &t, int64_t tokens, bool grad) {
+    LossPlan p = {};
+    p.T = tokens;
+    p.Tpad = tokens > 0 ? round_up(tokens, kLossTile) : kLossTile;
+    p.V = t.vocab;
+    p.vt = (t.vocab + kLossTile - 1) / kLossTile;
+    p.H = t.hidden;
+    p.Hp = static_cast<int32_t>(round_up(t.hidden, 8));
+    p.bf16 = t.dtype == LHS_BF16;
+    p.grad = grad;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += align256(bytes);
+        return o;
+    };
+    p.off_meta = take(sizeof(LossMeta));
+    p.off_act = take(p.Tpad * 4);
+    p.off_tgt = take(p.Tpad * 4);
+    p.off_x = take(p.Tpad * p.Hp * 2);
+    if (!grad) {
+        p.off_stats = take(p.vt * p.Tpad * 8);
+        p.off_zt = take(p.Tpad * 4);
+    } else {
+        p.piece = round_up(p.V < 8192 ? p.V : 8192, kLossTile);
+        p.off_pos = take(p.T * 4);
+        p.off_lse2 = take(p.Tpad * 4);
+        p.off_gs = take(p.Tpad * 4);
+        p.off_g = take(p.Tpad * p.piece * 2);
+        p.off_part = take(p.Tpad * p.H * 4);
+    }
+    p.bytes = at;
+    return p;
+}
+
+cudaError_t launch_loss(const LossArgs &a, const LossPlan &p, cudaStream_t stream) {
+    DeviceInfo dev;
+    cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return e;
+    if ((e = launch_pack(a, p, dev, stream)) != cudaSuccess) return e;
+    if ((e = launch_loss_stats(a, p, stream)) != cudaSuccess) return e;
+    return launch_pdl(loss_merge_kernel, dim3(static_cast<unsigned>(p.Tpad / 32)), dim3(32 * kMergeWarps), 0, stream,
+                      reinterpret_cast<const LossMeta *>(a.ws + p.off_meta),
+                      reinterpret_cast<const int32_t *>(a.ws + p.off_act),
+                      reinterpret_cast<const float2 *>(a.ws + p.off_stats),
+                      reinterpret_cast<const float *>(a.ws + p.off_zt), p.vt, p.Tpad, a.inv_temperature, a.loss, a.lse,
+                      a.err);
+}
+
+cudaError_t launch_loss_grad(const LossArgs &a, const LossPlan &p, cudaStream_t stream) {
+    if (p.T == 0) {
+        const size_t es = a.dtable_dtype == LHS_F32 ? 4 : 2;
+        return a.dtable && !a.accumulate ? launch_zero(a.dtable, static_cast<size_t>(p.V) * p.H * es, stream) : cudaSuccess;
+    }
+    DeviceInfo dev;
+    cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return e;
+    if ((e = launch_pack(a, p, dev, stream)) != cudaSuccess) return e;
+    if ((e = launch_loss_products(a, p, stream)) != cudaSuccess) return e;
+    if (!a.dx) return cudaSuccess;
+    const LossMeta *meta = reinterpret_cast<const LossMeta *>(a.ws + p.off_meta);
+    const int32_t *pos = reinterpret_cast<const int32_t *>(a.ws + p.off_pos);
+    const float *part = reinterpret_cast<const float *>(a.ws + p.off_part);
+    const int64_t want = (p.T + 7) / 8;
+    const dim3 grid(static_cast<unsigned>(want < 8 * dev.num_sms ? want : 8 * dev.num_sms)), block(256);
+    if (a.dx_dtype == LHS_F32)
+        return launch_pdl(loss_dx_kernel<float>, grid, block, 0, stream, meta, pos, part, p.T, p.H,
+                          static_cast<float *>(a.dx), a.dx_stride);
+    if (p.bf16)
+        return launch_pdl(loss_dx_kernel<__nv_bfloat16>, grid, block, 0, stream, meta, pos, part, p.T, p.H,
+                          static_cast<__nv_bfloat16 *>(a.dx), a.dx_stride);
+    return launch_pdl(loss_dx_kernel<__half>, grid, block, 0, stream, meta, pos, part, p.T, p.H,
+                      static_cast<__half *>(a.dx), a.dx_stride);
+}
+
+}  // namespace lhs

@@ -1,0 +1,102 @@
+// train.cuh — plans and launcher prototypes of the cross entropy over the tied
+// table, its gradient, and the gradient of the lookup (loss.cu, loss_gemm.cu,
+// embed_grad.cu; checked in train_abi.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "decode.cuh"
+
+namespace lhs {
+
+constexpr int kLossTile = 256;  // tokens, and vocabulary rows, of a tile of logits
+
+inline int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+
+// What one call needs to know on the device, written by its first kernel.
+struct LossMeta {
+    int32_t count;    // positions that take part
+    float scale;      // g is multiplied by this power of two before it is rounded
+    float unscale;    // its inverse
+};
+
+// Workspace of one call.  The positions that take part are numbered 0 .. count
+// in their order ("compact"); rows of x that do not are never read again.
+struct LossPlan {
+    int64_t T, Tpad;        // positions; rounded up to whole tiles (one at least)
+    int64_t V, vt;          // vocabulary rows; tiles of them
+    int32_t H, Hp;          // hidden; rounded up to 8 (rows of whole 16-byte words)
+    bool bf16, grad;
+    size_t off_meta;        // LossMeta
+    size_t off_act;         // int32 [Tpad]: position of a compact row, -1 past count
+    size_t off_tgt;         // int32 [Tpad]: its target, -1 past count
+    size_t off_x;           // [Tpad x Hp]: its residual, zeros past hidden and count
+    // loss
+    size_t off_stats;       // float2 [vt x Tpad]: maximum and sum of exponentials of a tile
+    size_t off_zt;          // f32 [Tpad]: the target's logit
+    // gradient
+    size_t off_pos;         // int32 [T]: compact row of a position, -1
+    size_t off_lse2;        // f32 [Tpad]: lse * log2(e), +inf past count
+    size_t off_gs;          // f32 [Tpad]: dloss / temperature, 0 past count
+    size_t off_g;           // [Tpad x piece]: g of a piece of the vocabulary
+    size_t off_part;        // f32 [Tpad x H]: dx so far
+    int64_t piece;          // vocabulary rows of a piece, a multiple of kLossTile
+    size_t bytes;
+};
+LossPlan plan_loss(const lhs_table &t, int64_t tokens, bool grad);
+
+struct LossArgs {
+    lhs_table t;
+    const void *x;
+    int64_t x_stride;
+    const int32_t *targets;
+    int32_t ignore;
+    float inv_temperature;
+    float *loss, *lse;              // loss
+    const float *lse_in, *dloss;    // gradient
+    void *dx;
+    int32_t dx_dtype;
+    int64_t dx_stride;
+    void *dtable;
+    int32_t dtable_dtype;
+    bool accumulate;
+    uint8_t *ws;
+    int32_t *err;
+};
+cudaError_t launch_loss(const LossArgs &a, const LossPlan &p, cudaStream_t stream);
+cudaError_t launch_loss_grad(const LossArgs &a, const LossPlan &p, cudaStream_t stream);
+
+// The products between the first and the last kernel of a call (loss_gemm.cu).
+cudaError_t launch_loss_stats(const LossArgs &a, const LossPlan &p, cudaStream_t stream);
+cudaError_t launch_loss_products(const LossArgs &a, const LossPlan &p, cudaStream_t stream);
+
+struct EmbedGradArgs {
+    int64_t vocab;
+    int32_t hidden;
+    const int32_t *ids;
+    int64_t n;
+    int32_t ignore;
+    float scale;
+    const void *dout;
+    int32_t dout_dtype;
+    int64_t dout_stride;
+    void *dtable;
+    int32_t dtable_dtype;
+    bool accumulate;
+    uint8_t *ws;
+    int32_t *err;
+};
+size_t embed_grad_workspace(int64_t vocab, int32_t hidden, int64_t n);
+cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t stream);
+// Zeroes `bytes` at a 16-byte aligned address.
+cudaError_t launch_zero(void *p, size_t bytes, cudaStream_t stream);
+
+// A value rounded to an output type (beyond the f16 range +-inf).
+__device__ __forceinline__ void put_rn(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put_rn(__half *p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void put_rn(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ float wide(float v) { return v; }
+__device__ __forceinline__ float wide(__half v) { return __half2float(v); }
+__device__ __forceinline__ float wide(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+}  // namespace lhs

@@ -56,7 +56,8 @@ extern "C" {
 #define LHS_ERRBIT_BAD_TOKEN 1  /* a token id < 0 or >= vocab; its row is zero */
 #define LHS_ERRBIT_MALFORMED 2  /* wire message header / zero_point mismatch */
 #define LHS_ERRBIT_NONFINITE 4  /* i8 encode of a non-finite value; f16-table
-                                   lm_head residual outside the f16 range */
+                                   lm_head residual outside the f16 range; logits,
+                                   lse or dloss of a loss that are not finite */
 #define LHS_ERRBIT_TIMEOUT 8    /* a bounded on-device wait gave up */
 #define LHS_ERRBIT_BAD_PARAM 16 /* lhs_sample: a row's parameter or random number
                                    is outside its range */
@@ -449,6 +450,92 @@ LHS_API int lhs_sample(const void *d_logits, int32_t dtype, int64_t stride, int6
                        int64_t vocab, const float *d_u, const float *d_temperature,
                        const int32_t *d_top_k, const float *d_top_p, const float *d_min_p,
                        int32_t *d_ids, float *d_probs, int32_t *d_err, void *stream);
+
+/* ---- scoring and training the tied table ----------------------------------- */
+
+/* Softmax cross entropy of given targets over the whole vocabulary, without
+ * the logits.  For a position t whose target y = d_targets[t] lies in
+ * [0, vocab):
+ *   z[v]    = (sum_j x[t][j] * element(row v, j)) / temperature
+ *   lse[t]  = log(sum_v exp(z[v]))
+ *   loss[t] = lse[t] - z[y]
+ * A position with target `ignore` takes no part: its loss and lse are 0 and
+ * its residual is not looked at (NaN there reaches nothing).  Any other target
+ * outside [0, vocab) is treated the same and sets LHS_ERRBIT_BAD_TOKEN.  The
+ * work is that of the positions that take part.
+ *   t         : LHS_F16 or LHS_BF16 (LHS_ERR_UNSUPPORTED for others)
+ *   d_x       : [tokens] rows of the table's type (x_dtype = t->dtype), row t
+ *               at element t*x_stride (x_stride >= hidden), 2-byte aligned
+ *   d_targets : int32 [tokens]
+ *   d_loss, d_lse : f32 [tokens]
+ *   d_ws      : 256-byte aligned, >= lhs_loss_workspace bytes, overwritten
+ * The logits are f32 sums of exact products; they and their exponentials'
+ * sums are never rounded to fewer bits.  A position whose logits hold NaN or
+ * +inf, or nothing above -inf, gives loss and lse NaN and sets
+ * LHS_ERRBIT_NONFINITE.  0 <= tokens <= 2^24 (0 enqueues nothing); hidden <=
+ * 65536; temperature finite and > 0.  Results do not depend on the run.
+ * Errors: LHS_ERR_INVALID_ARG, LHS_ERR_BUFFER_TOO_SMALL, LHS_ERR_UNSUPPORTED,
+ * LHS_ERR_CUDA. */
+LHS_API int lhs_loss_workspace(const lhs_table *t, int64_t tokens, size_t *bytes);
+LHS_API int lhs_loss(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t x_stride,
+                     int64_t tokens, const int32_t *d_targets, int32_t ignore, float temperature,
+                     float *d_loss, float *d_lse, void *d_ws, size_t ws_bytes, int32_t *d_err,
+                     void *stream);
+
+/* The gradient of sum_t dloss[t] * loss[t], for the residuals and the table.
+ * With z, lse, the targets and `ignore` as in lhs_loss:
+ *   g[t][v]      = (exp(z[t][v] - lse[t]) - [v == y_t]) * dloss[t] / temperature
+ *   dx[t][j]     = sum_v g[t][v] * element(row v, j)      (0 where t takes no part)
+ *   dtable[v][j] = sum_t g[t][v] * x[t][j]  (+ what dtable held, if accumulate)
+ *   d_lse        : f32 [tokens], what lhs_loss gave for the same call
+ *   d_dloss      : f32 [tokens]
+ *   d_dx         : of dx_dtype (the table's type or LHS_F32), row t at element
+ *                  t*dx_stride (>= hidden), aligned to its element size; or
+ *                  NULL: not wanted
+ *   d_dtable     : [vocab x hidden] row-major of dtable_dtype (the table's type
+ *                  or LHS_F32), 16-byte aligned; or NULL: not wanted.  One of
+ *                  the two has to be wanted.
+ *   d_ws         : 256-byte aligned, >= lhs_loss_grad_workspace bytes, overwritten
+ * The logits are computed again, a piece of the vocabulary at a time.  g is
+ * rounded to the table's type (scaled by a power of two taken from the largest
+ * |dloss|, so that f16 holds it), as the other factor of both products is of
+ * that type; the sums are f32, rounded once to the output's type (with
+ * accumulate once more for what dtable held, if it is of 16 bits).  Positions
+ * that take part with an lse or dloss that is not finite set
+ * LHS_ERRBIT_NONFINITE and make what they reach NaN.  tokens == 0 clears dtable
+ * (unless accumulate).  Ranges, errors and determinism as lhs_loss. */
+LHS_API int lhs_loss_grad_workspace(const lhs_table *t, int64_t tokens, size_t *bytes);
+LHS_API int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t x_stride,
+                          int64_t tokens, const int32_t *d_targets, int32_t ignore,
+                          float temperature, const float *d_lse, const float *d_dloss, void *d_dx,
+                          int32_t dx_dtype, int64_t dx_stride, void *d_dtable, int32_t dtable_dtype,
+                          int32_t accumulate, void *d_ws, size_t ws_bytes, int32_t *d_err,
+                          void *stream);
+
+/* The gradient of lhs_embed for the table:
+ *   dtable[v][j] = scale * sum_{i: ids[i] == v} dout[i][j]  (+ what dtable
+ *                  held, if accumulate)
+ * An id equal to `ignore` takes no part; any other id outside [0, vocab) does
+ * not either and sets LHS_ERRBIT_BAD_TOKEN.  Rows that no id names are 0 (left
+ * as they are, if accumulate).  The positions of an id are added up in f32, in
+ * an order that depends on the ids alone; the sum is scaled (and added to what
+ * dtable held) with one f32 rounding and then rounded to dtable_dtype.
+ *   d_ids    : int32 [n]
+ *   d_dout   : LHS_F32, LHS_F16 or LHS_BF16, row i at element i*dout_stride
+ *              (>= hidden), aligned to its element size
+ *   d_dtable : [vocab x hidden] row-major, LHS_F32, LHS_F16 or LHS_BF16,
+ *              16-byte aligned
+ *   d_ws     : 256-byte aligned, >= lhs_embed_grad_workspace bytes, overwritten
+ * 0 <= n <= 2^30 (n == 0 clears dtable, unless accumulate); 1 <= vocab <=
+ * 2^31-1; 1 <= hidden <= 65536; scale finite.  lhs_embed_grad_workspace gives
+ * -1 outside these.  Errors: LHS_ERR_INVALID_ARG, LHS_ERR_BUFFER_TOO_SMALL,
+ * LHS_ERR_CUDA. */
+LHS_API int64_t lhs_embed_grad_workspace(int64_t vocab, int32_t hidden, int64_t n);
+LHS_API int lhs_embed_grad(int64_t vocab, int32_t hidden, const int32_t *d_ids, int64_t n,
+                           int32_t ignore, float scale, const void *d_dout, int32_t dout_dtype,
+                           int64_t dout_stride, void *d_dtable, int32_t dtable_dtype,
+                           int32_t accumulate, void *d_ws, size_t ws_bytes, int32_t *d_err,
+                           void *stream);
 
 /* Diagnostic: launch one tiny kernel whose wait on an on-chip barrier is
  * never satisfied, bounded by timeout_ns; the kernel gives up, sets
