@@ -36,6 +36,8 @@ struct PackParams {
     int32_t *act, *tgt, *pos;
     float *lse2, *gs;
     uint16_t *xc;
+    uint32_t *queue;         // cleared
+    int n_queue;
     int32_t *err;
 };
 
@@ -161,6 +163,7 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
     if (bad) set_err(p.err, LHS_ERRBIT_BAD_TOKEN);
     if (nonfinite) set_err(p.err, LHS_ERRBIT_NONFINITE);
     if (blockIdx.x == 0) {
+        for (int i = tid; i < p.n_queue; i += kPackThreads) p.queue[i] = 0u;
         // The power of two that brings the largest |g| into (1/4, 1] (bf16: its range needs no
         // more, and larger terms could overflow sums that fit) or up to 2^15 (f16: what lies
         // 2^-29 below it is still normal, 2^-39 below it the last subnormal).
@@ -189,8 +192,21 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
     }
 }
 
-// Joins a token's tiles: 32 tokens to a CTA, whose warps share the tiles.  The
-// maximum is exact, and the sums of the warps are joined in their order.
+// The table in rows of whole 16-byte words, where its own are not.  A warp to a row.
+__global__ void __launch_bounds__(256)
+    loss_table_kernel(const uint16_t *w, int64_t V, int H, int Hp, uint16_t *out) {
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_trigger();
+    for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < V;
+         r += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5)
+        pack_row(w + r * H, out + r * Hp, H, Hp, false, lane);
+}
+
+// Joins a token's tiles: 32 tokens to a CTA, whose warps share the tiles.  A
+// pair (m, s) stands for (1 + s) exp(m): the 1 is the maximum's own term, kept
+// out of the sums so that log1p sees a small rest unspoilt.  The warps' pairs
+// are joined in their order.
 constexpr int kMergeWarps = 32;
 __global__ void __launch_bounds__(32 * kMergeWarps)
     loss_merge_kernel(const LossMeta *meta, const int32_t *act, const float2 *stats, const float *zt, int64_t vt,
@@ -205,12 +221,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     const float l2 = kLog2e * inv_temperature;
     float m = -INFINITY, s = 0.0f;
     auto join = [&](float om, float os) {
-        const float n = fmaxf(m, om);
-        // an empty side adds nothing; a sum that is NaN stays NaN
-        const float a = m == -INFINITY ? s : s * exp2f((m - n) * l2);
-        const float b = om == -INFINITY ? os : os * exp2f((om - n) * l2);
-        s = a + b;
-        m = n;
+        if (om == -INFINITY) {
+            s += os;  // nothing, or NaN
+        } else if (m == -INFINITY) {
+            m = om;
+            s += os;
+        } else {
+            const float lo = fminf(m, om), hi = fmaxf(m, om);
+            s = (om > m ? os : s) + (1.0f + (om > m ? s : os)) * exp2f((lo - hi) * l2);
+            m = hi;
+        }
     };
     if (i < count)
 #pragma unroll 4
@@ -222,7 +242,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     __syncthreads();
     if (warp == 0 && i < count) {
         for (int w = 1; w < kMergeWarps; ++w) join(part[w][lane].x, part[w][lane].y);
-        const float ls = logf(s);
+        const float ls = log1pf(s);
         float l = m * inv_temperature + ls;
         float c = (m - ld_dep(zt + i)) * inv_temperature + ls;
         if (!isfinite(l)) {
@@ -235,22 +255,56 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     }
 }
 
-// dx of every position: its compact row of sums times the inverse of g's scale,
-// or zeros.  A warp to a position.
+// dx of every position: its compact row's sums, joined in order, times the
+// inverse of g's scale; or zeros.  A warp to a position.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    loss_dx_kernel(const LossMeta *meta, const int32_t *pos, const float *part, int64_t n, int32_t H, T *dx,
-                   int64_t dx_stride) {
+    loss_dx_kernel(const LossMeta *meta, const int32_t *pos, const float *part, int splits, int64_t Tpad, int pitch,
+                   int64_t n, int32_t H, T *dx, int64_t dx_stride, bool vec) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
     const float u = ld_dep(&meta->unscale);
     for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < n;
          r += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5) {
         const int32_t c = ld_dep(pos + r);
-        const float *src = part + static_cast<int64_t>(c) * H;
         T *d = dx + r * dx_stride;
-        for (int j = lane; j < H; j += 32) put_rn(d + j, c < 0 ? 0.0f : ld_dep(src + j) * u);
+        for (int j = lane * 4; j < H; j += 128) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (c >= 0) {
+                const float4 *src = reinterpret_cast<const float4 *>(part + static_cast<int64_t>(c) * pitch + j);
+                const int64_t step = Tpad * pitch / 4;
+                v = ld_dep(src);
+#pragma unroll 4
+                for (int k = 1; k < splits; ++k) {
+                    const float4 a = ld_dep(src + k * step);
+                    v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+                }
+                v.x *= u, v.y *= u, v.z *= u, v.w *= u;
+            }
+            const float f[4] = {v.x, v.y, v.z, v.w};
+            if (vec && j + 4 <= H) {
+                T o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) put_rn(&o[k], f[k]);
+                if (sizeof(T) == 4) *reinterpret_cast<float4 *>(d + j) = *reinterpret_cast<const float4 *>(o);
+                else *reinterpret_cast<uint2 *>(d + j) = *reinterpret_cast<const uint2 *>(o);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (j + k < H) put_rn(d + j + k, f[k]);
+            }
+        }
     }
+}
+
+template <typename T>
+cudaError_t launch_dx(const LossArgs &a, const LossPlan &p, const DeviceInfo &dev, cudaStream_t stream) {
+    const int64_t want = (p.T + 7) / 8;
+    const bool vec = reinterpret_cast<uintptr_t>(a.dx) % (4 * sizeof(T)) == 0 && a.dx_stride % 4 == 0;
+    return launch_pdl(loss_dx_kernel<T>, dim3(static_cast<unsigned>(want < 8 * dev.num_sms ? want : 8 * dev.num_sms)),
+                      dim3(256), 0, stream, reinterpret_cast<const LossMeta *>(a.ws + p.off_meta),
+                      reinterpret_cast<const int32_t *>(a.ws + p.off_pos), reinterpret_cast<const float *>(a.ws + p.off_part),
+                      p.splits, p.Tpad, p.part_pitch, p.T, p.H, static_cast<T *>(a.dx), a.dx_stride, vec);
 }
 
 cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &dev, cudaStream_t stream) {
@@ -277,11 +331,50 @@ cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &
     k.lse2 = reinterpret_cast<float *>(a.ws + p.off_lse2);
     k.gs = reinterpret_cast<float *>(a.ws + p.off_gs);
     k.xc = reinterpret_cast<uint16_t *>(a.ws + p.off_x);
+    k.queue = reinterpret_cast<uint32_t *>(a.ws + p.off_queue);
+    k.n_queue = p.pieces + 1;
     k.err = a.err;
+    cudaError_t e = cudaSuccess;
+    if (p.H % 8) {
+        const int64_t ctas = (p.V + 7) / 8;
+        e = launch_pdl(loss_table_kernel, dim3(static_cast<unsigned>(ctas < 8 * dev.num_sms ? ctas : 8 * dev.num_sms)), dim3(256), 0,
+                       stream, static_cast<const uint16_t *>(a.t.data), p.V, p.H, p.Hp,
+                       reinterpret_cast<uint16_t *>(a.ws + p.off_w));
+        if (e != cudaSuccess) return e;
+    }
     const int64_t want = (p.T + kPackWarps - 1) / kPackWarps;
     const unsigned grid = static_cast<unsigned>(want < 4 * dev.num_sms ? want : 4 * dev.num_sms);
     return launch_pdl(p.grad ? loss_pack_kernel<true> : loss_pack_kernel<false>, dim3(grid), dim3(kPackThreads), 0,
                       stream, k);
+}
+
+}  // namespace
+
+namespace {
+
+// Rows of a piece: g of two pieces and the table's rows of one should stay in
+// L2 between the launch that writes or reads them first and the next.
+constexpr int64_t kPieceBytes = 64ll << 20;
+constexpr int kPairs = 76;  // of CTAs that run at once
+
+void choose_pieces(LossPlan *p) {
+    int64_t rows = kPieceBytes / (2 * (p->Tpad > p->Hp ? p->Tpad : p->Hp));
+    if (rows < 2048) rows = 2048;
+    p->pieces = static_cast<int>((p->V + rows - 1) / rows);
+    p->piece = round_up((p->V + p->pieces - 1) / p->pieces, kLossTile);
+    p->pieces = static_cast<int>((p->V + p->piece - 1) / p->piece);
+    p->part_pitch = static_cast<int32_t>(round_up(p->H, 4));
+    // stages (64 of k of a 256 x 256 tile) of a launch, and of one tile of dx: no item should
+    // take more than a third of a pair's share
+    const int64_t blocks = p->Tpad / kLossTile, gt = p->piece / kLossTile, ht = (p->H + kLossTile - 1) / kLossTile;
+    const int64_t kh = (p->H + 63) / 64, kp = (p->V < p->piece ? p->V + 63 : p->piece) / 64;
+    const int64_t total = blocks * gt * kh + blocks * ht * kp + gt * ht * (p->Tpad / 64);
+    int64_t most = total / kPairs / 3;
+    if (most < 16) most = 16;
+    int64_t splits = (kp + most - 1) / most;
+    if (splits > 32) splits = 32;
+    if (splits > kp) splits = kp;
+    p->splits = static_cast<int>(splits < 1 ? 1 : splits);
 }
 
 }  // namespace
@@ -306,16 +399,19 @@ LossPlan plan_loss(const lhs_table &t, int64_t tokens, bool grad) {
     p.off_act = take(p.Tpad * 4);
     p.off_tgt = take(p.Tpad * 4);
     p.off_x = take(p.Tpad * p.Hp * 2);
+    p.off_w = take(p.H % 8 ? p.V * p.Hp * 2 : 0);
     if (!grad) {
+        p.off_queue = take(4);
         p.off_stats = take(p.vt * p.Tpad * 8);
         p.off_zt = take(p.Tpad * 4);
     } else {
-        p.piece = round_up(p.V < 8192 ? p.V : 8192, kLossTile);
+        choose_pieces(&p);
+        p.off_queue = take((p.pieces + 1) * 4);
         p.off_pos = take(p.T * 4);
         p.off_lse2 = take(p.Tpad * 4);
         p.off_gs = take(p.Tpad * 4);
-        p.off_g = take(p.Tpad * p.piece * 2);
-        p.off_part = take(p.Tpad * p.H * 4);
+        p.off_g = take(2 * p.Tpad * p.piece * 2);
+        p.off_part = take(p.splits * p.Tpad * p.part_pitch * 4);
     }
     p.bytes = at;
     return p;
@@ -346,19 +442,8 @@ cudaError_t launch_loss_grad(const LossArgs &a, const LossPlan &p, cudaStream_t 
     if ((e = launch_pack(a, p, dev, stream)) != cudaSuccess) return e;
     if ((e = launch_loss_products(a, p, stream)) != cudaSuccess) return e;
     if (!a.dx) return cudaSuccess;
-    const LossMeta *meta = reinterpret_cast<const LossMeta *>(a.ws + p.off_meta);
-    const int32_t *pos = reinterpret_cast<const int32_t *>(a.ws + p.off_pos);
-    const float *part = reinterpret_cast<const float *>(a.ws + p.off_part);
-    const int64_t want = (p.T + 7) / 8;
-    const dim3 grid(static_cast<unsigned>(want < 8 * dev.num_sms ? want : 8 * dev.num_sms)), block(256);
-    if (a.dx_dtype == LHS_F32)
-        return launch_pdl(loss_dx_kernel<float>, grid, block, 0, stream, meta, pos, part, p.T, p.H,
-                          static_cast<float *>(a.dx), a.dx_stride);
-    if (p.bf16)
-        return launch_pdl(loss_dx_kernel<__nv_bfloat16>, grid, block, 0, stream, meta, pos, part, p.T, p.H,
-                          static_cast<__nv_bfloat16 *>(a.dx), a.dx_stride);
-    return launch_pdl(loss_dx_kernel<__half>, grid, block, 0, stream, meta, pos, part, p.T, p.H,
-                      static_cast<__half *>(a.dx), a.dx_stride);
+    if (a.dx_dtype == LHS_F32) return launch_dx<float>(a, p, dev, stream);
+    return p.bf16 ? launch_dx<__nv_bfloat16>(a, p, dev, stream) : launch_dx<__half>(a, p, dev, stream);
 }
 
 }  // namespace lhs

@@ -1,224 +1,823 @@
-// loss_gemm.cu — the products of the cross entropy and of its gradient.
+// loss_gemm.cu — the products of the cross entropy and of its gradient, on the
+// 5th-generation tensor cores (tcgen05 + TMEM).
 //
-// First form: 64 x 64 tiles of f32 sums on the CUDA cores, one kernel a
-// product, a piece of the vocabulary at a time.
+// Four products share one kernel.  With X the packed residuals, W the table and
+// g a piece of the logits' gradient ([tokens x rows of the piece]):
+//   logits   z  = X W^T   M = tokens,  N = rows,   K = hidden   (statistics, or g)
+//   dx      += g W        M = tokens,  N = hidden, K = rows of the piece
+//   dtable   = g^T X      M = rows,    N = hidden, K = tokens
+// A pair of CTAs owns a tile of 256 x up to 256 (cta_group::2): each stages its
+// own 128 rows of A and half of B's columns, 64 of k at a time, by TMA with
+// 128-byte swizzle, and receives the f32 sums of its rows in its TMEM, which
+// holds two tiles, so that the next one's MMAs run while one is taken out.
+// Operands whose k is not the contiguous index (W for dx, both for dtable) are
+// staged as they lie and read "MN-major": no transposed copy is made.
+//
+// The gradient goes through the vocabulary in pieces.  One launch computes g of
+// a piece and the two products with g of the piece before, which no item of
+// the launch has to wait for.  Items (tiles) come from one queue, long ones
+// first, so that the short ones (g) even the pairs' loads out.  dx's tiles are
+// few and their k is long, so they are split along k; each split adds up in f32
+// sums of its own, which one kernel joins in order at the end.
+//
+// The logits are never stored: statistics leave a tile as (maximum, sum of the
+// other exponentials) of each token, g as 16-bit values that the products read
+// back from L2.
+#include <mutex>
+
+#include "i8_common.cuh"
 #include "train.cuh"
 
 namespace lhs {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int TS = 64, TK = 16;
+constexpr int kCtaM = 128;                    // rows of a tile that a CTA holds (TMEM lanes)
+constexpr int kTileK = 64;
+constexpr int kBoxBytes = 64 * 64 * 2;        // what one TMA load brings: 64 x 64 values
+constexpr int kOperandBytes = 2 * kBoxBytes;  // a CTA's part of A, or of B, of a stage
+constexpr int kEpiWarps = 4;
+constexpr int kThreads = 32 * (3 + kEpiWarps);  // producer, MMA issuer, scheduler, epilogue
+constexpr int kTmemCols = 512;
+constexpr int kStoreBytes = 32 * 128;         // an epilogue warp's store: 32 rows of 128 bytes
+constexpr int kQueue = 4;                     // items handed out ahead
 
-// acc[a][b] = sum_k A(m0 + ty*4 + a, k) * B(n0 + tx*4 + b, k); element (i, k)
-// of an operand lies i*si + k*sk further on; zeros from mm, nn, kk on.
-template <typename T>
-__device__ void tile_product(const T *A, int64_t sam, int64_t sak, int64_t mm, const T *B, int64_t sbn, int64_t sbk,
-                             int64_t nn, int64_t kk, float (&acc)[4][4], float (*sa)[TS + 4], float (*sb)[TS + 4]) {
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[a][b] = 0.0f;
-    for (int64_t k0 = 0; k0 < kk; k0 += TK) {
-        for (int i = tid; i < TS * TK; i += 256) {
-            // consecutive threads along whichever index is contiguous
-            const int ma = sak == 1 ? i / TK : i % TS, ka = sak == 1 ? i % TK : i / TS;
-            sa[ka][ma] = ma < mm && k0 + ka < kk ? wide(A[ma * sam + (k0 + ka) * sak]) : 0.0f;
-            const int nb = sbk == 1 ? i / TK : i % TS, kb = sbk == 1 ? i % TK : i / TS;
-            sb[kb][nb] = nb < nn && k0 + kb < kk ? wide(B[nb * sbn + (k0 + kb) * sbk]) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < TK; ++k) {
-            float va[4], vb[4];
-#pragma unroll
-            for (int a = 0; a < 4; ++a) va[a] = sa[k][ty * 4 + a];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) vb[b] = sb[k][tx * 4 + b];
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-#pragma unroll
-                for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(va[a], vb[b], acc[a][b]);
-        }
-        __syncthreads();
+enum { kLogits = 0, kDx = 1, kDtable = 2 };
+enum { kStore16 = 0, kStore32 = 1, kAdd32 = 2, kPlain = 3 };  // how dtable is written
+
+struct Params {
+    const LossMeta *meta;
+    const int32_t *tgt;
+    int64_t V, Tpad;
+    int H, ht;               // hidden; tiles of it
+    float l2;                // log2(e) / temperature
+    uint32_t *queue;         // items handed out beyond every pair's first; 0 at the start
+    int32_t *err;
+    int64_t g_v0;            // logits: first row and tiles
+    int g_tiles;
+    float2 *stats;           // statistics
+    float *zt;
+    const float *lse2, *gs;  // g
+    bool dx, first;
+    int64_t d_v0;            // dx, dtable: first row, tiles and stages of the piece
+    int d_tiles, d_stages, splits;
+    int dt_mode, dt_dtype;
+    bool accumulate;
+    void *dtable;
+};
+
+template <int MODE>
+struct Conf {
+    static constexpr bool kGrad = MODE == 1;
+    static constexpr int kStages = kGrad ? 6 : 7;
+};
+
+template <int MODE>
+struct Smem {
+    static constexpr int S = Conf<MODE>::kStages;
+    uint8_t a[S][kOperandBytes];
+    uint8_t b[S][kOperandBytes];
+    uint8_t out[Conf<MODE>::kGrad ? kEpiWarps : 1][Conf<MODE>::kGrad ? 2 : 1][Conf<MODE>::kGrad ? kStoreBytes : 16];
+    uint64_t full[S], empty[S];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t item_full[kQueue], item_empty[kQueue];
+    int item[kQueue];
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+// ---------------------------------------------------------------------------
+// instructions
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_ctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The shared::cluster address of a variable of CTA `cta` of the pair.
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t cta) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(cta));
+    return r;
+}
+// TMA load into this CTA's shared memory, counted on a barrier of either CTA.
+__device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_add(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Arrive on a barrier of either CTA for what tcgen05 waits and fences order.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same, releasing what this thread has read or written in shared memory.
+__device__ __forceinline__ void arrive_release(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Bounded wait that gives up at once when the CTA has already aborted.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, int *abort_flag, int32_t *err) {
+    if (try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<const volatile int *>(abort_flag)) return false;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (try_wait(bar, parity)) return true;
+        if (global_ns() - t0 > kWaitTimeoutNs) break;
     }
+    set_err(err, LHS_ERRBIT_TIMEOUT);
+    *reinterpret_cast<volatile int *>(abort_flag) = 1;
+    return false;
+}
+// One lane of the warp for the MMAs: the whole warp runs the loop around them,
+// so that their operands stay in uniform registers.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p)::"memory");
+    return p;
+}
+// Shared-memory matrix descriptors, 128-byte swizzle.  High word: groups of 8
+// rows 1024 bytes apart (SBO).  Low word: address, and for an MN-major operand
+// the distance of its second 64 columns, one box further on (LBO).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kLboK = 1u << 16, kLboMn = static_cast<uint32_t>(kBoxBytes >> 4) << 16;
+// 16 of k further on: 32 bytes along the rows, or 16 rows of 128 bytes
+constexpr uint32_t kStepK = 32 >> 4, kStepMn = 2048 >> 4;
+__device__ __forceinline__ void umma(uint32_t elected, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                     uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(elected), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void commit_both(uint32_t elected, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::
+            "r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(0x3)), "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// 32 consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 2^x, relative error below 2^-21: a thousandth of what g is rounded by, and
+// of the order of an f32 logit's own rounding in a sum of exponentials.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if (BF) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// 16-byte piece i of row r of a store's 128-byte rows, swizzled.
+__device__ __forceinline__ void put_piece(uint8_t *buf, int r, int i, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    *reinterpret_cast<uint4 *>(buf + r * 128 + ((i ^ (r & 7)) << 4)) = make_uint4(x, y, z, w);
 }
 
-// grid: vocabulary tiles of 256 x blocks of 64 tokens
-template <typename T>
-__global__ void __launch_bounds__(256)
-    loss_stats_kernel(const LossMeta *meta, const int32_t *tgt, const T *x, int Hp, const T *w, int64_t V, int H,
-                      float inv_temperature, int64_t Tpad, float2 *stats, float *zt) {
-    __shared__ float sa[TK][TS + 4], sb[TK][TS + 4];
-    pdl_wait();
-    const int count = ld_dep(&meta->count);
-    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * TS;
-    if (t0 >= count) return;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const float l2 = kLog2e * inv_temperature;
-    float m[4], s[4];
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        m[a] = -INFINITY;
-        s[a] = 0.0f;
+// ---------------------------------------------------------------------------
+// items
+// ---------------------------------------------------------------------------
+struct Item {
+    int kind;
+    int m;        // tile of M: block of tokens, or of the piece's rows
+    int n;        // tile of N: of rows (logits), or of hidden
+    int split;    // dx
+    int k0, k1;   // stages
+    int width;    // N of the MMAs, a multiple of 32
+};
+struct Work {
+    uint32_t blocks, n_dx, n_dt, total;
+    int token_stages;
+};
+template <int MODE>
+__device__ __forceinline__ Work work_of(const Params &p) {
+    Work w = {};
+    const int count = ld_dep(&p.meta->count);
+    w.blocks = count > 0 ? (static_cast<uint32_t>(count) + kLossTile - 1) / kLossTile : 1u;
+    w.token_stages = count > 0 ? (count + kTileK - 1) / kTileK : 1;
+    if (MODE == 1) {
+        w.n_dx = p.dx && p.d_tiles ? w.blocks * p.ht * p.splits : 0;
+        w.n_dt = p.dtable ? static_cast<uint32_t>(p.d_tiles) * p.ht : 0;
     }
-    auto join = [&](int a, float om, float os) {
-        const float n = fmaxf(m[a], om);
-        s[a] = (m[a] == -INFINITY ? s[a] : s[a] * exp2f((m[a] - n) * l2)) +
-               (om == -INFINITY ? os : os * exp2f((om - n) * l2));
-        m[a] = n;
+    w.total = w.n_dx + w.n_dt + w.blocks * p.g_tiles;
+    return w;
+}
+__device__ __forceinline__ int width_of(int H, int tile) {
+    const int left = H - tile * kLossTile;
+    return left >= kLossTile ? kLossTile : (left + 31) / 32 * 32;
+}
+template <int MODE>
+__device__ __forceinline__ Item item_of(const Params &p, const Work &w, uint32_t i) {
+    Item t = {};
+    if (MODE == 1 && i < w.n_dx) {
+        t.kind = kDx;
+        t.n = i % p.ht;
+        i /= p.ht;
+        t.split = i % p.splits;
+        t.m = i / p.splits;
+        t.k0 = static_cast<int>(static_cast<int64_t>(p.d_stages) * t.split / p.splits);
+        t.k1 = static_cast<int>(static_cast<int64_t>(p.d_stages) * (t.split + 1) / p.splits);
+        t.width = width_of(p.H, t.n);
+    } else if (MODE == 1 && i < w.n_dx + w.n_dt) {
+        i -= w.n_dx;
+        t.kind = kDtable;
+        t.n = i % p.ht;
+        t.m = i / p.ht;
+        t.k1 = w.token_stages;
+        t.width = width_of(p.H, t.n);
+    } else {
+        i -= w.n_dx + w.n_dt;
+        t.kind = kLogits;
+        t.m = i % w.blocks;
+        t.n = i / w.blocks;
+        t.k1 = (p.H + kTileK - 1) / kTileK;
+        t.width = kLossTile;
+    }
+    return t;
+}
+
+// ---------------------------------------------------------------------------
+// kernel
+// ---------------------------------------------------------------------------
+template <int MODE, bool BF>
+__global__ void __launch_bounds__(kThreads, 1)
+    loss_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                const __grid_constant__ CUtensorMap tm_g_read, const __grid_constant__ CUtensorMap tm_g_write,
+                const __grid_constant__ CUtensorMap tm_part, const __grid_constant__ CUtensorMap tm_dt, const Params p) {
+    constexpr int S = Conf<MODE>::kStages;
+    extern __shared__ uint8_t dyn_smem[];
+    Smem<MODE> &sm = *reinterpret_cast<Smem<MODE> *>(smem_align<1024>(dyn_smem));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&sm.full[s], 1);   // leader: its producer's expect_tx; both CTAs' bytes
+            mbar_init(&sm.empty[s], 1);  // the leader's commit, to both
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.acc_full[i], 1);
+            mbar_init(&sm.acc_empty[i], 2 * kEpiWarps);
+        }
+        for (int i = 0; i < kQueue; ++i) {
+            mbar_init(&sm.item_full[i], 1);
+            mbar_init(&sm.item_empty[i], 2 + 1 + 2 * kEpiWarps);  // leader: producers, MMA issuer, epilogues
+        }
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {  // with the peer's warp 1
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync_all();  // the peer's barriers exist
+    const uint32_t tmem = sm.tmem_base;
+    pdl_wait();
+    const Work work = work_of<MODE>(p);
+
+    // The next item, for one role (a warp, or the producer's lane): -1 at the end or after an abort.
+    int slot = 0;
+    uint32_t slot_parity = 0;
+    auto next_item = [&](bool whole_warp) -> int {
+        const bool ok = wait_or_abort(&sm.item_full[slot], slot_parity, &sm.abort_flag, p.err);
+        if (whole_warp ? !__all_sync(0xFFFFFFFFu, ok) : !ok) return -1;
+        const int i = *reinterpret_cast<const volatile int *>(&sm.item[slot]);
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || lane == 0) arrive_release(cluster_addr(&sm.item_empty[slot], 0));
+        if (++slot == kQueue) {
+            slot = 0;
+            slot_parity ^= 1u;
+        }
+        return i;
     };
-    for (int sub = 0; sub < kLossTile / TS; ++sub) {
-        const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kLossTile + sub * TS;
-        if (v0 >= V) break;
-        float acc[4][4];
-        tile_product(x + t0 * Hp, Hp, 1, Tpad - t0, w + v0 * H, H, 1, V - v0, H, acc, sa, sb);
+
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        if (lane == 0) {
+            uint32_t j = 0;  // stages issued
+            bool ok = true;
+            const int r = static_cast<int>(rank);
+            for (;;) {
+                const int i = next_item(false);
+                if (i < 0) break;
+                const Item t = item_of<MODE>(p, work, i);
+                const int half = t.width / 2, b_boxes = half > 64 ? 2 : 1;
+                // first coordinates of A and B: (x, y) of the box at stage 0, whether k runs along x,
+                // and the second box's offset
+                const CUtensorMap *ma, *mb;
+                int ax, ay, bx, by;
+                bool ak, bk;
+                if (MODE == 0 || t.kind == kLogits) {
+                    ma = &tm_x, ax = 0, ay = t.m * kLossTile + r * kCtaM, ak = true;
+                    mb = &tm_w, bx = 0, by = static_cast<int>(p.g_v0) + t.n * kLossTile + r * half, bk = true;
+                } else if (t.kind == kDx) {
+                    ma = &tm_g_read, ax = 0, ay = t.m * kLossTile + r * kCtaM, ak = true;
+                    mb = &tm_w, bx = t.n * kLossTile + r * half, by = static_cast<int>(p.d_v0), bk = false;
+                } else {
+                    ma = &tm_g_read, ax = t.m * kLossTile + r * kCtaM, ay = 0, ak = false;
+                    mb = &tm_x, bx = t.n * kLossTile + r * half, by = 0, bk = false;
+                }
+                for (int kc = t.k0; kc < t.k1; ++kc, ++j) {
+                    const int s = j % S;
+                    if (j >= S && !wait_or_abort(&sm.empty[s], ((j / S) & 1) ^ 1, &sm.abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * (2 + b_boxes) * kBoxBytes);
+                    const uint32_t bar = cluster_addr(&sm.full[s], 0);
+                    const int k = kc * kTileK;
+                    const int axk = ak ? ax + k : ax, ayk = ak ? ay : ay + k;
+                    tma_load_pair(sm.a[s], ma, bar, axk, ayk);
+                    tma_load_pair(sm.a[s] + kBoxBytes, ma, bar, ak ? axk : axk + 64, ak ? ayk + 64 : ayk);
+                    const int bxk = bk ? bx + k : bx, byk = bk ? by : by + k;
+                    tma_load_pair(sm.b[s], mb, bar, bxk, byk);
+                    if (b_boxes == 2)
+                        tma_load_pair(sm.b[s] + kBoxBytes, mb, bar, bk ? bxk : bxk + 64, bk ? byk + 64 : byk);
+                }
+                if (!ok) break;
+            }
+            // drain: the pair has consumed every stage issued, so no copy, completion or commit is still
+            // headed for either CTA (after an abort, when some never come, one more limit's time to land)
+            for (uint32_t i = j > static_cast<uint32_t>(S) ? j - S : 0; i < j; ++i)
+                if (!mbar_wait(&sm.empty[i % S], (i / S) & 1, kWaitTimeoutNs)) {
+                    if (!*reinterpret_cast<volatile int *>(&sm.abort_flag)) set_err(p.err, LHS_ERRBIT_TIMEOUT);
+                    break;
+                }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (the leader CTA only) ----------------
+        if (rank == 0) {
+            const uint32_t tm = __reduce_or_sync(0xFFFFFFFFu, tmem);
+            const uint32_t elected = elect_one();
+            uint32_t j = 0;
+            int n_acc = 0;
+            for (;;) {
+                const int i = next_item(true);
+                if (i < 0) break;
+                const Item t = item_of<MODE>(p, work, i);
+                const bool a_mn = MODE == 1 && t.kind == kDtable, b_mn = MODE == 1 && t.kind != kLogits;
+                const uint32_t idesc = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
+                                       (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(t.width >> 3) << 17) |
+                                       (static_cast<uint32_t>((2 * kCtaM) >> 4) << 24);
+                const uint32_t la = a_mn ? kLboMn : kLboK, lb = b_mn ? kLboMn : kLboK;
+                const uint32_t sa = a_mn ? kStepMn : kStepK, sb = b_mn ? kStepMn : kStepK;
+                const int buf = n_acc & 1;
+                bool ok = wait_or_abort(&sm.acc_empty[buf], ((n_acc >> 1) & 1) ^ 1, &sm.abort_flag, p.err);
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                tc_fence_after();
+                const uint32_t d = tm + buf * (kTmemCols / 2);
+                for (int kc = t.k0; kc < t.k1; ++kc, ++j) {
+                    const int s = j % S;
+                    ok = wait_or_abort(&sm.full[s], (j / S) & 1, &sm.abort_flag, p.err);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = ((smem_u32(sm.a[s]) >> 4) & 0x3FFFu) | la, b = ((smem_u32(sm.b[s]) >> 4) & 0x3FFFu) | lb;
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            const int y = ld_dep(tgt + t0 + ty * 4 + a);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int64_t v = v0 + tx * 4 + b;
-                if (v < V) join(a, acc[a][b], acc[a][b] == -INFINITY ? 0.0f : acc[a][b] == INFINITY ? NAN : acc[a][b] == acc[a][b] ? 1.0f : NAN);
-                if (v == y) zt[t0 + ty * 4 + a] = acc[a][b];
+                    for (int ks = 0; ks < kTileK / 16; ++ks)
+                        umma(elected, d, a + ks * sa, b + ks * sb, idesc, kc != t.k0 || ks != 0);
+                    commit_both(elected, &sm.empty[s]);
+                }
+                if (!ok) break;
+                commit_both(elected, &sm.acc_full[buf]);
+                ++n_acc;
             }
         }
-    }
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-            join(a, __shfl_xor_sync(0xFFFFFFFFu, m[a], o), __shfl_xor_sync(0xFFFFFFFFu, s[a], o));
-        if (tx == 0) stats[blockIdx.x * Tpad + t0 + ty * 4 + a] = make_float2(m[a], s[a]);
-    }
-}
-
-// grid: 64 vocabulary rows of the piece x blocks of 64 tokens
-template <typename T>
-__global__ void __launch_bounds__(256)
-    loss_g_kernel(const LossMeta *meta, const int32_t *tgt, const float *lse2, const float *gs, const T *x, int Hp,
-                  const T *w, int64_t V, int H, float inv_temperature, int64_t Tpad, int64_t v0, int64_t piece, T *g) {
-    __shared__ float sa[TK][TS + 4], sb[TK][TS + 4];
-    pdl_wait();
-    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * TS, c0 = static_cast<int64_t>(blockIdx.x) * TS;
-    const int count = ld_dep(&meta->count);
-    if (t0 >= (count > 0 ? (count + kLossTile - 1) / kLossTile * kLossTile : kLossTile)) return;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4];
-    tile_product(x + t0 * Hp, Hp, 1, Tpad - t0, w + (v0 + c0) * H, H, 1, V - v0 - c0, H, acc, sa, sb);
-    const float sc = ld_dep(&meta->scale);
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        const int64_t t = t0 + ty * 4 + a;
-        const int y = ld_dep(tgt + t);
-        const float l = ld_dep(lse2 + t), d = ld_dep(gs + t) * sc;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int64_t v = v0 + c0 + tx * 4 + b;
-            const float p = exp2f(fmaf(acc[a][b], kLog2e * inv_temperature, -l)) - (v == y ? 1.0f : 0.0f);
-            put_rn(g + t * piece + c0 + tx * 4 + b, v < V ? p * d : 0.0f);
-        }
-    }
-}
-
-// part (+)= g w over a piece; grid: 64 columns x 64 tokens
-template <typename T>
-__global__ void __launch_bounds__(256)
-    loss_gw_kernel(const LossMeta *meta, const T *g, int64_t piece, const T *w, int64_t V, int H, int64_t v0, bool first,
-                   int64_t Tpad, float *part) {
-    __shared__ float sa[TK][TS + 4], sb[TK][TS + 4];
-    pdl_wait();
-    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * TS, h0 = static_cast<int64_t>(blockIdx.x) * TS;
-    if (t0 >= ld_dep(&meta->count)) return;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4];
-    const int64_t kk = V - v0 < piece ? V - v0 : piece;
-    tile_product(g + t0 * piece, piece, 1, Tpad - t0, w + v0 * H + h0, 1, static_cast<int64_t>(H), H - h0, kk, acc, sa, sb);
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int64_t h = h0 + tx * 4 + b;
-            if (h < H) {
-                float *o = part + (t0 + ty * 4 + a) * H + h;
-                *o = acc[a][b] + (first ? 0.0f : *o);
+    } else if (warp == 2) {
+        // ---------------- scheduler (the leader CTA only) ----------------
+        if (rank == 0 && lane == 0) {
+            int q = 0;
+            uint32_t parity = 1;
+            uint32_t i = pair;  // every pair's first item is its number
+            for (;;) {
+                if (!wait_or_abort(&sm.item_empty[q], parity, &sm.abort_flag, p.err)) break;
+                const int v = i < work.total ? static_cast<int>(i) : -1;
+                *reinterpret_cast<volatile int *>(&sm.item[q]) = v;
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&sm.item[q], 1)), "r"(v) : "memory");
+                arrive_release(cluster_addr(&sm.item_full[q], 0));
+                arrive_release(cluster_addr(&sm.item_full[q], 1));
+                if (v < 0) break;
+                i = pairs + atomicAdd(p.queue, 1u);
+                if (++q == kQueue) {
+                    q = 0;
+                    parity ^= 1u;
+                }
             }
         }
-}
-
-// dtable (+)= g^T x over a piece; grid: 64 columns x 64 vocabulary rows
-template <typename T, typename O>
-__global__ void __launch_bounds__(256)
-    loss_gx_kernel(const LossMeta *meta, const T *g, int64_t piece, const T *x, int Hp, int64_t V, int H, int64_t v0,
-                   bool accumulate, O *dtable) {
-    __shared__ float sa[TK][TS + 4], sb[TK][TS + 4];
-    pdl_wait();
-    const int64_t c0 = static_cast<int64_t>(blockIdx.y) * TS, h0 = static_cast<int64_t>(blockIdx.x) * TS;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4];
-    tile_product(g + c0, 1, piece, V - v0 - c0, x + h0, 1, static_cast<int64_t>(Hp), H - h0,
-                 static_cast<int64_t>(ld_dep(&meta->count)), acc, sa, sb);
-    const float u = ld_dep(&meta->unscale);
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int64_t v = v0 + c0 + ty * 4 + a, h = h0 + tx * 4 + b;
-            if (v < V && h < H) {
-                O *o = dtable + v * H + h;
-                put_rn(o, acc[a][b] * u + (accumulate ? wide(*o) : 0.0f));
+    } else {
+        // ---------------- epilogue ----------------
+        const int q = warp & 3;  // TMEM lane quarter
+        const int row = static_cast<int>(rank) * kCtaM + q * 32 + lane;  // of the tile
+        const int row0 = static_cast<int>(rank) * kCtaM + q * 32;
+        const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+        const float scale = MODE == 1 ? ld_dep(&p.meta->scale) : 1.0f, unscale = MODE == 1 ? ld_dep(&p.meta->unscale) : 1.0f;
+        int n_acc = 0, n_out = 0;
+        // A buffer of this warp's that no store reads any more.
+        auto out_buffer = [&]() -> uint8_t * {
+            if (lane == 0) bulk_wait_read1();
+            __syncwarp();
+            return sm.out[MODE == 1 ? warp - 3 : 0][MODE == 1 ? n_out & 1 : 0];
+        };
+        auto send = [&](const CUtensorMap *map, const uint8_t *buf, int x, int y, bool add) {
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                if (add) tma_add(map, buf, x, y);
+                else tma_store(map, buf, x, y);
+                bulk_commit();
             }
+            ++n_out;
+        };
+        for (;;) {
+            const int i = next_item(true);
+            if (i < 0) break;
+            const Item t = item_of<MODE>(p, work, i);
+            const int buf = n_acc & 1;
+            const uint32_t acc = tmem + lanes + buf * (kTmemCols / 2);
+            // what the tile needs besides its sums, asked for before they are waited for
+            int y = -1;
+            bool none = false;  // a row past the last token
+            float lse2 = 0.0f, gs = 0.0f;
+            int64_t v0 = 0;
+            const int64_t tok = static_cast<int64_t>(t.m) * kLossTile + row;
+            if (MODE == 0 || t.kind == kLogits) {
+                v0 = p.g_v0 + static_cast<int64_t>(t.n) * kLossTile;
+                const int target = ld_dep(p.tgt + tok);
+                none = target < 0;
+                y = target >= v0 && target < v0 + kLossTile ? static_cast<int>(target - v0) : -1;
+                if (MODE == 1) {
+                    lse2 = ld_dep(p.lse2 + tok);
+                    gs = ld_dep(p.gs + tok) * scale;
+                }
+            }
+            const bool ok = wait_or_abort(&sm.acc_full[buf], (n_acc >> 1) & 1, &sm.abort_flag, p.err);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;  // tcgen05.ld is warp-collective
+            tc_fence_after();
+            ++n_acc;
+            if (MODE == 0) {
+                // Statistics: the maximum m, the sum s of the exponentials below it and the number
+                // of equals.  The maximum's own 1 is left out of the sum, so that a loss near 0 (the
+                // target is the maximum, the rest small) keeps its relative accuracy.
+                float m = -INFINITY, s = 0.0f, z = 0.0f;
+                int equal = 0;
+                for (int c = 0; c < kLossTile / 32; ++c) {
+                    float v[32];
+                    tmem_ld32(acc + c * 32, v);
+                    const int64_t left = p.V - v0 - c * 32;
+                    if (left <= 0) continue;
+                    if (left < 32) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (k >= left) v[k] = -INFINITY;  // counted as equal only where nothing is above -inf
+                    }
+                    if (__any_sync(0xFFFFFFFFu, y >= 0 && (y >> 5) == c)) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (y == c * 32 + k) z = v[k];
+                    }
+                    float top = m;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) top = fmaxf(top, v[k]);
+                    if (top > m) {
+                        s = m == -INFINITY ? s : (s + static_cast<float>(equal)) * ex2((m - top) * p.l2);
+                        equal = 0;
+                        m = top;
+                    }
+                    const float shift = m == -INFINITY ? 0.0f : -m * p.l2;
+                    float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float e = ex2(fmaf(v[k], p.l2, shift));
+                        if (v[k] == m) ++equal;
+                        else s4[k & 3] += e;
+                    }
+                    s += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                }
+                p.stats[static_cast<int64_t>(t.n) * p.Tpad + tok] =
+                    make_float2(m, m == -INFINITY ? s : s + static_cast<float>(equal - 1));
+                if (y >= 0) p.zt[tok] = z;
+            } else if (t.kind == kLogits) {
+                // g, 64 rows of the vocabulary at a time
+                for (int c = 0; c < kLossTile / 64; ++c) {
+                    uint8_t *out = out_buffer();
+                    const int64_t left = p.V - v0 - c * 64;
+                    const bool special = left < 64 || __any_sync(0xFFFFFFFFu, none || (y >= 0 && (y >> 6) == c));
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        float v[32];
+                        tmem_ld32(acc + c * 64 + o * 32, v);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = ex2(fmaf(v[k], p.l2, -lse2));
+                        if (special) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (y == c * 64 + o * 32 + k) v[k] -= 1.0f;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] *= gs;
+                        if (special) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (none || o * 32 + k >= left) v[k] = 0.0f;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            put_piece(out, lane, o * 4 + k, pack16<BF>(v[8 * k], v[8 * k + 1]),
+                                      pack16<BF>(v[8 * k + 2], v[8 * k + 3]), pack16<BF>(v[8 * k + 4], v[8 * k + 5]),
+                                      pack16<BF>(v[8 * k + 6], v[8 * k + 7]));
+                    }
+                    send(&tm_g_write, out, t.n * kLossTile + c * 64, t.m * kLossTile + row0, false);
+                }
+            } else {
+                // sums of dx, or of dtable times the inverse of g's scale
+                const bool dx = t.kind == kDx;
+                const int mode = dx ? (p.first ? kStore32 : kAdd32) : p.dt_mode;
+                const CUtensorMap *map = dx ? &tm_part : &tm_dt;
+                const float u = dx ? 1.0f : unscale;
+                const int h0 = t.n * kLossTile, cols = p.H - h0 < kLossTile ? p.H - h0 : kLossTile;
+                // (a piece starts at a multiple of the tile, and rows past the table's end are not stored)
+                const int64_t out_row = dx ? t.split * p.Tpad + static_cast<int64_t>(t.m) * kLossTile + row0
+                                           : p.d_v0 + static_cast<int64_t>(t.m) * kLossTile + row0;
+                if (mode == kStore16) {
+                    for (int c = 0; c < cols; c += 64) {
+                        uint8_t *out = out_buffer();
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            float v[32];
+                            tmem_ld32(acc + c + o * 32, v);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                put_piece(out, lane, o * 4 + k, pack16<BF>(v[8 * k] * u, v[8 * k + 1] * u),
+                                          pack16<BF>(v[8 * k + 2] * u, v[8 * k + 3] * u),
+                                          pack16<BF>(v[8 * k + 4] * u, v[8 * k + 5] * u),
+                                          pack16<BF>(v[8 * k + 6] * u, v[8 * k + 7] * u));
+                        }
+                        send(map, out, h0 + c, static_cast<int>(out_row), false);
+                    }
+                } else {
+                    for (int c = 0; c < cols; c += 32) {
+                        uint8_t *out = out_buffer();
+                        float v[32];
+                        tmem_ld32(acc + c, v);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            put_piece(out, lane, k, __float_as_uint(v[4 * k] * u), __float_as_uint(v[4 * k + 1] * u),
+                                      __float_as_uint(v[4 * k + 2] * u), __float_as_uint(v[4 * k + 3] * u));
+                        if (mode != kPlain) {
+                            send(map, out, h0 + c, static_cast<int>(out_row), mode == kAdd32);
+                            continue;
+                        }
+                        // a lane to a column: rows that TMA does not take, or sums in 16 bits
+                        __syncwarp();
+                        auto emit = [&](auto *dt) {
+                            const bool in = c + lane < cols;
+                            dt += out_row * p.H + h0 + c + lane;
+#pragma unroll 4
+                            for (int r = 0; r < 32; ++r)
+                                if (in && out_row + r < p.V) {
+                                    const float s = *reinterpret_cast<const float *>(
+                                        out + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+                                    auto *o = dt + static_cast<int64_t>(r) * p.H;
+                                    put_rn(o, p.accumulate ? wide(*o) + s : s);
+                                }
+                        };
+                        if (p.dt_dtype == LHS_F32) emit(static_cast<float *>(p.dtable));
+                        else if (BF) emit(static_cast<__nv_bfloat16 *>(p.dtable));
+                        else emit(static_cast<__half *>(p.dtable));
+                        __syncwarp();
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(cluster_addr(&sm.acc_empty[buf], 0));
         }
-}
-
-template <typename T>
-cudaError_t stats(const LossArgs &a, const LossPlan &p, cudaStream_t stream) {
-    return launch_pdl(loss_stats_kernel<T>, dim3(static_cast<unsigned>(p.vt), static_cast<unsigned>(p.Tpad / TS)), dim3(256),
-                      0, stream, reinterpret_cast<const LossMeta *>(a.ws + p.off_meta),
-                      reinterpret_cast<const int32_t *>(a.ws + p.off_tgt), reinterpret_cast<const T *>(a.ws + p.off_x),
-                      p.Hp, static_cast<const T *>(a.t.data), p.V, p.H, a.inv_temperature, p.Tpad,
-                      reinterpret_cast<float2 *>(a.ws + p.off_stats), reinterpret_cast<float *>(a.ws + p.off_zt));
-}
-
-template <typename T>
-cudaError_t products(const LossArgs &a, const LossPlan &p, cudaStream_t stream) {
-    const LossMeta *meta = reinterpret_cast<const LossMeta *>(a.ws + p.off_meta);
-    const T *x = reinterpret_cast<const T *>(a.ws + p.off_x), *w = static_cast<const T *>(a.t.data);
-    T *g = reinterpret_cast<T *>(a.ws + p.off_g);
-    float *part = reinterpret_cast<float *>(a.ws + p.off_part);
-    const unsigned ht = static_cast<unsigned>((p.H + TS - 1) / TS), tt = static_cast<unsigned>(p.Tpad / TS);
-    for (int64_t v0 = 0; v0 < p.V; v0 += p.piece) {
-        const unsigned vt = static_cast<unsigned>(((p.V - v0 < p.piece ? p.V - v0 : p.piece) + TS - 1) / TS);
-        cudaError_t e = launch_pdl(loss_g_kernel<T>, dim3(vt, tt), dim3(256), 0, stream, meta,
-                                   reinterpret_cast<const int32_t *>(a.ws + p.off_tgt),
-                                   reinterpret_cast<const float *>(a.ws + p.off_lse2),
-                                   reinterpret_cast<const float *>(a.ws + p.off_gs), x, p.Hp, w, p.V, p.H,
-                                   a.inv_temperature, p.Tpad, v0, p.piece, g);
-        if (e == cudaSuccess && a.dx)
-            e = launch_pdl(loss_gw_kernel<T>, dim3(ht, tt), dim3(256), 0, stream, meta, static_cast<const T *>(g), p.piece,
-                           w, p.V, p.H, v0, v0 == 0, p.Tpad, part);
-        if (e == cudaSuccess && a.dtable) {
-            if (a.dtable_dtype == LHS_F32)
-                e = launch_pdl(loss_gx_kernel<T, float>, dim3(ht, vt), dim3(256), 0, stream, meta,
-                               static_cast<const T *>(g), p.piece, x, p.Hp, p.V, p.H, v0, a.accumulate,
-                               static_cast<float *>(a.dtable));
-            else
-                e = launch_pdl(loss_gx_kernel<T, T>, dim3(ht, vt), dim3(256), 0, stream, meta, static_cast<const T *>(g),
-                               p.piece, x, p.Hp, p.V, p.H, v0, a.accumulate, static_cast<T *>(a.dtable));
-        }
-        if (e != cudaSuccess) return e;
+        if (MODE == 1 && lane == 0) bulk_wait_all();  // the stores are complete, and shared memory no longer read
     }
-    return cudaSuccess;
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // the pair is done with its accumulators and barriers
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+    cluster_sync_all();  // neither CTA leaves while its peer may still address it
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+struct Maps {
+    CUtensorMap x, w, g_read, g_write, part, dt;
+};
+
+bool make_box(CUtensorMap *map, int32_t dtype, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch,
+              uint32_t box_cols, uint32_t box_rows) {
+    return make_map(map, dtype == LHS_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                         : dtype == LHS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    base, cols, rows, pitch, box_cols, box_rows);
+}
+
+template <int MODE, bool BF>
+cudaError_t launch(const Maps &m, const Params &p, uint32_t items, cudaStream_t stream) {
+    DeviceInfo dev;
+    cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return e;
+    constexpr int smem = 1024 + static_cast<int>(sizeof(Smem<MODE>));
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    auto kern = loss_kernel<MODE, BF>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    static std::mutex mu;
+    static int pairs[64] = {};  // resident at once
+    int fit;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!pairs[dev.device]) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            int n = dev.num_sms / 2, active = 0;
+            cfg.gridDim = dim3(2 * n);
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&active, kern, &cfg) == cudaSuccess && active > 0 && active < n) n = active;
+            (void)cudaGetLastError();
+            pairs[dev.device] = n < 1 ? 1 : n;
+        }
+        fit = pairs[dev.device];
+    }
+    cfg.gridDim = dim3(2 * (items < static_cast<uint32_t>(fit) ? items : fit));
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, m.x, m.w, m.g_read, m.g_write, m.part, m.dt, p);
+}
+
+// What every launch of a call shares.
+bool common(const LossArgs &a, const LossPlan &p, Maps *m, Params *k) {
+    const int32_t dt = p.bf16 ? LHS_BF16 : LHS_F16;
+    const void *w = p.H % 8 ? static_cast<const void *>(a.ws + p.off_w) : a.t.data;
+    if (!make_box(&m->x, dt, a.ws + p.off_x, p.Hp, p.Tpad, static_cast<uint64_t>(p.Hp) * 2, 64, 64) ||
+        !make_box(&m->w, dt, w, p.Hp, p.V, static_cast<uint64_t>(p.Hp) * 2, 64, 64))
+        return false;
+    m->g_read = m->g_write = m->part = m->dt = m->x;  // replaced where they are used
+    k->meta = reinterpret_cast<const LossMeta *>(a.ws + p.off_meta);
+    k->tgt = reinterpret_cast<const int32_t *>(a.ws + p.off_tgt);
+    k->V = p.V;
+    k->Tpad = p.Tpad;
+    k->H = p.H;
+    k->ht = (p.H + kLossTile - 1) / kLossTile;
+    k->l2 = kLog2e * a.inv_temperature;
+    k->err = a.err;
+    return true;
 }
 
 }  // namespace
 
 cudaError_t launch_loss_stats(const LossArgs &a, const LossPlan &p, cudaStream_t stream) {
-    return p.bf16 ? stats<__nv_bfloat16>(a, p, stream) : stats<__half>(a, p, stream);
+    Maps m;
+    Params k = {};
+    if (!common(a, p, &m, &k)) return cudaErrorInvalidValue;
+    k.queue = reinterpret_cast<uint32_t *>(a.ws + p.off_queue);
+    k.g_tiles = static_cast<int>(p.vt);
+    k.stats = reinterpret_cast<float2 *>(a.ws + p.off_stats);
+    k.zt = reinterpret_cast<float *>(a.ws + p.off_zt);
+    const uint32_t items = static_cast<uint32_t>(p.Tpad / kLossTile * p.vt);
+    return p.bf16 ? launch<0, true>(m, k, items, stream) : launch<0, false>(m, k, items, stream);
 }
+
 cudaError_t launch_loss_products(const LossArgs &a, const LossPlan &p, cudaStream_t stream) {
-    return p.bf16 ? products<__nv_bfloat16>(a, p, stream) : products<__half>(a, p, stream);
+    const int32_t dt = p.bf16 ? LHS_BF16 : LHS_F16;
+    Maps m;
+    Params k = {};
+    if (!common(a, p, &m, &k)) return cudaErrorInvalidValue;
+    k.lse2 = reinterpret_cast<const float *>(a.ws + p.off_lse2);
+    k.gs = reinterpret_cast<const float *>(a.ws + p.off_gs);
+    k.dx = a.dx != nullptr;
+    k.dtable = a.dtable;
+    k.dt_dtype = a.dtable_dtype;
+    k.accumulate = a.accumulate;
+    if (a.dx && !make_box(&m.part, LHS_F32, a.ws + p.off_part, p.H, static_cast<uint64_t>(p.splits) * p.Tpad,
+                          static_cast<uint64_t>(p.part_pitch) * 4, 32, 32))
+        return cudaErrorInvalidValue;
+    if (a.dtable) {
+        // rows of whole 16-byte words go by TMA; sums in 16 bits are added to what the
+        // gradient held before they are rounded, which TMA's addition would do after
+        const bool f32 = a.dtable_dtype == LHS_F32;
+        k.dt_mode = p.H % (f32 ? 4 : 8) || (a.accumulate && !f32) ? kPlain
+                    : !f32                                        ? kStore16
+                    : a.accumulate                                ? kAdd32
+                                                                  : kStore32;
+        if (k.dt_mode != kPlain && !make_box(&m.dt, a.dtable_dtype, a.dtable, p.H, p.V,
+                                             static_cast<uint64_t>(p.H) * (f32 ? 4 : 2), f32 ? 32 : 64, 32))
+            return cudaErrorInvalidValue;
+    }
+    uint32_t *queue = reinterpret_cast<uint32_t *>(a.ws + p.off_queue);
+    const size_t g_bytes = static_cast<size_t>(p.Tpad) * p.piece * 2;
+    const uint64_t pitch = static_cast<uint64_t>(p.piece) * 2;
+    const uint32_t blocks = static_cast<uint32_t>(p.Tpad / kLossTile);
+    for (int i = 0; i <= p.pieces; ++i) {
+        // g of piece i, the products with piece i - 1
+        uint8_t *write = a.ws + p.off_g + (i & 1) * g_bytes, *read = a.ws + p.off_g + ((i & 1) ^ 1) * g_bytes;
+        if (!make_box(&m.g_read, dt, read, p.piece, p.Tpad, pitch, 64, 64) ||
+            !make_box(&m.g_write, dt, write, p.piece, p.Tpad, pitch, 64, 32))
+            return cudaErrorInvalidValue;
+        auto tiles = [&](int n) -> int {
+            if (n < 0 || n >= p.pieces) return 0;
+            const int64_t rows = p.V - n * p.piece < p.piece ? p.V - n * p.piece : p.piece;
+            return static_cast<int>((rows + kLossTile - 1) / kLossTile);
+        };
+        k.queue = queue + i;
+        k.g_v0 = i * p.piece;
+        k.g_tiles = tiles(i);
+        k.d_tiles = tiles(i - 1);
+        k.d_v0 = i > 0 ? (i - 1) * p.piece : 0;
+        const int64_t rows = p.V - k.d_v0 < p.piece ? p.V - k.d_v0 : p.piece;
+        k.d_stages = static_cast<int>((rows + kTileK - 1) / kTileK);
+        // (a last piece may be shorter than the splits; the first one, which writes their sums, is not)
+        k.splits = p.splits < k.d_stages ? p.splits : k.d_stages;
+        k.first = i == 1;
+        const uint32_t items = blocks * k.g_tiles + (k.d_tiles && k.dx ? blocks * k.ht * k.splits : 0u) +
+                               (k.dtable ? static_cast<uint32_t>(k.d_tiles) * k.ht : 0u);
+        const cudaError_t e = p.bf16 ? launch<1, true>(m, k, items, stream) : launch<1, false>(m, k, items, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace lhs

@@ -31,16 +31,20 @@ struct LossPlan {
     size_t off_act;         // int32 [Tpad]: position of a compact row, -1 past count
     size_t off_tgt;         // int32 [Tpad]: its target, -1 past count
     size_t off_x;           // [Tpad x Hp]: its residual, zeros past hidden and count
+    size_t off_w;           // [V x Hp]: the table, where its rows are not whole 16-byte words
+    size_t off_queue;       // uint32 [pieces + 1]: items handed out, of each launch
     // loss
-    size_t off_stats;       // float2 [vt x Tpad]: maximum and sum of exponentials of a tile
+    size_t off_stats;       // float2 [vt x Tpad]: maximum of a tile, sum of its other exponentials
     size_t off_zt;          // f32 [Tpad]: the target's logit
     // gradient
     size_t off_pos;         // int32 [T]: compact row of a position, -1
     size_t off_lse2;        // f32 [Tpad]: lse * log2(e), +inf past count
     size_t off_gs;          // f32 [Tpad]: dloss / temperature, 0 past count
-    size_t off_g;           // [Tpad x piece]: g of a piece of the vocabulary
-    size_t off_part;        // f32 [Tpad x H]: dx so far
+    size_t off_g;           // 2 x [Tpad x piece]: g of a piece of the vocabulary
+    size_t off_part;        // f32 [splits x Tpad x part_pitch]: dx so far
     int64_t piece;          // vocabulary rows of a piece, a multiple of kLossTile
+    int pieces, splits;     // dx's sums are split along a piece's rows
+    int32_t part_pitch;     // hidden rounded up to 4
     size_t bytes;
 };
 LossPlan plan_loss(const lhs_table &t, int64_t tokens, bool grad);

@@ -16,6 +16,7 @@ sums over n terms in f32: n 2^-23 of the sum of magnitudes.  The result's own
 rounding: its type's eps / 2 (f16 subnormals: 2^-25).
 """
 import ctypes
+import math
 
 import pytest
 import torch
@@ -344,9 +345,13 @@ def test_certain_and_hopeless_targets(dtype):
     r = reference(w, x, y, dl)
     loss, lse, err = lhs.lhs_loss(table_of(w), x, y)
     check_loss(loss, lse, r)
-    assert float(loss[0]) == 0.0  # 599 exp(-100) does not show beside 1
-    # 599 exp(-20): what is left of 1 + s, s to half a step of 1
-    assert abs(float(loss[2]) - float(r["loss"][2])) <= 2.0 ** -23
+    # log(1 + 599 exp(-d)): an exponential is good to 2^-21 and 2^-23 d log2(e) of its argument, a sum
+    # of 599 to 2^-15 (the first form's 1 + s, which gave 0 for the first, lost what the second keeps)
+    for k, d in ((0, 100.0), (2, 20.0)):
+        want = math.log1p(599 * math.exp(-d))
+        # exp(-100) = 3.7e-44 lies among the subnormals, whose step is 2^-149: each of the 599 terms is
+        # off by up to one of them besides
+        assert abs(float(loss[k]) - want) <= 2.0 ** -13 * want + 599 * 2.0 ** -149
     dx, dw, _ = lhs.lhs_loss_grad(table_of(w), x, y, lse, dl, err=err)
     check_grad(dx, dw, r)
     assert int(err.item()) == 0
