@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(256)
             }
             const float f[4] = {v.x, v.y, v.z, v.w};
             if (vec && j + 4 <= H) {
-                T o[4];
+                alignas(16) T o[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) put_rn(&o[k], f[k]);
                 if (sizeof(T) == 4) *reinterpret_cast<float4 *>(d + j) = *reinterpret_cast<const float4 *>(o);

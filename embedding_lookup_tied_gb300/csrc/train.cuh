@@ -90,7 +90,7 @@ struct EmbedGradArgs {
     uint8_t *ws;
     int32_t *err;
 };
-size_t embed_grad_workspace(int64_t vocab, int32_t hidden, int64_t n);
+size_t embed_grad_workspace(int32_t hidden, int64_t n);
 cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t stream);
 // Zeroes `bytes` at a 16-byte aligned address.
 cudaError_t launch_zero(void *p, size_t bytes, cudaStream_t stream);

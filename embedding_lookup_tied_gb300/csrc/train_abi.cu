@@ -133,7 +133,7 @@ int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t 
 
 int64_t lhs_embed_grad_workspace(int64_t vocab, int32_t hidden, int64_t n) {
     if (vocab < 1 || vocab > 0x7FFFFFFFll || hidden < 1 || hidden > kMaxTrainHidden || n < 0 || n > kMaxLookups) return -1;
-    return static_cast<int64_t>(embed_grad_workspace(vocab, hidden, n));
+    return static_cast<int64_t>(embed_grad_workspace(hidden, n));
 }
 
 int lhs_embed_grad(int64_t vocab, int32_t hidden, const int32_t *d_ids, int64_t n, int32_t ignore, float scale,
