@@ -36,8 +36,8 @@ struct PackParams {
     int32_t *act, *tgt, *pos;
     float *lse2, *gs;
     uint16_t *xc;
-    uint32_t *queue;         // cleared
-    int n_queue;
+    uint32_t *sync;          // cleared
+    int64_t n_sync;
     int32_t *err;
 };
 
@@ -61,23 +61,13 @@ __device__ __forceinline__ int block_rank(bool flag, int &total, int *warp_n) {
     return before + __popc(m & ((1u << lane) - 1u));
 }
 
-// Copies one residual (or zeros, src null) into a compact row.  Warp-collective.
-__device__ __forceinline__ void pack_row(const uint16_t *src, uint16_t *dst, int H, int Hp, bool vec, int lane) {
-    uint4 *d4 = reinterpret_cast<uint4 *>(dst);
-    for (int j = lane; j < Hp / 8; j += 32) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (src) {
-            if (vec && 8 * j + 8 <= H) {
-                w = ld_dep(reinterpret_cast<const uint4 *>(src) + j);
-            } else {
-                uint32_t u[8];
+// Word c (8 values) of a row of H values; zeros past them.
+__device__ __forceinline__ uint4 row_word(const uint16_t *row, int c, int H, bool vec) {
+    if (vec && 8 * c + 8 <= H) return ld_dep(reinterpret_cast<const uint4 *>(row) + c);
+    uint32_t u[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = 8 * j + i < H ? ld_dep(src + 8 * j + i) : 0u;
-                w = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
-            }
-        }
-        d4[j] = w;
-    }
+    for (int i = 0; i < 8; ++i) u[i] = 8 * c + i < H ? ld_dep(row + 8 * c + i) : 0u;
+    return make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
 }
 
 // Each CTA takes an equal range of positions.  It counts the ones before it
@@ -97,6 +87,7 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
     pdl_trigger();  // after the wait, so that whoever follows has everything earlier behind it
     __syncthreads();
     int before = 0, all = 0;
+#pragma unroll 8
     for (int64_t i = tid; i < p.T; i += kPackThreads) {
         const int on = takes_part(p, ld_dep(p.targets + i)) ? 1 : 0;
         all += on;
@@ -140,9 +131,14 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
         }
         __syncthreads();
         const int n = static_cast<int>(r1 - b < kPackThreads ? r1 - b : kPackThreads);
-        for (int i = warp; i < n; i += kPackWarps) {
-            const int k = rank_of[i];
-            if (k >= 0) pack_row(p.x + (b + i) * p.x_stride, p.xc + static_cast<int64_t>(k) * p.Hp, p.H, p.Hp, p.vec, lane);
+        const uint32_t words = p.Hp / 8;
+#pragma unroll 4
+        for (uint32_t i = tid; i < n * words; i += kPackThreads) {
+            const uint32_t r = i / words, c = i - r * words;
+            const int k = rank_of[r];
+            if (k >= 0)
+                reinterpret_cast<uint4 *>(p.xc + static_cast<int64_t>(k) * p.Hp)[c] =
+                    row_word(p.x + (b + r) * p.x_stride, c, p.H, p.vec);
         }
         __syncthreads();
         base += total;
@@ -150,7 +146,8 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
     // rows past the last one, to the end of its tile: zeros, no target, no gradient
     const int64_t end = count > 0 ? (static_cast<int64_t>(count) + kLossTile - 1) / kLossTile * kLossTile : kLossTile;
     for (int64_t r = count + blockIdx.x * kPackWarps + warp; r < end; r += static_cast<int64_t>(gridDim.x) * kPackWarps) {
-        pack_row(nullptr, p.xc + r * p.Hp, p.H, p.Hp, p.vec, lane);
+        for (int c = lane; c < p.Hp / 8; c += 32)
+            reinterpret_cast<uint4 *>(p.xc + r * p.Hp)[c] = make_uint4(0u, 0u, 0u, 0u);
         if (lane == 0) {
             p.act[r] = -1;
             p.tgt[r] = -1;
@@ -160,20 +157,22 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
             }
         }
     }
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPackThreads + tid; i < p.n_sync;
+         i += static_cast<int64_t>(gridDim.x) * kPackThreads)
+        p.sync[i] = 0u;
     if (bad) set_err(p.err, LHS_ERRBIT_BAD_TOKEN);
     if (nonfinite) set_err(p.err, LHS_ERRBIT_NONFINITE);
     if (blockIdx.x == 0) {
-        for (int i = tid; i < p.n_queue; i += kPackThreads) p.queue[i] = 0u;
         // The power of two that brings the largest |g| into (1/4, 1] (bf16: its range needs no
         // more, and larger terms could overflow sums that fit) or up to 2^15 (f16: what lies
         // 2^-29 below it is still normal, 2^-39 below it the last subnormal).
         float top = 0.0f;
         if (GRAD) {
-            for (int64_t i = tid; i < p.T; i += kPackThreads)
-                if (takes_part(p, ld_dep(p.targets + i))) {
-                    const float d = fabsf(ld_dep(p.dloss + i) * p.inv_temperature);
-                    if (isfinite(d)) top = fmaxf(top, d);
-                }
+#pragma unroll 8
+            for (int64_t i = tid; i < p.T; i += kPackThreads) {
+                const float d = fabsf(ld_dep(p.dloss + i) * p.inv_temperature);
+                if (takes_part(p, ld_dep(p.targets + i)) && isfinite(d)) top = fmaxf(top, d);
+            }
             __shared__ float warp_top[kPackWarps];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
@@ -200,63 +199,77 @@ __global__ void __launch_bounds__(256)
     pdl_trigger();
     for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < V;
          r += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5)
-        pack_row(w + r * H, out + r * Hp, H, Hp, false, lane);
+        for (int c = lane; c < Hp / 8; c += 32)
+            reinterpret_cast<uint4 *>(out + r * Hp)[c] = row_word(w + r * H, c, H, false);
 }
 
-// Joins a token's tiles: 32 tokens to a CTA, whose warps share the tiles.  A
-// pair (m, s) stands for (1 + s) exp(m): the 1 is the maximum's own term, kept
-// out of the sums so that log1p sees a small rest unspoilt.  The warps' pairs
-// are joined in their order.
-constexpr int kMergeWarps = 32;
-__global__ void __launch_bounds__(32 * kMergeWarps)
+// A pair (m, s) stands for (1 + s) exp(m): the 1 is the maximum's own term, kept
+// out of the sums so that log1p sees a small rest unspoilt.
+__device__ __forceinline__ void join_pair(float &m, float &s, float om, float os, float l2) {
+    if (om == -INFINITY) {
+        s += os;  // nothing, or NaN
+    } else if (m == -INFINITY) {
+        m = om;
+        s += os;
+    } else {
+        const float lo = fminf(m, om), hi = fmaxf(m, om);
+        s = (om > m ? os : s) + (1.0f + (om > m ? s : os)) * exp2f((lo - hi) * l2);
+        m = hi;
+    }
+}
+
+// Joins a token's tiles: 8 tokens to a CTA, 128 threads to a token, which take the
+// tiles in turn; their pairs are joined in a fixed order.  (32 tokens to a CTA with
+// 32 threads each: 22 us for 256 tokens and 1,024 tiles.)
+constexpr int kMergeTokens = 8, kMergeWarps = 32, kMergeThreads = 32 * kMergeWarps;
+__global__ void __launch_bounds__(kMergeThreads)
     loss_merge_kernel(const LossMeta *meta, const int32_t *act, const float2 *stats, const float *zt, int64_t vt,
                       int64_t Tpad, float inv_temperature, float *loss, float *lse, int32_t *err) {
-    __shared__ float2 part[kMergeWarps][32];
+    constexpr int kShare = kMergeThreads / kMergeTokens, kBatch = 8;
+    __shared__ float2 part[kMergeWarps][kMergeTokens];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kMergeTokens, i = i0 + threadIdx.x % kMergeTokens;
     const int count = ld_dep(&meta->count);
-    if (static_cast<int64_t>(blockIdx.x) * 32 >= count) return;
+    if (i0 >= count) return;
     const float l2 = kLog2e * inv_temperature;
     float m = -INFINITY, s = 0.0f;
-    auto join = [&](float om, float os) {
-        if (om == -INFINITY) {
-            s += os;  // nothing, or NaN
-        } else if (m == -INFINITY) {
-            m = om;
-            s += os;
-        } else {
-            const float lo = fminf(m, om), hi = fmaxf(m, om);
-            s = (om > m ? os : s) + (1.0f + (om > m ? s : os)) * exp2f((lo - hi) * l2);
-            m = hi;
-        }
-    };
-    if (i < count)
-#pragma unroll 4
-        for (int64_t v = warp; v < vt; v += kMergeWarps) {
-            const float2 t = ld_dep(stats + v * Tpad + i);
-            join(t.x, t.y);
-        }
-    part[warp][lane] = make_float2(m, s);
+    for (int64_t v0 = threadIdx.x / kMergeTokens; v0 < vt; v0 += kShare * kBatch) {
+        float2 t[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            t[k] = v0 + k * kShare < vt ? ld_dep(stats + (v0 + k * kShare) * Tpad + i) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) join_pair(m, s, t[k].x, t[k].y, l2);
+    }
+#pragma unroll
+    for (int o = kMergeTokens; o < 32; o <<= 1)
+        join_pair(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o), l2);
+    if (lane < kMergeTokens) part[warp][lane] = make_float2(m, s);
     __syncthreads();
-    if (warp == 0 && i < count) {
-        for (int w = 1; w < kMergeWarps; ++w) join(part[w][lane].x, part[w][lane].y);
+    if (warp >= kMergeTokens) return;
+    const float2 t = part[lane][warp];  // a warp to a token
+    m = t.x, s = t.y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+        join_pair(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o), l2);
+    if (lane == 0 && i0 + warp < count) {
         const float ls = log1pf(s);
         float l = m * inv_temperature + ls;
-        float c = (m - ld_dep(zt + i)) * inv_temperature + ls;
+        float c = (m - ld_dep(zt + i0 + warp)) * inv_temperature + ls;
         if (!isfinite(l)) {
             l = c = __int_as_float(0x7FC00000);
             set_err(err, LHS_ERRBIT_NONFINITE);
         }
-        const int32_t r = ld_dep(act + i);
+        const int32_t r = ld_dep(act + i0 + warp);
         loss[r] = c;
         lse[r] = l;
     }
 }
 
 // dx of every position: its compact row's sums, joined in order, times the
-// inverse of g's scale; or zeros.  A warp to a position.
+// inverse of g's scale; or zeros.  A warp to 128 columns of a position.
 template <typename T>
 __global__ void __launch_bounds__(256)
     loss_dx_kernel(const LossMeta *meta, const int32_t *pos, const float *part, int splits, int64_t Tpad, int pitch,
@@ -264,11 +277,14 @@ __global__ void __launch_bounds__(256)
     const int lane = threadIdx.x & 31;
     pdl_wait();
     const float u = ld_dep(&meta->unscale);
-    for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < n;
-         r += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5) {
+    const uint32_t blocks = (H + 127) / 128;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; i < n * blocks;
+         i += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5) {
+        const int64_t r = i / blocks;
         const int32_t c = ld_dep(pos + r);
         T *d = dx + r * dx_stride;
-        for (int j = lane * 4; j < H; j += 128) {
+        const int j = static_cast<int>(i - r * blocks) * 128 + lane * 4;
+        if (j < H) {
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (c >= 0) {
                 const float4 *src = reinterpret_cast<const float4 *>(part + static_cast<int64_t>(c) * pitch + j);
@@ -299,7 +315,7 @@ __global__ void __launch_bounds__(256)
 
 template <typename T>
 cudaError_t launch_dx(const LossArgs &a, const LossPlan &p, const DeviceInfo &dev, cudaStream_t stream) {
-    const int64_t want = (p.T + 7) / 8;
+    const int64_t want = (p.T * ((p.H + 127) / 128) + 7) / 8;
     const bool vec = reinterpret_cast<uintptr_t>(a.dx) % (4 * sizeof(T)) == 0 && a.dx_stride % 4 == 0;
     return launch_pdl(loss_dx_kernel<T>, dim3(static_cast<unsigned>(want < 8 * dev.num_sms ? want : 8 * dev.num_sms)),
                       dim3(256), 0, stream, reinterpret_cast<const LossMeta *>(a.ws + p.off_meta),
@@ -331,8 +347,8 @@ cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &
     k.lse2 = reinterpret_cast<float *>(a.ws + p.off_lse2);
     k.gs = reinterpret_cast<float *>(a.ws + p.off_gs);
     k.xc = reinterpret_cast<uint16_t *>(a.ws + p.off_x);
-    k.queue = reinterpret_cast<uint32_t *>(a.ws + p.off_queue);
-    k.n_queue = p.pieces + 1;
+    k.sync = reinterpret_cast<uint32_t *>(a.ws + p.off_sync);
+    k.n_sync = p.n_sync;
     k.err = a.err;
     cudaError_t e = cudaSuccess;
     if (p.H % 8) {
@@ -342,7 +358,8 @@ cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &
                        reinterpret_cast<uint16_t *>(a.ws + p.off_w));
         if (e != cudaSuccess) return e;
     }
-    const int64_t want = (p.T + kPackWarps - 1) / kPackWarps;
+    // (by whole tiles of tokens: the rows that fill the last one up are written too)
+    const int64_t want = p.Tpad;
     const unsigned grid = static_cast<unsigned>(want < 4 * dev.num_sms ? want : 4 * dev.num_sms);
     return launch_pdl(p.grad ? loss_pack_kernel<true> : loss_pack_kernel<false>, dim3(grid), dim3(kPackThreads), 0,
                       stream, k);
@@ -352,29 +369,39 @@ cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &
 
 namespace {
 
-// Rows of a piece: g of two pieces and the table's rows of one should stay in
-// L2 between the launch that writes or reads them first and the next.
-constexpr int64_t kPieceBytes = 64ll << 20;
+// A piece's g and rows of the table should still be in L2 (129 MB) when the products
+// read them; three to five pieces are under way at a time.
+constexpr int64_t kPieceBytes = 32ll << 20;
 constexpr int kPairs = 76;  // of CTAs that run at once
 
 void choose_pieces(LossPlan *p) {
-    int64_t rows = kPieceBytes / (2 * (p->Tpad > p->Hp ? p->Tpad : p->Hp));
-    if (rows < 2048) rows = 2048;
-    p->pieces = static_cast<int>((p->V + rows - 1) / rows);
-    p->piece = round_up((p->V + p->pieces - 1) / p->pieces, kLossTile);
+    // A tile of dtable has T / 64 stages (64 of k of a 256 x 256 tile), a pair's share of a piece
+    // 3 T rows H / (kPairs 256 256 64): where the share is no shorter than the tile, that is rows * H >=
+    // 1.7 M, pieces follow each other without waiting.
+    int64_t rows = kPieceBytes / (2 * (p->Tpad + p->Hp));
+    if (rows < (1700ll << 10) / p->H) rows = (1700ll << 10) / p->H;
+    if (rows < 2 * kLossTile) rows = 2 * kLossTile;
+    const int64_t n = (p->V + rows - 1) / rows;
+    p->piece = round_up((p->V + n - 1) / n, kLossTile);
     p->pieces = static_cast<int>((p->V + p->piece - 1) / p->piece);
     p->part_pitch = static_cast<int32_t>(round_up(p->H, 4));
-    // stages (64 of k of a 256 x 256 tile) of a launch, and of one tile of dx: no item should
-    // take more than a third of a pair's share
     const int64_t blocks = p->Tpad / kLossTile, gt = p->piece / kLossTile, ht = (p->H + kLossTile - 1) / kLossTile;
     const int64_t kh = (p->H + 63) / 64, kp = (p->V < p->piece ? p->V + 63 : p->piece) / 64;
-    const int64_t total = blocks * gt * kh + blocks * ht * kp + gt * ht * (p->Tpad / 64);
-    int64_t most = total / kPairs / 3;
-    if (most < 16) most = 16;
+    const int64_t share = (blocks * gt * kh + blocks * ht * kp + gt * ht * (p->Tpad / 64)) / kPairs + 1;
+    // a tile of dx takes no longer than a share; the logits run ahead of the products by the pieces
+    // that their tiles take
+    const int64_t most = share > 16 ? share : 16;
     int64_t splits = (kp + most - 1) / most;
     if (splits > 32) splits = 32;
     if (splits > kp) splits = kp;
     p->splits = static_cast<int>(splits < 1 ? 1 : splits);
+    const int64_t ahead = 2 + kh / share;
+    p->ahead = static_cast<int>(ahead < 6 ? ahead : 6);
+    if (p->ahead > p->pieces) p->ahead = p->pieces;
+    p->slots = p->ahead + 2 < p->pieces ? p->ahead + 2 : p->pieces;
+    // the queue, two counters to a piece, a word to each warp's part of dx's sums
+    p->n_sync = 1 + 2ll * p->pieces + blocks * ht * p->splits * kLossSyncWarps;
+    p->items = blocks * p->vt + p->pieces * blocks * ht * p->splits + p->vt * ht;
 }
 
 }  // namespace
@@ -401,16 +428,17 @@ LossPlan plan_loss(const lhs_table &t, int64_t tokens, bool grad) {
     p.off_x = take(p.Tpad * p.Hp * 2);
     p.off_w = take(p.H % 8 ? p.V * p.Hp * 2 : 0);
     if (!grad) {
-        p.off_queue = take(4);
+        p.n_sync = 1;
+        p.off_sync = take(4);
         p.off_stats = take(p.vt * p.Tpad * 8);
         p.off_zt = take(p.Tpad * 4);
     } else {
         choose_pieces(&p);
-        p.off_queue = take((p.pieces + 1) * 4);
+        p.off_sync = take(p.n_sync * 4);
         p.off_pos = take(p.T * 4);
         p.off_lse2 = take(p.Tpad * 4);
         p.off_gs = take(p.Tpad * 4);
-        p.off_g = take(2 * p.Tpad * p.piece * 2);
+        p.off_g = take(p.slots * p.Tpad * p.piece * 2);
         p.off_part = take(p.splits * p.Tpad * p.part_pitch * 4);
     }
     p.bytes = at;
@@ -423,7 +451,7 @@ cudaError_t launch_loss(const LossArgs &a, const LossPlan &p, cudaStream_t strea
     if (e != cudaSuccess) return e;
     if ((e = launch_pack(a, p, dev, stream)) != cudaSuccess) return e;
     if ((e = launch_loss_stats(a, p, stream)) != cudaSuccess) return e;
-    return launch_pdl(loss_merge_kernel, dim3(static_cast<unsigned>(p.Tpad / 32)), dim3(32 * kMergeWarps), 0, stream,
+    return launch_pdl(loss_merge_kernel, dim3(static_cast<unsigned>(p.Tpad / kMergeTokens)), dim3(kMergeThreads), 0, stream,
                       reinterpret_cast<const LossMeta *>(a.ws + p.off_meta),
                       reinterpret_cast<const int32_t *>(a.ws + p.off_act),
                       reinterpret_cast<const float2 *>(a.ws + p.off_stats),

@@ -13,12 +13,15 @@
 // Operands whose k is not the contiguous index (W for dx, both for dtable) are
 // staged as they lie and read "MN-major": no transposed copy is made.
 //
-// The gradient goes through the vocabulary in pieces.  One launch computes g of
-// a piece and the two products with g of the piece before, which no item of
-// the launch has to wait for.  Items (tiles) come from one queue, long ones
-// first, so that the short ones (g) even the pairs' loads out.  dx's tiles are
-// few and their k is long, so they are split along k; each split adds up in f32
-// sums of its own, which one kernel joins in order at the end.
+// The gradient goes through the vocabulary in pieces, in one launch: the logits
+// of a few pieces run ahead, so that a piece's g and rows are still in L2 when its
+// products read them.  Items (tiles) come from one queue, in an order in which an
+// item waits only for items before it: g for the products that read the slot
+// which it overwrites, the products for the piece's g, and the sums of dx for the
+// piece before (so that they are added up in order).  Pairs take items as they
+// run, so what is waited for is always with a pair that runs, however many do.
+// dx's tiles are few and their k is long, so they are split along k; each split
+// adds up in f32 sums of its own, which one kernel joins in order at the end.
 //
 // The logits are never stored: statistics leave a tile as (maximum, sum of the
 // other exponentials) of each token, g as 16-bit values that the products read
@@ -36,11 +39,9 @@ constexpr int kCtaM = 128;                    // rows of a tile that a CTA holds
 constexpr int kTileK = 64;
 constexpr int kBoxBytes = 64 * 64 * 2;        // what one TMA load brings: 64 x 64 values
 constexpr int kOperandBytes = 2 * kBoxBytes;  // a CTA's part of A, or of B, of a stage
-constexpr int kEpiWarps = 4;
-constexpr int kThreads = 32 * (3 + kEpiWarps);  // producer, MMA issuer, scheduler, epilogue
 constexpr int kTmemCols = 512;
 constexpr int kStoreBytes = 32 * 128;         // an epilogue warp's store: 32 rows of 128 bytes
-constexpr int kQueue = 4;                     // items handed out ahead
+constexpr int kQueue = 3;                     // items handed out ahead
 
 enum { kLogits = 0, kDx = 1, kDtable = 2 };
 enum { kStore16 = 0, kStore32 = 1, kAdd32 = 2, kPlain = 3 };  // how dtable is written
@@ -51,16 +52,18 @@ struct Params {
     int64_t V, Tpad;
     int H, ht;               // hidden; tiles of it
     float l2;                // log2(e) / temperature
-    uint32_t *queue;         // items handed out beyond every pair's first; 0 at the start
+    uint32_t *queue;         // items handed out; 0 at the start
     int32_t *err;
-    int64_t g_v0;            // logits: first row and tiles
-    int g_tiles;
+    int64_t piece;           // rows of a piece, and tiles of them (statistics: one piece)
+    int pieces, piece_tiles, last_tiles;
     float2 *stats;           // statistics
     float *zt;
     const float *lse2, *gs;  // g
-    bool dx, first;
-    int64_t d_v0;            // dx, dtable: first row, tiles and stages of the piece
-    int d_tiles, d_stages, splits;
+    bool dx;
+    int ahead, slots, splits;
+    uint32_t *g_done;        // [pieces] warps that have written a tile of g
+    uint32_t *read_done;     // [pieces] products that have read it
+    uint32_t *dx_done;       // [tiles of dx x splits x kLossSyncWarps] pieces added up
     int dt_mode, dt_dtype;
     bool accumulate;
     void *dtable;
@@ -70,18 +73,35 @@ template <int MODE>
 struct Conf {
     static constexpr bool kGrad = MODE == 1;
     static constexpr int kStages = kGrad ? 6 : 7;
+    // The gradient's tiles are taken out by two warps to each quarter of TMEM's lanes, which share
+    // the columns 64 at a time.
+    static constexpr int kEpiWarps = kGrad ? 8 : 4;
+    static constexpr int kThreads = 32 * (3 + kEpiWarps);  // producer, MMA issuer, scheduler, epilogue
+    static constexpr int kOutBuffers = 1;
 };
+
+// A tile to work on, as the scheduler hands it out.
+struct alignas(16) Item {
+    int kind;     // -1: the end
+    int piece;
+    int m;        // tile of M: block of tokens, or of the piece's rows
+    int n;        // tile of N: of the piece's rows (logits), or of hidden
+    int split;    // dx
+    int k0, k1;   // stages
+    int width;    // N of the MMAs, a multiple of 32
+};
+static_assert(sizeof(Item) == 32, "two words of 16 bytes");
 
 template <int MODE>
 struct Smem {
     static constexpr int S = Conf<MODE>::kStages;
     uint8_t a[S][kOperandBytes];
     uint8_t b[S][kOperandBytes];
-    uint8_t out[Conf<MODE>::kGrad ? kEpiWarps : 1][Conf<MODE>::kGrad ? 2 : 1][Conf<MODE>::kGrad ? kStoreBytes : 16];
+    uint8_t out[Conf<MODE>::kGrad ? Conf<MODE>::kEpiWarps : 1][Conf<MODE>::kOutBuffers][Conf<MODE>::kGrad ? kStoreBytes : 16];
     uint64_t full[S], empty[S];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t item_full[kQueue], item_empty[kQueue];
-    int item[kQueue];
+    Item item[kQueue];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -124,7 +144,10 @@ __device__ __forceinline__ void tma_add(const CUtensorMap *map, const void *src,
                  : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -132,15 +155,23 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same, releasing what this thread has read or written in shared memory.
-__device__ __forceinline__ void arrive_release(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Whether the phase is over, without a wait.
+__device__ __forceinline__ bool test_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(smem_u32(bar)), "r"(parity)
@@ -161,6 +192,37 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, in
     set_err(err, LHS_ERRBIT_TIMEOUT);
     *reinterpret_cast<volatile int *>(abort_flag) = 1;
     return false;
+}
+// Counters in global memory that CTAs tell one another by.
+__device__ __forceinline__ void add_release(uint32_t *p, uint32_t v) {
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void add_relaxed(uint32_t *p, uint32_t v) {
+    asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t *p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+// What TMA reads or writes next comes after what this thread has acquired.
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+// Bounded wait of one thread until *p reaches `target`.
+__device__ __forceinline__ bool wait_count(const uint32_t *p, uint32_t target, int *abort_flag, int32_t *err) {
+    if (load_acquire(p) < target) {
+        const uint64_t t0 = global_ns();
+        while (load_acquire(p) < target) {
+            if (*reinterpret_cast<const volatile int *>(abort_flag)) return false;
+            if (global_ns() - t0 > kWaitTimeoutNs) {
+                set_err(err, LHS_ERRBIT_TIMEOUT);
+                *reinterpret_cast<volatile int *>(abort_flag) = 1;
+                return false;
+            }
+            __nanosleep(64);
+        }
+    }
+    fence_async_global();
+    return true;
 }
 // One lane of the warp for the MMAs: the whole warp runs the loop around them,
 // so that their operands stay in uniform registers.
@@ -211,6 +273,29 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+// 64 columns: both loads are under way before the first is waited for.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+            "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+            : "=r"(r[32 * o + 0]), "=r"(r[32 * o + 1]), "=r"(r[32 * o + 2]), "=r"(r[32 * o + 3]), "=r"(r[32 * o + 4]),
+              "=r"(r[32 * o + 5]), "=r"(r[32 * o + 6]), "=r"(r[32 * o + 7]), "=r"(r[32 * o + 8]), "=r"(r[32 * o + 9]),
+              "=r"(r[32 * o + 10]), "=r"(r[32 * o + 11]), "=r"(r[32 * o + 12]), "=r"(r[32 * o + 13]),
+              "=r"(r[32 * o + 14]), "=r"(r[32 * o + 15]), "=r"(r[32 * o + 16]), "=r"(r[32 * o + 17]),
+              "=r"(r[32 * o + 18]), "=r"(r[32 * o + 19]), "=r"(r[32 * o + 20]), "=r"(r[32 * o + 21]),
+              "=r"(r[32 * o + 22]), "=r"(r[32 * o + 23]), "=r"(r[32 * o + 24]), "=r"(r[32 * o + 25]),
+              "=r"(r[32 * o + 26]), "=r"(r[32 * o + 27]), "=r"(r[32 * o + 28]), "=r"(r[32 * o + 29]),
+              "=r"(r[32 * o + 30]), "=r"(r[32 * o + 31])
+            : "r"(taddr + 32 * o)
+            : "memory");
+    // the values are not there before this; nothing that uses them moves above it
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
+}
 // 2^x, relative error below 2^-21: a thousandth of what g is rounded by, and
 // of the order of an f32 logit's own rounding in a sum of exponentials.
 __device__ __forceinline__ float ex2(float x) {
@@ -235,30 +320,68 @@ __device__ __forceinline__ void put_piece(uint8_t *buf, int r, int i, uint32_t x
 // ---------------------------------------------------------------------------
 // items
 // ---------------------------------------------------------------------------
-struct Item {
-    int kind;
-    int m;        // tile of M: block of tokens, or of the piece's rows
-    int n;        // tile of N: of rows (logits), or of hidden
-    int split;    // dx
-    int k0, k1;   // stages
-    int width;    // N of the MMAs, a multiple of 32
+// The queue: g of the first `ahead` pieces; then each piece's products, dx first,
+// followed by g of the piece `ahead` of it.
+// Quotients of numbers below 2^31: with 2^(l-1) < d <= 2^l and mul = ceil(2^(31+l) / d), which is
+// below 2^32, n mul / 2^(31+l) exceeds n / d by less than n / 2^(31+l) < 1 / d.
+struct Divisor {
+    uint32_t d, mul, shift;
+    __device__ __forceinline__ void set(uint32_t d_) {
+        d = d_;
+        uint32_t l = 0;
+        while (l < 31 && (1u << l) < d) ++l;
+        shift = 31 + l;
+        mul = static_cast<uint32_t>(((1ull << shift) + d - 1) / d);
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t n) const {
+        return static_cast<uint32_t>((static_cast<uint64_t>(n) * mul) >> shift);
+    }
 };
 struct Work {
-    uint32_t blocks, n_dx, n_dt, total;
+    uint32_t blocks, total;
     int token_stages;
+    uint32_t before;      // g of the first pieces
+    Divisor block, head, period, ht, splits;  // what the scheduler divides by
 };
+__device__ __forceinline__ int tiles_of(const Params &p, int piece) {
+    return piece + 1 < p.pieces ? p.piece_tiles : p.last_tiles;
+}
+__device__ __forceinline__ int stages_of(const Params &p, int piece) {
+    const int64_t rows = piece + 1 < p.pieces ? p.piece : p.V - piece * p.piece;
+    return static_cast<int>((rows + kTileK - 1) / kTileK);
+}
+__device__ __forceinline__ int splits_of(const Params &p, int piece) {
+    const int stages = stages_of(p, piece);
+    return p.splits < stages ? p.splits : stages;
+}
+__device__ __forceinline__ uint32_t n_dx_of(const Params &p, const Work &w, int piece) {
+    return p.dx ? w.blocks * p.ht * splits_of(p, piece) : 0u;
+}
+__device__ __forceinline__ uint32_t n_products_of(const Params &p, const Work &w, int piece) {
+    return n_dx_of(p, w, piece) + (p.dtable ? static_cast<uint32_t>(tiles_of(p, piece)) * p.ht : 0u);
+}
 template <int MODE>
 __device__ __forceinline__ Work work_of(const Params &p) {
     Work w = {};
     const int count = ld_dep(&p.meta->count);
     w.blocks = count > 0 ? (static_cast<uint32_t>(count) + kLossTile - 1) / kLossTile : 1u;
     w.token_stages = count > 0 ? (count + kTileK - 1) / kTileK : 1;
+    w.total = w.blocks * (static_cast<uint32_t>(p.pieces - 1) * p.piece_tiles + p.last_tiles);
     if (MODE == 1) {
-        w.n_dx = p.dx && p.d_tiles ? w.blocks * p.ht * p.splits : 0;
-        w.n_dt = p.dtable ? static_cast<uint32_t>(p.d_tiles) * p.ht : 0;
+        w.before = p.ahead < p.pieces ? w.blocks * p.ahead * p.piece_tiles : w.total;
+        w.total += static_cast<uint32_t>(p.pieces - 1) * n_products_of(p, w, 0) + n_products_of(p, w, p.pieces - 1);
     }
-    w.total = w.n_dx + w.n_dt + w.blocks * p.g_tiles;
     return w;
+}
+template <int MODE>
+__device__ __forceinline__ void set_divisors(const Params &p, Work &w) {
+    w.block.set(w.blocks);
+    if (MODE == 1) {
+        w.head.set(w.blocks * p.piece_tiles);
+        w.period.set(n_products_of(p, w, 0) + w.blocks * p.piece_tiles);
+        w.ht.set(p.ht);
+        w.splits.set(p.splits);
+    }
 }
 __device__ __forceinline__ int width_of(int H, int tile) {
     const int left = H - tile * kLossTile;
@@ -267,29 +390,63 @@ __device__ __forceinline__ int width_of(int H, int tile) {
 template <int MODE>
 __device__ __forceinline__ Item item_of(const Params &p, const Work &w, uint32_t i) {
     Item t = {};
-    if (MODE == 1 && i < w.n_dx) {
-        t.kind = kDx;
-        t.n = i % p.ht;
-        i /= p.ht;
-        t.split = i % p.splits;
-        t.m = i / p.splits;
-        t.k0 = static_cast<int>(static_cast<int64_t>(p.d_stages) * t.split / p.splits);
-        t.k1 = static_cast<int>(static_cast<int64_t>(p.d_stages) * (t.split + 1) / p.splits);
-        t.width = width_of(p.H, t.n);
-    } else if (MODE == 1 && i < w.n_dx + w.n_dt) {
-        i -= w.n_dx;
-        t.kind = kDtable;
-        t.n = i % p.ht;
-        t.m = i / p.ht;
-        t.k1 = w.token_stages;
-        t.width = width_of(p.H, t.n);
-    } else {
-        i -= w.n_dx + w.n_dt;
+    bool logits = true;
+    if (MODE == 1) {
+        if (i < w.before) {
+            t.piece = w.head.of(i);
+            i -= t.piece * w.head.d;
+        } else {
+            i -= w.before;
+            // pieces whose products, and the logits that follow them, are whole
+            const int whole = p.pieces - p.ahead - 1;
+            int q = 0;
+            if (whole > 0) {
+                q = static_cast<int>(w.period.of(i));
+                q = q < whole ? q : whole;
+                i -= q * w.period.d;
+            }
+            for (;; ++q) {  // a few steps at the end
+                const uint32_t nq = n_products_of(p, w, q);
+                if (i < nq) {
+                    t.piece = q;
+                    logits = false;
+                    break;
+                }
+                i -= nq;
+                const uint32_t g = q + p.ahead < p.pieces ? w.blocks * tiles_of(p, q + p.ahead) : 0u;
+                if (i < g) {
+                    t.piece = q + p.ahead;
+                    break;
+                }
+                i -= g;
+            }
+        }
+    }
+    if (logits) {
         t.kind = kLogits;
-        t.m = i % w.blocks;
-        t.n = i / w.blocks;
+        t.n = w.block.of(i);
+        t.m = i - t.n * w.blocks;
         t.k1 = (p.H + kTileK - 1) / kTileK;
         t.width = kLossTile;
+        return t;
+    }
+    const uint32_t n_dx = n_dx_of(p, w, t.piece);
+    t.kind = i < n_dx ? kDx : kDtable;
+    if (i >= n_dx) i -= n_dx;
+    const uint32_t above = w.ht.of(i);
+    t.n = i - above * p.ht;
+    t.width = width_of(p.H, t.n);
+    if (t.kind == kDx) {
+        const int splits = splits_of(p, t.piece), stages = stages_of(p, t.piece);
+        const bool same = splits == p.splits;  // but perhaps in the last piece
+        t.m = same ? w.splits.of(above) : above / splits;
+        t.split = above - t.m * splits;
+        // (stages * splits stays far below 2^31: pieces are rows below 2^31 / 64 stages, splits at most 32)
+        t.k0 = same ? w.splits.of(stages * t.split) : stages * t.split / splits;
+        t.k1 = same ? w.splits.of(stages * (t.split + 1)) : stages * (t.split + 1) / splits;
+    } else {
+        t.m = above;
+        t.k1 = w.token_stages;
     }
     return t;
 }
@@ -298,16 +455,15 @@ __device__ __forceinline__ Item item_of(const Params &p, const Work &w, uint32_t
 // kernel
 // ---------------------------------------------------------------------------
 template <int MODE, bool BF>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
     loss_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                const __grid_constant__ CUtensorMap tm_g_read, const __grid_constant__ CUtensorMap tm_g_write,
+                const __grid_constant__ CUtensorMap tm_g, const __grid_constant__ CUtensorMap tm_g_out,
                 const __grid_constant__ CUtensorMap tm_part, const __grid_constant__ CUtensorMap tm_dt, const Params p) {
-    constexpr int S = Conf<MODE>::kStages;
+    constexpr int S = Conf<MODE>::kStages, kEpiWarps = Conf<MODE>::kEpiWarps, kOutBuffers = Conf<MODE>::kOutBuffers;
     extern __shared__ uint8_t dyn_smem[];
     Smem<MODE> &sm = *reinterpret_cast<Smem<MODE> *>(smem_align<1024>(dyn_smem));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
-    const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
@@ -339,20 +495,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     const Work work = work_of<MODE>(p);
 
-    // The next item, for one role (a warp, or the producer's lane): -1 at the end or after an abort.
+    // The next item, for one role (a warp, or the producer's lane); kind -1 at the end or after an abort.
     int slot = 0;
     uint32_t slot_parity = 0;
-    auto next_item = [&](bool whole_warp) -> int {
+    auto next_item = [&](bool whole_warp) -> Item {
+        Item t;
+        t.kind = -1;
         const bool ok = wait_or_abort(&sm.item_full[slot], slot_parity, &sm.abort_flag, p.err);
-        if (whole_warp ? !__all_sync(0xFFFFFFFFu, ok) : !ok) return -1;
-        const int i = *reinterpret_cast<const volatile int *>(&sm.item[slot]);
+        if (whole_warp ? !__all_sync(0xFFFFFFFFu, ok) : !ok) return t;
+        t = sm.item[slot];
+        // (the branch needs the loaded word, so the slot is not handed back before it is read; a release
+        // at cluster scope would wait for all memory, 0.5 us of every item)
+        if ((!whole_warp || lane == 0) && t.kind >= -1) arrive_cluster(cluster_addr(&sm.item_empty[slot], 0));
         if (whole_warp) __syncwarp();
-        if (!whole_warp || lane == 0) arrive_release(cluster_addr(&sm.item_empty[slot], 0));
         if (++slot == kQueue) {
             slot = 0;
             slot_parity ^= 1u;
         }
-        return i;
+        return t;
     };
 
     if (warp == 0) {
@@ -360,11 +520,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             uint32_t j = 0;  // stages issued
             bool ok = true;
+            int seen = -1;   // the last piece whose g is known to be complete
             const int r = static_cast<int>(rank);
             for (;;) {
-                const int i = next_item(false);
-                if (i < 0) break;
-                const Item t = item_of<MODE>(p, work, i);
+                const Item t = next_item(false);
+                if (t.kind < 0) break;
                 const int half = t.width / 2, b_boxes = half > 64 ? 2 : 1;
                 // first coordinates of A and B: (x, y) of the box at stage 0, whether k runs along x,
                 // and the second box's offset
@@ -373,13 +533,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool ak, bk;
                 if (MODE == 0 || t.kind == kLogits) {
                     ma = &tm_x, ax = 0, ay = t.m * kLossTile + r * kCtaM, ak = true;
-                    mb = &tm_w, bx = 0, by = static_cast<int>(p.g_v0) + t.n * kLossTile + r * half, bk = true;
-                } else if (t.kind == kDx) {
-                    ma = &tm_g_read, ax = 0, ay = t.m * kLossTile + r * kCtaM, ak = true;
-                    mb = &tm_w, bx = t.n * kLossTile + r * half, by = static_cast<int>(p.d_v0), bk = false;
+                    mb = &tm_w, bx = 0, by = t.piece * static_cast<int>(p.piece) + t.n * kLossTile + r * half, bk = true;
                 } else {
-                    ma = &tm_g_read, ax = t.m * kLossTile + r * kCtaM, ay = 0, ak = false;
-                    mb = &tm_x, bx = t.n * kLossTile + r * half, by = 0, bk = false;
+                    if (t.piece > seen) {  // all of the piece's g
+                        if (!wait_count(p.g_done + t.piece, work.blocks * tiles_of(p, t.piece) * kLossSyncWarps,
+                                        &sm.abort_flag, p.err))
+                            break;
+                        seen = t.piece;
+                    }
+                    const int g0 = t.piece % p.slots * static_cast<int>(p.Tpad);
+                    if (t.kind == kDx) {
+                        ma = &tm_g, ax = 0, ay = g0 + t.m * kLossTile + r * kCtaM, ak = true;
+                        mb = &tm_w, bx = t.n * kLossTile + r * half, by = t.piece * static_cast<int>(p.piece), bk = false;
+                    } else {
+                        ma = &tm_g, ax = t.m * kLossTile + r * kCtaM, ay = g0, ak = false;
+                        mb = &tm_x, bx = t.n * kLossTile + r * half, by = 0, bk = false;
+                    }
                 }
                 for (int kc = t.k0; kc < t.k1; ++kc, ++j) {
                     const int s = j % S;
@@ -416,9 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t j = 0;
             int n_acc = 0;
             for (;;) {
-                const int i = next_item(true);
-                if (i < 0) break;
-                const Item t = item_of<MODE>(p, work, i);
+                const Item t = next_item(true);
+                if (t.kind < 0) break;
                 const bool a_mn = MODE == 1 && t.kind == kDtable, b_mn = MODE == 1 && t.kind != kLogits;
                 const uint32_t idesc = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
                                        (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(t.width >> 3) << 17) |
@@ -452,18 +620,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
         // ---------------- scheduler (the leader CTA only) ----------------
         if (rank == 0 && lane == 0) {
+            Work w = work;
+            set_divisors<MODE>(p, w);
             int q = 0;
             uint32_t parity = 1;
-            uint32_t i = pair;  // every pair's first item is its number
+            uint32_t i = atomicAdd(p.queue, 1u);
             for (;;) {
+                Item t = {};
+                t.kind = -1;
+                uint32_t next = 0;
+                if (i < w.total) {
+                    next = atomicAdd(p.queue, 1u);  // on its way while this one is worked out
+                    t = item_of<MODE>(p, w, i);
+                }
                 if (!wait_or_abort(&sm.item_empty[q], parity, &sm.abort_flag, p.err)) break;
-                const int v = i < work.total ? static_cast<int>(i) : -1;
-                *reinterpret_cast<volatile int *>(&sm.item[q]) = v;
-                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&sm.item[q], 1)), "r"(v) : "memory");
-                arrive_release(cluster_addr(&sm.item_full[q], 0));
-                arrive_release(cluster_addr(&sm.item_full[q], 1));
-                if (v < 0) break;
-                i = pairs + atomicAdd(p.queue, 1u);
+                const int4 *v = reinterpret_cast<const int4 *>(&t);
+#pragma unroll
+                for (uint32_t cta = 0; cta < 2; ++cta) {  // the words' arrival completes the phase
+                    const uint32_t bar = cluster_addr(&sm.item_full[q], cta), dst = cluster_addr(&sm.item[q], cta);
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
+                                 "r"(static_cast<uint32_t>(sizeof(Item)))
+                                 : "memory");
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        asm volatile(
+                            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                                dst + 16 * h),
+                            "r"(v[h].x), "r"(v[h].y), "r"(v[h].z), "r"(v[h].w), "r"(bar)
+                            : "memory");
+                }
+                if (t.kind < 0) break;
+                i = next;
                 if (++q == kQueue) {
                     q = 0;
                     parity ^= 1u;
@@ -472,17 +659,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------- epilogue ----------------
-        const int q = warp & 3;  // TMEM lane quarter
+        const int q = warp & 3, part = (warp - 3) / 4;  // TMEM lane quarter; of the warps that share it
+        constexpr int kParts = kEpiWarps / 4;
         const int row = static_cast<int>(rank) * kCtaM + q * 32 + lane;  // of the tile
         const int row0 = static_cast<int>(rank) * kCtaM + q * 32;
         const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
         const float scale = MODE == 1 ? ld_dep(&p.meta->scale) : 1.0f, unscale = MODE == 1 ? ld_dep(&p.meta->unscale) : 1.0f;
-        int n_acc = 0, n_out = 0;
+        int n_acc = 0, n_out = 0, free_seen = -1;
+        uint32_t *told = nullptr;  // lane 0: whom to tell of the stores so far
+        auto tell = [&]() {
+            if (told) {
+                bulk_wait_all();  // written, for whoever acquires it
+                add_release(told, 1u);
+                told = nullptr;
+            }
+        };
         // A buffer of this warp's that no store reads any more.
         auto out_buffer = [&]() -> uint8_t * {
-            if (lane == 0) bulk_wait_read1();
+            if (lane == 0) bulk_wait_read<kOutBuffers - 1>();
             __syncwarp();
-            return sm.out[MODE == 1 ? warp - 3 : 0][MODE == 1 ? n_out & 1 : 0];
+            return sm.out[MODE == 1 ? warp - 3 : 0][n_out % kOutBuffers];
         };
         auto send = [&](const CUtensorMap *map, const uint8_t *buf, int x, int y, bool add) {
             fence_async_shared();
@@ -494,10 +690,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++n_out;
         };
+        // Lane 0: a counter has reached `target`, at the latest after what this warp has to tell.
+        auto after = [&](const uint32_t *count, uint32_t target) -> bool {
+            if (load_acquire(count) < target) tell();
+            return wait_count(count, target, &sm.abort_flag, p.err);
+        };
+        // 64 values of this lane's row, times u, rounded to 16 bits, to (x, y).  The buffer is waited for
+        // when they are there.
+        auto put_half = [&](const float (&v)[64], float u, int x, int y, const CUtensorMap *map) {
+            uint32_t w[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) w[k] = pack16<BF>(v[2 * k] * u, v[2 * k + 1] * u);
+            if (lane == 0) tell();
+            uint8_t *out = out_buffer();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) put_piece(out, lane, k, w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            send(map, out, x, y, false);
+        };
         for (;;) {
-            const int i = next_item(true);
-            if (i < 0) break;
-            const Item t = item_of<MODE>(p, work, i);
+            const Item t = next_item(true);
+            if (t.kind < 0) break;
             const int buf = n_acc & 1;
             const uint32_t acc = tmem + lanes + buf * (kTmemCols / 2);
             // what the tile needs besides its sums, asked for before they are waited for
@@ -507,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int64_t v0 = 0;
             const int64_t tok = static_cast<int64_t>(t.m) * kLossTile + row;
             if (MODE == 0 || t.kind == kLogits) {
-                v0 = p.g_v0 + static_cast<int64_t>(t.n) * kLossTile;
+                v0 = t.piece * p.piece + static_cast<int64_t>(t.n) * kLossTile;
                 const int target = ld_dep(p.tgt + tok);
                 none = target < 0;
                 y = target >= v0 && target < v0 + kLossTile ? static_cast<int>(target - v0) : -1;
@@ -516,7 +728,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     gs = ld_dep(p.gs + tok) * scale;
                 }
             }
-            const bool ok = wait_or_abort(&sm.acc_full[buf], (n_acc >> 1) & 1, &sm.abort_flag, p.err);
+            // What was written and not yet told of is told of before anything is waited for that may
+            // depend on it; where the tile is there already, after its first part, when the stores
+            // have long completed.
+            uint32_t *dx_done = nullptr;
+            bool go = true;
+            if (MODE == 1 && lane == 0) {
+                if (t.kind == kLogits) {
+                    // the slot is free once the products with the piece that was there have read it
+                    const int old = t.piece - p.slots;
+                    if (old > free_seen) {
+                        go = after(p.read_done + old, n_products_of(p, work, old));
+                        free_seen = old;
+                    }
+                } else if (t.kind == kDx) {
+                    dx_done = p.dx_done + ((static_cast<int64_t>(t.m) * p.ht + t.n) * p.splits + t.split) * kLossSyncWarps +
+                              rank * kEpiWarps + warp - 3;
+                    if (t.piece > 0) go = after(dx_done, t.piece);
+                }
+                if (told && !test_wait(&sm.acc_full[buf], (n_acc >> 1) & 1)) tell();
+            }
+            const bool ok = go && wait_or_abort(&sm.acc_full[buf], (n_acc >> 1) & 1, &sm.abort_flag, p.err);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;  // tcgen05.ld is warp-collective
             tc_fence_after();
             ++n_acc;
@@ -564,67 +796,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (y >= 0) p.zt[tok] = z;
             } else if (t.kind == kLogits) {
                 // g, 64 rows of the vocabulary at a time
-                for (int c = 0; c < kLossTile / 64; ++c) {
-                    uint8_t *out = out_buffer();
+                for (int c = part; c < kLossTile / 64; c += kParts) {
                     const int64_t left = p.V - v0 - c * 64;
                     const bool special = left < 64 || __any_sync(0xFFFFFFFFu, none || (y >= 0 && (y >> 6) == c));
+                    float v[64];
+                    tmem_ld64(acc + c * 64, v);
 #pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        float v[32];
-                        tmem_ld32(acc + c * 64 + o * 32, v);
+                    for (int k = 0; k < 64; ++k) v[k] = ex2(fmaf(v[k], p.l2, -lse2));
+                    if (special) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = ex2(fmaf(v[k], p.l2, -lse2));
-                        if (special) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (y == c * 64 + o * 32 + k) v[k] -= 1.0f;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] *= gs;
-                        if (special) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (none || o * 32 + k >= left) v[k] = 0.0f;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            put_piece(out, lane, o * 4 + k, pack16<BF>(v[8 * k], v[8 * k + 1]),
-                                      pack16<BF>(v[8 * k + 2], v[8 * k + 3]), pack16<BF>(v[8 * k + 4], v[8 * k + 5]),
-                                      pack16<BF>(v[8 * k + 6], v[8 * k + 7]));
+                        for (int k = 0; k < 64; ++k)
+                            if (y == c * 64 + k) v[k] -= 1.0f;
                     }
-                    send(&tm_g_write, out, t.n * kLossTile + c * 64, t.m * kLossTile + row0, false);
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) v[k] *= gs;
+                    if (special) {
+#pragma unroll
+                        for (int k = 0; k < 64; ++k)
+                            if (none || k >= left) v[k] = 0.0f;
+                    }
+                    put_half(v, 1.0f, t.n * kLossTile + c * 64, t.piece % p.slots * static_cast<int>(p.Tpad) + t.m * kLossTile + row0,
+                             &tm_g_out);
                 }
             } else {
                 // sums of dx, or of dtable times the inverse of g's scale
                 const bool dx = t.kind == kDx;
-                const int mode = dx ? (p.first ? kStore32 : kAdd32) : p.dt_mode;
+                const int mode = dx ? (t.piece == 0 ? kStore32 : kAdd32) : p.dt_mode;
                 const CUtensorMap *map = dx ? &tm_part : &tm_dt;
                 const float u = dx ? 1.0f : unscale;
                 const int h0 = t.n * kLossTile, cols = p.H - h0 < kLossTile ? p.H - h0 : kLossTile;
                 // (a piece starts at a multiple of the tile, and rows past the table's end are not stored)
                 const int64_t out_row = dx ? t.split * p.Tpad + static_cast<int64_t>(t.m) * kLossTile + row0
-                                           : p.d_v0 + static_cast<int64_t>(t.m) * kLossTile + row0;
+                                           : t.piece * p.piece + static_cast<int64_t>(t.m) * kLossTile + row0;
                 if (mode == kStore16) {
-                    for (int c = 0; c < cols; c += 64) {
-                        uint8_t *out = out_buffer();
-#pragma unroll
-                        for (int o = 0; o < 2; ++o) {
-                            float v[32];
-                            tmem_ld32(acc + c + o * 32, v);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                put_piece(out, lane, o * 4 + k, pack16<BF>(v[8 * k] * u, v[8 * k + 1] * u),
-                                          pack16<BF>(v[8 * k + 2] * u, v[8 * k + 3] * u),
-                                          pack16<BF>(v[8 * k + 4] * u, v[8 * k + 5] * u),
-                                          pack16<BF>(v[8 * k + 6] * u, v[8 * k + 7] * u));
-                        }
-                        send(map, out, h0 + c, static_cast<int>(out_row), false);
+                    for (int c = part * 64; c < cols; c += kParts * 64) {
+                        float v[64];
+                        tmem_ld64(acc + c, v);
+                        put_half(v, u, h0 + c, static_cast<int>(out_row), map);
                     }
                 } else {
-                    for (int c = 0; c < cols; c += 32) {
-                        uint8_t *out = out_buffer();
+                    for (int c = part * 32; c < cols; c += kParts * 32) {
                         float v[32];
                         tmem_ld32(acc + c, v);
+                        if (lane == 0) tell();
+                        uint8_t *out = out_buffer();
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             put_piece(out, lane, k, __float_as_uint(v[4 * k] * u), __float_as_uint(v[4 * k + 1] * u),
@@ -656,8 +871,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(cluster_addr(&sm.acc_empty[buf], 0));
+            if (lane == 0) {
+                arrive_cluster(cluster_addr(&sm.acc_empty[buf], 0));
+                if (MODE == 1) {
+                    tell();  // (a warp without columns in this tile has not yet)
+                    if (t.kind == kLogits) told = p.g_done + t.piece;
+                    else if (t.kind == kDx) told = dx_done;
+                    // both CTAs' MMAs are done, and with them their reads of g
+                    if (t.kind != kLogits && rank == 0 && warp == 3) add_relaxed(p.read_done + t.piece, 1u);
+                }
+            }
         }
+        if (MODE == 1 && lane == 0) tell();
         if (MODE == 1 && lane == 0) bulk_wait_all();  // the stores are complete, and shared memory no longer read
     }
 
@@ -675,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // host
 // ---------------------------------------------------------------------------
 struct Maps {
-    CUtensorMap x, w, g_read, g_write, part, dt;
+    CUtensorMap x, w, g, g_out, part, dt;
 };
 
 bool make_box(CUtensorMap *map, int32_t dtype, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch,
@@ -693,9 +918,10 @@ cudaError_t launch(const Maps &m, const Params &p, uint32_t items, cudaStream_t 
     if (e != cudaSuccess) return e;
     constexpr int smem = 1024 + static_cast<int>(sizeof(Smem<MODE>));
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    static_assert(MODE == 0 || 2 * Conf<MODE>::kEpiWarps == kLossSyncWarps, "warps that tell of a tile");
     auto kern = loss_kernel<MODE, BF>;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Conf<MODE>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -725,7 +951,7 @@ cudaError_t launch(const Maps &m, const Params &p, uint32_t items, cudaStream_t 
     }
     cfg.gridDim = dim3(2 * (items < static_cast<uint32_t>(fit) ? items : fit));
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, m.x, m.w, m.g_read, m.g_write, m.part, m.dt, p);
+    return cudaLaunchKernelEx(&cfg, kern, m.x, m.w, m.g, m.g_out, m.part, m.dt, p);
 }
 
 // What every launch of a call shares.
@@ -735,7 +961,7 @@ bool common(const LossArgs &a, const LossPlan &p, Maps *m, Params *k) {
     if (!make_box(&m->x, dt, a.ws + p.off_x, p.Hp, p.Tpad, static_cast<uint64_t>(p.Hp) * 2, 64, 64) ||
         !make_box(&m->w, dt, w, p.Hp, p.V, static_cast<uint64_t>(p.Hp) * 2, 64, 64))
         return false;
-    m->g_read = m->g_write = m->part = m->dt = m->x;  // replaced where they are used
+    m->g = m->g_out = m->part = m->dt = m->x;  // replaced where they are used
     k->meta = reinterpret_cast<const LossMeta *>(a.ws + p.off_meta);
     k->tgt = reinterpret_cast<const int32_t *>(a.ws + p.off_tgt);
     k->V = p.V;
@@ -743,6 +969,7 @@ bool common(const LossArgs &a, const LossPlan &p, Maps *m, Params *k) {
     k->H = p.H;
     k->ht = (p.H + kLossTile - 1) / kLossTile;
     k->l2 = kLog2e * a.inv_temperature;
+    k->queue = reinterpret_cast<uint32_t *>(a.ws + p.off_sync);
     k->err = a.err;
     return true;
 }
@@ -753,8 +980,9 @@ cudaError_t launch_loss_stats(const LossArgs &a, const LossPlan &p, cudaStream_t
     Maps m;
     Params k = {};
     if (!common(a, p, &m, &k)) return cudaErrorInvalidValue;
-    k.queue = reinterpret_cast<uint32_t *>(a.ws + p.off_queue);
-    k.g_tiles = static_cast<int>(p.vt);
+    k.piece = p.V;
+    k.pieces = 1;
+    k.piece_tiles = k.last_tiles = static_cast<int>(p.vt);
     k.stats = reinterpret_cast<float2 *>(a.ws + p.off_stats);
     k.zt = reinterpret_cast<float *>(a.ws + p.off_zt);
     const uint32_t items = static_cast<uint32_t>(p.Tpad / kLossTile * p.vt);
@@ -787,37 +1015,24 @@ cudaError_t launch_loss_products(const LossArgs &a, const LossPlan &p, cudaStrea
                                              static_cast<uint64_t>(p.H) * (f32 ? 4 : 2), f32 ? 32 : 64, 32))
             return cudaErrorInvalidValue;
     }
-    uint32_t *queue = reinterpret_cast<uint32_t *>(a.ws + p.off_queue);
-    const size_t g_bytes = static_cast<size_t>(p.Tpad) * p.piece * 2;
-    const uint64_t pitch = static_cast<uint64_t>(p.piece) * 2;
-    const uint32_t blocks = static_cast<uint32_t>(p.Tpad / kLossTile);
-    for (int i = 0; i <= p.pieces; ++i) {
-        // g of piece i, the products with piece i - 1
-        uint8_t *write = a.ws + p.off_g + (i & 1) * g_bytes, *read = a.ws + p.off_g + ((i & 1) ^ 1) * g_bytes;
-        if (!make_box(&m.g_read, dt, read, p.piece, p.Tpad, pitch, 64, 64) ||
-            !make_box(&m.g_write, dt, write, p.piece, p.Tpad, pitch, 64, 32))
-            return cudaErrorInvalidValue;
-        auto tiles = [&](int n) -> int {
-            if (n < 0 || n >= p.pieces) return 0;
-            const int64_t rows = p.V - n * p.piece < p.piece ? p.V - n * p.piece : p.piece;
-            return static_cast<int>((rows + kLossTile - 1) / kLossTile);
-        };
-        k.queue = queue + i;
-        k.g_v0 = i * p.piece;
-        k.g_tiles = tiles(i);
-        k.d_tiles = tiles(i - 1);
-        k.d_v0 = i > 0 ? (i - 1) * p.piece : 0;
-        const int64_t rows = p.V - k.d_v0 < p.piece ? p.V - k.d_v0 : p.piece;
-        k.d_stages = static_cast<int>((rows + kTileK - 1) / kTileK);
-        // (a last piece may be shorter than the splits; the first one, which writes their sums, is not)
-        k.splits = p.splits < k.d_stages ? p.splits : k.d_stages;
-        k.first = i == 1;
-        const uint32_t items = blocks * k.g_tiles + (k.d_tiles && k.dx ? blocks * k.ht * k.splits : 0u) +
-                               (k.dtable ? static_cast<uint32_t>(k.d_tiles) * k.ht : 0u);
-        const cudaError_t e = p.bf16 ? launch<1, true>(m, k, items, stream) : launch<1, false>(m, k, items, stream);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    const uint64_t pitch = static_cast<uint64_t>(p.piece) * 2, g_rows = static_cast<uint64_t>(p.slots) * p.Tpad;
+    if (!make_box(&m.g, dt, a.ws + p.off_g, p.piece, g_rows, pitch, 64, 64) ||
+        !make_box(&m.g_out, dt, a.ws + p.off_g, p.piece, g_rows, pitch, 64, 32))
+        return cudaErrorInvalidValue;
+    k.piece = p.piece;
+    k.pieces = p.pieces;
+    k.piece_tiles = static_cast<int>(p.piece / kLossTile);
+    k.last_tiles = static_cast<int>((p.V - (p.pieces - 1) * p.piece + kLossTile - 1) / kLossTile);
+    k.ahead = p.ahead;
+    k.slots = p.slots;
+    k.splits = p.splits;
+    k.g_done = k.queue + 1;
+    k.read_done = k.g_done + p.pieces;
+    k.dx_done = k.read_done + p.pieces;
+    // (as many pairs as have an item, at the most positions)
+    const int64_t items = p.Tpad / kLossTile * p.vt;
+    const uint32_t grid = static_cast<uint32_t>(items < 65536 ? items * (1 + k.ht) : 65536);
+    return p.bf16 ? launch<1, true>(m, k, grid, stream) : launch<1, false>(m, k, grid, stream);
 }
 
 }  // namespace lhs

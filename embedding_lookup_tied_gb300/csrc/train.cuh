@@ -9,7 +9,8 @@
 
 namespace lhs {
 
-constexpr int kLossTile = 256;  // tokens, and vocabulary rows, of a tile of logits
+constexpr int kLossTile = 256;      // tokens, and vocabulary rows, of a tile of logits
+constexpr int kLossSyncWarps = 16;  // warps of a pair of CTAs that take a tile of the gradient out
 
 inline int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
@@ -32,7 +33,8 @@ struct LossPlan {
     size_t off_tgt;         // int32 [Tpad]: its target, -1 past count
     size_t off_x;           // [Tpad x Hp]: its residual, zeros past hidden and count
     size_t off_w;           // [V x Hp]: the table, where its rows are not whole 16-byte words
-    size_t off_queue;       // uint32 [pieces + 1]: items handed out, of each launch
+    size_t off_sync;        // uint32 [n_sync]: what CTAs tell one another; 0 at the start
+    int64_t n_sync;
     // loss
     size_t off_stats;       // float2 [vt x Tpad]: maximum of a tile, sum of its other exponentials
     size_t off_zt;          // f32 [Tpad]: the target's logit
@@ -40,10 +42,13 @@ struct LossPlan {
     size_t off_pos;         // int32 [T]: compact row of a position, -1
     size_t off_lse2;        // f32 [Tpad]: lse * log2(e), +inf past count
     size_t off_gs;          // f32 [Tpad]: dloss / temperature, 0 past count
-    size_t off_g;           // 2 x [Tpad x piece]: g of a piece of the vocabulary
+    size_t off_g;           // [slots x Tpad x piece]: g of a piece of the vocabulary
     size_t off_part;        // f32 [splits x Tpad x part_pitch]: dx so far
     int64_t piece;          // vocabulary rows of a piece, a multiple of kLossTile
-    int pieces, splits;     // dx's sums are split along a piece's rows
+    int pieces;
+    int ahead, slots;       // pieces whose logits precede a piece's products; whose g is kept
+    int64_t items;          // tiles of all products
+    int splits;             // dx's sums are split along a piece's rows
     int32_t part_pitch;     // hidden rounded up to 4
     size_t bytes;
 };

@@ -26,9 +26,8 @@ int check_loss_table(const lhs_table *t, int64_t tokens) {
     if (t->row_bytes != again.row_bytes) return LHS_ERR_INVALID_ARG;
     if (tokens < 0 || tokens > kMaxLossTokens || t->hidden > kMaxTrainHidden) return LHS_ERR_INVALID_ARG;
     if (t->dtype != LHS_F16 && t->dtype != LHS_BF16) return LHS_ERR_UNSUPPORTED;
-    // tiles of logits are numbered in 31 bits (2^47 logits)
-    if ((tokens + kLossTile - 1) / kLossTile * ((t->vocab + kLossTile - 1) / kLossTile) > 0x7FFFFFFFll - (1 << 24))
-        return LHS_ERR_UNSUPPORTED;
+    // tiles are numbered in 31 bits
+    if (plan_loss(*t, tokens, true).items > 0x7FFFFFFFll - (1 << 20)) return LHS_ERR_UNSUPPORTED;
     return LHS_OK;
 }
 

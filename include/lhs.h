@@ -472,9 +472,10 @@ LHS_API int lhs_sample(const void *d_logits, int32_t dtype, int64_t stride, int6
  * The logits are f32 sums of exact products; they and their exponentials'
  * sums are never rounded to fewer bits.  A position whose logits hold NaN or
  * +inf, or nothing above -inf, gives loss and lse NaN and sets
- * LHS_ERRBIT_NONFINITE.  0 <= tokens <= 2^24 (0 enqueues nothing); tokens
- * times vocab below 2^46 (LHS_ERR_UNSUPPORTED beyond); hidden <= 65536;
- * temperature finite and > 0.  Results do not depend on the run.
+ * LHS_ERRBIT_NONFINITE.  0 <= tokens <= 2^24 (0 enqueues nothing); hidden <=
+ * 65536; tokens * vocab * (2 + hidden / 128) below 2^46, give or take
+ * (LHS_ERR_UNSUPPORTED where the tiles outnumber 2^31); temperature finite and
+ * > 0.  Results do not depend on the run.
  * Errors: LHS_ERR_INVALID_ARG, LHS_ERR_BUFFER_TOO_SMALL, LHS_ERR_UNSUPPORTED,
  * LHS_ERR_CUDA. */
 LHS_API int lhs_loss_workspace(const lhs_table *t, int64_t tokens, size_t *bytes);
