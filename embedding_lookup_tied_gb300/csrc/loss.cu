@@ -369,19 +369,24 @@ cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &
 
 namespace {
 
-// A piece's g and rows of the table should still be in L2 (129 MB) when the products
-// read them; three to five pieces are under way at a time.
-constexpr int64_t kPieceBytes = 32ll << 20;
-constexpr int kPairs = 76;  // of CTAs that run at once
+// Pieces: small ones leave g and the table's rows in L2 between the logits and the
+// products, but add dx up more often and make pairs wait for one another more.  At
+// 8,192 x 151,936 x 896 under the power cap: 3 pieces 4.55 ms, 6 4.61, 10 4.54, 20
+// 4.42, 40 4.60, 80 4.68.  Where logits are few, pieces are at least two waves of tiles
+// (256 x 262,144 x 5,120: 4 pieces 1.45 ms, 10 1.48, 16 1.51; 1 x 151,936 x 896: 4
+// pieces 204 us, 10 249).
+constexpr int64_t kPieces = 18;
+constexpr int64_t kPieceBytes = 512ll << 20;  // of g, at most, as several pieces' is kept
+constexpr int kAhead = 3;
+constexpr int kPairs = 76;                    // of CTAs that run at once
 
 void choose_pieces(LossPlan *p) {
-    // A tile of dtable has T / 64 stages (64 of k of a 256 x 256 tile), a pair's share of a piece
-    // 3 T rows H / (kPairs 256 256 64): where the share is no shorter than the tile, that is rows * H >=
-    // 1.7 M, pieces follow each other without waiting.
-    int64_t rows = kPieceBytes / (2 * (p->Tpad + p->Hp));
-    if (rows < (1700ll << 10) / p->H) rows = (1700ll << 10) / p->H;
-    if (rows < 2 * kLossTile) rows = 2 * kLossTile;
-    const int64_t n = (p->V + rows - 1) / rows;
+    const int64_t tiles = p->Tpad / kLossTile * p->vt;
+    int64_t n = tiles / (2 * kPairs) < kPieces ? tiles / (2 * kPairs) : kPieces;
+    const int64_t least = (2 * p->Tpad * p->V + kPieceBytes - 1) / kPieceBytes;
+    if (n < least) n = least;
+    if (n > (p->vt + 1) / 2) n = (p->vt + 1) / 2;  // two tiles' rows at least
+    if (n < 1) n = 1;
     p->piece = round_up((p->V + n - 1) / n, kLossTile);
     p->pieces = static_cast<int>((p->V + p->piece - 1) / p->piece);
     p->part_pitch = static_cast<int32_t>(round_up(p->H, 4));
@@ -395,7 +400,7 @@ void choose_pieces(LossPlan *p) {
     if (splits > 32) splits = 32;
     if (splits > kp) splits = kp;
     p->splits = static_cast<int>(splits < 1 ? 1 : splits);
-    const int64_t ahead = 2 + kh / share;
+    const int64_t ahead = kAhead + kh / share;
     p->ahead = static_cast<int>(ahead < 6 ? ahead : 6);
     if (p->ahead > p->pieces) p->ahead = p->pieces;
     p->slots = p->ahead + 2 < p->pieces ? p->ahead + 2 : p->pieces;

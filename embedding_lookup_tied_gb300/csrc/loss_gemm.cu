@@ -303,6 +303,13 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The same, 0 for results below 2^-126: one instruction instead of several.  For g, where they are
+// of no account beside the 2^-9 or 2^-12 of itself that p is rounded by.
+__device__ __forceinline__ float ex2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 template <bool BF>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     if (BF) {
@@ -800,20 +807,25 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                     const int64_t left = p.V - v0 - c * 64;
                     const bool special = left < 64 || __any_sync(0xFFFFFFFFu, none || (y >= 0 && (y >> 6) == c));
                     float v[64];
-                    tmem_ld64(acc + c * 64, v);
+                    if (__all_sync(0xFFFFFFFFu, none)) {
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) v[k] = ex2(fmaf(v[k], p.l2, -lse2));
-                    if (special) {
+                        for (int k = 0; k < 64; ++k) v[k] = 0.0f;
+                    } else {
+                        tmem_ld64(acc + c * 64, v);
 #pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if (y == c * 64 + k) v[k] -= 1.0f;
-                    }
+                        for (int k = 0; k < 64; ++k) v[k] = ex2_ftz(fmaf(v[k], p.l2, -lse2));
+                        if (special) {
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) v[k] *= gs;
-                    if (special) {
+                            for (int k = 0; k < 64; ++k)
+                                if (y == c * 64 + k) v[k] -= 1.0f;
+                        }
 #pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if (none || k >= left) v[k] = 0.0f;
+                        for (int k = 0; k < 64; ++k) v[k] *= gs;
+                        if (special) {
+#pragma unroll
+                            for (int k = 0; k < 64; ++k)
+                                if (none || k >= left) v[k] = 0.0f;
+                        }
                     }
                     put_half(v, 1.0f, t.n * kLossTile + c * 64, t.piece % p.slots * static_cast<int>(p.Tpad) + t.m * kLossTile + row0,
                              &tm_g_out);
