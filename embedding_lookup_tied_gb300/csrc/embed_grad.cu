@@ -12,21 +12,21 @@
 //    below its own, and of equal ones before it (67 M comparisons at most, spread
 //    over the chip, one launch).  More ids are sorted by two (18 bits of id) to
 //    four passes over digits of up to 9 bits, stable, two launches a pass.
-//  * Sums.  A group of threads walks 32 sorted positions over the columns that
-//    it holds.  A run of one id that lies within them is finished there.  One
-//    that crosses their ends leaves an f32 sum for each 32, which a last kernel
-//    joins in a fixed order, spread over threads: the hottest id of natural
-//    text names a tenth of all positions.
-//  * Rows that no id names are zeroed by further CTAs of the launches that order
-//    the ids, which use little of the chip (8,192 ids: 402 MB of zeros beside a
-//    few us of comparisons).
+//  * Sums.  A group of threads walks a run of 16 to 128 sorted positions over the
+//    columns that it holds.  An id that lies within the run is finished there.  One
+//    that crosses its ends leaves an f32 sum for each run, which a last kernel joins
+//    in a fixed order: a warp to an id, or a CTA where it has many runs (the hottest
+//    id of natural text names a tenth of all positions).
+//  * The table's gradient is zeroed first, by further CTAs of the launches that order
+//    the ids, which use little of the chip (8,192 ids: 402 MB of zeros, 55 us, beside
+//    13 us of comparisons).
 #include "train.cuh"
 
 namespace lhs {
 namespace {
 
 constexpr int kRankMost = 8192;     // ids whose places are counted
-constexpr int kRankThreads = 256;   // 32 ids to a CTA, its warps share the others
+constexpr int kRankThreads = 512;   // 32 ids to a CTA, its warps share the others
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9;
@@ -34,14 +34,17 @@ constexpr int kBins = 1 << kDigitBits;
 constexpr int kSortSteps = 8;       // keys of a thread in a round
 constexpr int kRound = kSortThreads * kSortSteps;
 constexpr int kMostTiles = 128;     // each reads the counts of all
-constexpr int kRun = 32;            // sorted positions that a group of threads sums
+constexpr int kMostRun = 128;       // sorted positions that a group of threads sums
 constexpr int kSumThreads = 128;
-constexpr int kJoinCols = 64;       // threads along the columns, four columns each
-constexpr int kJoinRows = 8;        // threads that share a column's sums
+constexpr int kJoinWarps = 16;
+constexpr int kJoinCols = 128;      // columns of a warp, four to a lane
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// Zeros that CTAs `first` and up of a launch write.
+// Zeros that CTAs `first` and up of a launch write, kZeroWords words of 16 bytes to a
+// thread.  Many short CTAs walk through memory in order: 402 MB in 55 us; a CTA to an
+// equal range each 69 us, one wave of CTAs striding through it 63 us.
+constexpr int kZeroWords = 2;
 struct Zero {
     uint4 *p;
     size_t n16;       // 16-byte words
@@ -50,13 +53,14 @@ struct Zero {
     int first;
 };
 __device__ __forceinline__ void write_zeros(const Zero &z) {
-    const size_t step = static_cast<size_t>(gridDim.x - z.first) * blockDim.x;
-    for (size_t i = static_cast<size_t>(blockIdx.x - z.first) * blockDim.x + threadIdx.x; i < z.n16; i += step)
-        __stcs(z.p + i, make_uint4(0u, 0u, 0u, 0u));
-    if (static_cast<int>(blockIdx.x) == z.first && static_cast<int>(threadIdx.x) < z.ntail) z.tail[threadIdx.x] = 0;
+    const size_t c = blockIdx.x - z.first, i0 = c * (kZeroWords * blockDim.x) + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kZeroWords; ++k)
+        if (i0 + k * blockDim.x < z.n16) z.p[i0 + k * blockDim.x] = make_uint4(0u, 0u, 0u, 0u);
+    if (c == 0 && static_cast<int>(threadIdx.x) < z.ntail) z.tail[threadIdx.x] = 0;
 }
 
-__global__ void __launch_bounds__(256) zero_kernel(const Zero z) {
+__global__ void __launch_bounds__(512) zero_kernel(const Zero z) {
     pdl_wait();
     write_zeros(z);
 }
@@ -72,39 +76,45 @@ __device__ __forceinline__ uint32_t key_of(int32_t id, uint32_t vocab, int32_t i
 __global__ void __launch_bounds__(kRankThreads)
     rank_ids_kernel(const int32_t *ids, int n, uint32_t vocab, int32_t ignore, uint32_t *keys, int32_t *order,
                     uint32_t *n_cross, const Zero z, int32_t *err) {
-    extern __shared__ uint32_t all[];  // the keys, to a multiple of 32 with the largest value
-    __shared__ int part[kRankThreads / 32][32];
+    extern __shared__ uint32_t all[];  // the keys, to a multiple of 32 with a larger value
+    __shared__ uint32_t part[kRankThreads / 32][32];
     pdl_wait();
     pdl_trigger();
     if (static_cast<int>(blockIdx.x) >= z.first) return write_zeros(z);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kRankThreads / 32;
     const int padded = (n + 31) / 32 * 32;
     bool bad = false;
+#pragma unroll 8
     for (int i = threadIdx.x; i < padded; i += kRankThreads) {
         const int32_t id = i < n ? ld_dep(ids + i) : ignore;
         const uint32_t k = key_of(id, vocab, ignore);
         if (k == vocab && id != ignore) bad = true;
-        all[i] = i < n ? k : 0xFFFFFFFFu;
+        all[i] = i < n ? k : 0x7FFFFFFFu;
     }
     if (bad && blockIdx.x == 0) set_err(err, LHS_ERRBIT_BAD_TOKEN);
     if (blockIdx.x == 0 && threadIdx.x == 0) *n_cross = 0u;
     __syncthreads();
     const int i = blockIdx.x * 32 + lane;
-    const uint32_t k = all[i < padded ? i : 0];
-    int rank = 0;
-    // words of four keys; those of other CTAs' positions lie wholly before or behind this one's
-    for (int w = warp; w < padded / 4; w += warps) {
-        const uint4 a = reinterpret_cast<const uint4 *>(all)[w];
-        if (w < static_cast<int>(blockIdx.x) * 8) {
-            rank += (a.x <= k) + (a.y <= k) + (a.z <= k) + (a.w <= k);
-        } else if (w >= static_cast<int>(blockIdx.x) * 8 + 8) {
-            rank += (a.x < k) + (a.y < k) + (a.z < k) + (a.w < k);
-        } else {
-            const int j = w * 4;
-            rank += (a.x < k || (a.x == k && j < i)) + (a.y < k || (a.y == k && j + 1 < i)) +
-                    (a.z < k || (a.z == k && j + 2 < i)) + (a.w < k || (a.w == k && j + 3 < i));
-        }
+    const uint32_t k = all[i];
+    uint32_t rank = 0;
+    // Words of four keys.  Those of other CTAs' positions lie wholly before this one's, where equal
+    // keys count, or wholly behind.  Keys are below 2^31 (a pad equals vocab at most, which takes no
+    // part in the order), so a < k is the sign of a - k: two instructions a key.
+    const int own = static_cast<int>(blockIdx.x) * 8, words = padded / 4;
+    const uint4 *word = reinterpret_cast<const uint4 *>(all);
+    auto below = [](const uint4 &a, uint32_t b) {
+        return ((a.x - b) >> 31) + ((a.y - b) >> 31) + ((a.z - b) >> 31) + ((a.w - b) >> 31);
+    };
+#pragma unroll 4
+    for (int w = warp; w < own; w += warps) rank += below(word[w], k + 1u);
+    if (warp < 8) {
+        const uint4 a = word[own + warp];
+        const int j = (own + warp) * 4;
+        rank += (a.x < k || (a.x == k && j < i)) + (a.y < k || (a.y == k && j + 1 < i)) +
+                (a.z < k || (a.z == k && j + 2 < i)) + (a.w < k || (a.w == k && j + 3 < i));
     }
+#pragma unroll 4
+    for (int w = own + 8 + warp; w < words; w += warps) rank += below(word[w], k);
     part[warp][lane] = rank;
     __syncthreads();
     if (warp == 0 && i < n) {
@@ -135,11 +145,10 @@ __device__ __forceinline__ uint32_t pass_key(const Pass &p, int64_t i) {
     return p.ids ? key_of(ld_dep(p.ids + i), p.vocab, p.ignore) : ld_dep(p.keys_in + i);
 }
 
-__global__ void __launch_bounds__(kSortThreads) count_digits_kernel(const Pass p, const Zero z) {
+__global__ void __launch_bounds__(kSortThreads) count_digits_kernel(const Pass p) {
     __shared__ uint32_t bins[kBins];
     pdl_wait();
     pdl_trigger();
-    if (static_cast<int>(blockIdx.x) >= z.first) return write_zeros(z);
     for (int b = threadIdx.x; b < kBins; b += kSortThreads) bins[b] = 0u;
     __syncthreads();
     const int64_t i0 = blockIdx.x * p.per, i1 = i0 + p.per < p.n ? i0 + p.per : p.n;
@@ -233,6 +242,17 @@ __global__ void __launch_bounds__(kSortThreads) move_digits_kernel(const Pass p,
 // ---------------------------------------------------------------------------
 // sums
 // ---------------------------------------------------------------------------
+template <int BYTES>
+struct Word;
+template <>
+struct Word<8> {
+    using T = uint2;
+};
+template <>
+struct Word<16> {
+    using T = uint4;
+};
+
 // VEC consecutive values of a row, widened.
 template <int DT, int VEC>
 struct Pack;
@@ -268,33 +288,42 @@ struct Pack<DT, 8> {
     }
 };
 
-// N sums scaled, added to what the gradient held if asked, and stored.
+// N values of the gradient.
 template <int N, typename O>
-__device__ __forceinline__ void finish(O *o, const float (&s)[N], float scale, bool accumulate) {
-    alignas(16) O v[N];
-    if (N == 8) {
-        uint4 *w = reinterpret_cast<uint4 *>(v);
-        uint4 *g = reinterpret_cast<uint4 *>(o);
-        if (accumulate) {
+struct Out {
+    alignas(N == 8 ? 16 : sizeof(O)) O v[N];
+    __device__ __forceinline__ void load(const O *o) {
+        if (N == 8) {
 #pragma unroll
-            for (int i = 0; i < static_cast<int>(sizeof(v) / 16); ++i) w[i] = g[i];
+            for (int i = 0; i < static_cast<int>(sizeof(v) / 16); ++i)
+                reinterpret_cast<uint4 *>(v)[i] = reinterpret_cast<const uint4 *>(o)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = o[i];
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i) put_rn(&v[i], fmaf(s[i], scale, accumulate ? wide(v[i]) : 0.0f));
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(v) / 16); ++i) g[i] = w[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) put_rn(o + i, fmaf(s[i], scale, accumulate ? wide(o[i]) : 0.0f));
     }
-}
+    // sums scaled, added to what was loaded if `add`, and stored
+    __device__ __forceinline__ void store(O *o, const float (&s)[N], float scale, bool add) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) put_rn(&v[i], fmaf(s[i], scale, add ? wide(v[i]) : 0.0f));
+        if (N == 8) {
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(sizeof(v) / 16); ++i)
+                reinterpret_cast<uint4 *>(o)[i] = reinterpret_cast<const uint4 *>(v)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) o[i] = v[i];
+        }
+    }
+};
 
 struct Sums {
     const uint32_t *keys;
     const int32_t *order;
     int64_t n;
+    int run;                // sorted positions of a run, a multiple of 8
     int hidden, pitch;      // f32 sums of a run: rows of pitch, a multiple of 8
-    uint32_t vocab;
+    int64_t vocab;
     float scale;
     int64_t dout_stride;
     bool accumulate;
@@ -306,133 +335,150 @@ struct Sums {
 
 // A group of `cols` threads (a power of two) to a run; thread c of it holds
 // columns VEC (c + cols blockIdx.y) and up.
-template <int DT, int VEC, typename O>
+template <int DT, int VEC, typename O, bool ADD>
 __global__ void __launch_bounds__(kSumThreads)
     sum_runs_kernel(const Sums p, const typename Elem<DT>::T *dout, O *dtable, int cols) {
-    constexpr int kAhead = 8;  // rows asked for at a time
-    __shared__ uint32_t key[kSumThreads / 8][kRun];
-    __shared__ int32_t pos[kSumThreads / 8][kRun];
+    constexpr int kAhead = ADD && sizeof(O) == 4 ? 4 : 8;  // rows (and sums to add to) asked for at a time
+    extern __shared__ uint32_t lists[];
     pdl_wait();
-    const int group = threadIdx.x / cols, c = threadIdx.x % cols;
-    const int64_t run = static_cast<int64_t>(blockIdx.x) * (kSumThreads / cols) + group;
-    const int64_t i0 = run * kRun;
-    const int len = i0 < p.n ? static_cast<int>(p.n - i0 < kRun ? p.n - i0 : kRun) : 0;
-    for (int e = c; e < kRun; e += cols) {
-        key[group][e] = e < len ? ld_dep(p.keys + i0 + e) : p.vocab;
-        pos[group][e] = e < len ? ld_dep(p.order + i0 + e) : 0;
+    const uint32_t none = static_cast<uint32_t>(p.vocab);
+    const int groups = kSumThreads / cols, group = threadIdx.x / cols, c = threadIdx.x % cols;
+    uint32_t *key = lists + group * p.run;                                               // none past the end
+    int32_t *pos = reinterpret_cast<int32_t *>(lists + (groups + group) * p.run);
+    const int64_t run = static_cast<int64_t>(blockIdx.x) * groups + group;
+    const int64_t i0 = run * p.run;
+    for (int e = c; e < p.run; e += cols) {
+        key[e] = i0 + e < p.n ? ld_dep(p.keys + i0 + e) : none;
+        pos[e] = i0 + e < p.n ? ld_dep(p.order + i0 + e) : 0;
     }
+    const uint32_t prev = i0 > 0 && i0 < p.n ? ld_dep(p.keys + i0 - 1) : none;
+    const uint32_t next = i0 + p.run < p.n ? ld_dep(p.keys + i0 + p.run) : none;
     __syncthreads();
-    if (len == 0 || key[group][0] == p.vocab) return;
-    const uint32_t prev = i0 > 0 ? ld_dep(p.keys + i0 - 1) : p.vocab;
-    const uint32_t next = i0 + kRun < p.n ? ld_dep(p.keys + i0 + kRun) : p.vocab;
+    if (key[0] == none) return;
+    const uint32_t head = key[0] == prev ? prev : none;  // an id that came from the run before
     const int j = (c + cols * static_cast<int>(blockIdx.y)) * VEC;
     const bool in = j < p.hidden;
     float s[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) s[i] = 0.0f;
-    uint32_t cur = key[group][0];
-    bool head = cur == prev;
     auto keep = [&](int64_t row) {
         if (!in) return;
         float *o = p.part + row * p.pitch + j;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) o[i] = s[i];
     };
-    for (int e0 = 0; e0 < kRun; e0 += kAhead) {
-        Pack<DT, VEC> v[kAhead];
+    for (int e0 = 0; e0 < p.run; e0 += kAhead) {
+        uint32_t k[kAhead + 1];
 #pragma unroll
-        for (int e = 0; e < kAhead; ++e)
-            if (in && key[group][e0 + e] != p.vocab) v[e].load(dout + pos[group][e0 + e] * p.dout_stride + j);
+        for (int e = 0; e < kAhead; ++e) k[e] = key[e0 + e];
+        k[kAhead] = e0 + kAhead < p.run ? key[e0 + kAhead] : next;
+        Pack<DT, VEC> v[kAhead];
+        Out<VEC, O> old[kAhead];
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) {
-            const uint32_t k = key[group][e0 + e];
-            if (k != cur) {
-                if (cur != p.vocab) {
-                    if (head) keep(2 * run);
-                    else if (in) finish<VEC>(dtable + static_cast<int64_t>(cur) * p.hidden + j, s, p.scale, p.accumulate);
-                }
-                head = false;
-                cur = k;
+            if (in && k[e] != none) v[e].load(dout + pos[e0 + e] * p.dout_stride + j);
+            if (ADD && in && k[e] != none && k[e] != k[e + 1] && k[e] != head)
+                old[e].load(dtable + static_cast<int64_t>(k[e]) * p.hidden + j);
+        }
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) s[i] = 0.0f;
-            }
-            if (in && k != p.vocab) v[e].add(s);
+        for (int e = 0; e < kAhead; ++e) {
+            if (k[e] == none) continue;
+            if (in) v[e].add(s);
+            if (k[e] == k[e + 1]) continue;
+            // the id's last position
+            if (k[e] == head) keep(2 * run);
+            else if (in) old[e].store(dtable + static_cast<int64_t>(k[e]) * p.hidden + j, s, p.scale, ADD);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s[i] = 0.0f;
         }
     }
-    if (cur == p.vocab) return;
-    if (cur == next) {
-        keep(head ? 2 * run : 2 * run + 1);
-        if (!head && c == 0 && blockIdx.y == 0) p.cross[atomicAdd(p.n_cross, 1u)] = static_cast<int32_t>(run);
-    } else if (head) {
-        keep(2 * run);
-    } else if (in) {
-        finish<VEC>(dtable + static_cast<int64_t>(cur) * p.hidden + j, s, p.scale, p.accumulate);
+    if (key[p.run - 1] != none && key[p.run - 1] == next) {  // the last id goes on
+        keep(next == head ? 2 * run : 2 * run + 1);
+        if (next != head && c == 0 && blockIdx.y == 0) p.cross[atomicAdd(p.n_cross, 1u)] = static_cast<int32_t>(run);
     }
 }
 
-// The ids that cross runs: an item is one of them and 4 kJoinCols columns.  The
-// sums of its runs are dealt out to kJoinRows threads, whose results are joined in
-// their order.
+// The ids that cross runs: an item is one of them and kJoinCols columns, a warp to an
+// item.  One with more than 32 further runs is shared by the CTA's warps, whose sums are
+// joined in their order.  (Items of a CTA of 512 threads each: 61 us for 262,144 positions.)
 template <typename O>
-__global__ void __launch_bounds__(kJoinCols *kJoinRows)
+__global__ void __launch_bounds__(32 * kJoinWarps)
     join_runs_kernel(const Sums p, O *dtable, int col_blocks, bool vec) {
-    constexpr int kThreads = kJoinCols * kJoinRows;
-    __shared__ float4 part[kJoinRows][kJoinCols];
-    __shared__ int ends[kThreads / 32];
+    __shared__ float4 part[kJoinWarps][32];
+    __shared__ int ends[kJoinWarps];
+    __shared__ int64_t large[kJoinWarps];
     pdl_wait();
-    const int c = threadIdx.x % kJoinCols, row = threadIdx.x / kJoinCols;
-    const int64_t items = static_cast<int64_t>(ld_dep(p.n_cross)) * col_blocks;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int64_t run = ld_dep(p.cross + item / col_blocks);
-        const uint32_t id = ld_dep(p.keys + run * kRun + kRun - 1);
-        // runs after the first that start with the id
-        int64_t more = 0;
-        for (;;) {
-            const int64_t i = (run + 1 + more + threadIdx.x) * kRun;
-            const bool on = i < p.n && ld_dep(p.keys + i) == id;
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, on);
-            if ((threadIdx.x & 31) == 0) ends[threadIdx.x / 32] = __popc(m);
-            __syncthreads();
-            int n = 0;
-            for (int w = 0; w < kThreads / 32; ++w) n += ends[w];
-            more += n;
-            __syncthreads();
-            if (n < kThreads) break;
-        }
-        const int j = (static_cast<int>(item % col_blocks) * kJoinCols + c) * 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t n_cross = ld_dep(p.n_cross), items = n_cross * col_blocks;
+    auto starts = [&](int64_t run, uint32_t id) { return run * p.run < p.n && ld_dep(p.keys + run * p.run) == id; };
+    // runs first, first + step, ... of those from `run` to run + more
+    auto sum = [&](int64_t run, int64_t more, int first, int step, int j) -> float4 {
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (j < p.hidden) {
 #pragma unroll 8
-            for (int64_t r = row; r <= more; r += kJoinRows) {
+            for (int64_t r = first; r <= more; r += step) {
                 const float4 a = ld_dep(reinterpret_cast<const float4 *>(p.part + (2 * (run + r) + (r == 0 ? 1 : 0)) * p.pitch + j));
                 s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
             }
         }
-        part[row][c] = s;
+        return s;
+    };
+    auto finish = [&](uint32_t id, int j, const float4 &s) {
+        const float f[4] = {s.x, s.y, s.z, s.w};
+        O *o = dtable + static_cast<int64_t>(id) * p.hidden + j;
+        if (vec && j < p.hidden) {  // hidden % 4 == 0: four values are 8 or 16 aligned bytes
+            using W = typename Word<4 * sizeof(O)>::T;
+            alignas(16) O v[4];
+            if (p.accumulate) *reinterpret_cast<W *>(v) = *reinterpret_cast<const W *>(o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) put_rn(&v[k], fmaf(f[k], p.scale, p.accumulate ? wide(v[k]) : 0.0f));
+            *reinterpret_cast<W *>(o) = *reinterpret_cast<const W *>(v);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (j + k < p.hidden) put_rn(o + k, fmaf(f[k], p.scale, p.accumulate ? wide(o[k]) : 0.0f));
+        }
+    };
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kJoinWarps; i0 < items; i0 += static_cast<int64_t>(gridDim.x) * kJoinWarps) {
+        const int64_t item = i0 + warp;  // columns outermost, so that a large id's items go to different CTAs
+        int64_t left = -1;
+        if (item < items) {
+            const int64_t run = ld_dep(p.cross + item % n_cross);
+            const int j = static_cast<int>(item / n_cross) * kJoinCols + lane * 4;
+            const uint32_t id = ld_dep(p.keys + (run + 1) * p.run - 1);
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, starts(run + 1 + lane, id));
+            if (m == 0xFFFFFFFFu) left = item;
+            else finish(id, j, sum(run, __popc(m), 0, 1, j));
+        }
+        if (lane == 0) large[warp] = left;
         __syncthreads();
-        if (row == 0 && j < p.hidden) {
-            for (int r = 1; r < kJoinRows && r <= more; ++r) {
-                const float4 a = part[r][c];
-                s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (large[w] < 0) continue;
+            const int64_t run = ld_dep(p.cross + large[w] % n_cross);
+            const int j = static_cast<int>(large[w] / n_cross) * kJoinCols + lane * 4;
+            const uint32_t id = ld_dep(p.keys + (run + 1) * p.run - 1);
+            int64_t more = 0;
+            for (;;) {
+                const uint32_t m = __ballot_sync(0xFFFFFFFFu, starts(run + 1 + more + threadIdx.x, id));
+                if (lane == 0) ends[warp] = __popc(m);
+                __syncthreads();
+                int n = 0;
+                for (int k = 0; k < kJoinWarps; ++k) n += ends[k];
+                more += n;
+                __syncthreads();
+                if (n < 32 * kJoinWarps) break;
             }
-            const float f[4] = {s.x, s.y, s.z, s.w};
-            O *o = dtable + static_cast<int64_t>(id) * p.hidden + j;
-            if (vec) {  // hidden % 4 == 0: four values are 8 or 16 aligned bytes
-                alignas(16) O v[4];
-                if (sizeof(O) == 4) {
-                    if (p.accumulate) *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(o);
-                } else if (p.accumulate) {
-                    *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(o);
+            part[warp][lane] = sum(run, more, warp, kJoinWarps, j);
+            __syncthreads();
+            if (warp == 0) {
+                float4 s = part[0][lane];
+                for (int k = 1; k < kJoinWarps; ++k) {
+                    const float4 a = part[k][lane];
+                    s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
                 }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) put_rn(&v[k], fmaf(f[k], p.scale, p.accumulate ? wide(v[k]) : 0.0f));
-                if (sizeof(O) == 4) *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(v);
-                else *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(v);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (j + k < p.hidden) put_rn(o + k, fmaf(f[k], p.scale, p.accumulate ? wide(o[k]) : 0.0f));
+                finish(id, j, s);
             }
+            __syncthreads();
         }
         __syncthreads();
     }
@@ -444,7 +490,7 @@ __global__ void __launch_bounds__(kJoinCols *kJoinRows)
 struct Layout {
     size_t keys[2], order[2], counts, cross, n_cross, part, bytes;
     int64_t runs;
-    int pitch, tiles;
+    int run, pitch, tiles;
 };
 Layout layout_of(int32_t hidden, int64_t n) {
     Layout l = {};
@@ -454,7 +500,11 @@ Layout layout_of(int32_t hidden, int64_t n) {
         at += align256(bytes);
         return o;
     };
-    l.runs = (n + kRun - 1) / kRun;
+    // Short runs spread few positions over the chip (8,192 positions added to a bf16 gradient: 23 us in
+    // runs of 32, whose ids' rows are read one after another); long ones leave fewer sums to
+    // join (262,144 positions in runs of 32: 58 MB of them beside 470 MB of rows).
+    l.run = n <= kRankMost ? 16 : n <= 65536 ? 32 : n <= (1 << 17) ? 64 : kMostRun;
+    l.runs = (n + l.run - 1) / l.run;
     l.pitch = static_cast<int>(round_up(hidden, 8));
     for (int i = 0; i < (n > kRankMost ? 2 : 1); ++i) {
         l.keys[i] = take(n * 4);
@@ -476,10 +526,10 @@ Zero zeros_of(void *p, size_t bytes) {
     const size_t n16 = bytes / 16;
     return {static_cast<uint4 *>(p), n16, static_cast<uint8_t *>(p) + n16 * 16, static_cast<int>(bytes % 16), 0};
 }
-// CTAs of `threads` that write zeros: enough to fill the chip, no more than there is to write.
-unsigned zero_ctas(const Zero &z, int threads, const DeviceInfo &dev) {
-    const size_t want = (z.n16 + threads - 1) / threads, most = static_cast<size_t>(dev.num_sms) * 2048 / threads;
-    return static_cast<unsigned>(want < most ? want : most) + (want == 0 && z.ntail ? 1u : 0u);
+// CTAs of `threads` that write zeros.
+unsigned zero_ctas(const Zero &z, int threads) {
+    const size_t each = static_cast<size_t>(kZeroWords) * threads;
+    return static_cast<unsigned>((z.n16 + each - 1) / each) + (z.n16 == 0 && z.ntail ? 1u : 0u);
 }
 
 template <int DT, int VEC, typename O>
@@ -489,8 +539,13 @@ cudaError_t sum_runs(const EmbedGradArgs &a, const Sums &s, int64_t runs, cudaSt
     const int groups = kSumThreads / cols;
     const dim3 grid(static_cast<unsigned>((runs + groups - 1) / groups),
                     static_cast<unsigned>((a.hidden + cols * VEC - 1) / (cols * VEC)));
-    return launch_pdl(sum_runs_kernel<DT, VEC, O>, grid, dim3(kSumThreads), 0, stream, s,
-                      static_cast<const typename Elem<DT>::T *>(a.dout), static_cast<O *>(a.dtable), cols);
+    const size_t smem = static_cast<size_t>(2 * groups) * s.run * 4;
+    const auto *d = static_cast<const typename Elem<DT>::T *>(a.dout);
+    if (a.accumulate)
+        return launch_pdl(sum_runs_kernel<DT, VEC, O, true>, grid, dim3(kSumThreads), smem, stream, s, d,
+                          static_cast<O *>(a.dtable), cols);
+    return launch_pdl(sum_runs_kernel<DT, VEC, O, false>, grid, dim3(kSumThreads), smem, stream, s, d,
+                      static_cast<O *>(a.dtable), cols);
 }
 
 template <typename O>
@@ -507,20 +562,17 @@ cudaError_t sums(const EmbedGradArgs &a, const Sums &s, int64_t runs, const Devi
     else
         e = wide8 ? sum_runs<LHS_BF16, 8, O>(a, s, runs, stream) : sum_runs<LHS_BF16, 1, O>(a, s, runs, stream);
     if (e != cudaSuccess || runs < 2) return e;
-    const int col_blocks = (a.hidden + 4 * kJoinCols - 1) / (4 * kJoinCols);
-    const int64_t most = runs * col_blocks, cap = 4ll * dev.num_sms;
-    return launch_pdl(join_runs_kernel<O>, dim3(static_cast<unsigned>(most < cap ? most : cap)),
-                      dim3(kJoinCols * kJoinRows), 0, stream, s, static_cast<O *>(a.dtable), col_blocks, a.hidden % 4 == 0);
+    const int col_blocks = (a.hidden + kJoinCols - 1) / kJoinCols;
+    const int64_t most = (runs * col_blocks + kJoinWarps - 1) / kJoinWarps, cap = 4ll * dev.num_sms;
+    return launch_pdl(join_runs_kernel<O>, dim3(static_cast<unsigned>(most < cap ? most : cap)), dim3(32 * kJoinWarps), 0,
+                      stream, s, static_cast<O *>(a.dtable), col_blocks, a.hidden % 4 == 0);
 }
 
 }  // namespace
 
 cudaError_t launch_zero(void *p, size_t bytes, cudaStream_t stream) {
-    DeviceInfo dev;
-    const cudaError_t e = device_info(&dev);
-    if (e != cudaSuccess) return e;
     const Zero z = zeros_of(p, bytes);
-    return launch_pdl(zero_kernel, dim3(zero_ctas(z, 256, dev)), dim3(256), 0, stream, z);
+    return launch_pdl(zero_kernel, dim3(zero_ctas(z, 512)), dim3(512), 0, stream, z);
 }
 
 size_t embed_grad_workspace(int32_t hidden, int64_t n) { return layout_of(hidden, n).bytes; }
@@ -542,9 +594,9 @@ cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t stream) {
     if (a.n <= kRankMost) {
         Zero z = zeros_of(a.dtable, table_bytes);
         z.first = static_cast<int>((a.n + 31) / 32);
-        const unsigned grid = z.first + zero_ctas(z, kRankThreads, dev);
-        e = launch_pdl(rank_ids_kernel, dim3(grid), dim3(kRankThreads), round_up(a.n, 32) * 4, stream, a.ids,
-                       static_cast<int>(a.n), vocab, a.ignore, keys[0], order[0], s.n_cross, z, a.err);
+        e = launch_pdl(rank_ids_kernel, dim3(z.first + zero_ctas(z, kRankThreads)), dim3(kRankThreads),
+                       round_up(a.n, 32) * 4, stream, a.ids, static_cast<int>(a.n), vocab, a.ignore, keys[0], order[0],
+                       s.n_cross, z, a.err);
         if (e != cudaSuccess) return e;
     } else {
         int bits = 1;
@@ -559,10 +611,10 @@ cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t stream) {
         p.ignore = a.ignore;
         p.n_cross = s.n_cross;
         p.err = a.err;
-        const int launches = 2 * passes;
-        auto share = [&](int i) {  // of the zeros, in whole words; the last takes the rest
-            const size_t each = table_bytes / 16 / launches * 16;
-            Zero z = zeros_of(static_cast<uint8_t *>(a.dtable) + i * each, i + 1 < launches ? each : table_bytes - i * each);
+        // the moves take the zeros (20 us a pass for 262,144 ids, as 136 MB of zeros do; a count takes 5)
+        auto share = [&](int i) {  // in whole words; the last takes the rest
+            const size_t each = table_bytes / 16 / passes * 16;
+            Zero z = zeros_of(static_cast<uint8_t *>(a.dtable) + i * each, i + 1 < passes ? each : table_bytes - i * each);
             z.first = l.tiles;
             return z;
         };
@@ -574,13 +626,10 @@ cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t stream) {
             p.order_in = order[(i & 1) ^ 1];
             p.keys_out = keys[i & 1];
             p.order_out = order[i & 1];
-            Zero z = share(2 * i);
-            e = launch_pdl(count_digits_kernel, dim3(l.tiles + zero_ctas(z, kSortThreads, dev)), dim3(kSortThreads), 0,
-                           stream, p, z);
+            e = launch_pdl(count_digits_kernel, dim3(l.tiles), dim3(kSortThreads), 0, stream, p);
             if (e != cudaSuccess) return e;
-            z = share(2 * i + 1);
-            e = launch_pdl(move_digits_kernel, dim3(l.tiles + zero_ctas(z, kSortThreads, dev)), dim3(kSortThreads), 0,
-                           stream, p, z);
+            const Zero z = share(i);
+            e = launch_pdl(move_digits_kernel, dim3(l.tiles + zero_ctas(z, kSortThreads)), dim3(kSortThreads), 0, stream, p, z);
             if (e != cudaSuccess) return e;
             last = i & 1;
         }
@@ -588,9 +637,10 @@ cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t stream) {
     s.keys = keys[last];
     s.order = order[last];
     s.n = a.n;
+    s.run = l.run;
     s.hidden = a.hidden;
     s.pitch = l.pitch;
-    s.vocab = vocab;
+    s.vocab = a.vocab;
     s.scale = a.scale;
     s.dout_stride = a.dout_stride;
     s.accumulate = a.accumulate;
