@@ -191,16 +191,43 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
     }
 }
 
-// The table in rows of whole 16-byte words, where its own are not.  A warp to a row.
+// The table in rows of whole 16-byte words, where its own are not.  A warp to a row; a
+// word is cut out of the two aligned ones that it lies in, but at the table's end, where the
+// second may reach past it.
 __global__ void __launch_bounds__(256)
     loss_table_kernel(const uint16_t *w, int64_t V, int H, int Hp, uint16_t *out) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
+    const int64_t end = V * H * 2;  // bytes; the table starts on a 16-byte boundary
+    const uint8_t *bytes = reinterpret_cast<const uint8_t *>(w);
     for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < V;
-         r += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5)
-        for (int c = lane; c < Hp / 8; c += 32)
-            reinterpret_cast<uint4 *>(out + r * Hp)[c] = row_word(w + r * H, c, H, false);
+         r += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5) {
+#pragma unroll 2
+        for (int c = lane; c < Hp / 8; c += 32) {
+            const int64_t at = r * H * 2 + c * 16, a = at & ~int64_t(15);
+            uint4 v;
+            if (8 * c + 8 <= H && a + 32 <= end) {
+                const uint4 lo = ld_dep(reinterpret_cast<const uint4 *>(bytes + a));
+                const uint4 hi = ld_dep(reinterpret_cast<const uint4 *>(bytes + a + 16));
+                const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                const int skip = static_cast<int>(at - a) / 4, bits = static_cast<int>(at - a) % 4 * 8;
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t x = 0, y = 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (skip == q) x = u[k + q], y = u[k + q + 1];
+                    o[k] = __funnelshift_r(x, y, bits);
+                }
+                v = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+                v = row_word(w + r * H, c, H, false);
+            }
+            reinterpret_cast<uint4 *>(out + r * Hp)[c] = v;
+        }
+    }
 }
 
 // A pair (m, s) stands for (1 + s) exp(m): the 1 is the maximum's own term, kept
@@ -218,7 +245,7 @@ __device__ __forceinline__ void join_pair(float &m, float &s, float om, float os
     }
 }
 
-// Joins a token's tiles: 8 tokens to a CTA, 128 threads to a token, which take the
+// Joins a token's parts of tiles: 8 tokens to a CTA, 128 threads to a token, which take the
 // tiles in turn; their pairs are joined in a fixed order.  (32 tokens to a CTA with
 // 32 threads each: 22 us for 256 tokens and 1,024 tiles.)
 constexpr int kMergeTokens = 8, kMergeWarps = 32, kMergeThreads = 32 * kMergeWarps;
@@ -435,7 +462,7 @@ LossPlan plan_loss(const lhs_table &t, int64_t tokens, bool grad) {
     if (!grad) {
         p.n_sync = 1;
         p.off_sync = take(4);
-        p.off_stats = take(p.vt * p.Tpad * 8);
+        p.off_stats = take(p.vt * kLossParts * p.Tpad * 8);
         p.off_zt = take(p.Tpad * 4);
     } else {
         choose_pieces(&p);
@@ -460,7 +487,7 @@ cudaError_t launch_loss(const LossArgs &a, const LossPlan &p, cudaStream_t strea
                       reinterpret_cast<const LossMeta *>(a.ws + p.off_meta),
                       reinterpret_cast<const int32_t *>(a.ws + p.off_act),
                       reinterpret_cast<const float2 *>(a.ws + p.off_stats),
-                      reinterpret_cast<const float *>(a.ws + p.off_zt), p.vt, p.Tpad, a.inv_temperature, a.loss, a.lse,
+                      reinterpret_cast<const float *>(a.ws + p.off_zt), p.vt * kLossParts, p.Tpad, a.inv_temperature, a.loss, a.lse,
                       a.err);
 }
 

@@ -73,9 +73,9 @@ template <int MODE>
 struct Conf {
     static constexpr bool kGrad = MODE == 1;
     static constexpr int kStages = kGrad ? 6 : 7;
-    // The gradient's tiles are taken out by two warps to each quarter of TMEM's lanes, which share
-    // the columns 64 at a time.
-    static constexpr int kEpiWarps = kGrad ? 8 : 4;
+    // Two warps to each quarter of TMEM's lanes take a tile out: half of its columns each for the
+    // statistics, 64 in turn for the gradient's products.
+    static constexpr int kEpiWarps = 8;
     static constexpr int kThreads = 32 * (3 + kEpiWarps);  // producer, MMA issuer, scheduler, epilogue
     static constexpr int kOutBuffers = 1;
 };
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                 // target is the maximum, the rest small) keeps its relative accuracy.
                 float m = -INFINITY, s = 0.0f, z = 0.0f;
                 int equal = 0;
-                for (int c = 0; c < kLossTile / 32; ++c) {
+                for (int c = part * (kLossTile / 64); c < (part + 1) * (kLossTile / 64); ++c) {
                     float v[32];
                     tmem_ld32(acc + c * 32, v);
                     const int64_t left = p.V - v0 - c * 32;
@@ -798,9 +798,9 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                     }
                     s += (s4[0] + s4[1]) + (s4[2] + s4[3]);
                 }
-                p.stats[static_cast<int64_t>(t.n) * p.Tpad + tok] =
+                p.stats[(static_cast<int64_t>(t.n) * kLossParts + part) * p.Tpad + tok] =
                     make_float2(m, m == -INFINITY ? s : s + static_cast<float>(equal - 1));
-                if (y >= 0) p.zt[tok] = z;
+                if (y >= 0 && y / (kLossTile / kParts) == part) p.zt[tok] = z;
             } else if (t.kind == kLogits) {
                 // g, 64 rows of the vocabulary at a time
                 for (int c = part; c < kLossTile / 64; c += kParts) {
@@ -930,7 +930,7 @@ cudaError_t launch(const Maps &m, const Params &p, uint32_t items, cudaStream_t 
     if (e != cudaSuccess) return e;
     constexpr int smem = 1024 + static_cast<int>(sizeof(Smem<MODE>));
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    static_assert(MODE == 0 || 2 * Conf<MODE>::kEpiWarps == kLossSyncWarps, "warps that tell of a tile");
+    static_assert(2 * Conf<MODE>::kEpiWarps == kLossSyncWarps && Conf<MODE>::kEpiWarps == 4 * kLossParts, "warps that take a tile out");
     auto kern = loss_kernel<MODE, BF>;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(Conf<MODE>::kThreads);

@@ -10,7 +10,8 @@
 namespace lhs {
 
 constexpr int kLossTile = 256;      // tokens, and vocabulary rows, of a tile of logits
-constexpr int kLossSyncWarps = 16;  // warps of a pair of CTAs that take a tile of the gradient out
+constexpr int kLossSyncWarps = 16;  // warps of a pair of CTAs that take a tile out
+constexpr int kLossParts = 2;       // parts of a tile's columns with statistics of their own
 
 inline int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
@@ -36,7 +37,7 @@ struct LossPlan {
     size_t off_sync;        // uint32 [n_sync]: what CTAs tell one another; 0 at the start
     int64_t n_sync;
     // loss
-    size_t off_stats;       // float2 [vt x Tpad]: maximum of a tile, sum of its other exponentials
+    size_t off_stats;       // float2 [vt x kLossParts x Tpad]: maximum of a part, sum of its other exponentials
     size_t off_zt;          // f32 [Tpad]: the target's logit
     // gradient
     size_t off_pos;         // int32 [T]: compact row of a position, -1
