@@ -749,6 +749,8 @@ def lhs_loss(table: Table, x: torch.Tensor, targets: torch.Tensor, ignore: int =
     the target is ``ignore``.  Returns (loss, lse, err word)."""
     xp, xdt, stride, n, tp = _loss_args(table, x, targets)
     dev = x.device
+    if loss is None and lse is None:
+        loss, lse = torch.empty((2, n), dtype=torch.float32, device=dev).unbind(0)
     loss = torch.empty(n, dtype=torch.float32, device=dev) if loss is None else loss
     lse = torch.empty(n, dtype=torch.float32, device=dev) if lse is None else lse
     if ws is None:
