@@ -41,6 +41,11 @@ constexpr int kBoxBytes = 64 * 64 * 2;        // what one TMA load brings: 64 x 
 constexpr int kOperandBytes = 2 * kBoxBytes;  // a CTA's part of A, or of B, of a stage
 constexpr int kTmemCols = 512;
 constexpr int kStoreBytes = 32 * 128;         // an epilogue warp's store: 32 rows of 128 bytes
+// The tensor cores cut their f32 sums instead of rounding them, so that a long one is short
+// by about 2^-25 of itself for every 16 of k (5.7e-6 of the loss for hidden 5,376 in one sum; f32 on the
+// CUDA cores: 1e-6).  Logits whose statistics are taken are summed 512 of k at a time, and those
+// sums added up, rounded, in registers.
+constexpr int kChunk = 512 / kTileK;
 constexpr int kQueue = 3;                     // items handed out ahead
 
 enum { kLogits = 0, kDx = 1, kDtable = 2 };
@@ -76,7 +81,8 @@ struct Conf {
     // Two warps to each quarter of TMEM's lanes take a tile out: half of its columns each for the
     // statistics, 64 in turn for the gradient's products.
     static constexpr int kEpiWarps = 8;
-    static constexpr int kThreads = 32 * (3 + kEpiWarps);  // producer, MMA issuer, scheduler, epilogue
+    static constexpr int kFirstEpi = 4;  // after the producer, the MMA issuer, the scheduler and an idle one
+    static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
     static constexpr int kOutBuffers = 1;
 };
 
@@ -296,16 +302,10 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
 #pragma unroll
     for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
 }
-// 2^x, relative error below 2^-21: a thousandth of what g is rounded by, and
-// of the order of an f32 logit's own rounding in a sum of exponentials.
+// 2^x, relative error below 2^-21: a thousandth of what g is rounded by, and of the order of an
+// f32 logit's own rounding in a sum of exponentials.  Results below 2^-126 (of the row's largest, or
+// as a probability) are 0: one instruction instead of several.
 __device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// The same, 0 for results below 2^-126: one instruction instead of several.  For g, where they are
-// of no account beside the 2^-9 or 2^-12 of itself that p is rounded by.
-__device__ __forceinline__ float ex2_ftz(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
@@ -466,7 +466,8 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
     loss_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_g, const __grid_constant__ CUtensorMap tm_g_out,
                 const __grid_constant__ CUtensorMap tm_part, const __grid_constant__ CUtensorMap tm_dt, const Params p) {
-    constexpr int S = Conf<MODE>::kStages, kEpiWarps = Conf<MODE>::kEpiWarps, kOutBuffers = Conf<MODE>::kOutBuffers;
+    constexpr int S = Conf<MODE>::kStages, kEpiWarps = Conf<MODE>::kEpiWarps, kFirstEpi = Conf<MODE>::kFirstEpi,
+                  kOutBuffers = Conf<MODE>::kOutBuffers;
     extern __shared__ uint8_t dyn_smem[];
     Smem<MODE> &sm = *reinterpret_cast<Smem<MODE> *>(smem_align<1024>(dyn_smem));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -522,7 +523,11 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
         return t;
     };
 
-    if (warp == 0) {
+    // The warps that hold sums take registers from the others: 8 x 216 + 4 x 72 a lane are what 12 warps
+    // are launched with at 168.
+    if (warp < kFirstEpi) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      if (warp == 0) {
         // ---------------- TMA producer ----------------
         if (lane == 0) {
             uint32_t j = 0;  // stages issued
@@ -600,28 +605,33 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                                        (static_cast<uint32_t>((2 * kCtaM) >> 4) << 24);
                 const uint32_t la = a_mn ? kLboMn : kLboK, lb = b_mn ? kLboMn : kLboK;
                 const uint32_t sa = a_mn ? kStepMn : kStepK, sb = b_mn ? kStepMn : kStepK;
-                const int buf = n_acc & 1;
-                bool ok = wait_or_abort(&sm.acc_empty[buf], ((n_acc >> 1) & 1) ^ 1, &sm.abort_flag, p.err);
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
-                tc_fence_after();
-                const uint32_t d = tm + buf * (kTmemCols / 2);
-                for (int kc = t.k0; kc < t.k1; ++kc, ++j) {
-                    const int s = j % S;
-                    ok = wait_or_abort(&sm.full[s], (j / S) & 1, &sm.abort_flag, p.err);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        break;
-                    }
+                // (a sum of its own for every kChunk stages of logits whose statistics are taken)
+                const int chunk = MODE == 0 ? kChunk : t.k1 - t.k0;
+                bool ok = true;
+                for (int k0 = t.k0; k0 < t.k1 && ok; k0 += chunk) {
+                    const int buf = n_acc & 1, k1 = k0 + chunk < t.k1 ? k0 + chunk : t.k1;
+                    ok = wait_or_abort(&sm.acc_empty[buf], ((n_acc >> 1) & 1) ^ 1, &sm.abort_flag, p.err);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = ((smem_u32(sm.a[s]) >> 4) & 0x3FFFu) | la, b = ((smem_u32(sm.b[s]) >> 4) & 0x3FFFu) | lb;
+                    const uint32_t d = tm + buf * (kTmemCols / 2);
+                    for (int kc = k0; kc < k1; ++kc, ++j) {
+                        const int s = j % S;
+                        ok = wait_or_abort(&sm.full[s], (j / S) & 1, &sm.abort_flag, p.err);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t a = ((smem_u32(sm.a[s]) >> 4) & 0x3FFFu) | la, b = ((smem_u32(sm.b[s]) >> 4) & 0x3FFFu) | lb;
 #pragma unroll
-                    for (int ks = 0; ks < kTileK / 16; ++ks)
-                        umma(elected, d, a + ks * sa, b + ks * sb, idesc, kc != t.k0 || ks != 0);
-                    commit_both(elected, &sm.empty[s]);
+                        for (int ks = 0; ks < kTileK / 16; ++ks)
+                            umma(elected, d, a + ks * sa, b + ks * sb, idesc, kc != k0 || ks != 0);
+                        commit_both(elected, &sm.empty[s]);
+                    }
+                    if (!ok) break;
+                    commit_both(elected, &sm.acc_full[buf]);
+                    ++n_acc;
                 }
                 if (!ok) break;
-                commit_both(elected, &sm.acc_full[buf]);
-                ++n_acc;
             }
         }
     } else if (warp == 2) {
@@ -664,9 +674,11 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                 }
             }
         }
+      }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---------------- epilogue ----------------
-        const int q = warp & 3, part = (warp - 3) / 4;  // TMEM lane quarter; of the warps that share it
+        const int q = warp & 3, part = (warp - kFirstEpi) / 4;  // TMEM lane quarter; of the warps that share it
         constexpr int kParts = kEpiWarps / 4;
         const int row = static_cast<int>(rank) * kCtaM + q * 32 + lane;  // of the tile
         const int row0 = static_cast<int>(rank) * kCtaM + q * 32;
@@ -685,7 +697,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
         auto out_buffer = [&]() -> uint8_t * {
             if (lane == 0) bulk_wait_read<kOutBuffers - 1>();
             __syncwarp();
-            return sm.out[MODE == 1 ? warp - 3 : 0][n_out % kOutBuffers];
+            return sm.out[MODE == 1 ? warp - kFirstEpi : 0][n_out % kOutBuffers];
         };
         auto send = [&](const CUtensorMap *map, const uint8_t *buf, int x, int y, bool add) {
             fence_async_shared();
@@ -717,7 +729,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
         for (;;) {
             const Item t = next_item(true);
             if (t.kind < 0) break;
-            const int buf = n_acc & 1;
+            int buf = n_acc & 1;
             const uint32_t acc = tmem + lanes + buf * (kTmemCols / 2);
             // what the tile needs besides its sums, asked for before they are waited for
             int y = -1;
@@ -750,7 +762,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                     }
                 } else if (t.kind == kDx) {
                     dx_done = p.dx_done + ((static_cast<int64_t>(t.m) * p.ht + t.n) * p.splits + t.split) * kLossSyncWarps +
-                              rank * kEpiWarps + warp - 3;
+                              rank * kEpiWarps + warp - kFirstEpi;
                     if (t.piece > 0) go = after(dx_done, t.piece);
                 }
                 if (told && !test_wait(&sm.acc_full[buf], (n_acc >> 1) & 1)) tell();
@@ -763,22 +775,45 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                 // Statistics: the maximum m, the sum s of the exponentials below it and the number
                 // of equals.  The maximum's own 1 is left out of the sum, so that a loss near 0 (the
                 // target is the maximum, the rest small) keeps its relative accuracy.
+                constexpr int kCols = kLossTile / kParts;
                 float m = -INFINITY, s = 0.0f, z = 0.0f;
                 int equal = 0;
-                for (int c = part * (kLossTile / 64); c < (part + 1) * (kLossTile / 64); ++c) {
-                    float v[32];
-                    tmem_ld32(acc + c * 32, v);
-                    const int64_t left = p.V - v0 - c * 32;
+                float sum[kCols];
+                bool all = true;
+                for (int k0 = t.k0;;) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 32) {
+                        float v[32];
+                        tmem_ld32(tmem + lanes + buf * (kTmemCols / 2) + part * kCols + c, v);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) sum[c + k] = k0 == t.k0 ? v[k] : sum[c + k] + v[k];
+                    }
+                    k0 += kChunk;
+                    if (k0 >= t.k1) break;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(cluster_addr(&sm.acc_empty[buf], 0));
+                    buf = n_acc & 1;
+                    all = __all_sync(0xFFFFFFFFu, wait_or_abort(&sm.acc_full[buf], (n_acc >> 1) & 1, &sm.abort_flag, p.err));
+                    if (!all) break;
+                    tc_fence_after();
+                    ++n_acc;
+                }
+                if (!all) break;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) {
+                    float *v = sum + c;
+                    const int64_t left = p.V - v0 - part * kCols - c;
                     if (left <= 0) continue;
                     if (left < 32) {
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             if (k >= left) v[k] = -INFINITY;  // counted as equal only where nothing is above -inf
                     }
-                    if (__any_sync(0xFFFFFFFFu, y >= 0 && (y >> 5) == c)) {
+                    if (__any_sync(0xFFFFFFFFu, y >= 0 && (y >> 5) == (part * kCols + c) / 32)) {
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            if (y == c * 32 + k) z = v[k];
+                            if (y == part * kCols + c + k) z = v[k];
                     }
                     float top = m;
 #pragma unroll
@@ -813,7 +848,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                     } else {
                         tmem_ld64(acc + c * 64, v);
 #pragma unroll
-                        for (int k = 0; k < 64; ++k) v[k] = ex2_ftz(fmaf(v[k], p.l2, -lse2));
+                        for (int k = 0; k < 64; ++k) v[k] = ex2(fmaf(v[k], p.l2, -lse2));
                         if (special) {
 #pragma unroll
                             for (int k = 0; k < 64; ++k)
@@ -890,7 +925,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                     if (t.kind == kLogits) told = p.g_done + t.piece;
                     else if (t.kind == kDx) told = dx_done;
                     // both CTAs' MMAs are done, and with them their reads of g
-                    if (t.kind != kLogits && rank == 0 && warp == 3) add_relaxed(p.read_done + t.piece, 1u);
+                    if (t.kind != kLogits && rank == 0 && warp == kFirstEpi) add_relaxed(p.read_done + t.piece, 1u);
                 }
             }
         }
