@@ -101,6 +101,12 @@ int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t 
     if (accumulate != 0 && accumulate != 1) return LHS_ERR_INVALID_ARG;
     if (d_dtable && ((dtable_dtype != t->dtype && dtable_dtype != LHS_F32) || !aligned(d_dtable, 16)))
         return LHS_ERR_INVALID_ARG;
+    if (d_dtable) {  // the table is read while its gradient is written
+        const uintptr_t w = reinterpret_cast<uintptr_t>(t->data), g = reinterpret_cast<uintptr_t>(d_dtable);
+        const uintptr_t w1 = w + static_cast<uintptr_t>(t->vocab) * t->row_bytes;
+        const uintptr_t g1 = g + static_cast<uintptr_t>(t->vocab) * t->hidden * elem_size(dtable_dtype);
+        if (g < w1 && w < g1) return LHS_ERR_INVALID_ARG;
+    }
     if (d_dx && ((dx_dtype != t->dtype && dx_dtype != LHS_F32) || dx_stride < t->hidden || dx_stride > kMaxStride ||
                  !aligned(d_dx, elem_size(dx_dtype))))
         return LHS_ERR_INVALID_ARG;

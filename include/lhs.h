@@ -469,8 +469,9 @@ LHS_API int lhs_sample(const void *d_logits, int32_t dtype, int64_t stride, int6
  *   d_targets : int32 [tokens]
  *   d_loss, d_lse : f32 [tokens]
  *   d_ws      : 256-byte aligned, >= lhs_loss_workspace bytes, overwritten
- * The logits are f32 sums of exact products; they and their exponentials'
- * sums are never rounded to fewer bits.  A position whose logits hold NaN or
+ * The logits are f32 sums of exact products (512 of hidden at a time in the
+ * tensor cores); neither they nor their exponentials' sums are rounded to fewer
+ * bits.  A position whose logits hold NaN or
  * +inf, or nothing above -inf, gives loss and lse NaN and sets
  * LHS_ERRBIT_NONFINITE.  0 <= tokens <= 2^24 (0 enqueues nothing); hidden <=
  * 65536; tokens * vocab * (2 + hidden / 128) below 2^46, give or take
@@ -494,17 +495,21 @@ LHS_API int lhs_loss(const lhs_table *t, const void *d_x, int32_t x_dtype, int64
  *   d_dx         : of dx_dtype (the table's type or LHS_F32), row t at element
  *                  t*dx_stride (>= hidden), aligned to its element size; or
  *                  NULL: not wanted
+ *                  (it may be d_x itself)
  *   d_dtable     : [vocab x hidden] row-major of dtable_dtype (the table's type
- *                  or LHS_F32), 16-byte aligned; or NULL: not wanted.  One of
- *                  the two has to be wanted.
+ *                  or LHS_F32), 16-byte aligned, apart from the table; or NULL:
+ *                  not wanted.  One of the two has to be wanted.
  *   d_ws         : 256-byte aligned, >= lhs_loss_grad_workspace bytes, overwritten
- * The logits are computed again, a piece of the vocabulary at a time.  g is
+ * The logits are computed again, a piece of the vocabulary at a time, in one
+ * kernel whose CTAs wait only for work that running CTAs have taken: calls on
+ * several streams may share the GPU in any way.  g is
  * rounded to the table's type (scaled by a power of two taken from the largest
  * |dloss|, so that f16 holds it), as the other factor of both products is of
  * that type; the sums are f32, rounded once to the output's type (with
  * accumulate once more for what dtable held, if it is of 16 bits).  Positions
  * that take part with an lse or dloss that is not finite set
- * LHS_ERRBIT_NONFINITE and make what they reach NaN.  tokens == 0 clears dtable
+ * LHS_ERRBIT_NONFINITE and make what they reach NaN; results beyond the range
+ * of f16 are +-inf.  tokens == 0 clears dtable
  * (unless accumulate).  Ranges, errors and determinism as lhs_loss. */
 LHS_API int lhs_loss_grad_workspace(const lhs_table *t, int64_t tokens, size_t *bytes);
 LHS_API int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t x_stride,

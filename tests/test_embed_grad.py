@@ -53,7 +53,7 @@ def sums(ids, rows, v, ignore=-100):
 
 SIZES = [(1, 1, 1), (1, 100, 8), (2, 3, 5), (5, 7, 33), (16, 8192, 256), (31, 50, 100), (100, 1, 64), (333, 1000, 1001),
          (1000, 40, 24), (628, 15000, 896), (2048, 5000, 64), (4097, 300, 130), (8192, 30000, 40), (8193, 2000, 36),
-         (20000, 70000, 16), (40000, 3, 8), (70001, 9000, 12), (100000, 300000, 4)]
+         (20000, 70000, 16), (40000, 3, 8), (70001, 9000, 12), (100000, 300000, 4), (300001, 20000, 24), (600000, 500, 8)]
 
 
 @pytest.mark.gpu
@@ -230,6 +230,25 @@ def test_offsets_pass_32_bits():
     assert int(err.item()) == 0
     assert bool((d[-1] == 7).all()) and float(d[-2, 5]) == 2.0 and float(d[-2].float().sum()) == 2.0
     assert float(d[:-2].abs().max()) == 0.0
+
+
+@pytest.mark.gpu
+def test_ids_of_29_bits():
+    # four passes over the digits
+    v, n = (1 << 28) + 5, 9000
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB")
+    g = torch.Generator().manual_seed(2)
+    ids = torch.randint(0, v, (n,), generator=g, dtype=torch.int32)
+    ids[:4000] = ids[4000:8000]
+    ids[:3] = torch.tensor([v - 1, 0, v - 1], dtype=torch.int32)
+    rows = torch.randint(-8, 9, (n, 1), generator=g).to(torch.bfloat16)
+    d, err = lhs.lhs_embed_grad(ids.cuda(), rows.cuda(), v, 1.0, dtype=torch.bfloat16)
+    at, inv = torch.unique(ids.long(), return_inverse=True)
+    ref = torch.zeros(len(at), dtype=torch.float64).index_add_(0, inv, rows[:, 0].double())
+    assert int(err.item()) == 0 and torch.equal(d[at.cuda(), 0].cpu(), ref.to(torch.bfloat16))
+    d[at.cuda()] = 0
+    assert int(torch.count_nonzero(d)) == 0
 
 
 @pytest.mark.gpu

@@ -64,16 +64,16 @@ def test_loss_refuses():
 
 def test_grad_refuses():
     L, t = lhs.lib(), c_table()
-    big = 1 << 40
+    big, DW = 1 << 40, FAKE + 1000 * 64 * 2  # right behind the table
 
     def call(t=t, x=FAKE, dt=lhs.LHS_BF16, stride=64, n=5, y=FAKE, temp=1.0, lse=FAKE, dl=FAKE, dx=FAKE,
-             dxt=lhs.LHS_BF16, dxs=64, dw=FAKE, dwt=lhs.LHS_BF16, acc=0, ws=FAKE, wb=big, err=FAKE):
+             dxt=lhs.LHS_BF16, dxs=64, dw=DW, dwt=lhs.LHS_BF16, acc=0, ws=FAKE, wb=big, err=FAKE):
         return L.lhs_loss_grad(ctypes.byref(t), x, dt, stride, n, y, -100, temp, lse, dl, dx, dxt, dxs, dw, dwt, acc, ws,
                                wb, err, None)
     for bad in (dict(x=None), dict(dt=lhs.LHS_F16), dict(stride=63), dict(n=-1), dict(n=2 ** 24 + 1), dict(y=None),
                 dict(temp=0.0), dict(lse=None), dict(lse=FAKE + 2), dict(dl=None), dict(dl=FAKE + 2),
                 dict(dx=None, dw=None), dict(dx=FAKE + 1), dict(dx=FAKE + 2, dxt=lhs.LHS_F32), dict(dxt=lhs.LHS_F16),
-                dict(dxs=63), dict(dw=FAKE + 8), dict(dwt=lhs.LHS_F16), dict(dwt=lhs.LHS_Q8_0), dict(acc=2),
+                dict(dxs=63), dict(dw=DW + 8), dict(dw=FAKE), dict(dw=DW - 16), dict(dw=FAKE - 16), dict(dwt=lhs.LHS_F16), dict(dwt=lhs.LHS_Q8_0), dict(acc=2),
                 dict(acc=-1), dict(ws=None), dict(ws=FAKE + 16), dict(err=None)):
         assert call(**bad) == lhs.LHS_ERR_INVALID_ARG, bad
     assert call(t=c_table(lhs.LHS_F32), dt=lhs.LHS_F32) == lhs.LHS_ERR_UNSUPPORTED

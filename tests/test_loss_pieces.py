@@ -45,7 +45,7 @@ def flat(t, v, h, dtype, seed=0, masked=0.1):
 # (tokens, vocabulary, hidden): several pieces, whole and ragged last ones, splits of dx, odd rows
 SIZES = [(1, 100003, 64), (1, 180000, 200), (130, 90001, 72), (256, 262144, 16), (300, 60000, 320), (513, 50021, 40),
          (1500, 30011, 136), (2049, 20000, 264), (5000, 9000, 48), (20000, 2100, 24), (9000, 700, 520),
-         (260, 80000, 33), (700, 41001, 101), (3000, 12345, 7), (70000, 300, 16), (4, 400003, 8)]
+         (260, 80000, 33), (700, 41001, 101), (3000, 12345, 7), (70000, 300, 16), (4, 400003, 8), (30, 700, 9000), (600, 300, 20008)]
 
 
 @pytest.mark.parametrize("dtype", HALF, ids=str)
