@@ -20,6 +20,11 @@
 //  * The table's gradient is zeroed first, by further CTAs of the launches that order
 //    the ids, which use little of the chip (8,192 ids: 402 MB of zeros, 55 us, beside
 //    13 us of comparisons).
+//
+// What bounds it.  262,144 positions of 151,936 x 896 bf16: 168 us for 110 of HBM; the
+// sums read 470 MB in 95 us (5.6 TB/s with what they write), the sort takes 50 us
+// beside the zeros' 40, the join 20.  8,192 positions into 262,144 x 768 bf16: 73 us
+// for 63, nearly all of it zeros.
 #include "train.cuh"
 
 namespace lhs {

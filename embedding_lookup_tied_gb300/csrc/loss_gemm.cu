@@ -14,8 +14,9 @@
 // staged as they lie and read "MN-major": no transposed copy is made.
 //
 // The gradient goes through the vocabulary in pieces, in one launch: the logits
-// of a few pieces run ahead, so that a piece's g and rows are still in L2 when its
-// products read them.  Items (tiles) come from one queue, in an order in which an
+// of a few pieces run ahead of their products.  (A launch for each piece left a
+// tail of idle pairs at its end: 4.63 ms at 8,192 x 151,936 x 896 in pieces of 4,096
+// rows.)  Items (tiles) come from one queue, in an order in which an
 // item waits only for items before it: g for the products that read the slot
 // which it overwrites, the products for the piece's g, and the sums of dx for the
 // piece before (so that they are added up in order).  Pairs take items as they
@@ -25,7 +26,16 @@
 //
 // The logits are never stored: statistics leave a tile as (maximum, sum of the
 // other exponentials) of each token, g as 16-bit values that the products read
-// back from L2.
+// back from L2 or HBM.
+//
+// What bounds it.  Many tokens: the tensor cores and the power cap.  8,192 x
+// 151,936 x 896: statistics 1.24 ms (1,800 TFLOP/s; 1,660 for seconds on end),
+// gradient 3.8 to 4.1 ms (1,630 to 1,770; 1,515 for seconds on end, where a
+// library product of the same shape does 1,597); 2,048 x 262,144 x 5,376: 3.1 ms
+// (1,880).  256 x 262,144 x 5,120: 1.46 ms for 1.18 at the sustained rate; the
+// table is read twice and its gradient written, 1.2 ms of HBM.  One token, 151,936 x
+// 896: statistics 49 us, 5.6 TB/s; gradient 189 us for 80: reading the table twice,
+// and taking 2,376 tiles of its gradient out.
 #include <mutex>
 
 #include "i8_common.cuh"
@@ -526,155 +536,155 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
     // The warps that hold sums take registers from the others: 8 x 216 + 4 x 72 a lane are what 12 warps
     // are launched with at 168.
     if (warp < kFirstEpi) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-      if (warp == 0) {
-        // ---------------- TMA producer ----------------
-        if (lane == 0) {
-            uint32_t j = 0;  // stages issued
-            bool ok = true;
-            int seen = -1;   // the last piece whose g is known to be complete
-            const int r = static_cast<int>(rank);
-            for (;;) {
-                const Item t = next_item(false);
-                if (t.kind < 0) break;
-                const int half = t.width / 2, b_boxes = half > 64 ? 2 : 1;
-                // first coordinates of A and B: (x, y) of the box at stage 0, whether k runs along x,
-                // and the second box's offset
-                const CUtensorMap *ma, *mb;
-                int ax, ay, bx, by;
-                bool ak, bk;
-                if (MODE == 0 || t.kind == kLogits) {
-                    ma = &tm_x, ax = 0, ay = t.m * kLossTile + r * kCtaM, ak = true;
-                    mb = &tm_w, bx = 0, by = t.piece * static_cast<int>(p.piece) + t.n * kLossTile + r * half, bk = true;
-                } else {
-                    if (t.piece > seen) {  // all of the piece's g
-                        if (!wait_count(p.g_done + t.piece, work.blocks * tiles_of(p, t.piece) * kLossSyncWarps,
-                                        &sm.abort_flag, p.err))
-                            break;
-                        seen = t.piece;
-                    }
-                    const int g0 = t.piece % p.slots * static_cast<int>(p.Tpad);
-                    if (t.kind == kDx) {
-                        ma = &tm_g, ax = 0, ay = g0 + t.m * kLossTile + r * kCtaM, ak = true;
-                        mb = &tm_w, bx = t.n * kLossTile + r * half, by = t.piece * static_cast<int>(p.piece), bk = false;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 0) {
+            // ---------------- TMA producer ----------------
+            if (lane == 0) {
+                uint32_t j = 0;  // stages issued
+                bool ok = true;
+                int seen = -1;   // the last piece whose g is known to be complete
+                const int r = static_cast<int>(rank);
+                for (;;) {
+                    const Item t = next_item(false);
+                    if (t.kind < 0) break;
+                    const int half = t.width / 2, b_boxes = half > 64 ? 2 : 1;
+                    // first coordinates of A and B: (x, y) of the box at stage 0, whether k runs along x,
+                    // and the second box's offset
+                    const CUtensorMap *ma, *mb;
+                    int ax, ay, bx, by;
+                    bool ak, bk;
+                    if (MODE == 0 || t.kind == kLogits) {
+                        ma = &tm_x, ax = 0, ay = t.m * kLossTile + r * kCtaM, ak = true;
+                        mb = &tm_w, bx = 0, by = t.piece * static_cast<int>(p.piece) + t.n * kLossTile + r * half, bk = true;
                     } else {
-                        ma = &tm_g, ax = t.m * kLossTile + r * kCtaM, ay = g0, ak = false;
-                        mb = &tm_x, bx = t.n * kLossTile + r * half, by = 0, bk = false;
+                        if (t.piece > seen) {  // all of the piece's g
+                            if (!wait_count(p.g_done + t.piece, work.blocks * tiles_of(p, t.piece) * kLossSyncWarps,
+                                            &sm.abort_flag, p.err))
+                                break;
+                            seen = t.piece;
+                        }
+                        const int g0 = t.piece % p.slots * static_cast<int>(p.Tpad);
+                        if (t.kind == kDx) {
+                            ma = &tm_g, ax = 0, ay = g0 + t.m * kLossTile + r * kCtaM, ak = true;
+                            mb = &tm_w, bx = t.n * kLossTile + r * half, by = t.piece * static_cast<int>(p.piece), bk = false;
+                        } else {
+                            ma = &tm_g, ax = t.m * kLossTile + r * kCtaM, ay = g0, ak = false;
+                            mb = &tm_x, bx = t.n * kLossTile + r * half, by = 0, bk = false;
+                        }
                     }
+                    for (int kc = t.k0; kc < t.k1; ++kc, ++j) {
+                        const int s = j % S;
+                        if (j >= S && !wait_or_abort(&sm.empty[s], ((j / S) & 1) ^ 1, &sm.abort_flag, p.err)) {
+                            ok = false;
+                            break;
+                        }
+                        if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * (2 + b_boxes) * kBoxBytes);
+                        const uint32_t bar = cluster_addr(&sm.full[s], 0);
+                        const int k = kc * kTileK;
+                        const int axk = ak ? ax + k : ax, ayk = ak ? ay : ay + k;
+                        tma_load_pair(sm.a[s], ma, bar, axk, ayk);
+                        tma_load_pair(sm.a[s] + kBoxBytes, ma, bar, ak ? axk : axk + 64, ak ? ayk + 64 : ayk);
+                        const int bxk = bk ? bx + k : bx, byk = bk ? by : by + k;
+                        tma_load_pair(sm.b[s], mb, bar, bxk, byk);
+                        if (b_boxes == 2)
+                            tma_load_pair(sm.b[s] + kBoxBytes, mb, bar, bk ? bxk : bxk + 64, bk ? byk + 64 : byk);
+                    }
+                    if (!ok) break;
                 }
-                for (int kc = t.k0; kc < t.k1; ++kc, ++j) {
-                    const int s = j % S;
-                    if (j >= S && !wait_or_abort(&sm.empty[s], ((j / S) & 1) ^ 1, &sm.abort_flag, p.err)) {
-                        ok = false;
+                // drain: the pair has consumed every stage issued, so no copy, completion or commit is still
+                // headed for either CTA (after an abort, when some never come, one more limit's time to land)
+                for (uint32_t i = j > static_cast<uint32_t>(S) ? j - S : 0; i < j; ++i)
+                    if (!mbar_wait(&sm.empty[i % S], (i / S) & 1, kWaitTimeoutNs)) {
+                        if (!*reinterpret_cast<volatile int *>(&sm.abort_flag)) set_err(p.err, LHS_ERRBIT_TIMEOUT);
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * (2 + b_boxes) * kBoxBytes);
-                    const uint32_t bar = cluster_addr(&sm.full[s], 0);
-                    const int k = kc * kTileK;
-                    const int axk = ak ? ax + k : ax, ayk = ak ? ay : ay + k;
-                    tma_load_pair(sm.a[s], ma, bar, axk, ayk);
-                    tma_load_pair(sm.a[s] + kBoxBytes, ma, bar, ak ? axk : axk + 64, ak ? ayk + 64 : ayk);
-                    const int bxk = bk ? bx + k : bx, byk = bk ? by : by + k;
-                    tma_load_pair(sm.b[s], mb, bar, bxk, byk);
-                    if (b_boxes == 2)
-                        tma_load_pair(sm.b[s] + kBoxBytes, mb, bar, bk ? bxk : bxk + 64, bk ? byk + 64 : byk);
-                }
-                if (!ok) break;
             }
-            // drain: the pair has consumed every stage issued, so no copy, completion or commit is still
-            // headed for either CTA (after an abort, when some never come, one more limit's time to land)
-            for (uint32_t i = j > static_cast<uint32_t>(S) ? j - S : 0; i < j; ++i)
-                if (!mbar_wait(&sm.empty[i % S], (i / S) & 1, kWaitTimeoutNs)) {
-                    if (!*reinterpret_cast<volatile int *>(&sm.abort_flag)) set_err(p.err, LHS_ERRBIT_TIMEOUT);
-                    break;
-                }
-        }
-    } else if (warp == 1) {
-        // ---------------- MMA issuer (the leader CTA only) ----------------
-        if (rank == 0) {
-            const uint32_t tm = __reduce_or_sync(0xFFFFFFFFu, tmem);
-            const uint32_t elected = elect_one();
-            uint32_t j = 0;
-            int n_acc = 0;
-            for (;;) {
-                const Item t = next_item(true);
-                if (t.kind < 0) break;
-                const bool a_mn = MODE == 1 && t.kind == kDtable, b_mn = MODE == 1 && t.kind != kLogits;
-                const uint32_t idesc = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
-                                       (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(t.width >> 3) << 17) |
-                                       (static_cast<uint32_t>((2 * kCtaM) >> 4) << 24);
-                const uint32_t la = a_mn ? kLboMn : kLboK, lb = b_mn ? kLboMn : kLboK;
-                const uint32_t sa = a_mn ? kStepMn : kStepK, sb = b_mn ? kStepMn : kStepK;
-                // (a sum of its own for every kChunk stages of logits whose statistics are taken)
-                const int chunk = MODE == 0 ? kChunk : t.k1 - t.k0;
-                bool ok = true;
-                for (int k0 = t.k0; k0 < t.k1 && ok; k0 += chunk) {
-                    const int buf = n_acc & 1, k1 = k0 + chunk < t.k1 ? k0 + chunk : t.k1;
-                    ok = wait_or_abort(&sm.acc_empty[buf], ((n_acc >> 1) & 1) ^ 1, &sm.abort_flag, p.err);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t d = tm + buf * (kTmemCols / 2);
-                    for (int kc = k0; kc < k1; ++kc, ++j) {
-                        const int s = j % S;
-                        ok = wait_or_abort(&sm.full[s], (j / S) & 1, &sm.abort_flag, p.err);
+        } else if (warp == 1) {
+            // ---------------- MMA issuer (the leader CTA only) ----------------
+            if (rank == 0) {
+                const uint32_t tm = __reduce_or_sync(0xFFFFFFFFu, tmem);
+                const uint32_t elected = elect_one();
+                uint32_t j = 0;
+                int n_acc = 0;
+                for (;;) {
+                    const Item t = next_item(true);
+                    if (t.kind < 0) break;
+                    const bool a_mn = MODE == 1 && t.kind == kDtable, b_mn = MODE == 1 && t.kind != kLogits;
+                    const uint32_t idesc = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
+                                           (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(t.width >> 3) << 17) |
+                                           (static_cast<uint32_t>((2 * kCtaM) >> 4) << 24);
+                    const uint32_t la = a_mn ? kLboMn : kLboK, lb = b_mn ? kLboMn : kLboK;
+                    const uint32_t sa = a_mn ? kStepMn : kStepK, sb = b_mn ? kStepMn : kStepK;
+                    // (a sum of its own for every kChunk stages of logits whose statistics are taken)
+                    const int chunk = MODE == 0 ? kChunk : t.k1 - t.k0;
+                    bool ok = true;
+                    for (int k0 = t.k0; k0 < t.k1 && ok; k0 += chunk) {
+                        const int buf = n_acc & 1, k1 = k0 + chunk < t.k1 ? k0 + chunk : t.k1;
+                        ok = wait_or_abort(&sm.acc_empty[buf], ((n_acc >> 1) & 1) ^ 1, &sm.abort_flag, p.err);
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t a = ((smem_u32(sm.a[s]) >> 4) & 0x3FFFu) | la, b = ((smem_u32(sm.b[s]) >> 4) & 0x3FFFu) | lb;
+                        const uint32_t d = tm + buf * (kTmemCols / 2);
+                        for (int kc = k0; kc < k1; ++kc, ++j) {
+                            const int s = j % S;
+                            ok = wait_or_abort(&sm.full[s], (j / S) & 1, &sm.abort_flag, p.err);
+                            ok = __all_sync(0xFFFFFFFFu, ok);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t a = ((smem_u32(sm.a[s]) >> 4) & 0x3FFFu) | la, b = ((smem_u32(sm.b[s]) >> 4) & 0x3FFFu) | lb;
 #pragma unroll
-                        for (int ks = 0; ks < kTileK / 16; ++ks)
-                            umma(elected, d, a + ks * sa, b + ks * sb, idesc, kc != k0 || ks != 0);
-                        commit_both(elected, &sm.empty[s]);
+                            for (int ks = 0; ks < kTileK / 16; ++ks)
+                                umma(elected, d, a + ks * sa, b + ks * sb, idesc, kc != k0 || ks != 0);
+                            commit_both(elected, &sm.empty[s]);
+                        }
+                        if (!ok) break;
+                        commit_both(elected, &sm.acc_full[buf]);
+                        ++n_acc;
                     }
                     if (!ok) break;
-                    commit_both(elected, &sm.acc_full[buf]);
-                    ++n_acc;
                 }
-                if (!ok) break;
             }
-        }
-    } else if (warp == 2) {
-        // ---------------- scheduler (the leader CTA only) ----------------
-        if (rank == 0 && lane == 0) {
-            Work w = work;
-            set_divisors<MODE>(p, w);
-            int q = 0;
-            uint32_t parity = 1;
-            uint32_t i = atomicAdd(p.queue, 1u);
-            for (;;) {
-                Item t = {};
-                t.kind = -1;
-                uint32_t next = 0;
-                if (i < w.total) {
-                    next = atomicAdd(p.queue, 1u);  // on its way while this one is worked out
-                    t = item_of<MODE>(p, w, i);
-                }
-                if (!wait_or_abort(&sm.item_empty[q], parity, &sm.abort_flag, p.err)) break;
-                const int4 *v = reinterpret_cast<const int4 *>(&t);
+        } else if (warp == 2) {
+            // ---------------- scheduler (the leader CTA only) ----------------
+            if (rank == 0 && lane == 0) {
+                Work w = work;
+                set_divisors<MODE>(p, w);
+                int q = 0;
+                uint32_t parity = 1;
+                uint32_t i = atomicAdd(p.queue, 1u);
+                for (;;) {
+                    Item t = {};
+                    t.kind = -1;
+                    uint32_t next = 0;
+                    if (i < w.total) {
+                        next = atomicAdd(p.queue, 1u);  // on its way while this one is worked out
+                        t = item_of<MODE>(p, w, i);
+                    }
+                    if (!wait_or_abort(&sm.item_empty[q], parity, &sm.abort_flag, p.err)) break;
+                    const int4 *v = reinterpret_cast<const int4 *>(&t);
 #pragma unroll
-                for (uint32_t cta = 0; cta < 2; ++cta) {  // the words' arrival completes the phase
-                    const uint32_t bar = cluster_addr(&sm.item_full[q], cta), dst = cluster_addr(&sm.item[q], cta);
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
-                                 "r"(static_cast<uint32_t>(sizeof(Item)))
-                                 : "memory");
+                    for (uint32_t cta = 0; cta < 2; ++cta) {  // the words' arrival completes the phase
+                        const uint32_t bar = cluster_addr(&sm.item_full[q], cta), dst = cluster_addr(&sm.item[q], cta);
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
+                                     "r"(static_cast<uint32_t>(sizeof(Item)))
+                                     : "memory");
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        asm volatile(
-                            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                                dst + 16 * h),
-                            "r"(v[h].x), "r"(v[h].y), "r"(v[h].z), "r"(v[h].w), "r"(bar)
-                            : "memory");
-                }
-                if (t.kind < 0) break;
-                i = next;
-                if (++q == kQueue) {
-                    q = 0;
-                    parity ^= 1u;
+                        for (int h = 0; h < 2; ++h)
+                            asm volatile(
+                                "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                                    dst + 16 * h),
+                                "r"(v[h].x), "r"(v[h].y), "r"(v[h].z), "r"(v[h].w), "r"(bar)
+                                : "memory");
+                    }
+                    if (t.kind < 0) break;
+                    i = next;
+                    if (++q == kQueue) {
+                        q = 0;
+                        parity ^= 1u;
+                    }
                 }
             }
         }
-      }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---------------- epilogue ----------------
