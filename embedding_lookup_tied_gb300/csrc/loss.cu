@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
     }
     __syncthreads();
     const int count = sum_all;
+    const bool twin = GRAD && count <= kLossTwin;  // every residual twice (see kLossTwin)
     int base = sum_before;
     bool bad = false, nonfinite = false;
     for (int64_t b = r0; b < r1; b += kPackThreads) {
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
         if (on) {
             p.act[c] = static_cast<int32_t>(r);
             p.tgt[c] = y;
+            if (twin) p.tgt[c + kLossTwin] = y;
         }
         if (r < r1) {
             if (GRAD) {
@@ -123,6 +125,10 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
                     if (!isfinite(l) || !isfinite(d)) nonfinite = true;
                     p.lse2[c] = l * kLog2e;
                     p.gs[c] = d * p.inv_temperature;
+                    if (twin) {
+                        p.lse2[c + kLossTwin] = l * kLog2e;
+                        p.gs[c + kLossTwin] = d * p.inv_temperature;
+                    }
                 }
             } else if (!on) {
                 p.loss[r] = 0.0f;
@@ -136,9 +142,11 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
         for (uint32_t i = tid; i < n * words; i += kPackThreads) {
             const uint32_t r = i / words, c = i - r * words;
             const int k = rank_of[r];
-            if (k >= 0)
-                reinterpret_cast<uint4 *>(p.xc + static_cast<int64_t>(k) * p.Hp)[c] =
-                    row_word(p.x + (b + r) * p.x_stride, c, p.H, p.vec);
+            if (k >= 0) {
+                const uint4 v = row_word(p.x + (b + r) * p.x_stride, c, p.H, p.vec);
+                reinterpret_cast<uint4 *>(p.xc + static_cast<int64_t>(k) * p.Hp)[c] = v;
+                if (twin) reinterpret_cast<uint4 *>(p.xc + static_cast<int64_t>(k + kLossTwin) * p.Hp)[c] = v;
+            }
         }
         __syncthreads();
         base += total;
@@ -146,6 +154,7 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
     // rows past the last one, to the end of its tile: zeros, no target, no gradient
     const int64_t end = count > 0 ? (static_cast<int64_t>(count) + kLossTile - 1) / kLossTile * kLossTile : kLossTile;
     for (int64_t r = count + blockIdx.x * kPackWarps + warp; r < end; r += static_cast<int64_t>(gridDim.x) * kPackWarps) {
+        if (twin && r >= kLossTwin && r < kLossTwin + count) continue;
         for (int c = lane; c < p.Hp / 8; c += 32)
             reinterpret_cast<uint4 *>(p.xc + r * p.Hp)[c] = make_uint4(0u, 0u, 0u, 0u);
         if (lane == 0) {
@@ -295,8 +304,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
 }
 
-// dx of every position: its compact row's sums, joined in order, times the
-// inverse of g's scale; or zeros.  A warp to 128 columns of a position.
+// dx of every position: its compact row's sums (and its twin's), joined in order,
+// times the inverse of g's scale; or zeros.  A warp to 128 columns of a position.
 template <typename T>
 __global__ void __launch_bounds__(256)
     loss_dx_kernel(const LossMeta *meta, const int32_t *pos, const float *part, int splits, int64_t Tpad, int pitch,
@@ -304,6 +313,7 @@ __global__ void __launch_bounds__(256)
     const int lane = threadIdx.x & 31;
     pdl_wait();
     const float u = ld_dep(&meta->unscale);
+    const bool twin = ld_dep(&meta->count) <= kLossTwin;
     const uint32_t blocks = (H + 127) / 128;
     for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; i < n * blocks;
          i += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5) {
@@ -321,6 +331,13 @@ __global__ void __launch_bounds__(256)
                 for (int k = 1; k < splits; ++k) {
                     const float4 a = ld_dep(src + k * step);
                     v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+                }
+                if (twin) {
+                    src += kLossTwin * pitch / 4;
+                    for (int k = 0; k < splits; ++k) {
+                        const float4 a = ld_dep(src + k * step);
+                        v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+                    }
                 }
                 v.x *= u, v.y *= u, v.z *= u, v.w *= u;
             }

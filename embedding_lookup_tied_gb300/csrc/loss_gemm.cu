@@ -26,7 +26,8 @@
 //
 // The logits are never stored: statistics leave a tile as (maximum, sum of the
 // other exponentials) of each token, g as 16-bit values that the products read
-// back from L2 or HBM.
+// back from L2 or HBM; of up to 128 tokens in two terms, the second in the rows of the
+// tile's other half, with the residuals there too, so that both products add them up.
 //
 // What bounds it.  Many tokens: the tensor cores and the power cap.  8,192 x
 // 151,936 x 896: statistics 1.24 ms (1,800 TFLOP/s; 1,660 for seconds on end),
@@ -321,6 +322,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 template <bool BF>
+__device__ __forceinline__ float round16(float x) {
+    return BF ? __bfloat162float(__float2bfloat16_rn(x)) : __half2float(__float2half_rn(x));
+}
+template <bool BF>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     if (BF) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -382,7 +387,8 @@ __device__ __forceinline__ Work work_of(const Params &p) {
     Work w = {};
     const int count = ld_dep(&p.meta->count);
     w.blocks = count > 0 ? (static_cast<uint32_t>(count) + kLossTile - 1) / kLossTile : 1u;
-    w.token_stages = count > 0 ? (count + kTileK - 1) / kTileK : 1;
+    // (rows of both terms; without any position one stage of zeros)
+    w.token_stages = count == 0 ? 1 : MODE == 1 && count <= kLossTwin ? kLossTile / kTileK : (count + kTileK - 1) / kTileK;
     w.total = w.blocks * (static_cast<uint32_t>(p.pieces - 1) * p.piece_tiles + p.last_tiles);
     if (MODE == 1) {
         w.before = p.ahead < p.pieces ? w.blocks * p.ahead * p.piece_tiles : w.total;
@@ -694,6 +700,8 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
         const int row0 = static_cast<int>(rank) * kCtaM + q * 32;
         const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
         const float scale = MODE == 1 ? ld_dep(&p.meta->scale) : 1.0f, unscale = MODE == 1 ? ld_dep(&p.meta->unscale) : 1.0f;
+        // the second CTA's rows hold what the rounding of the first one's left (see kLossTwin)
+        const bool rest = MODE == 1 && rank == 1 && ld_dep(&p.meta->count) <= kLossTwin;
         int n_acc = 0, n_out = 0, free_seen = -1;
         uint32_t *told = nullptr;  // lane 0: whom to tell of the stores so far
         auto tell = [&]() {
@@ -870,6 +878,10 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 64; ++k)
                                 if (none || k >= left) v[k] = 0.0f;
+                        }
+                        if (rest) {
+#pragma unroll
+                            for (int k = 0; k < 64; ++k) v[k] -= round16<BF>(v[k]);
                         }
                     }
                     put_half(v, 1.0f, t.n * kLossTile + c * 64, t.piece % p.slots * static_cast<int>(p.Tpad) + t.m * kLossTile + row0,

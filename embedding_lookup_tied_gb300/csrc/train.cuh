@@ -15,6 +15,10 @@ constexpr int kLossParts = 2;       // parts of a tile's columns with statistics
 
 inline int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
+// Up to this many positions, g is held in two 16-bit terms: a tile has as many rows again, which
+// would be empty, and they hold what the first term's rounding left.
+constexpr int kLossTwin = kLossTile / 2;
+
 // What one call needs to know on the device, written by its first kernel.
 struct LossMeta {
     int32_t count;    // positions that take part

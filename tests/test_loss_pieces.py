@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import embedding_lookup_tied_gb300 as lhs
-from test_loss import CODE, check_grad, check_loss, make, reference, table_of
+from test_loss import check_grad, check_loss, make, reference, table_of, within
 
 pytestmark = pytest.mark.gpu
 
@@ -80,6 +80,29 @@ def test_pieces_against_the_formula(t, v, h, dtype):
     dx, dw, _ = lhs.lhs_loss_grad(tab, x, y, lse, dl, err=err)
     check_grad(dx, dw, r)
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=str)
+@pytest.mark.parametrize("t,v,h", [(1, 600, 64), (3, 40000, 72), (64, 8192, 256), (128, 3000, 33), (140, 100, 200)])
+def test_few_positions_keep_g_in_two_terms(t, v, h, dtype):
+    """Up to 128 positions that take part (of 140, a fifth does not): g is off by eps / 2 of eps / 2
+    of itself; the rest as in test_loss."""
+    w, x, y, dl = make(t, v, h, dtype, masked=0.2)
+    r = reference(w, x, y, dl)
+    on = r["on"]
+    assert int(on.sum()) <= 128
+    u = torch.finfo(dtype).eps / 2
+    W, X, d = w.double(), x[on].double(), dl[on].double()[:, None]
+    p = torch.exp(X @ W.T - r["lse"][:, None])
+    g = (p - torch.zeros_like(p).scatter_(1, y[on].long()[:, None], 1.0)) * d
+    dg = (u * u + 2.0 ** -22) * g.abs() + 2 * 2.0 ** -14 * p * d.abs() + (float(d.abs().max()) if len(d) else 0.0) * 2.0 ** -39
+    tab = table_of(w)
+    _, lse, err = lhs.lhs_loss(tab, x, y)
+    dx, dw = torch.empty((t, h), device="cuda"), torch.empty((v, h), device="cuda")
+    lhs.lhs_loss_grad(tab, x, y, lse, dl, dx=dx, dtable=dw, err=err)
+    within(dx[on], r["dx"], dg @ W.abs() + v * 2.0 ** -23 * (g.abs() @ W.abs()))
+    within(dw, r["dw"], dg.T @ X.abs() + 260 * 2.0 ** -23 * (g.abs().T @ X.abs()))
+    assert bool((dx[~on] == 0).all()) and int(err.item()) == 0
 
 
 @pytest.mark.parametrize("t,v,h", [(300, 60000, 320), (1500, 30011, 136)])
