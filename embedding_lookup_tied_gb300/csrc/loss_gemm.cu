@@ -35,7 +35,7 @@
 // library product of the same shape does 1,597); 2,048 x 262,144 x 5,376: 3.1 ms
 // (1,880).  256 x 262,144 x 5,120: 1.46 ms for 1.18 at the sustained rate; the
 // table is read twice and its gradient written, 1.2 ms of HBM.  One token, 151,936 x
-// 896: statistics 49 us, 5.6 TB/s; gradient 189 us for 80: reading the table twice,
+// 896: statistics 49 us, 5.6 TB/s; gradient 195 us for 80: reading the table twice,
 // and taking 2,376 tiles of its gradient out.
 #include <mutex>
 
@@ -361,7 +361,8 @@ struct Divisor {
 };
 struct Work {
     uint32_t blocks, total;
-    int token_stages;
+    int token_stages;     // k of dtable
+    int turn, gap;        // from stage `turn` on, tokens lie `gap` rows further on (the second terms)
     uint32_t before;      // g of the first pieces
     Divisor block, head, period, ht, splits;  // what the scheduler divides by
 };
@@ -387,8 +388,12 @@ __device__ __forceinline__ Work work_of(const Params &p) {
     Work w = {};
     const int count = ld_dep(&p.meta->count);
     w.blocks = count > 0 ? (static_cast<uint32_t>(count) + kLossTile - 1) / kLossTile : 1u;
-    // (rows of both terms; without any position one stage of zeros)
-    w.token_stages = count == 0 ? 1 : MODE == 1 && count <= kLossTwin ? kLossTile / kTileK : (count + kTileK - 1) / kTileK;
+    w.token_stages = count > 0 ? (count + kTileK - 1) / kTileK : 1;  // (without any position one of zeros)
+    w.turn = w.token_stages;
+    if (MODE == 1 && count <= kLossTwin) {
+        w.gap = kLossTwin - w.turn * kTileK;
+        w.token_stages *= 2;
+    }
     w.total = w.blocks * (static_cast<uint32_t>(p.pieces - 1) * p.piece_tiles + p.last_tiles);
     if (MODE == 1) {
         w.before = p.ahead < p.pieces ? w.blocks * p.ahead * p.piece_tiles : w.total;
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                         }
                         if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * (2 + b_boxes) * kBoxBytes);
                         const uint32_t bar = cluster_addr(&sm.full[s], 0);
-                        const int k = kc * kTileK;
+                        const int k = kc * kTileK + (MODE == 1 && t.kind == kDtable && kc >= work.turn ? work.gap : 0);
                         const int axk = ak ? ax + k : ax, ayk = ak ? ay : ay + k;
                         tma_load_pair(sm.a[s], ma, bar, axk, ayk);
                         tma_load_pair(sm.a[s] + kBoxBytes, ma, bar, ak ? axk : axk + 64, ak ? ayk + 64 : ayk);
