@@ -713,7 +713,7 @@ def _one_device(device, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != device:
             raise ValueError(f"{name} is on {t.device}, not {device}")
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on {device}, which is not the current device")
 
 
