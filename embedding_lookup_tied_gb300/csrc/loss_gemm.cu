@@ -534,10 +534,16 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
         const bool ok = wait_or_abort(&sm.item_full[slot], slot_parity, &sm.abort_flag, p.err);
         if (whole_warp ? !__all_sync(0xFFFFFFFFu, ok) : !ok) return t;
         t = sm.item[slot];
-        // (the branch needs the loaded word, so the slot is not handed back before it is read; a release
-        // at cluster scope would wait for all memory, 0.5 us of every item)
-        if ((!whole_warp || lane == 0) && t.kind >= -1) arrive_cluster(cluster_addr(&sm.item_empty[slot], 0));
-        if (whole_warp) __syncwarp();
+        // One lane hands the slot back, after every lane has read it: the vote needs a word of each of
+        // the item's two loads from all of them (both conditions always hold), and what follows it is
+        // ordered behind their reads.  (A release at cluster scope would wait for all memory, 0.5 us of
+        // every item.)
+        bool read = t.kind >= -1 && t.width <= kLossTile;
+        if (whole_warp) {
+            read = __all_sync(0xFFFFFFFFu, read);
+            __syncwarp();
+        }
+        if ((!whole_warp || lane == 0) && read) arrive_cluster(cluster_addr(&sm.item_empty[slot], 0));
         if (++slot == kQueue) {
             slot = 0;
             slot_parity ^= 1u;

@@ -130,6 +130,23 @@ def test_several_at_once(t, v, h):
             dw.fill_(float("nan"))
 
 
+@pytest.mark.parametrize("t,v,h", [(6000, 30000, 8), (300, 400003, 16), (2000, 60001, 64)])
+def test_items_handed_over_as_fast_as_they_can(t, v, h):
+    # one stage of k to a tile of logits and one tile of columns: the items' slots are written again
+    # as soon as the last of the roles has read them
+    w, x, y, lse, dl, rx, rw = flat(t, v, h, torch.bfloat16)
+    tab = table_of(w)
+    ws = torch.empty(lhs.lhs_loss_grad_workspace(tab, t), dtype=torch.uint8, device="cuda")
+    dx, dw = torch.empty((t, h), device="cuda"), torch.empty((v, h), device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(20):
+        dx.fill_(float("nan"))
+        dw.fill_(float("nan"))
+        lhs.lhs_loss_grad(tab, x, y, lse, dl, dx=dx, dtable=dw, ws=ws, err=err)
+        assert torch.equal(dx, rx.float()) and torch.equal(dw, rw.float())
+    assert int(err.item()) == 0
+
+
 def test_captured_with_other_numbers_of_positions():
     # the tiles of a captured call follow the positions that take part at its replay
     t, v, h = 1200, 40000, 72
