@@ -785,8 +785,8 @@ def lhs_loss_grad(table: Table, x: torch.Tensor, targets: torch.Tensor, lse: tor
     """Gradients of ``sum(dloss * loss)`` for the residuals ([tokens, hidden])
     and for the table ([vocab, hidden]), given :func:`lhs_loss`'s ``lse``.
     ``dx`` and ``dtable`` are of the table's type, or f32 where such a tensor is
-    given; ``accumulate`` adds to ``dtable``.  Returns (dx|None, dtable|None, err
-    word)."""
+    given; ``dx`` may be ``x``, all else lies apart; ``accumulate`` adds to
+    ``dtable``.  Returns (dx|None, dtable|None, err word)."""
     xp, xdt, stride, n, tp = _loss_args(table, x, targets)
     dev, f = x.device, torch.float32
     if want_dx:

@@ -1,6 +1,7 @@
 // train_abi.cu — the C-ABI boundary of the cross entropy over the tied table,
 // its gradient and the lookup's gradient: argument checks, then the launchers.
 #include <cmath>
+#include <initializer_list>
 
 #include "train.cuh"
 
@@ -17,6 +18,31 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 int elem_size(int32_t dtype) {
     return dtype == LHS_F32 ? 4 : (dtype == LHS_F16 || dtype == LHS_BF16) ? 2 : 0;
 }
+
+// Memory of an argument: rows of row_bytes, stride bytes apart.
+struct Rows {
+    uintptr_t at;
+    uint64_t rows, stride, row_bytes;
+};
+Rows bytes_of(const void *p, uint64_t n) { return {reinterpret_cast<uintptr_t>(p), p && n ? 1u : 0u, n, n}; }
+Rows rows_of(const void *p, int64_t rows, int64_t stride, int64_t row, int size) {
+    return {reinterpret_cast<uintptr_t>(p), p ? static_cast<uint64_t>(rows) : 0u, static_cast<uint64_t>(stride) * size,
+            static_cast<uint64_t>(row) * size};
+}
+// Whether a row of r lies in the bytes of one that is contiguous.
+bool meet(const Rows &one, const Rows &r) {
+    const uintptr_t end = one.at + one.row_bytes;
+    if (!one.rows || !r.rows || end <= r.at) return false;
+    const uint64_t from = one.at > r.at ? one.at - r.at : 0;
+    const uint64_t k = from < r.row_bytes ? 0 : (from - r.row_bytes) / r.stride + 1;  // the first row that ends behind it
+    return k < r.rows && k * r.stride < end - r.at;
+}
+bool meet(const Rows &one, std::initializer_list<Rows> others) {
+    for (const Rows &r : others)
+        if (meet(one, r)) return true;
+    return false;
+}
+Rows table_rows(const lhs_table &t) { return bytes_of(t.data, static_cast<uint64_t>(t.vocab) * t.row_bytes); }
 
 int check_loss_table(const lhs_table *t, int64_t tokens) {
     if (!t) return LHS_ERR_INVALID_ARG;
@@ -77,6 +103,12 @@ int lhs_loss(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t x_str
     if (!d_loss || !aligned(d_loss, 4) || !d_lse || !aligned(d_lse, 4)) return LHS_ERR_INVALID_ARG;
     const LossPlan p = plan_loss(*t, tokens, false);
     if (ws_bytes < p.bytes) return LHS_ERR_BUFFER_TOO_SMALL;
+    const Rows table = table_rows(*t), x = rows_of(d_x, tokens, x_stride, t->hidden, elem_size(x_dtype)),
+               y = bytes_of(d_targets, 4 * tokens), loss = bytes_of(d_loss, 4 * tokens),
+               lse = bytes_of(d_lse, 4 * tokens), ws = bytes_of(d_ws, p.bytes), err = bytes_of(d_err, 4);
+    if (meet(loss, {table, x, y, lse, ws, err}) || meet(lse, {table, x, y, ws, err}) || meet(ws, {table, x, y, err}) ||
+        meet(err, {table, x, y}))
+        return LHS_ERR_INVALID_ARG;
     LossArgs a = {};
     a.t = *t;
     a.x = d_x;
@@ -101,12 +133,6 @@ int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t 
     if (accumulate != 0 && accumulate != 1) return LHS_ERR_INVALID_ARG;
     if (d_dtable && ((dtable_dtype != t->dtype && dtable_dtype != LHS_F32) || !aligned(d_dtable, 16)))
         return LHS_ERR_INVALID_ARG;
-    if (d_dtable) {  // the table is read while its gradient is written
-        const uintptr_t w = reinterpret_cast<uintptr_t>(t->data), g = reinterpret_cast<uintptr_t>(d_dtable);
-        const uintptr_t w1 = w + static_cast<uintptr_t>(t->vocab) * t->row_bytes;
-        const uintptr_t g1 = g + static_cast<uintptr_t>(t->vocab) * t->hidden * elem_size(dtable_dtype);
-        if (g < w1 && w < g1) return LHS_ERR_INVALID_ARG;
-    }
     if (d_dx && ((dx_dtype != t->dtype && dx_dtype != LHS_F32) || dx_stride < t->hidden || dx_stride > kMaxStride ||
                  !aligned(d_dx, elem_size(dx_dtype))))
         return LHS_ERR_INVALID_ARG;
@@ -115,7 +141,20 @@ int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t 
         if (!d_lse || !aligned(d_lse, 4) || !d_dloss || !aligned(d_dloss, 4)) return LHS_ERR_INVALID_ARG;
     }
     const LossPlan p = plan_loss(*t, tokens, true);
-    if (tokens > 0 && ws_bytes < p.bytes) return LHS_ERR_BUFFER_TOO_SMALL;
+    const Rows table = table_rows(*t),
+               dtable = bytes_of(d_dtable, static_cast<uint64_t>(t->vocab) * t->hidden * elem_size(dtable_dtype));
+    if (meet(dtable, table)) return LHS_ERR_INVALID_ARG;  // also of no positions
+    if (tokens > 0) {
+        if (ws_bytes < p.bytes) return LHS_ERR_BUFFER_TOO_SMALL;
+        const Rows x = rows_of(d_x, tokens, x_stride, t->hidden, elem_size(x_dtype)), y = bytes_of(d_targets, 4 * tokens),
+                   lse = bytes_of(d_lse, 4 * tokens), dloss = bytes_of(d_dloss, 4 * tokens),
+                   dx = rows_of(d_dx, tokens, dx_stride, t->hidden, elem_size(dx_dtype)), ws = bytes_of(d_ws, p.bytes),
+                   err = bytes_of(d_err, 4);
+        // (dx may lie over x, which the first kernel has read)
+        if (meet(dtable, {x, y, lse, dloss, dx, ws, err}) || meet(ws, {table, x, y, lse, dloss, dx, err}) ||
+            meet(err, {table, x, y, lse, dloss, dx}) || meet(table, dx) || meet(y, dx) || meet(lse, dx) || meet(dloss, dx))
+            return LHS_ERR_INVALID_ARG;
+    }
     LossArgs a = {};
     a.t = *t;
     a.x = d_x;
@@ -154,6 +193,12 @@ int lhs_embed_grad(int64_t vocab, int32_t hidden, const int32_t *d_ids, int64_t 
             !aligned(d_err, 4))
             return LHS_ERR_INVALID_ARG;
         if (ws_bytes < static_cast<size_t>(need)) return LHS_ERR_BUFFER_TOO_SMALL;
+        // ids that change while they are sorted would be moved to places that were not counted
+        const Rows dout = rows_of(d_dout, n, dout_stride, hidden, es), ids = bytes_of(d_ids, 4 * n),
+                   dtable = bytes_of(d_dtable, static_cast<uint64_t>(vocab) * hidden * elem_size(dtable_dtype)),
+                   ws = bytes_of(d_ws, need), err = bytes_of(d_err, 4);
+        if (meet(dtable, {dout, ids, ws, err}) || meet(ws, {dout, ids, err}) || meet(err, {dout, ids}))
+            return LHS_ERR_INVALID_ARG;
     }
     if (n == 0 && accumulate) return LHS_OK;
     EmbedGradArgs a = {vocab, hidden, d_ids, n, ignore, scale, d_dout, dout_dtype, dout_stride, d_dtable, dtable_dtype,

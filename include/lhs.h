@@ -469,6 +469,8 @@ LHS_API int lhs_sample(const void *d_logits, int32_t dtype, int64_t stride, int6
  *   d_targets : int32 [tokens]
  *   d_loss, d_lse : f32 [tokens]
  *   d_ws      : 256-byte aligned, >= lhs_loss_workspace bytes, overwritten
+ * What is written (d_loss, d_lse, the workspace, d_err) lies apart from
+ * everything else (LHS_ERR_INVALID_ARG); it may lie between rows of x.
  * The logits are f32 sums of exact products (512 of hidden at a time in the
  * tensor cores); neither they nor their exponentials' sums are rounded to fewer
  * bits.  A position whose logits hold NaN or
@@ -497,9 +499,11 @@ LHS_API int lhs_loss(const lhs_table *t, const void *d_x, int32_t x_dtype, int64
  *                  NULL: not wanted
  *                  (it may be d_x itself)
  *   d_dtable     : [vocab x hidden] row-major of dtable_dtype (the table's type
- *                  or LHS_F32), 16-byte aligned, apart from the table; or NULL:
- *                  not wanted.  One of the two has to be wanted.
+ *                  or LHS_F32), 16-byte aligned; or NULL: not wanted.  One of
+ *                  the two has to be wanted.
  *   d_ws         : 256-byte aligned, >= lhs_loss_grad_workspace bytes, overwritten
+ * What is written (d_dx, d_dtable, the workspace, d_err) lies apart from
+ * everything else but for d_dx over d_x (LHS_ERR_INVALID_ARG).
  * The logits are computed again, a piece of the vocabulary at a time, in one
  * kernel whose CTAs wait only for work that running CTAs have taken: calls on
  * several streams may share the GPU in any way.  g is
@@ -534,6 +538,8 @@ LHS_API int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, 
  *   d_dtable : [vocab x hidden] row-major, LHS_F32, LHS_F16 or LHS_BF16,
  *              16-byte aligned
  *   d_ws     : 256-byte aligned, >= lhs_embed_grad_workspace bytes, overwritten
+ * What is written (d_dtable, the workspace, d_err) lies apart from everything
+ * else (LHS_ERR_INVALID_ARG).
  * 0 <= n <= 2^30 (n == 0 clears dtable, unless accumulate); 1 <= vocab <=
  * 2^31-1; 1 <= hidden <= 65536; scale finite.  lhs_embed_grad_workspace gives
  * -1 outside these.  Errors: LHS_ERR_INVALID_ARG, LHS_ERR_BUFFER_TOO_SMALL,
