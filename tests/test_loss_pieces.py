@@ -147,6 +147,23 @@ def test_items_handed_over_as_fast_as_they_can(t, v, h):
     assert int(err.item()) == 0
 
 
+@pytest.mark.parametrize("t,v,h", [(3000, 60000, 520), (1025, 200000, 40)])
+def test_slots_of_g_are_overwritten_after_their_last_reader(t, v, h):
+    # more pieces than slots; dx's and dtable's tiles read a slot at their own pace, for one of the
+    # two products, the other and both
+    w, x, y, lse, dl, rx, rw = flat(t, v, h, torch.float16)
+    tab = table_of(w)
+    dx, dw = torch.empty((t, h), device="cuda"), torch.empty((v, h), device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for k in range(12):
+        dx.fill_(float("nan"))
+        dw.fill_(float("nan"))
+        lhs.lhs_loss_grad(tab, x, y, lse, dl, dx=dx, dtable=dw, want_dx=k % 3 != 1, want_dtable=k % 3 != 2, err=err)
+        assert k % 3 == 1 or torch.equal(dx, rx.float())
+        assert k % 3 == 2 or torch.equal(dw, rw.float())
+    assert int(err.item()) == 0
+
+
 def test_captured_with_other_numbers_of_positions():
     # the tiles of a captured call follow the positions that take part at its replay
     t, v, h = 1200, 40000, 72
