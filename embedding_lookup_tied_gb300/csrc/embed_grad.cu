@@ -21,6 +21,8 @@
 //    the ids, which use little of the chip (8,192 ids: 402 MB of zeros, 55 us, beside
 //    13 us of comparisons).
 //
+// The same order and sums serve the loss's gradient: weighted rows of residuals by target.
+//
 // What bounds it.  262,144 positions of 151,936 x 896 bf16: 168 us for 110 of HBM; the
 // sums read 470 MB in 95 us (5.6 TB/s with what they write), the sort takes 50 us
 // beside the zeros' 40, the join 20.  8,192 positions into 262,144 x 768 bf16: 73 us
@@ -258,14 +260,14 @@ struct Word<16> {
     using T = uint4;
 };
 
-// VEC consecutive values of a row, widened.
+// VEC consecutive values of a row, widened; added with a weight (1: a plain addition).
 template <int DT, int VEC>
 struct Pack;
 template <int DT>
 struct Pack<DT, 1> {
     typename Elem<DT>::T v;
     __device__ __forceinline__ void load(const typename Elem<DT>::T *p) { v = ld_dep(p); }
-    __device__ __forceinline__ void add(float (&s)[1]) const { s[0] += Elem<DT>::widen(v); }
+    __device__ __forceinline__ void add(float (&s)[1], float w) const { s[0] = fmaf(Elem<DT>::widen(v), w, s[0]); }
 };
 template <>
 struct Pack<LHS_F32, 8> {
@@ -274,21 +276,21 @@ struct Pack<LHS_F32, 8> {
         a = ld_dep(reinterpret_cast<const float4 *>(p));
         b = ld_dep(reinterpret_cast<const float4 *>(p) + 1);
     }
-    __device__ __forceinline__ void add(float (&s)[8]) const {
-        s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
-        s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
+    __device__ __forceinline__ void add(float (&s)[8], float w) const {
+        s[0] = fmaf(a.x, w, s[0]), s[1] = fmaf(a.y, w, s[1]), s[2] = fmaf(a.z, w, s[2]), s[3] = fmaf(a.w, w, s[3]);
+        s[4] = fmaf(b.x, w, s[4]), s[5] = fmaf(b.y, w, s[5]), s[6] = fmaf(b.z, w, s[6]), s[7] = fmaf(b.w, w, s[7]);
     }
 };
 template <int DT>
 struct Pack<DT, 8> {
     uint4 w;
     __device__ __forceinline__ void load(const uint16_t *p) { w = ld_dep(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void add(float (&s)[8]) const {
+    __device__ __forceinline__ void add(float (&s)[8], float weight) const {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            s[2 * i] += Elem<DT>::widen(static_cast<uint16_t>(u[i]));
-            s[2 * i + 1] += Elem<DT>::widen(static_cast<uint16_t>(u[i] >> 16));
+            s[2 * i] = fmaf(Elem<DT>::widen(static_cast<uint16_t>(u[i])), weight, s[2 * i]);
+            s[2 * i + 1] = fmaf(Elem<DT>::widen(static_cast<uint16_t>(u[i] >> 16)), weight, s[2 * i + 1]);
         }
     }
 };
@@ -336,11 +338,26 @@ struct Sums {
                             // last where it goes on
     uint32_t *n_cross;      // runs whose last id starts there and goes on
     int32_t *cross;
+    // sums of target rows: weighted, and not all rows of a table
+    const int32_t *row_of;  // row of x of a position
+    const float *weight;    // of a row of x
+    int32_t *slot_of;       // [vocab] row of the sum of an id, told here; [tiles of them] 0 where one is
+    int64_t out_pitch;
+    bool by_id;             // sums lie by id, else by the sorted place of an id's last position in its first run
 };
+// Where the sum of an id goes.
+template <bool TARGETS, typename O>
+__device__ __forceinline__ O *sum_row(const Sums &p, O *out, uint32_t id, int64_t place) {
+    return TARGETS ? out + (p.by_id ? static_cast<int64_t>(id) : place) * p.out_pitch : out + static_cast<int64_t>(id) * p.hidden;
+}
+__device__ __forceinline__ void tell_slot(const Sums &p, uint32_t id, int64_t place) {
+    p.slot_of[id] = p.by_id ? static_cast<int32_t>(id) : static_cast<int32_t>(place);
+    p.slot_of[p.vocab + id / kLossTile] = 0;
+}
 
 // A group of `cols` threads (a power of two) to a run; thread c of it holds
 // columns VEC (c + cols blockIdx.y) and up.
-template <int DT, int VEC, typename O, bool ADD>
+template <int DT, int VEC, typename O, bool ADD, bool TARGETS>
 __global__ void __launch_bounds__(kSumThreads)
     sum_runs_kernel(const Sums p, const typename Elem<DT>::T *dout, O *dtable, int cols) {
     constexpr int kAhead = ADD && sizeof(O) == 4 ? 4 : 8;  // rows (and sums to add to) asked for at a time
@@ -350,11 +367,16 @@ __global__ void __launch_bounds__(kSumThreads)
     const int groups = kSumThreads / cols, group = threadIdx.x / cols, c = threadIdx.x % cols;
     uint32_t *key = lists + group * p.run;                                               // none past the end
     int32_t *pos = reinterpret_cast<int32_t *>(lists + (groups + group) * p.run);
+    float *weight = reinterpret_cast<float *>(lists + (2 * groups + group) * p.run);     // (TARGETS)
     const int64_t run = static_cast<int64_t>(blockIdx.x) * groups + group;
     const int64_t i0 = run * p.run;
     for (int e = c; e < p.run; e += cols) {
         key[e] = i0 + e < p.n ? ld_dep(p.keys + i0 + e) : none;
         pos[e] = i0 + e < p.n ? ld_dep(p.order + i0 + e) : 0;
+        if (TARGETS && key[e] != none) {
+            pos[e] = ld_dep(p.row_of + pos[e]);
+            weight[e] = ld_dep(p.weight + pos[e]);
+        }
     }
     const uint32_t prev = i0 > 0 && i0 < p.n ? ld_dep(p.keys + i0 - 1) : none;
     const uint32_t next = i0 + p.run < p.n ? ld_dep(p.keys + i0 + p.run) : none;
@@ -388,11 +410,12 @@ __global__ void __launch_bounds__(kSumThreads)
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) {
             if (k[e] == none) continue;
-            if (in) v[e].add(s);
+            if (in) v[e].add(s, TARGETS ? weight[e0 + e] : 1.0f);
             if (k[e] == k[e + 1]) continue;
             // the id's last position
             if (k[e] == head) keep(2 * run);
-            else if (in) old[e].store(dtable + static_cast<int64_t>(k[e]) * p.hidden + j, s, p.scale, ADD);
+            else if (in) old[e].store(sum_row<TARGETS>(p, dtable, k[e], i0 + e0 + e) + j, s, p.scale, ADD);
+            if (TARGETS && k[e] != head && c == 0 && blockIdx.y == 0) tell_slot(p, k[e], i0 + e0 + e);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) s[i] = 0.0f;
         }
@@ -406,7 +429,7 @@ __global__ void __launch_bounds__(kSumThreads)
 // The ids that cross runs: an item is one of them and kJoinCols columns, a warp to an
 // item.  One with more than 32 further runs is shared by the CTA's warps, whose sums are
 // joined in their order.  (Items of a CTA of 512 threads each: 61 us for 262,144 positions.)
-template <typename O>
+template <typename O, bool TARGETS>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     join_runs_kernel(const Sums p, O *dtable, int col_blocks, bool vec) {
     __shared__ float4 part[kJoinWarps][32];
@@ -428,9 +451,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
         }
         return s;
     };
-    auto finish = [&](uint32_t id, int j, const float4 &s) {
+    auto finish = [&](uint32_t id, int64_t run, int j, const float4 &s) {
         const float f[4] = {s.x, s.y, s.z, s.w};
-        O *o = dtable + static_cast<int64_t>(id) * p.hidden + j;
+        const int64_t place = (run + 1) * p.run - 1;
+        O *o = sum_row<TARGETS>(p, dtable, id, place) + j;
+        if (TARGETS && j == 0) tell_slot(p, id, place);
         if (vec && j < p.hidden) {  // hidden % 4 == 0: four values are 8 or 16 aligned bytes
             using W = typename Word<4 * sizeof(O)>::T;
             alignas(16) O v[4];
@@ -453,7 +478,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
             const uint32_t id = ld_dep(p.keys + (run + 1) * p.run - 1);
             const uint32_t m = __ballot_sync(0xFFFFFFFFu, starts(run + 1 + lane, id));
             if (m == 0xFFFFFFFFu) left = item;
-            else finish(id, j, sum(run, __popc(m), 0, 1, j));
+            else finish(id, run, j, sum(run, __popc(m), 0, 1, j));
         }
         if (lane == 0) large[warp] = left;
         __syncthreads();
@@ -481,7 +506,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
                     const float4 a = part[k][lane];
                     s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
                 }
-                finish(id, j, s);
+                finish(id, run, j, s);
             }
             __syncthreads();
         }
@@ -537,24 +562,37 @@ unsigned zero_ctas(const Zero &z, int threads) {
     return static_cast<unsigned>((z.n16 + each - 1) / each) + (z.n16 == 0 && z.ntail ? 1u : 0u);
 }
 
-template <int DT, int VEC, typename O>
-cudaError_t sum_runs(const EmbedGradArgs &a, const Sums &s, int64_t runs, cudaStream_t stream) {
+template <int DT, int VEC, typename O, bool ADD, bool TARGETS>
+cudaError_t launch_sums(const Sums &s, const void *rows, O *out, int64_t runs, cudaStream_t stream) {
     int cols = 8;
-    while (cols < kSumThreads && cols * VEC < a.hidden) cols *= 2;
+    while (cols < kSumThreads && cols * VEC < s.hidden) cols *= 2;
     const int groups = kSumThreads / cols;
     const dim3 grid(static_cast<unsigned>((runs + groups - 1) / groups),
-                    static_cast<unsigned>((a.hidden + cols * VEC - 1) / (cols * VEC)));
-    const size_t smem = static_cast<size_t>(2 * groups) * s.run * 4;
-    const auto *d = static_cast<const typename Elem<DT>::T *>(a.dout);
-    if (a.accumulate)
-        return launch_pdl(sum_runs_kernel<DT, VEC, O, true>, grid, dim3(kSumThreads), smem, stream, s, d,
-                          static_cast<O *>(a.dtable), cols);
-    return launch_pdl(sum_runs_kernel<DT, VEC, O, false>, grid, dim3(kSumThreads), smem, stream, s, d,
-                      static_cast<O *>(a.dtable), cols);
+                    static_cast<unsigned>((s.hidden + cols * VEC - 1) / (cols * VEC)));
+    const size_t smem = static_cast<size_t>((TARGETS ? 3 : 2) * groups) * s.run * 4;
+    return launch_pdl(sum_runs_kernel<DT, VEC, O, ADD, TARGETS>, grid, dim3(kSumThreads), smem, stream, s,
+                      static_cast<const typename Elem<DT>::T *>(rows), out, cols);
+}
+template <typename O, bool TARGETS>
+cudaError_t launch_join(const Sums &s, O *out, int64_t runs, cudaStream_t stream) {
+    DeviceInfo dev;
+    const cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return e;
+    const int col_blocks = (s.hidden + kJoinCols - 1) / kJoinCols;
+    const int64_t most = (runs * col_blocks + kJoinWarps - 1) / kJoinWarps, cap = 4ll * dev.num_sms;
+    return launch_pdl(join_runs_kernel<O, TARGETS>, dim3(static_cast<unsigned>(most < cap ? most : cap)), dim3(32 * kJoinWarps), 0,
+                      stream, s, out, col_blocks, s.hidden % 4 == 0);
+}
+
+template <int DT, int VEC, typename O>
+cudaError_t sum_runs(const EmbedGradArgs &a, const Sums &s, int64_t runs, cudaStream_t stream) {
+    O *out = static_cast<O *>(a.dtable);
+    return a.accumulate ? launch_sums<DT, VEC, O, true, false>(s, a.dout, out, runs, stream)
+                        : launch_sums<DT, VEC, O, false, false>(s, a.dout, out, runs, stream);
 }
 
 template <typename O>
-cudaError_t sums(const EmbedGradArgs &a, const Sums &s, int64_t runs, const DeviceInfo &dev, cudaStream_t stream) {
+cudaError_t sums(const EmbedGradArgs &a, const Sums &s, int64_t runs, cudaStream_t stream) {
     // eight values at a time where every row of dout and of the table starts on the words they make
     const size_t es = a.dout_dtype == LHS_F32 ? 4 : 2;
     const bool wide8 = a.hidden % 8 == 0 && reinterpret_cast<uintptr_t>(a.dout) % 16 == 0 &&
@@ -567,10 +605,70 @@ cudaError_t sums(const EmbedGradArgs &a, const Sums &s, int64_t runs, const Devi
     else
         e = wide8 ? sum_runs<LHS_BF16, 8, O>(a, s, runs, stream) : sum_runs<LHS_BF16, 1, O>(a, s, runs, stream);
     if (e != cudaSuccess || runs < 2) return e;
-    const int col_blocks = (a.hidden + kJoinCols - 1) / kJoinCols;
-    const int64_t most = (runs * col_blocks + kJoinWarps - 1) / kJoinWarps, cap = 4ll * dev.num_sms;
-    return launch_pdl(join_runs_kernel<O>, dim3(static_cast<unsigned>(most < cap ? most : cap)), dim3(32 * kJoinWarps), 0,
-                      stream, s, static_cast<O *>(a.dtable), col_blocks, a.hidden % 4 == 0);
+    return launch_join<O, false>(s, static_cast<O *>(a.dtable), runs, stream);
+}
+
+// Orders the ids, and writes zeros beside that; `s` gets the sorted keys and positions, and what sums
+// of runs need besides.
+cudaError_t order_ids(const int32_t *ids, int64_t n, int64_t vocab, int32_t ignore, const Layout &l, uint8_t *ws,
+                      void *zeros, size_t zero_bytes, int32_t *err, Sums *s, cudaStream_t stream) {
+    uint32_t *keys[2] = {reinterpret_cast<uint32_t *>(ws + l.keys[0]), reinterpret_cast<uint32_t *>(ws + l.keys[1])};
+    int32_t *order[2] = {reinterpret_cast<int32_t *>(ws + l.order[0]), reinterpret_cast<int32_t *>(ws + l.order[1])};
+    s->n_cross = reinterpret_cast<uint32_t *>(ws + l.n_cross);
+    cudaError_t e = cudaSuccess;
+    int last = 0;
+    if (n <= kRankMost) {
+        Zero z = zeros_of(zeros, zero_bytes);
+        z.first = static_cast<int>((n + 31) / 32);
+        e = launch_pdl(rank_ids_kernel, dim3(z.first + zero_ctas(z, kRankThreads)), dim3(kRankThreads),
+                       round_up(n, 32) * 4, stream, ids, static_cast<int>(n), static_cast<uint32_t>(vocab), ignore, keys[0], order[0],
+                       s->n_cross, z, err);
+        if (e != cudaSuccess) return e;
+    } else {
+        int bits = 1;
+        while ((vocab >> bits) != 0) ++bits;  // keys are 0 .. vocab
+        const int passes = (bits + kDigitBits - 1) / kDigitBits;
+        Pass p = {};
+        p.counts = reinterpret_cast<uint32_t *>(ws + l.counts);
+        p.n = n;
+        p.tiles = l.tiles;
+        p.per = round_up((n + l.tiles - 1) / l.tiles, kRound);
+        p.vocab = static_cast<uint32_t>(vocab);
+        p.ignore = ignore;
+        p.n_cross = s->n_cross;
+        p.err = err;
+        // the moves take the zeros (20 us a pass for 262,144 ids, as 136 MB of zeros do; a count takes 5)
+        auto share = [&](int i) {  // in whole words; the last takes the rest
+            const size_t each = zero_bytes / 16 / passes * 16;
+            Zero z = zeros_of(static_cast<uint8_t *>(zeros) + i * each, i + 1 < passes ? each : zero_bytes - i * each);
+            z.first = l.tiles;
+            return z;
+        };
+        for (int i = 0; i < passes; ++i) {
+            p.shift = bits * i / passes;
+            p.bits = bits * (i + 1) / passes - p.shift;
+            p.ids = i == 0 ? ids : nullptr;
+            p.keys_in = keys[(i & 1) ^ 1];
+            p.order_in = order[(i & 1) ^ 1];
+            p.keys_out = keys[i & 1];
+            p.order_out = order[i & 1];
+            e = launch_pdl(count_digits_kernel, dim3(l.tiles), dim3(kSortThreads), 0, stream, p);
+            if (e != cudaSuccess) return e;
+            const Zero z = share(i);
+            e = launch_pdl(move_digits_kernel, dim3(l.tiles + zero_ctas(z, kSortThreads)), dim3(kSortThreads), 0, stream, p, z);
+            if (e != cudaSuccess) return e;
+            last = i & 1;
+        }
+    }
+    s->keys = keys[last];
+    s->order = order[last];
+    s->n = n;
+    s->run = l.run;
+    s->pitch = l.pitch;
+    s->vocab = vocab;
+    s->part = reinterpret_cast<float *>(ws + l.part);
+    s->cross = reinterpret_cast<int32_t *>(ws + l.cross);
+    return e;
 }
 
 }  // namespace
@@ -586,74 +684,36 @@ cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t stream) {
     const size_t es = a.dtable_dtype == LHS_F32 ? 4 : 2;
     const size_t table_bytes = a.accumulate ? 0 : static_cast<size_t>(a.vocab) * a.hidden * es;
     if (a.n == 0) return a.accumulate ? cudaSuccess : launch_zero(a.dtable, table_bytes, stream);
-    DeviceInfo dev;
-    cudaError_t e = device_info(&dev);
-    if (e != cudaSuccess) return e;
     const Layout l = layout_of(a.hidden, a.n);
-    uint32_t *keys[2] = {reinterpret_cast<uint32_t *>(a.ws + l.keys[0]), reinterpret_cast<uint32_t *>(a.ws + l.keys[1])};
-    int32_t *order[2] = {reinterpret_cast<int32_t *>(a.ws + l.order[0]), reinterpret_cast<int32_t *>(a.ws + l.order[1])};
     Sums s = {};
-    s.n_cross = reinterpret_cast<uint32_t *>(a.ws + l.n_cross);
-    const uint32_t vocab = static_cast<uint32_t>(a.vocab);
-    int last = 0;
-    if (a.n <= kRankMost) {
-        Zero z = zeros_of(a.dtable, table_bytes);
-        z.first = static_cast<int>((a.n + 31) / 32);
-        e = launch_pdl(rank_ids_kernel, dim3(z.first + zero_ctas(z, kRankThreads)), dim3(kRankThreads),
-                       round_up(a.n, 32) * 4, stream, a.ids, static_cast<int>(a.n), vocab, a.ignore, keys[0], order[0],
-                       s.n_cross, z, a.err);
-        if (e != cudaSuccess) return e;
-    } else {
-        int bits = 1;
-        while ((a.vocab >> bits) != 0) ++bits;  // keys are 0 .. vocab
-        const int passes = (bits + kDigitBits - 1) / kDigitBits;
-        Pass p = {};
-        p.counts = reinterpret_cast<uint32_t *>(a.ws + l.counts);
-        p.n = a.n;
-        p.tiles = l.tiles;
-        p.per = round_up((a.n + l.tiles - 1) / l.tiles, kRound);
-        p.vocab = vocab;
-        p.ignore = a.ignore;
-        p.n_cross = s.n_cross;
-        p.err = a.err;
-        // the moves take the zeros (20 us a pass for 262,144 ids, as 136 MB of zeros do; a count takes 5)
-        auto share = [&](int i) {  // in whole words; the last takes the rest
-            const size_t each = table_bytes / 16 / passes * 16;
-            Zero z = zeros_of(static_cast<uint8_t *>(a.dtable) + i * each, i + 1 < passes ? each : table_bytes - i * each);
-            z.first = l.tiles;
-            return z;
-        };
-        for (int i = 0; i < passes; ++i) {
-            p.shift = bits * i / passes;
-            p.bits = bits * (i + 1) / passes - p.shift;
-            p.ids = i == 0 ? a.ids : nullptr;
-            p.keys_in = keys[(i & 1) ^ 1];
-            p.order_in = order[(i & 1) ^ 1];
-            p.keys_out = keys[i & 1];
-            p.order_out = order[i & 1];
-            e = launch_pdl(count_digits_kernel, dim3(l.tiles), dim3(kSortThreads), 0, stream, p);
-            if (e != cudaSuccess) return e;
-            const Zero z = share(i);
-            e = launch_pdl(move_digits_kernel, dim3(l.tiles + zero_ctas(z, kSortThreads)), dim3(kSortThreads), 0, stream, p, z);
-            if (e != cudaSuccess) return e;
-            last = i & 1;
-        }
-    }
-    s.keys = keys[last];
-    s.order = order[last];
-    s.n = a.n;
-    s.run = l.run;
+    const cudaError_t e = order_ids(a.ids, a.n, a.vocab, a.ignore, l, a.ws, a.dtable, table_bytes, a.err, &s, stream);
+    if (e != cudaSuccess) return e;
     s.hidden = a.hidden;
-    s.pitch = l.pitch;
-    s.vocab = a.vocab;
     s.scale = a.scale;
     s.dout_stride = a.dout_stride;
     s.accumulate = a.accumulate;
-    s.part = reinterpret_cast<float *>(a.ws + l.part);
-    s.cross = reinterpret_cast<int32_t *>(a.ws + l.cross);
-    if (a.dtable_dtype == LHS_F32) return sums<float>(a, s, l.runs, dev, stream);
-    if (a.dtable_dtype == LHS_F16) return sums<__half>(a, s, l.runs, dev, stream);
-    return sums<__nv_bfloat16>(a, s, l.runs, dev, stream);
+    if (a.dtable_dtype == LHS_F32) return sums<float>(a, s, l.runs, stream);
+    if (a.dtable_dtype == LHS_F16) return sums<__half>(a, s, l.runs, stream);
+    return sums<__nv_bfloat16>(a, s, l.runs, stream);
+}
+
+cudaError_t launch_target_rows(const TargetRowsArgs &a, cudaStream_t stream) {
+    const Layout l = layout_of(a.Hp, a.T);
+    Sums s = {};
+    cudaError_t e = order_ids(a.targets, a.T, a.V, a.ignore, l, a.ws, nullptr, 0, a.err, &s, stream);
+    if (e != cudaSuccess) return e;
+    s.hidden = a.Hp;
+    s.scale = 1.0f;
+    s.dout_stride = a.Hp;
+    s.row_of = a.pos;
+    s.weight = a.coef;
+    s.slot_of = a.slot_of;
+    s.out_pitch = a.pitch;
+    s.by_id = a.V <= a.T;
+    e = a.bf16 ? launch_sums<LHS_BF16, 8, float, false, true>(s, a.x, a.rows, l.runs, stream)
+               : launch_sums<LHS_F16, 8, float, false, true>(s, a.x, a.rows, l.runs, stream);
+    if (e != cudaSuccess || l.runs < 2) return e;
+    return launch_join<float, true>(s, a.rows, l.runs, stream);
 }
 
 }  // namespace lhs

@@ -35,6 +35,11 @@ struct PackParams {
     LossMeta *meta;
     int32_t *act, *tgt, *pos;
     float *lse2, *gs;
+    const uint16_t *w;       // the table, where the targets' entries are kept apart
+    bool w_vec;              // its rows start on 16-byte boundaries
+    float *coef;
+    int32_t *slot;           // set to -1
+    int64_t n_slot;
     uint16_t *xc;
     uint32_t *sync;          // cleared
     int64_t n_sync;
@@ -68,6 +73,22 @@ __device__ __forceinline__ uint4 row_word(const uint16_t *row, int c, int H, boo
 #pragma unroll
     for (int i = 0; i < 8; ++i) u[i] = 8 * c + i < H ? ld_dep(row + 8 * c + i) : 0u;
     return make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+}
+
+// The sum of the products of two words' values.
+__device__ __forceinline__ float word_dot(const uint4 &a, const uint4 &b, bool f16) {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (f16)
+            s[i] = fmaf(f16_bits_to_f32(static_cast<uint16_t>(u[i])), f16_bits_to_f32(static_cast<uint16_t>(v[i])),
+                        f16_bits_to_f32(static_cast<uint16_t>(u[i] >> 16)) * f16_bits_to_f32(static_cast<uint16_t>(v[i] >> 16)));
+        else
+            s[i] = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16),
+                        __uint_as_float(u[i] & 0xFFFF0000u) * __uint_as_float(v[i] & 0xFFFF0000u));
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 // Each CTA takes an equal range of positions.  It counts the ones before it
@@ -148,6 +169,29 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
                 if (twin) reinterpret_cast<uint4 *>(p.xc + static_cast<int64_t>(k + kLossTwin) * p.Hp)[c] = v;
             }
         }
+        if (GRAD && p.coef) {
+            // the target's entry of g, from a logit of its own in f32 (the products' kernel adds to g what
+            // its logit makes of it beyond this); a warp to a position, whose row has just been read
+            for (int r = warp; r < n; r += kPackWarps) {
+                const int k = rank_of[r];
+                if (k < 0) continue;
+                const uint16_t *x = p.x + (b + r) * p.x_stride;
+                const uint16_t *w = p.w + static_cast<int64_t>(ld_dep(p.targets + b + r)) * p.H;
+                float z = 0.0f;
+#pragma unroll 2
+                for (int c = lane; c < p.Hp / 8; c += 32)
+                    z += word_dot(row_word(x, c, p.H, p.vec), row_word(w, c, p.H, p.w_vec), p.f16);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+                if (lane == 0) {
+                    const float lse2 = ld_dep(p.lse_in + b + r) * kLog2e;
+                    const float e = exp2f(fmaf(z, kLog2e * p.inv_temperature, -lse2)) - 1.0f;
+                    const float coef = e * (ld_dep(p.dloss + b + r) * p.inv_temperature);
+                    p.coef[k] = coef;
+                    if (twin) p.coef[k + kLossTwin] = coef;
+                }
+            }
+        }
         __syncthreads();
         base += total;
     }
@@ -163,12 +207,16 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
             if (GRAD) {
                 p.lse2[r] = INFINITY;
                 p.gs[r] = 0.0f;
+                if (p.coef) p.coef[r] = 0.0f;
             }
         }
     }
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPackThreads + tid; i < p.n_sync;
          i += static_cast<int64_t>(gridDim.x) * kPackThreads)
         p.sync[i] = 0u;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPackThreads + tid; i < p.n_slot;
+         i += static_cast<int64_t>(gridDim.x) * kPackThreads)
+        p.slot[i] = -1;
     if (bad) set_err(p.err, LHS_ERRBIT_BAD_TOKEN);
     if (nonfinite) set_err(p.err, LHS_ERRBIT_NONFINITE);
     if (blockIdx.x == 0) {
@@ -305,11 +353,13 @@ __global__ void __launch_bounds__(kMergeThreads)
 }
 
 // dx of every position: its compact row's sums (and its twin's), joined in order,
-// times the inverse of g's scale; or zeros.  A warp to 128 columns of a position.
+// times the inverse of g's scale, and the target's row of the table by what is kept apart of
+// its entry (w null: nothing is); or zeros.  A warp to 128 columns of a position.
 template <typename T>
 __global__ void __launch_bounds__(256)
     loss_dx_kernel(const LossMeta *meta, const int32_t *pos, const float *part, int splits, int64_t Tpad, int pitch,
-                   int64_t n, int32_t H, T *dx, int64_t dx_stride, bool vec) {
+                   int64_t n, int32_t H, T *dx, int64_t dx_stride, bool vec, const uint16_t *w, bool f16, int Hp,
+                   const int32_t *tgt, const float *coef) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
     const float u = ld_dep(&meta->unscale);
@@ -339,7 +389,18 @@ __global__ void __launch_bounds__(256)
                         v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
                     }
                 }
-                v.x *= u, v.y *= u, v.z *= u, v.w *= u;
+                if (w) {  // (rows of whole 16-byte words)
+                    const uint2 row = ld_dep(reinterpret_cast<const uint2 *>(w + static_cast<int64_t>(ld_dep(tgt + c)) * Hp + j));
+                    const float e = ld_dep(coef + c);
+                    const uint16_t b[4] = {static_cast<uint16_t>(row.x), static_cast<uint16_t>(row.x >> 16),
+                                           static_cast<uint16_t>(row.y), static_cast<uint16_t>(row.y >> 16)};
+                    float t[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) t[k] = e * (f16 ? f16_bits_to_f32(b[k]) : bf16_bits_to_f32(b[k]));
+                    v.x = fmaf(v.x, u, t[0]), v.y = fmaf(v.y, u, t[1]), v.z = fmaf(v.z, u, t[2]), v.w = fmaf(v.w, u, t[3]);
+                } else {
+                    v.x *= u, v.y *= u, v.z *= u, v.w *= u;
+                }
             }
             const float f[4] = {v.x, v.y, v.z, v.w};
             if (vec && j + 4 <= H) {
@@ -357,6 +418,11 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// The table in rows of whole 16-byte words.
+const uint16_t *whole_rows(const LossArgs &a, const LossPlan &p) {
+    return p.H % 8 ? reinterpret_cast<const uint16_t *>(a.ws + p.off_w) : static_cast<const uint16_t *>(a.t.data);
+}
+
 template <typename T>
 cudaError_t launch_dx(const LossArgs &a, const LossPlan &p, const DeviceInfo &dev, cudaStream_t stream) {
     const int64_t want = (p.T * ((p.H + 127) / 128) + 7) / 8;
@@ -364,7 +430,9 @@ cudaError_t launch_dx(const LossArgs &a, const LossPlan &p, const DeviceInfo &de
     return launch_pdl(loss_dx_kernel<T>, dim3(static_cast<unsigned>(want < 8 * dev.num_sms ? want : 8 * dev.num_sms)),
                       dim3(256), 0, stream, reinterpret_cast<const LossMeta *>(a.ws + p.off_meta),
                       reinterpret_cast<const int32_t *>(a.ws + p.off_pos), reinterpret_cast<const float *>(a.ws + p.off_part),
-                      p.splits, p.Tpad, p.part_pitch, p.T, p.H, static_cast<T *>(a.dx), a.dx_stride, vec);
+                      p.splits, p.Tpad, p.part_pitch, p.T, p.H, static_cast<T *>(a.dx), a.dx_stride, vec,
+                      p.apart ? whole_rows(a, p) : nullptr, !p.bf16, p.Hp,
+                      reinterpret_cast<const int32_t *>(a.ws + p.off_tgt), reinterpret_cast<const float *>(a.ws + p.off_coef));
 }
 
 cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &dev, cudaStream_t stream) {
@@ -390,6 +458,13 @@ cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &
     k.pos = reinterpret_cast<int32_t *>(a.ws + p.off_pos);
     k.lse2 = reinterpret_cast<float *>(a.ws + p.off_lse2);
     k.gs = reinterpret_cast<float *>(a.ws + p.off_gs);
+    if (p.apart) {
+        k.w = static_cast<const uint16_t *>(a.t.data);
+        k.w_vec = p.H % 8 == 0;
+        k.coef = reinterpret_cast<float *>(a.ws + p.off_coef);
+        k.slot = reinterpret_cast<int32_t *>(a.ws + p.off_slot);
+        k.n_slot = a.dtable ? p.V + p.vt : 0;
+    }
     k.xc = reinterpret_cast<uint16_t *>(a.ws + p.off_x);
     k.sync = reinterpret_cast<uint32_t *>(a.ws + p.off_sync);
     k.n_sync = p.n_sync;
@@ -487,6 +562,14 @@ LossPlan plan_loss(const lhs_table &t, int64_t tokens, bool grad) {
         p.off_pos = take(p.T * 4);
         p.off_lse2 = take(p.Tpad * 4);
         p.off_gs = take(p.Tpad * 4);
+        p.apart = p.T > kLossTwin;
+        if (p.apart) {
+            p.rows_pitch = round_up(p.H, 64);
+            p.off_coef = take(p.Tpad * 4);
+            p.off_slot = take((p.V + p.vt) * 4);
+            p.off_rows = take((p.T < p.V ? p.T : p.V) * p.rows_pitch * 4);
+            p.off_order = take(embed_grad_workspace(p.Hp, p.T));
+        }
         p.off_g = take(p.slots * p.Tpad * p.piece * 2);
         p.off_part = take(p.splits * p.Tpad * p.part_pitch * 4);
     }
@@ -517,6 +600,15 @@ cudaError_t launch_loss_grad(const LossArgs &a, const LossPlan &p, cudaStream_t 
     cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return e;
     if ((e = launch_pack(a, p, dev, stream)) != cudaSuccess) return e;
+    if (p.apart && a.dtable) {
+        const TargetRowsArgs r = {a.targets, p.T, p.V, a.ignore, p.Hp, p.bf16,
+                                  reinterpret_cast<const uint16_t *>(a.ws + p.off_x),
+                                  reinterpret_cast<const int32_t *>(a.ws + p.off_pos),
+                                  reinterpret_cast<const float *>(a.ws + p.off_coef),
+                                  reinterpret_cast<float *>(a.ws + p.off_rows), p.rows_pitch,
+                                  reinterpret_cast<int32_t *>(a.ws + p.off_slot), a.ws + p.off_order, a.err};
+        if ((e = launch_target_rows(r, stream)) != cudaSuccess) return e;
+    }
     if ((e = launch_loss_products(a, p, stream)) != cudaSuccess) return e;
     if (!a.dx) return cudaSuccess;
     if (a.dx_dtype == LHS_F32) return launch_dx<float>(a, p, dev, stream);

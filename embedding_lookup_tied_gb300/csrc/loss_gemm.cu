@@ -28,6 +28,9 @@
 // other exponentials) of each token, g as 16-bit values that the products read
 // back from L2 or HBM; of up to 128 tokens in two terms, the second in the rows of the
 // tile's other half, with the residuals there too, so that both products add them up.
+// Of more positions the targets' entries are kept apart in f32 (train.cuh): g holds what a
+// logit of the tensor cores makes of one beyond that, and a tile of dtable adds the sums of
+// its targets' rows before it rounds.
 //
 // What bounds it.  Many tokens: the tensor cores and the power cap.  8,192 x
 // 151,936 x 896: statistics 1.24 ms (1,800 TFLOP/s; 1,660 for seconds on end),
@@ -76,6 +79,10 @@ struct Params {
     float2 *stats;           // statistics
     float *zt;
     const float *lse2, *gs;  // g
+    const float *coef;       // what is kept apart of the targets' entries, or null
+    const int32_t *slot_of;  // dtable: [V] rows of what it makes there, [tiles] whether there is one; or null
+    const float *rows;
+    int64_t rows_pitch;
     bool dx;
     int ahead, slots, splits;
     uint32_t *g_done;        // [pieces] warps that have written a tile of g
@@ -104,7 +111,7 @@ struct alignas(16) Item {
     int piece;
     int m;        // tile of M: block of tokens, or of the piece's rows
     int n;        // tile of N: of the piece's rows (logits), or of hidden
-    int split;    // dx
+    int split;    // dx; dtable: whether a row of the tile is a target
     int k0, k1;   // stages
     int width;    // N of the MMAs, a multiple of 32
 };
@@ -677,6 +684,10 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                     if (i < w.total) {
                         next = atomicAdd(p.queue, 1u);  // on its way while this one is worked out
                         t = item_of<MODE>(p, w, i);
+                        // (asked here, items ahead: a warp that takes tiles out would wait for the answer,
+                        // 256 x 262,144 x 5,120 1.48 -> 1.63 ms)
+                        if (MODE == 1 && t.kind == kDtable && p.slot_of)
+                            t.split = ld_dep(p.slot_of + p.V + t.piece * p.piece_tiles + t.m) >= 0;
                     }
                     if (!wait_or_abort(&sm.item_empty[q], parity, &sm.abort_flag, p.err)) break;
                     const int4 *v = reinterpret_cast<const int4 *>(&t);
@@ -744,12 +755,12 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
             if (load_acquire(count) < target) tell();
             return wait_count(count, target, &sm.abort_flag, p.err);
         };
-        // 64 values of this lane's row, times u, rounded to 16 bits, to (x, y).  The buffer is waited for
-        // when they are there.
-        auto put_half = [&](const float (&v)[64], float u, int x, int y, const CUtensorMap *map) {
+        // 64 values of this lane's row, rounded to 16 bits, to (x, y).  The buffer is waited for when they
+        // are there.
+        auto put_half = [&](const float (&v)[64], int x, int y, const CUtensorMap *map) {
             uint32_t w[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) w[k] = pack16<BF>(v[2 * k] * u, v[2 * k + 1] * u);
+            for (int k = 0; k < 32; ++k) w[k] = pack16<BF>(v[2 * k], v[2 * k + 1]);
             if (lane == 0) tell();
             uint8_t *out = out_buffer();
 #pragma unroll
@@ -764,7 +775,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
             // what the tile needs besides its sums, asked for before they are waited for
             int y = -1;
             bool none = false;  // a row past the last token
-            float lse2 = 0.0f, gs = 0.0f;
+            float lse2 = 0.0f, gs = 0.0f, apart = 0.0f;
             int64_t v0 = 0;
             const int64_t tok = static_cast<int64_t>(t.m) * kLossTile + row;
             if (MODE == 0 || t.kind == kLogits) {
@@ -775,7 +786,13 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                 if (MODE == 1) {
                     lse2 = ld_dep(p.lse2 + tok);
                     gs = ld_dep(p.gs + tok) * scale;
+                    if (p.coef) apart = ld_dep(p.coef + tok) * scale;
                 }
+            }
+            int at = -1;  // where the row's sums of what is kept apart are
+            if (MODE == 1 && t.kind == kDtable && t.split) {
+                const int64_t v = t.piece * p.piece + static_cast<int64_t>(t.m) * kLossTile + row;
+                if (v < p.V) at = ld_dep(p.slot_of + v);
             }
             // What was written and not yet told of is told of before anything is waited for that may
             // depend on it; where the tile is there already, after its first part, when the stores
@@ -888,15 +905,17 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                         for (int k = 0; k < 64; ++k) v[k] *= gs;
                         if (special) {
 #pragma unroll
-                            for (int k = 0; k < 64; ++k)
+                            for (int k = 0; k < 64; ++k) {
+                                if (y == c * 64 + k) v[k] -= apart;
                                 if (none || k >= left) v[k] = 0.0f;
+                            }
                         }
                         if (rest) {
 #pragma unroll
                             for (int k = 0; k < 64; ++k) v[k] -= round16<BF>(v[k]);
                         }
                     }
-                    put_half(v, 1.0f, t.n * kLossTile + c * 64, t.piece % p.slots * static_cast<int>(p.Tpad) + t.m * kLossTile + row0,
+                    put_half(v, t.n * kLossTile + c * 64, t.piece % p.slots * static_cast<int>(p.Tpad) + t.m * kLossTile + row0,
                              &tm_g_out);
                 }
             } else {
@@ -909,22 +928,42 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                 // (a piece starts at a multiple of the tile, and rows past the table's end are not stored)
                 const int64_t out_row = dx ? t.split * p.Tpad + static_cast<int64_t>(t.m) * kLossTile + row0
                                            : t.piece * p.piece + static_cast<int64_t>(t.m) * kLossTile + row0;
+                const bool any = __any_sync(0xFFFFFFFFu, at >= 0);
+                const float *targets = at >= 0 ? p.rows + at * p.rows_pitch + h0 : nullptr;
+                // sums times u, and what is kept apart of this row's
+                auto finish = [&](auto &v, int c) {
+                    constexpr int N = sizeof(v) / sizeof(v[0]);
+                    if (any) {
+#pragma unroll
+                        for (int k = 0; k < N; k += 4) {
+                            const float4 a = targets ? ld_dep(reinterpret_cast<const float4 *>(targets + c + k))
+                                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            v[k] = fmaf(v[k], u, a.x), v[k + 1] = fmaf(v[k + 1], u, a.y);
+                            v[k + 2] = fmaf(v[k + 2], u, a.z), v[k + 3] = fmaf(v[k + 3], u, a.w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < N; ++k) v[k] *= u;
+                    }
+                };
                 if (mode == kStore16) {
                     for (int c = part * 64; c < cols; c += kParts * 64) {
                         float v[64];
                         tmem_ld64(acc + c, v);
-                        put_half(v, u, h0 + c, static_cast<int>(out_row), map);
+                        finish(v, c);
+                        put_half(v, h0 + c, static_cast<int>(out_row), map);
                     }
                 } else {
                     for (int c = part * 32; c < cols; c += kParts * 32) {
                         float v[32];
                         tmem_ld32(acc + c, v);
+                        finish(v, c);
                         if (lane == 0) tell();
                         uint8_t *out = out_buffer();
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            put_piece(out, lane, k, __float_as_uint(v[4 * k] * u), __float_as_uint(v[4 * k + 1] * u),
-                                      __float_as_uint(v[4 * k + 2] * u), __float_as_uint(v[4 * k + 3] * u));
+                            put_piece(out, lane, k, __float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),
+                                      __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
                         if (mode != kPlain) {
                             send(map, out, h0 + c, static_cast<int>(out_row), mode == kAdd32);
                             continue;
@@ -1095,6 +1134,12 @@ cudaError_t launch_loss_products(const LossArgs &a, const LossPlan &p, cudaStrea
     if (!common(a, p, &m, &k)) return cudaErrorInvalidValue;
     k.lse2 = reinterpret_cast<const float *>(a.ws + p.off_lse2);
     k.gs = reinterpret_cast<const float *>(a.ws + p.off_gs);
+    if (p.apart) {
+        k.coef = reinterpret_cast<const float *>(a.ws + p.off_coef);
+        if (a.dtable) k.slot_of = reinterpret_cast<const int32_t *>(a.ws + p.off_slot);
+        k.rows = reinterpret_cast<const float *>(a.ws + p.off_rows);
+        k.rows_pitch = p.rows_pitch;
+    }
     k.dx = a.dx != nullptr;
     k.dtable = a.dtable;
     k.dt_dtype = a.dtable_dtype;

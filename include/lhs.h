@@ -509,9 +509,10 @@ LHS_API int lhs_loss(const lhs_table *t, const void *d_x, int32_t x_dtype, int64
  * several streams may share the GPU in any way.  g is
  * rounded to the table's type (scaled by a power of two taken from the largest
  * |dloss|, so that f16 holds it), as the other factor of both products is of
- * that type; the sums are f32, rounded once to the output's type (with
- * accumulate once more for what dtable held, if it is of 16 bits).  Of up to 128
- * positions g is held in two such terms, where one rounding would show.  Positions
+ * that type, but for the targets' entries (v == y_t), whose part of both
+ * gradients is summed in f32; of up to 128 positions, all of g is held in two such
+ * terms instead.  The sums are f32, rounded once to the output's type (with
+ * accumulate once more for what dtable held, if it is of 16 bits).  Positions
  * that take part with an lse or dloss that is not finite set
  * LHS_ERRBIT_NONFINITE and make what they reach NaN; results beyond the range
  * of f16 are +-inf.  tokens == 0 clears dtable
