@@ -34,7 +34,7 @@ struct PackParams {
     bool f16;
     LossMeta *meta;
     int32_t *act, *tgt, *pos;
-    float *lse2, *gs;
+    float *lse_c, *gs;      // packed
     const uint16_t *w;       // the table, where the targets' entries are kept apart
     bool w_vec;              // its rows start on 16-byte boundaries
     float *coef;
@@ -144,10 +144,10 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
                 if (on) {
                     const float l = ld_dep(p.lse_in + r), d = ld_dep(p.dloss + r);
                     if (!isfinite(l) || !isfinite(d)) nonfinite = true;
-                    p.lse2[c] = l * kLog2e;
+                    p.lse_c[c] = l;
                     p.gs[c] = d * p.inv_temperature;
                     if (twin) {
-                        p.lse2[c + kLossTwin] = l * kLog2e;
+                        p.lse_c[c + kLossTwin] = l;
                         p.gs[c + kLossTwin] = d * p.inv_temperature;
                     }
                 }
@@ -184,8 +184,7 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
                 if (lane == 0) {
-                    const float lse2 = ld_dep(p.lse_in + b + r) * kLog2e;
-                    const float e = exp2f(fmaf(z, kLog2e * p.inv_temperature, -lse2)) - 1.0f;
+                    const float e = exp2f(fmaf(z, p.inv_temperature, -ld_dep(p.lse_in + b + r)) * kLog2e) - 1.0f;
                     const float coef = e * (ld_dep(p.dloss + b + r) * p.inv_temperature);
                     p.coef[k] = coef;
                     if (twin) p.coef[k + kLossTwin] = coef;
@@ -205,7 +204,7 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
             p.act[r] = -1;
             p.tgt[r] = -1;
             if (GRAD) {
-                p.lse2[r] = INFINITY;
+                p.lse_c[r] = INFINITY;
                 p.gs[r] = 0.0f;
                 if (p.coef) p.coef[r] = 0.0f;
             }
@@ -456,7 +455,7 @@ cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &
     k.act = reinterpret_cast<int32_t *>(a.ws + p.off_act);
     k.tgt = reinterpret_cast<int32_t *>(a.ws + p.off_tgt);
     k.pos = reinterpret_cast<int32_t *>(a.ws + p.off_pos);
-    k.lse2 = reinterpret_cast<float *>(a.ws + p.off_lse2);
+    k.lse_c = reinterpret_cast<float *>(a.ws + p.off_lse);
     k.gs = reinterpret_cast<float *>(a.ws + p.off_gs);
     if (p.apart) {
         k.w = static_cast<const uint16_t *>(a.t.data);
@@ -560,7 +559,7 @@ LossPlan plan_loss(const lhs_table &t, int64_t tokens, bool grad) {
         choose_pieces(&p);
         p.off_sync = take(p.n_sync * 4);
         p.off_pos = take(p.T * 4);
-        p.off_lse2 = take(p.Tpad * 4);
+        p.off_lse = take(p.Tpad * 4);
         p.off_gs = take(p.Tpad * 4);
         p.apart = p.T > kLossTwin;
         if (p.apart) {

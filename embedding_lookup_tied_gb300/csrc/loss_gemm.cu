@@ -56,10 +56,13 @@ constexpr int kBoxBytes = 64 * 64 * 2;        // what one TMA load brings: 64 x 
 constexpr int kOperandBytes = 2 * kBoxBytes;  // a CTA's part of A, or of B, of a stage
 constexpr int kTmemCols = 512;
 constexpr int kStoreBytes = 32 * 128;         // an epilogue warp's store: 32 rows of 128 bytes
-// The tensor cores cut their f32 sums instead of rounding them, so that a long one is short
-// by about 2^-25 of itself for every 16 of k (5.7e-6 of the loss for hidden 5,376 in one sum; f32 on the
-// CUDA cores: 1e-6).  Logits whose statistics are taken are summed 512 of k at a time, and those
-// sums added up, rounded, in registers.
+// The tensor cores cut their f32 sums instead of rounding them: each of a step's 17 addends at 2^-25 of
+// the largest.  512 terms of one sign fall short by 2.6e-6 of their sum in f16, whose products have that
+// many bits to lose, and by 2e-7 in bf16; a longer sum by as much for every 512 (hidden 5,376 in one sum: 5.7e-6
+// of the loss; f32 on the CUDA cores 1e-6).  Logits are summed 512 of k at a time, and those sums added up, rounded,
+// in registers: for g as for the statistics, whose lse they are compared with (one long sum for g left
+// a row's probabilities short of 1, always to one side: 6e-5 in bf16 and 8e-4 in f16 for logits
+// of 30, hidden 5,376 and terms of one sign).
 constexpr int kChunk = 512 / kTileK;
 constexpr int kQueue = 3;                     // items handed out ahead
 
@@ -78,7 +81,8 @@ struct Params {
     int pieces, piece_tiles, last_tiles;
     float2 *stats;           // statistics
     float *zt;
-    const float *lse2, *gs;  // g
+    float inv_t;             // 1 / temperature
+    const float *lse, *gs;   // g
     const float *coef;       // what is kept apart of the targets' entries, or null
     const int32_t *slot_of;  // dtable: [V] rows of what it makes there, [tiles] whether there is one; or null
     const float *rows;
@@ -298,11 +302,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-// 64 columns: both loads are under way before the first is waited for.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+// Four times 32 columns: all loads are under way before the first is waited for.
+__device__ __forceinline__ void tmem_ld128(const uint32_t (&taddr)[4], float (&v)[128]) {
     uint32_t *r = reinterpret_cast<uint32_t *>(v);
 #pragma unroll
-    for (int o = 0; o < 2; ++o)
+    for (int o = 0; o < 4; ++o)
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
             "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -314,12 +318,12 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
               "=r"(r[32 * o + 22]), "=r"(r[32 * o + 23]), "=r"(r[32 * o + 24]), "=r"(r[32 * o + 25]),
               "=r"(r[32 * o + 26]), "=r"(r[32 * o + 27]), "=r"(r[32 * o + 28]), "=r"(r[32 * o + 29]),
               "=r"(r[32 * o + 30]), "=r"(r[32 * o + 31])
-            : "r"(taddr + 32 * o)
+            : "r"(taddr[o])
             : "memory");
     // the values are not there before this; nothing that uses them moves above it
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
+    for (int i = 0; i < 128; ++i) asm volatile("" : "+r"(r[i]));
 }
 // 2^x, relative error below 2^-21: a thousandth of what g is rounded by, and of the order of an
 // f32 logit's own rounding in a sum of exponentials.  Results below 2^-126 (of the row's largest, or
@@ -558,10 +562,10 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
         return t;
     };
 
-    // The warps that hold sums take registers from the others: 8 x 216 + 4 x 72 a lane are what 12 warps
+    // The warps that hold sums take registers from the others: 8 x 224 + 4 x 56 a lane are what 12 warps
     // are launched with at 168.
     if (warp < kFirstEpi) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {
             // ---------------- TMA producer ----------------
             if (lane == 0) {
@@ -640,8 +644,8 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                                            (static_cast<uint32_t>((2 * kCtaM) >> 4) << 24);
                     const uint32_t la = a_mn ? kLboMn : kLboK, lb = b_mn ? kLboMn : kLboK;
                     const uint32_t sa = a_mn ? kStepMn : kStepK, sb = b_mn ? kStepMn : kStepK;
-                    // (a sum of its own for every kChunk stages of logits whose statistics are taken)
-                    const int chunk = MODE == 0 ? kChunk : t.k1 - t.k0;
+                    // (a sum of its own for every kChunk stages of logits)
+                    const int chunk = MODE == 0 || t.kind == kLogits ? kChunk : t.k1 - t.k0;
                     bool ok = true;
                     for (int k0 = t.k0; k0 < t.k1 && ok; k0 += chunk) {
                         const int buf = n_acc & 1, k1 = k0 + chunk < t.k1 ? k0 + chunk : t.k1;
@@ -715,7 +719,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ---------------- epilogue ----------------
         const int q = warp & 3, part = (warp - kFirstEpi) / 4;  // TMEM lane quarter; of the warps that share it
         constexpr int kParts = kEpiWarps / 4;
@@ -733,6 +737,12 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                 add_release(told, 1u);
                 told = nullptr;
             }
+        };
+        // This warp has read an accumulator.
+        auto release = [&](int buf) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(cluster_addr(&sm.acc_empty[buf], 0));
         };
         // A buffer of this warp's that no store reads any more.
         auto out_buffer = [&]() -> uint8_t * {
@@ -755,12 +765,8 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
             if (load_acquire(count) < target) tell();
             return wait_count(count, target, &sm.abort_flag, p.err);
         };
-        // 64 values of this lane's row, rounded to 16 bits, to (x, y).  The buffer is waited for when they
-        // are there.
-        auto put_half = [&](const float (&v)[64], int x, int y, const CUtensorMap *map) {
-            uint32_t w[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) w[k] = pack16<BF>(v[2 * k], v[2 * k + 1]);
+        // 64 values of 16 bits of this lane's row, to (x, y).  The buffer is waited for when they are there.
+        auto put_half = [&](const uint32_t (&w)[32], int x, int y, const CUtensorMap *map) {
             if (lane == 0) tell();
             uint8_t *out = out_buffer();
 #pragma unroll
@@ -771,11 +777,10 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
             const Item t = next_item(true);
             if (t.kind < 0) break;
             int buf = n_acc & 1;
-            const uint32_t acc = tmem + lanes + buf * (kTmemCols / 2);
             // what the tile needs besides its sums, asked for before they are waited for
             int y = -1;
             bool none = false;  // a row past the last token
-            float lse2 = 0.0f, gs = 0.0f, apart = 0.0f;
+            float lse = 0.0f, gs = 0.0f, apart = 0.0f;
             int64_t v0 = 0;
             const int64_t tok = static_cast<int64_t>(t.m) * kLossTile + row;
             if (MODE == 0 || t.kind == kLogits) {
@@ -784,7 +789,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                 none = target < 0;
                 y = target >= v0 && target < v0 + kLossTile ? static_cast<int>(target - v0) : -1;
                 if (MODE == 1) {
-                    lse2 = ld_dep(p.lse2 + tok);
+                    lse = ld_dep(p.lse + tok);
                     gs = ld_dep(p.gs + tok) * scale;
                     if (p.coef) apart = ld_dep(p.coef + tok) * scale;
                 }
@@ -835,11 +840,9 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 32; ++k) sum[c + k] = k0 == t.k0 ? v[k] : sum[c + k] + v[k];
                     }
+                    release(buf);
                     k0 += kChunk;
                     if (k0 >= t.k1) break;
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_cluster(cluster_addr(&sm.acc_empty[buf], 0));
                     buf = n_acc & 1;
                     all = __all_sync(0xFFFFFFFFu, wait_or_abort(&sm.acc_full[buf], (n_acc >> 1) & 1, &sm.abort_flag, p.err));
                     if (!all) break;
@@ -883,141 +886,173 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                 p.stats[(static_cast<int64_t>(t.n) * kLossParts + part) * p.Tpad + tok] =
                     make_float2(m, m == -INFINITY ? s : s + static_cast<float>(equal - 1));
                 if (y >= 0 && y / (kLossTile / kParts) == part) p.zt[tok] = z;
-            } else if (t.kind == kLogits) {
-                // g, 64 rows of the vocabulary at a time
-                for (int c = part; c < kLossTile / 64; c += kParts) {
-                    const int64_t left = p.V - v0 - c * 64;
-                    const bool special = left < 64 || __any_sync(0xFFFFFFFFu, none || (y >= 0 && (y >> 6) == c));
-                    float v[64];
-                    if (__all_sync(0xFFFFFFFFu, none)) {
-#pragma unroll
-                        for (int k = 0; k < 64; ++k) v[k] = 0.0f;
-                    } else {
-                        tmem_ld64(acc + c * 64, v);
-#pragma unroll
-                        for (int k = 0; k < 64; ++k) v[k] = ex2(fmaf(v[k], p.l2, -lse2));
-                        if (special) {
-#pragma unroll
-                            for (int k = 0; k < 64; ++k)
-                                if (y == c * 64 + k) v[k] -= 1.0f;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 64; ++k) v[k] *= gs;
-                        if (special) {
-#pragma unroll
-                            for (int k = 0; k < 64; ++k) {
-                                if (y == c * 64 + k) v[k] -= apart;
-                                if (none || k >= left) v[k] = 0.0f;
-                            }
-                        }
-                        if (rest) {
-#pragma unroll
-                            for (int k = 0; k < 64; ++k) v[k] -= round16<BF>(v[k]);
-                        }
-                    }
-                    put_half(v, t.n * kLossTile + c * 64, t.piece % p.slots * static_cast<int>(p.Tpad) + t.m * kLossTile + row0,
-                             &tm_g_out);
-                }
             } else {
-                // sums of dx, or of dtable times the inverse of g's scale
-                const bool dx = t.kind == kDx;
-                const int mode = dx ? (t.piece == 0 ? kStore32 : kAdd32) : p.dt_mode;
-                const CUtensorMap *map = dx ? &tm_part : &tm_dt;
-                const float u = dx ? 1.0f : unscale;
-                const int h0 = t.n * kLossTile, cols = p.H - h0 < kLossTile ? p.H - h0 : kLossTile;
-                // (a piece starts at a multiple of the tile, and rows past the table's end are not stored)
-                const int64_t out_row = dx ? t.split * p.Tpad + static_cast<int64_t>(t.m) * kLossTile + row0
-                                           : t.piece * p.piece + static_cast<int64_t>(t.m) * kLossTile + row0;
-                const bool any = __any_sync(0xFFFFFFFFu, at >= 0);
-                const float *targets = at >= 0 ? p.rows + at * p.rows_pitch + h0 : nullptr;
-                // sums times u, and what is kept apart of this row's
-                auto finish = [&](auto &v, int c) {
-                    constexpr int N = sizeof(v) / sizeof(v[0]);
-                    if (any) {
+                const int mode = t.kind == kLogits ? kStore16 : t.kind == kDtable ? p.dt_mode : t.piece == 0 ? kStore32 : kAdd32;
+                const int left = p.H - t.n * kLossTile, cols = t.kind == kLogits || left > kLossTile ? kLossTile : left;
+                // This warp's columns, 32 at a time, in their order: two stores of 64, or four of 32, in
+                // turn with the other warp of its rows.
+                static_assert(kParts == 2, "two warps to a row's columns");
+                auto column = [&](int i) { return mode == kStore16 ? part * 64 + (i >> 1) * 128 + (i & 1) * 32 : part * 32 + i * 64; };
+                float sum[128];
+                const int chunk = t.kind == kLogits ? kChunk : t.k1 - t.k0;
+                bool all = true;
+                {
+                    const uint32_t acc = tmem + lanes + buf * (kTmemCols / 2);
+                    const uint32_t at[4] = {acc + column(0), acc + column(1), acc + column(2), acc + column(3)};
+                    tmem_ld128(at, sum);
+                    release(buf);
+                }
+                for (int k0 = t.k0 + chunk; k0 < t.k1; k0 += chunk) {
+                    // (the other warps, on whom the next sums wait too, may depend on what this one has to tell)
+                    if (lane == 0) tell();
+                    buf = n_acc & 1;
+                    all = __all_sync(0xFFFFFFFFu, wait_or_abort(&sm.acc_full[buf], (n_acc >> 1) & 1, &sm.abort_flag, p.err));
+                    if (!all) break;
+                    tc_fence_after();
+                    ++n_acc;
+                    const uint32_t acc = tmem + lanes + buf * (kTmemCols / 2);
 #pragma unroll
-                        for (int k = 0; k < N; k += 4) {
-                            const float4 a = targets ? ld_dep(reinterpret_cast<const float4 *>(targets + c + k))
-                                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            v[k] = fmaf(v[k], u, a.x), v[k + 1] = fmaf(v[k + 1], u, a.y);
-                            v[k + 2] = fmaf(v[k + 2], u, a.z), v[k + 3] = fmaf(v[k + 3], u, a.w);
-                        }
-                    } else {
+                    for (int i = 0; i < 4; ++i) {
+                        float v[32];
+                        tmem_ld32(acc + column(i), v);
 #pragma unroll
-                        for (int k = 0; k < N; ++k) v[k] *= u;
+                        for (int k = 0; k < 32; ++k) sum[32 * i + k] += v[k];
                     }
-                };
-                if (mode == kStore16) {
-                    for (int c = part * 64; c < cols; c += kParts * 64) {
-                        float v[64];
-                        tmem_ld64(acc + c, v);
-                        finish(v, c);
-                        put_half(v, h0 + c, static_cast<int>(out_row), map);
+                    release(buf);
+                }
+                if (!all) break;
+                if (t.kind == kLogits) {
+                    // g, 64 rows of the vocabulary at a time, packed eight by eight
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int c = part * 64 + b * 128;
+                        const int64_t left = p.V - v0 - c;
+                        const bool special = left < 64 || __any_sync(0xFFFFFFFFu, none || (y >= 0 && (y >> 6) == c / 64));
+                        uint32_t w[32];
+#pragma unroll
+                        for (int k = 0; k < 64; k += 8) {
+                            float v[8];
+                            // (the logarithm of the probability before it is scaled to base 2: lse times
+                            // log2(e) would be rounded to 2^-24 of itself, which is an error of all of a row's
+                            // probabilities alike)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[i] = ex2(fmaf(sum[64 * b + k + i], p.inv_t, -lse) * kLog2e);
+                            if (special) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    v[i] = y == c + k + i ? (v[i] - 1.0f) * gs - apart : v[i] * gs;
+                                    if (none || k + i >= left) v[i] = 0.0f;
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] *= gs;
+                            }
+                            if (rest) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] -= round16<BF>(v[i]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[k / 2 + i] = pack16<BF>(v[2 * i], v[2 * i + 1]);
+                        }
+                        put_half(w, t.n * kLossTile + c, t.piece % p.slots * static_cast<int>(p.Tpad) + t.m * kLossTile + row0,
+                                 &tm_g_out);
                     }
                 } else {
-                    for (int c = part * 32; c < cols; c += kParts * 32) {
-                        float v[32];
-                        tmem_ld32(acc + c, v);
-                        finish(v, c);
-                        if (lane == 0) tell();
-                        uint8_t *out = out_buffer();
+                    // sums of dx, or of dtable times the inverse of g's scale
+                    const bool dx = t.kind == kDx;
+                    const CUtensorMap *map = dx ? &tm_part : &tm_dt;
+                    const float u = dx ? 1.0f : unscale;
+                    const int h0 = t.n * kLossTile;
+                    // (a piece starts at a multiple of the tile, and rows past the table's end are not stored)
+                    const int64_t out_row = dx ? t.split * p.Tpad + static_cast<int64_t>(t.m) * kLossTile + row0
+                                               : t.piece * p.piece + static_cast<int64_t>(t.m) * kLossTile + row0;
+                    const float *targets = at >= 0 ? p.rows + at * p.rows_pitch + h0 : nullptr;
+                    // four sums times u, and what is kept apart of this row's
+                    auto finish = [&](const float *v, int c) -> float4 {
+                        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (targets) a = ld_dep(reinterpret_cast<const float4 *>(targets + c));
+                        return make_float4(fmaf(v[0], u, a.x), fmaf(v[1], u, a.y), fmaf(v[2], u, a.z), fmaf(v[3], u, a.w));
+                    };
+                    if (mode == kStore16) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            put_piece(out, lane, k, __float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),
-                                      __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
-                        if (mode != kPlain) {
-                            send(map, out, h0 + c, static_cast<int>(out_row), mode == kAdd32);
-                            continue;
+                        for (int b = 0; b < 2; ++b) {
+                            const int c = column(2 * b);
+                            if (c >= cols) break;
+                            uint32_t w[32];
+#pragma unroll
+                            for (int k = 0; k < 64; k += 4) {
+                                const float4 f = finish(sum + 64 * b + k, c + k);
+                                w[k / 2] = pack16<BF>(f.x, f.y), w[k / 2 + 1] = pack16<BF>(f.z, f.w);
+                            }
+                            put_half(w, h0 + c, static_cast<int>(out_row), map);
                         }
-                        // a lane to a column: rows that TMA does not take, or sums in 16 bits
-                        __syncwarp();
-                        // (eight rows' loads under way at a time: 64 x 100,000 x 1,001 277 -> 199 us)
-                        auto emit = [&](auto *dt) {
-                            using O = std::remove_pointer_t<decltype(dt)>;
-                            const bool in = c + lane < cols;
-                            dt += out_row * p.H + h0 + c + lane;
-                            for (int r0 = 0; r0 < 32; r0 += 8) {
-                                O old[8];
-                                if (p.accumulate) {
+                    } else {
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = column(i);
+                            if (c >= cols) break;
+                            if (lane == 0) tell();
+                            uint8_t *out = out_buffer();
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) {
+                                if (s != i) continue;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    const float4 f = finish(sum + 32 * s + 4 * k, c + 4 * k);
+                                    put_piece(out, lane, k, __float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z),
+                                              __float_as_uint(f.w));
+                                }
+                            }
+                            if (mode != kPlain) {
+                                send(map, out, h0 + c, static_cast<int>(out_row), mode == kAdd32);
+                                continue;
+                            }
+                            // a lane to a column: rows that TMA does not take, or sums in 16 bits
+                            __syncwarp();
+                            // (eight rows' loads under way at a time: 64 x 100,000 x 1,001 277 -> 199 us)
+                            auto emit = [&](auto *dt) {
+                                using O = std::remove_pointer_t<decltype(dt)>;
+                                const bool in = c + lane < cols;
+                                dt += out_row * p.H + h0 + c + lane;
+                                for (int r0 = 0; r0 < 32; r0 += 8) {
+                                    O old[8];
+                                    if (p.accumulate) {
+#pragma unroll
+                                        for (int k = 0; k < 8; ++k)
+                                            if (in && out_row + r0 + k < p.V) old[k] = dt[static_cast<int64_t>(r0 + k) * p.H];
+                                    }
+                                    float s[8];
 #pragma unroll
                                     for (int k = 0; k < 8; ++k)
-                                        if (in && out_row + r0 + k < p.V) old[k] = dt[static_cast<int64_t>(r0 + k) * p.H];
+                                        s[k] = *reinterpret_cast<const float *>(out + (r0 + k) * 128 + (((lane >> 2) ^ k) << 4) + (lane & 3) * 4);
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k)
+                                        if (in && out_row + r0 + k < p.V)
+                                            put_rn(dt + static_cast<int64_t>(r0 + k) * p.H, p.accumulate ? wide(old[k]) + s[k] : s[k]);
                                 }
-                                float s[8];
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    s[k] = *reinterpret_cast<const float *>(out + (r0 + k) * 128 + (((lane >> 2) ^ k) << 4) + (lane & 3) * 4);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    if (in && out_row + r0 + k < p.V)
-                                        put_rn(dt + static_cast<int64_t>(r0 + k) * p.H, p.accumulate ? wide(old[k]) + s[k] : s[k]);
-                            }
-                        };
-                        if (p.dt_dtype == LHS_F32) emit(static_cast<float *>(p.dtable));
-                        else if (BF) emit(static_cast<__nv_bfloat16 *>(p.dtable));
-                        else emit(static_cast<__half *>(p.dtable));
-                        __syncwarp();
+                            };
+                            if (p.dt_dtype == LHS_F32) emit(static_cast<float *>(p.dtable));
+                            else if (BF) emit(static_cast<__nv_bfloat16 *>(p.dtable));
+                            else emit(static_cast<__half *>(p.dtable));
+                            __syncwarp();
+                        }
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                arrive_cluster(cluster_addr(&sm.acc_empty[buf], 0));
-                if (MODE == 1) {
-                    tell();  // (a warp without columns in this tile has not yet)
-                    if (t.kind == kLogits) told = p.g_done + t.piece;
-                    else if (t.kind == kDx) told = dx_done;
-                    // Both CTAs' MMAs are done, and with them their reads of g: the copies' bytes were counted
-                    // on the barrier that the MMAs waited for, and the MMAs on the one that this thread has.
-                    // What the counter has to keep apart is those reads and the stores of whoever overwrites
-                    // the slot.  The reads have returned what they read before the barriers' phases end, the
-                    // add depends on this thread's wait for them, and the stores on the add being seen (by
-                    // an acquire, and a fence for the async proxy): no store can reach back to a read that
-                    // has returned.  There is no write of this thread's that the others have to see, which is
-                    // all that a release would add (256 x 262,144 x 5,120: 1.48 -> 1.59 ms with one,
-                    // 1 x 151,936 x 896 194 -> 217 us).
-                    if (t.kind != kLogits && rank == 0 && warp == kFirstEpi) add_relaxed(p.read_done + t.piece, 1u);
-                }
+            if (MODE == 1 && lane == 0) {
+                tell();  // (a warp without columns in this tile has not yet)
+                if (t.kind == kLogits) told = p.g_done + t.piece;
+                else if (t.kind == kDx) told = dx_done;
+                // Both CTAs' MMAs are done, and with them their reads of g: the copies' bytes were counted
+                // on the barrier that the MMAs waited for, and the MMAs on the one that this thread has.
+                // What the counter has to keep apart is those reads and the stores of whoever overwrites
+                // the slot.  The reads have returned what they read before the barriers' phases end, the
+                // add depends on this thread's wait for them, and the stores on the add being seen (by
+                // an acquire, and a fence for the async proxy): no store can reach back to a read that
+                // has returned.  There is no write of this thread's that the others have to see, which is
+                // all that a release would add (256 x 262,144 x 5,120: 1.48 -> 1.59 ms with one,
+                // 1 x 151,936 x 896 194 -> 217 us).
+                if (t.kind != kLogits && rank == 0 && warp == kFirstEpi) add_relaxed(p.read_done + t.piece, 1u);
             }
         }
         if (MODE == 1 && lane == 0) tell();
@@ -1132,7 +1167,8 @@ cudaError_t launch_loss_products(const LossArgs &a, const LossPlan &p, cudaStrea
     Maps m;
     Params k = {};
     if (!common(a, p, &m, &k)) return cudaErrorInvalidValue;
-    k.lse2 = reinterpret_cast<const float *>(a.ws + p.off_lse2);
+    k.inv_t = a.inv_temperature;
+    k.lse = reinterpret_cast<const float *>(a.ws + p.off_lse);
     k.gs = reinterpret_cast<const float *>(a.ws + p.off_gs);
     if (p.apart) {
         k.coef = reinterpret_cast<const float *>(a.ws + p.off_coef);

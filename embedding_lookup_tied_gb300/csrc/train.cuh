@@ -52,7 +52,7 @@ struct LossPlan {
     size_t off_zt;          // f32 [Tpad]: the target's logit
     // gradient
     size_t off_pos;         // int32 [T]: compact row of a position, -1
-    size_t off_lse2;        // f32 [Tpad]: lse * log2(e), +inf past count
+    size_t off_lse;         // f32 [Tpad]: lse, +inf past count
     size_t off_gs;          // f32 [Tpad]: dloss / temperature, 0 past count
     bool apart;             // the targets' entries are kept apart
     size_t off_coef;        // f32 [Tpad]: the part of a target's entry that is, 0 past count

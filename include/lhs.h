@@ -472,8 +472,9 @@ LHS_API int lhs_sample(const void *d_logits, int32_t dtype, int64_t stride, int6
  * What is written (d_loss, d_lse, the workspace, d_err) lies apart from
  * everything else (LHS_ERR_INVALID_ARG); it may lie between rows of x.
  * The logits are f32 sums of exact products (512 of hidden at a time in the
- * tensor cores); neither they nor their exponentials' sums are rounded to fewer
- * bits.  A position whose logits hold NaN or
+ * tensor cores, which cut their sums: terms of one sign fall short by 2.6e-6 of
+ * their sum in f16, 2e-7 in bf16, whatever their number); neither they nor their
+ * exponentials' sums are rounded to fewer bits.  A position whose logits hold NaN or
  * +inf, or nothing above -inf, gives loss and lse NaN and sets
  * LHS_ERRBIT_NONFINITE.  0 <= tokens <= 2^24 (0 enqueues nothing); hidden <=
  * 65536; tokens * vocab * (2 + hidden / 128) below 2^46, give or take
@@ -504,7 +505,7 @@ LHS_API int lhs_loss(const lhs_table *t, const void *d_x, int32_t x_dtype, int64
  *   d_ws         : 256-byte aligned, >= lhs_loss_grad_workspace bytes, overwritten
  * What is written (d_dx, d_dtable, the workspace, d_err) lies apart from
  * everything else but for d_dx over d_x (LHS_ERR_INVALID_ARG).
- * The logits are computed again, a piece of the vocabulary at a time, in one
+ * The same logits are computed again, a piece of the vocabulary at a time, in one
  * kernel whose CTAs wait only for work that running CTAs have taken: calls on
  * several streams may share the GPU in any way.  g is
  * rounded to the table's type (scaled by a power of two taken from the largest
