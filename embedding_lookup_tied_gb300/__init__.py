@@ -47,7 +47,8 @@ ABI_SYMBOLS = (
     "lhs_wire_decode", "lhs_wire_response_bytes", "lhs_wire_encode_response", "lhs_wire_decode_response",
     "lhs_i8_init", "lhs_i8_message", "lhs_i8_quantize", "lhs_i8_workspace", "lhs_i8_matmul", "lhs_i8_logits",
     "lhs_sample",
-    "lhs_loss_workspace", "lhs_loss", "lhs_loss_grad_workspace", "lhs_loss_grad", "lhs_embed_grad_workspace",
+    "lhs_loss_workspace", "lhs_loss", "lhs_loss_grad_workspace", "lhs_loss_grad", "lhs_loss_grad_of",
+    "lhs_embed_grad_workspace",
     "lhs_embed_grad",
     "lhs_selftest_bounded_wait", "lhs_strerror",
     "lhs_last_cuda_error", "lhs_version",
@@ -130,6 +131,8 @@ def lib() -> ctypes.CDLL:
         "lhs_loss_grad_workspace": (ctypes.c_int, [T, i64, P]),
         "lhs_loss_grad": (ctypes.c_int, [T, P, i32, i64, i64, P, i32, ctypes.c_float, P, P, P, i32, i64, P, i32,
                                          i32, P, sz, P, P]),
+        "lhs_loss_grad_of": (ctypes.c_int, [T, P, i32, i64, i64, P, i32, ctypes.c_float, P, P, P, P, i32, i64, P, i32,
+                                            i32, P, sz, P, P]),
         "lhs_embed_grad_workspace": (i64, [i64, i32, i64]),
         "lhs_embed_grad": (ctypes.c_int, [i64, i32, P, i64, i32, ctypes.c_float, P, i32, i64, P, i32, i32, P, sz,
                                           P, P]),
@@ -781,9 +784,11 @@ def _table_grad(dtable, vocab: int, hidden: int, dtype, device, accumulate: bool
 @_on_its_stream
 def lhs_loss_grad(table: Table, x: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, dloss: torch.Tensor,
                   ignore: int = IGNORE, temperature: float = 1.0, dx=None, dtable=None, want_dx: bool = True,
-                  want_dtable: bool = True, accumulate: bool = False, ws=None, err=None, stream=None):
+                  want_dtable: bool = True, accumulate: bool = False, ws=None, err=None, stream=None, loss=None):
     """Gradients of ``sum(dloss * loss)`` for the residuals ([tokens, hidden])
-    and for the table ([vocab, hidden]), given :func:`lhs_loss`'s ``lse``.
+    and for the table ([vocab, hidden]), given :func:`lhs_loss`'s ``lse``; with
+    its ``loss`` too, those of nearly certain targets keep their relative
+    accuracy, which the rounding of ``lse`` takes (1e-6 of p - 1).
     ``dx`` and ``dtable`` are of the table's type, or f32 where such a tensor is
     given; ``dx`` may be ``x``, all else lies apart; ``accumulate`` adds to
     ``dtable``.  Returns (dx|None, dtable|None, err word)."""
@@ -805,11 +810,14 @@ def lhs_loss_grad(table: Table, x: torch.Tensor, targets: torch.Tensor, lse: tor
     if ws is None:
         ws = torch.empty(lhs_loss_grad_workspace(table, n), dtype=torch.uint8, device=dev)
     err = _err_word(err, dev)
-    _one_device(dev, table=table, targets=targets, lse=lse, dloss=dloss, dx=dx, dtable=dtable, ws=ws, err=err)
-    _check(lib().lhs_loss_grad(ctypes.byref(table.c), xp, xdt, stride, n, tp, ignore, float(temperature),
-                               _per_row(lse, n, f, "lse"), _per_row(dloss, n, f, "dloss"), dxp, dxdt, dxs,
-                               dtp, dtdt, int(accumulate), _dev(ws, "ws"), ws.numel() * ws.element_size(),
-                               _dev(err, "err"), _stream(stream)), "lhs_loss_grad")
+    _one_device(dev, table=table, targets=targets, lse=lse, dloss=dloss, loss=loss, dx=dx, dtable=dtable, ws=ws, err=err)
+    head = (ctypes.byref(table.c), xp, xdt, stride, n, tp, ignore, float(temperature))
+    rest = (_per_row(lse, n, f, "lse"), _per_row(dloss, n, f, "dloss"), dxp, dxdt, dxs, dtp, dtdt, int(accumulate),
+            _dev(ws, "ws"), ws.numel() * ws.element_size(), _dev(err, "err"), _stream(stream))
+    if loss is None:
+        _check(lib().lhs_loss_grad(*head, *rest), "lhs_loss_grad")
+    else:
+        _check(lib().lhs_loss_grad_of(*head, _per_row(loss, n, f, "loss"), *rest), "lhs_loss_grad_of")
     return dx, dtable, err
 
 

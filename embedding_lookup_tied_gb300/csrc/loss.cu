@@ -34,7 +34,8 @@ struct PackParams {
     bool f16;
     LossMeta *meta;
     int32_t *act, *tgt, *pos;
-    float *lse_c, *gs;      // packed
+    const float *loss_in;    // or null
+    float *lse_c, *gs, *em;  // packed
     const uint16_t *w;       // the table, where the targets' entries are kept apart
     bool w_vec;              // its rows start on 16-byte boundaries
     float *coef;
@@ -143,10 +144,13 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
                 p.pos[r] = on ? c : -1;
                 if (on) {
                     const float l = ld_dep(p.lse_in + r), d = ld_dep(p.dloss + r);
-                    if (!isfinite(l) || !isfinite(d)) nonfinite = true;
+                    const float e = p.loss_in ? expm1f(-ld_dep(p.loss_in + r)) : 0.0f;
+                    if (!isfinite(l) || !isfinite(d) || !isfinite(e)) nonfinite = true;
                     p.lse_c[c] = l;
                     p.gs[c] = d * p.inv_temperature;
+                    if (p.loss_in) p.em[c] = e;
                     if (twin) {
+                        if (p.loss_in) p.em[c + kLossTwin] = e;
                         p.lse_c[c + kLossTwin] = l;
                         p.gs[c + kLossTwin] = d * p.inv_temperature;
                     }
@@ -184,7 +188,8 @@ __global__ void __launch_bounds__(kPackThreads) loss_pack_kernel(const PackParam
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
                 if (lane == 0) {
-                    const float e = exp2f(fmaf(z, p.inv_temperature, -ld_dep(p.lse_in + b + r)) * kLog2e) - 1.0f;
+                    const float l = fmaf(z, p.inv_temperature, -ld_dep(p.lse_in + b + r));
+                    const float e = p.loss_in ? expm1f(-ld_dep(p.loss_in + b + r)) : p_minus_1(l, exp2f(l * kLog2e));
                     const float coef = e * (ld_dep(p.dloss + b + r) * p.inv_temperature);
                     p.coef[k] = coef;
                     if (twin) p.coef[k + kLossTwin] = coef;
@@ -457,6 +462,8 @@ cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &
     k.pos = reinterpret_cast<int32_t *>(a.ws + p.off_pos);
     k.lse_c = reinterpret_cast<float *>(a.ws + p.off_lse);
     k.gs = reinterpret_cast<float *>(a.ws + p.off_gs);
+    k.loss_in = a.loss_in;
+    k.em = reinterpret_cast<float *>(a.ws + p.off_em);
     if (p.apart) {
         k.w = static_cast<const uint16_t *>(a.t.data);
         k.w_vec = p.H % 8 == 0;
@@ -561,6 +568,7 @@ LossPlan plan_loss(const lhs_table &t, int64_t tokens, bool grad) {
         p.off_pos = take(p.T * 4);
         p.off_lse = take(p.Tpad * 4);
         p.off_gs = take(p.Tpad * 4);
+        p.off_em = take(p.Tpad * 4);
         p.apart = p.T > kLossTwin;
         if (p.apart) {
             p.rows_pitch = round_up(p.H, 64);

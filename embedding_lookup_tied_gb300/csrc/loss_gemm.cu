@@ -83,6 +83,7 @@ struct Params {
     float *zt;
     float inv_t;             // 1 / temperature
     const float *lse, *gs;   // g
+    const float *em;         // the targets' p - 1, or null
     const float *coef;       // what is kept apart of the targets' entries, or null
     const int32_t *slot_of;  // dtable: [V] rows of what it makes there, [tiles] whether there is one; or null
     const float *rows;
@@ -780,7 +781,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
             // what the tile needs besides its sums, asked for before they are waited for
             int y = -1;
             bool none = false;  // a row past the last token
-            float lse = 0.0f, gs = 0.0f, apart = 0.0f;
+            float lse = 0.0f, gs = 0.0f, em = 0.0f, apart = 0.0f;
             int64_t v0 = 0;
             const int64_t tok = static_cast<int64_t>(t.m) * kLossTile + row;
             if (MODE == 0 || t.kind == kLogits) {
@@ -791,6 +792,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                 if (MODE == 1) {
                     lse = ld_dep(p.lse + tok);
                     gs = ld_dep(p.gs + tok) * scale;
+                    if (p.em) em = ld_dep(p.em + tok);
                     if (p.coef) apart = ld_dep(p.coef + tok) * scale;
                 }
             }
@@ -922,6 +924,19 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                 }
                 if (!all) break;
                 if (t.kind == kLogits) {
+                    // the target's entry, where it is among this warp's columns
+                    float entry = 0.0f;
+                    if (__any_sync(0xFFFFFFFFu, y >= 0 && ((y >> 6) & 1) == part)) {
+                        if (!p.em) {
+                            float z = 0.0f;
+#pragma unroll
+                            for (int k = 0; k < 128; ++k)
+                                if (y == column(k / 32) + k % 32) z = sum[k];
+                            const float l = fmaf(z, p.inv_t, -lse);
+                            em = p_minus_1(l, ex2(l * kLog2e));
+                        }
+                        entry = em * gs - apart;
+                    }
                     // g, 64 rows of the vocabulary at a time, packed eight by eight
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
@@ -940,7 +955,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                             if (special) {
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
-                                    v[i] = y == c + k + i ? (v[i] - 1.0f) * gs - apart : v[i] * gs;
+                                    v[i] = y == c + k + i ? entry : v[i] * gs;
                                     if (none || k + i >= left) v[i] = 0.0f;
                                 }
                             } else {
@@ -1170,6 +1185,7 @@ cudaError_t launch_loss_products(const LossArgs &a, const LossPlan &p, cudaStrea
     k.inv_t = a.inv_temperature;
     k.lse = reinterpret_cast<const float *>(a.ws + p.off_lse);
     k.gs = reinterpret_cast<const float *>(a.ws + p.off_gs);
+    if (a.loss_in) k.em = reinterpret_cast<const float *>(a.ws + p.off_em);
     if (p.apart) {
         k.coef = reinterpret_cast<const float *>(a.ws + p.off_coef);
         if (a.dtable) k.slot_of = reinterpret_cast<const int32_t *>(a.ws + p.off_slot);

@@ -55,6 +55,7 @@ struct LossPlan {
     size_t off_lse;         // f32 [Tpad]: lse, +inf past count
     size_t off_gs;          // f32 [Tpad]: dloss / temperature, 0 past count
     bool apart;             // the targets' entries are kept apart
+    size_t off_em;          // f32 [Tpad]: exp(-loss) - 1, where the losses are given
     size_t off_coef;        // f32 [Tpad]: the part of a target's entry that is, 0 past count
     size_t off_slot;        // int32 [V + vt]: the row's sum in off_rows, or -1; whether a row of a tile has one, or -1
     size_t off_rows;        // f32 [min(T, V) x rows_pitch]: sums of coef x over a target's positions
@@ -81,6 +82,7 @@ struct LossArgs {
     float inv_temperature;
     float *loss, *lse;              // loss
     const float *lse_in, *dloss;    // gradient
+    const float *loss_in;           // or null
     void *dx;
     int32_t dx_dtype;
     int64_t dx_stride;
@@ -135,6 +137,10 @@ cudaError_t launch_target_rows(const TargetRowsArgs &a, cudaStream_t stream);
 cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t stream);
 // Zeroes `bytes` at a 16-byte aligned address.
 cudaError_t launch_zero(void *p, size_t bytes, cudaStream_t stream);
+
+// p - 1 for the logarithm l of a probability p.  Above 1/2 the difference would lose what p
+// was rounded by.
+__device__ __forceinline__ float p_minus_1(float l, float p) { return p <= 0.5f ? p - 1.0f : expm1f(l); }
 
 // A value rounded to an output type (beyond the f16 range +-inf).
 __device__ __forceinline__ void put_rn(float *p, float v) { *p = v; }

@@ -128,6 +128,15 @@ int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t 
                   const float *d_dloss, void *d_dx, int32_t dx_dtype, int64_t dx_stride, void *d_dtable,
                   int32_t dtable_dtype, int32_t accumulate, void *d_ws, size_t ws_bytes, int32_t *d_err,
                   void *stream) {
+    return lhs_loss_grad_of(t, d_x, x_dtype, x_stride, tokens, d_targets, ignore, temperature, nullptr, d_lse, d_dloss,
+                            d_dx, dx_dtype, dx_stride, d_dtable, dtable_dtype, accumulate, d_ws, ws_bytes, d_err, stream);
+}
+
+int lhs_loss_grad_of(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t x_stride, int64_t tokens,
+                     const int32_t *d_targets, int32_t ignore, float temperature, const float *d_loss,
+                     const float *d_lse, const float *d_dloss, void *d_dx, int32_t dx_dtype, int64_t dx_stride,
+                     void *d_dtable, int32_t dtable_dtype, int32_t accumulate, void *d_ws, size_t ws_bytes,
+                     int32_t *d_err, void *stream) {
     const int rc = check_loss_args(t, d_x, x_dtype, x_stride, tokens, d_targets, temperature, d_ws, d_err);
     if (rc) return rc;
     if (accumulate != 0 && accumulate != 1) return LHS_ERR_INVALID_ARG;
@@ -138,7 +147,7 @@ int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t 
         return LHS_ERR_INVALID_ARG;
     if (tokens > 0) {
         if (!d_dx && !d_dtable) return LHS_ERR_INVALID_ARG;
-        if (!d_lse || !aligned(d_lse, 4) || !d_dloss || !aligned(d_dloss, 4)) return LHS_ERR_INVALID_ARG;
+        if (!d_lse || !aligned(d_lse, 4) || !d_dloss || !aligned(d_dloss, 4) || !aligned(d_loss, 4)) return LHS_ERR_INVALID_ARG;
     }
     const LossPlan p = plan_loss(*t, tokens, true);
     const Rows table = table_rows(*t),
@@ -147,12 +156,13 @@ int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t 
     if (tokens > 0) {
         if (ws_bytes < p.bytes) return LHS_ERR_BUFFER_TOO_SMALL;
         const Rows x = rows_of(d_x, tokens, x_stride, t->hidden, elem_size(x_dtype)), y = bytes_of(d_targets, 4 * tokens),
-                   lse = bytes_of(d_lse, 4 * tokens), dloss = bytes_of(d_dloss, 4 * tokens),
+                   lse = bytes_of(d_lse, 4 * tokens), dloss = bytes_of(d_dloss, 4 * tokens), loss = bytes_of(d_loss, 4 * tokens),
                    dx = rows_of(d_dx, tokens, dx_stride, t->hidden, elem_size(dx_dtype)), ws = bytes_of(d_ws, p.bytes),
                    err = bytes_of(d_err, 4);
         // (dx may lie over x, which the first kernel has read)
-        if (meet(dtable, {x, y, lse, dloss, dx, ws, err}) || meet(ws, {table, x, y, lse, dloss, dx, err}) ||
-            meet(err, {table, x, y, lse, dloss, dx}) || meet(table, dx) || meet(y, dx) || meet(lse, dx) || meet(dloss, dx))
+        if (meet(dtable, {x, y, loss, lse, dloss, dx, ws, err}) || meet(ws, {table, x, y, loss, lse, dloss, dx, err}) ||
+            meet(err, {table, x, y, loss, lse, dloss, dx}) || meet(table, dx) || meet(y, dx) || meet(loss, dx) ||
+            meet(lse, dx) || meet(dloss, dx))
             return LHS_ERR_INVALID_ARG;
     }
     LossArgs a = {};
@@ -163,6 +173,7 @@ int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t 
     a.ignore = ignore;
     a.inv_temperature = 1.0f / temperature;
     a.lse_in = d_lse;
+    a.loss_in = d_loss;
     a.dloss = d_dloss;
     a.dx = d_dx;
     a.dx_dtype = dx_dtype;

@@ -526,6 +526,20 @@ LHS_API int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, 
                           int32_t accumulate, void *d_ws, size_t ws_bytes, int32_t *d_err,
                           void *stream);
 
+/* lhs_loss_grad with the losses too.  lse is rounded to f32, so exp(z - lse) - 1
+ * of a target whose loss is small is off by 2^-24 |lse| (1e-6 at lse = 20: as much as
+ * the entry itself where the loss is 1e-6).  Given what lhs_loss gave for the same
+ * call, g[t][y_t] is (exp(-loss[t]) - 1) * dloss[t] / temperature, which keeps its
+ * relative accuracy.
+ *   d_loss : f32 [tokens], or NULL: as lhs_loss_grad.  One that is not finite sets
+ *            LHS_ERRBIT_NONFINITE. */
+LHS_API int lhs_loss_grad_of(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t x_stride,
+                             int64_t tokens, const int32_t *d_targets, int32_t ignore,
+                             float temperature, const float *d_loss, const float *d_lse,
+                             const float *d_dloss, void *d_dx, int32_t dx_dtype, int64_t dx_stride,
+                             void *d_dtable, int32_t dtable_dtype, int32_t accumulate, void *d_ws,
+                             size_t ws_bytes, int32_t *d_err, void *stream);
+
 /* The gradient of lhs_embed for the table:
  *   dtable[v][j] = scale * sum_{i: ids[i] == v} dout[i][j]  (+ what dtable
  *                  held, if accumulate)
