@@ -303,11 +303,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-// Four times 32 columns: all loads are under way before the first is waited for.
-__device__ __forceinline__ void tmem_ld128(const uint32_t (&taddr)[4], float (&v)[128]) {
+// Twice 32 columns: both loads are under way before the first is waited for.
+__device__ __forceinline__ void tmem_ld64(uint32_t lo, uint32_t hi, float (&v)[64]) {
+    const uint32_t taddr[2] = {lo, hi};
     uint32_t *r = reinterpret_cast<uint32_t *>(v);
 #pragma unroll
-    for (int o = 0; o < 4; ++o)
+    for (int o = 0; o < 2; ++o)
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
             "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -324,7 +325,7 @@ __device__ __forceinline__ void tmem_ld128(const uint32_t (&taddr)[4], float (&v
     // the values are not there before this; nothing that uses them moves above it
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 128; ++i) asm volatile("" : "+r"(r[i]));
+    for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
 }
 // 2^x, relative error below 2^-21: a thousandth of what g is rounded by, and of the order of an
 // f32 logit's own rounding in a sum of exponentials.  Results below 2^-126 (of the row's largest, or
@@ -645,7 +646,6 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                                            (static_cast<uint32_t>((2 * kCtaM) >> 4) << 24);
                     const uint32_t la = a_mn ? kLboMn : kLboK, lb = b_mn ? kLboMn : kLboK;
                     const uint32_t sa = a_mn ? kStepMn : kStepK, sb = b_mn ? kStepMn : kStepK;
-                    // (a sum of its own for every kChunk stages of logits)
                     const int chunk = MODE == 0 || t.kind == kLogits ? kChunk : t.k1 - t.k0;
                     bool ok = true;
                     for (int k0 = t.k0; k0 < t.k1 && ok; k0 += chunk) {
@@ -892,165 +892,173 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                 const int mode = t.kind == kLogits ? kStore16 : t.kind == kDtable ? p.dt_mode : t.piece == 0 ? kStore32 : kAdd32;
                 const int left = p.H - t.n * kLossTile, cols = t.kind == kLogits || left > kLossTile ? kLossTile : left;
                 // This warp's columns, 32 at a time, in their order: two stores of 64, or four of 32, in
-                // turn with the other warp of its rows.
+                // turn with the other warp of its rows.  They are read at once, which hands the accumulator back
+                // before they are worked on, 64 at a time by one copy of the code (two copies: 1 x 151,936 x 896
+                // 196 -> 213 us; the second 64 read when the first are done: 201).
                 static_assert(kParts == 2, "two warps to a row's columns");
                 auto column = [&](int i) { return mode == kStore16 ? part * 64 + (i >> 1) * 128 + (i & 1) * 32 : part * 32 + i * 64; };
-                float sum[128];
+                auto load = [&](int b, float (&o)[64]) {
+                    const uint32_t acc = tmem + lanes + buf * (kTmemCols / 2);
+                    tmem_ld64(acc + column(2 * b), acc + column(2 * b + 1), o);
+                };
                 const int chunk = t.kind == kLogits ? kChunk : t.k1 - t.k0;
-                bool all = true;
-                {
-                    const uint32_t acc = tmem + lanes + buf * (kTmemCols / 2);
-                    const uint32_t at[4] = {acc + column(0), acc + column(1), acc + column(2), acc + column(3)};
-                    tmem_ld128(at, sum);
-                    release(buf);
-                }
-                for (int k0 = t.k0 + chunk; k0 < t.k1; k0 += chunk) {
-                    // (the other warps, on whom the next sums wait too, may depend on what this one has to tell)
-                    if (lane == 0) tell();
-                    buf = n_acc & 1;
-                    all = __all_sync(0xFFFFFFFFu, wait_or_abort(&sm.acc_full[buf], (n_acc >> 1) & 1, &sm.abort_flag, p.err));
-                    if (!all) break;
-                    tc_fence_after();
-                    ++n_acc;
-                    const uint32_t acc = tmem + lanes + buf * (kTmemCols / 2);
+                float v[64], next[64];
+                load(0, v);
+                load(1, next);
+                release(buf);
+                if (t.k1 - t.k0 > chunk) {
+                    bool all = true;
+                    for (int k0 = t.k0 + chunk; k0 < t.k1; k0 += chunk) {
+                        // (the other warps, on whom the next sums wait too, may depend on what this one has to tell)
+                        if (lane == 0) tell();
+                        buf = n_acc & 1;
+                        all = __all_sync(0xFFFFFFFFu, wait_or_abort(&sm.acc_full[buf], (n_acc >> 1) & 1, &sm.abort_flag, p.err));
+                        if (!all) break;
+                        tc_fence_after();
+                        ++n_acc;
+                        const uint32_t acc = tmem + lanes + buf * (kTmemCols / 2);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float v[32];
-                        tmem_ld32(acc + column(i), v);
+                        for (int i = 0; i < 4; ++i) {
+                            float more[32];
+                            tmem_ld32(acc + column(i), more);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) sum[32 * i + k] += v[k];
-                    }
-                    release(buf);
-                }
-                if (!all) break;
-                if (t.kind == kLogits) {
-                    // the target's entry, where it is among this warp's columns
-                    float entry = 0.0f;
-                    if (__any_sync(0xFFFFFFFFu, y >= 0 && ((y >> 6) & 1) == part)) {
-                        if (!p.em) {
-                            float z = 0.0f;
-#pragma unroll
-                            for (int k = 0; k < 128; ++k)
-                                if (y == column(k / 32) + k % 32) z = sum[k];
-                            const float l = fmaf(z, p.inv_t, -lse);
-                            em = p_minus_1(l, ex2(l * kLog2e));
+                            for (int k = 0; k < 32; ++k) (i < 2 ? v : next)[32 * (i & 1) + k] += more[k];
                         }
-                        entry = em * gs - apart;
+                        release(buf);
                     }
-                    // g, 64 rows of the vocabulary at a time, packed eight by eight
+                    if (!all) break;
+                }
+                // what the blocks share: the target's entry; the place of a row of sums
+                const bool nothing = __all_sync(0xFFFFFFFFu, none);  // (few tokens: three quarters of the warps)
+                const bool dx = t.kind == kDx;
+                const float u = dx ? 1.0f : unscale;
+                const int h0 = t.n * kLossTile;
+                // (a piece starts at a multiple of the tile, and rows past the table's end are not stored)
+                const int64_t out_row = dx ? t.split * p.Tpad + static_cast<int64_t>(t.m) * kLossTile + row0
+                                           : t.piece * p.piece + static_cast<int64_t>(t.m) * kLossTile + row0;
+                const bool any = __any_sync(0xFFFFFFFFu, at >= 0);
+                const float *targets = at >= 0 ? p.rows + at * p.rows_pitch + h0 : nullptr;
+#pragma unroll 1
+                for (int b = 0; b < 2; ++b) {
+                    if (b == 1) {
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int c = part * 64 + b * 128;
+                        for (int k = 0; k < 64; ++k) v[k] = next[k];
+                    }
+                    const int c = column(2 * b);
+                    if (t.kind == kLogits) {
+                        // g
                         const int64_t left = p.V - v0 - c;
-                        const bool special = left < 64 || __any_sync(0xFFFFFFFFu, none || (y >= 0 && (y >> 6) == c / 64));
+                        const bool mine = y >= 0 && (y >> 6) == c / 64;
+                        const bool special = left < 64 || __any_sync(0xFFFFFFFFu, none || mine);
                         uint32_t w[32];
+                        if (nothing) {
 #pragma unroll
-                        for (int k = 0; k < 64; k += 8) {
-                            float v[8];
+                            for (int k = 0; k < 32; ++k) w[k] = 0u;
+                        } else {
+                            float entry = 0.0f;  // the target's
+                            if (__any_sync(0xFFFFFFFFu, mine)) {
+                                float e = em;
+                                if (!p.em) {
+                                    float z = 0.0f;
+#pragma unroll
+                                    for (int k = 0; k < 64; ++k)
+                                        if (y == c + k) z = v[k];
+                                    const float l = fmaf(z, p.inv_t, -lse);
+                                    e = p_minus_1(l, ex2(l * kLog2e));
+                                }
+                                entry = e * gs - apart;
+                            }
                             // (the logarithm of the probability before it is scaled to base 2: lse times
                             // log2(e) would be rounded to 2^-24 of itself, which is an error of all of a row's
                             // probabilities alike)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) v[i] = ex2(fmaf(sum[64 * b + k + i], p.inv_t, -lse) * kLog2e);
+                            for (int k = 0; k < 64; ++k) v[k] = ex2(fmaf(v[k], p.inv_t, -lse) * kLog2e) * gs;
                             if (special) {
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    v[i] = y == c + k + i ? entry : v[i] * gs;
-                                    if (none || k + i >= left) v[i] = 0.0f;
+                                for (int k = 0; k < 64; ++k) {
+                                    if (y == c + k) v[k] = entry;
+                                    if (none || k >= left) v[k] = 0.0f;
                                 }
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) v[i] *= gs;
                             }
                             if (rest) {
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) v[i] -= round16<BF>(v[i]);
+                                for (int k = 0; k < 64; ++k) v[k] -= round16<BF>(v[k]);
                             }
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) w[k / 2 + i] = pack16<BF>(v[2 * i], v[2 * i + 1]);
+                            for (int k = 0; k < 32; ++k) w[k] = pack16<BF>(v[2 * k], v[2 * k + 1]);
                         }
                         put_half(w, t.n * kLossTile + c, t.piece % p.slots * static_cast<int>(p.Tpad) + t.m * kLossTile + row0,
                                  &tm_g_out);
+                        continue;
                     }
-                } else {
-                    // sums of dx, or of dtable times the inverse of g's scale
-                    const bool dx = t.kind == kDx;
-                    const CUtensorMap *map = dx ? &tm_part : &tm_dt;
-                    const float u = dx ? 1.0f : unscale;
-                    const int h0 = t.n * kLossTile;
-                    // (a piece starts at a multiple of the tile, and rows past the table's end are not stored)
-                    const int64_t out_row = dx ? t.split * p.Tpad + static_cast<int64_t>(t.m) * kLossTile + row0
-                                               : t.piece * p.piece + static_cast<int64_t>(t.m) * kLossTile + row0;
-                    const float *targets = at >= 0 ? p.rows + at * p.rows_pitch + h0 : nullptr;
-                    // four sums times u, and what is kept apart of this row's
-                    auto finish = [&](const float *v, int c) -> float4 {
-                        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (targets) a = ld_dep(reinterpret_cast<const float4 *>(targets + c));
-                        return make_float4(fmaf(v[0], u, a.x), fmaf(v[1], u, a.y), fmaf(v[2], u, a.z), fmaf(v[3], u, a.w));
-                    };
-                    if (mode == kStore16) {
+                    // sums of dx, or of dtable times the inverse of g's scale, and what is kept apart of this row's
+                    if (any) {
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const int c = column(2 * b);
-                            if (c >= cols) break;
-                            uint32_t w[32];
-#pragma unroll
-                            for (int k = 0; k < 64; k += 4) {
-                                const float4 f = finish(sum + 64 * b + k, c + k);
-                                w[k / 2] = pack16<BF>(f.x, f.y), w[k / 2 + 1] = pack16<BF>(f.z, f.w);
-                            }
-                            put_half(w, h0 + c, static_cast<int>(out_row), map);
+                        for (int k = 0; k < 64; k += 4) {
+                            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            const int at_c = column(2 * b + k / 32) + k % 32;
+                            if (targets && at_c < cols) a = ld_dep(reinterpret_cast<const float4 *>(targets + at_c));
+                            v[k] = fmaf(v[k], u, a.x), v[k + 1] = fmaf(v[k + 1], u, a.y);
+                            v[k + 2] = fmaf(v[k + 2], u, a.z), v[k + 3] = fmaf(v[k + 3], u, a.w);
                         }
                     } else {
+#pragma unroll
+                        for (int k = 0; k < 64; ++k) v[k] *= u;
+                    }
+                    if (mode == kStore16) {
+                        if (c >= cols) continue;
+                        uint32_t w[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) w[k] = pack16<BF>(v[2 * k], v[2 * k + 1]);
+                        put_half(w, h0 + c, static_cast<int>(out_row), &tm_dt);
+                        continue;
+                    }
 #pragma unroll 1
-                        for (int i = 0; i < 4; ++i) {
-                            const int c = column(i);
-                            if (c >= cols) break;
-                            if (lane == 0) tell();
-                            uint8_t *out = out_buffer();
+                    for (int i = 0; i < 2; ++i) {
+                        const int c = column(2 * b + i);
+                        if (c >= cols) break;
+                        if (lane == 0) tell();
+                        uint8_t *out = out_buffer();
 #pragma unroll
-                            for (int s = 0; s < 4; ++s) {
-                                if (s != i) continue;
+                        for (int s = 0; s < 2; ++s) {
+                            if (s != i) continue;
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    const float4 f = finish(sum + 32 * s + 4 * k, c + 4 * k);
-                                    put_piece(out, lane, k, __float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z),
-                                              __float_as_uint(f.w));
-                                }
-                            }
-                            if (mode != kPlain) {
-                                send(map, out, h0 + c, static_cast<int>(out_row), mode == kAdd32);
-                                continue;
-                            }
-                            // a lane to a column: rows that TMA does not take, or sums in 16 bits
-                            __syncwarp();
-                            // (eight rows' loads under way at a time: 64 x 100,000 x 1,001 277 -> 199 us)
-                            auto emit = [&](auto *dt) {
-                                using O = std::remove_pointer_t<decltype(dt)>;
-                                const bool in = c + lane < cols;
-                                dt += out_row * p.H + h0 + c + lane;
-                                for (int r0 = 0; r0 < 32; r0 += 8) {
-                                    O old[8];
-                                    if (p.accumulate) {
-#pragma unroll
-                                        for (int k = 0; k < 8; ++k)
-                                            if (in && out_row + r0 + k < p.V) old[k] = dt[static_cast<int64_t>(r0 + k) * p.H];
-                                    }
-                                    float s[8];
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k)
-                                        s[k] = *reinterpret_cast<const float *>(out + (r0 + k) * 128 + (((lane >> 2) ^ k) << 4) + (lane & 3) * 4);
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k)
-                                        if (in && out_row + r0 + k < p.V)
-                                            put_rn(dt + static_cast<int64_t>(r0 + k) * p.H, p.accumulate ? wide(old[k]) + s[k] : s[k]);
-                                }
-                            };
-                            if (p.dt_dtype == LHS_F32) emit(static_cast<float *>(p.dtable));
-                            else if (BF) emit(static_cast<__nv_bfloat16 *>(p.dtable));
-                            else emit(static_cast<__half *>(p.dtable));
-                            __syncwarp();
+                            for (int k = 0; k < 8; ++k)
+                                put_piece(out, lane, k, __float_as_uint(v[32 * s + 4 * k]), __float_as_uint(v[32 * s + 4 * k + 1]),
+                                          __float_as_uint(v[32 * s + 4 * k + 2]), __float_as_uint(v[32 * s + 4 * k + 3]));
                         }
+                        if (mode != kPlain) {
+                            send(dx ? &tm_part : &tm_dt, out, h0 + c, static_cast<int>(out_row), mode == kAdd32);
+                            continue;
+                        }
+                        // a lane to a column: rows that TMA does not take, or sums in 16 bits
+                        __syncwarp();
+                        // (eight rows' loads under way at a time: 64 x 100,000 x 1,001 277 -> 199 us)
+                        auto emit = [&](auto *dt) {
+                            using O = std::remove_pointer_t<decltype(dt)>;
+                            const bool in = c + lane < cols;
+                            dt += out_row * p.H + h0 + c + lane;
+                            for (int r0 = 0; r0 < 32; r0 += 8) {
+                                O old[8];
+                                if (p.accumulate) {
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k)
+                                        if (in && out_row + r0 + k < p.V) old[k] = dt[static_cast<int64_t>(r0 + k) * p.H];
+                                }
+                                float s[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    s[k] = *reinterpret_cast<const float *>(out + (r0 + k) * 128 + (((lane >> 2) ^ k) << 4) + (lane & 3) * 4);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    if (in && out_row + r0 + k < p.V)
+                                        put_rn(dt + static_cast<int64_t>(r0 + k) * p.H, p.accumulate ? wide(old[k]) + s[k] : s[k]);
+                            }
+                        };
+                        if (p.dt_dtype == LHS_F32) emit(static_cast<float *>(p.dtable));
+                        else if (BF) emit(static_cast<__nv_bfloat16 *>(p.dtable));
+                        else emit(static_cast<__half *>(p.dtable));
+                        __syncwarp();
                     }
                 }
             }
