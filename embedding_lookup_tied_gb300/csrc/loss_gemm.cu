@@ -64,9 +64,18 @@ constexpr int kStoreBytes = 32 * 128;         // an epilogue warp's store: 32 ro
 // a row's probabilities short of 1, always to one side: 6e-5 in bf16 and 8e-4 in f16 for logits
 // of 30, hidden 5,376 and terms of one sign).
 constexpr int kChunk = 512 / kTileK;
+// Sums over positions (dtable) or rows of a piece (dx) are as long as the call is (2^19 positions of one sign in
+// one sum: 1.4e-3 short in bf16, 3.1e-3 in f16), and are cut into longer parts: 2,048 terms of one sign fall
+// short by 1e-5 (f16).  (1,024: 1 x 151,936 x 896, whose dx has 1,216 in a sum, 224 -> 260 us.)
+constexpr int kLongChunk = 2048 / kTileK;
 constexpr int kQueue = 3;                     // items handed out ahead
 
 enum { kLogits = 0, kDx = 1, kDtable = 2 };
+// Stages of a tile whose products make one sum in the tensor cores.
+template <int MODE>
+__device__ __forceinline__ int chunk_of(int kind) {
+    return MODE == 0 || kind == kLogits ? kChunk : kLongChunk;
+}
 enum { kStore16 = 0, kStore32 = 1, kAdd32 = 2, kPlain = 3 };  // how dtable is written
 
 struct Params {
@@ -646,7 +655,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                                            (static_cast<uint32_t>((2 * kCtaM) >> 4) << 24);
                     const uint32_t la = a_mn ? kLboMn : kLboK, lb = b_mn ? kLboMn : kLboK;
                     const uint32_t sa = a_mn ? kStepMn : kStepK, sb = b_mn ? kStepMn : kStepK;
-                    const int chunk = MODE == 0 || t.kind == kLogits ? kChunk : t.k1 - t.k0;
+                    const int chunk = chunk_of<MODE>(t.kind);
                     bool ok = true;
                     for (int k0 = t.k0; k0 < t.k1 && ok; k0 += chunk) {
                         const int buf = n_acc & 1, k1 = k0 + chunk < t.k1 ? k0 + chunk : t.k1;
@@ -901,7 +910,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                     const uint32_t acc = tmem + lanes + buf * (kTmemCols / 2);
                     tmem_ld64(acc + column(2 * b), acc + column(2 * b + 1), o);
                 };
-                const int chunk = t.kind == kLogits ? kChunk : t.k1 - t.k0;
+                const int chunk = chunk_of<MODE>(t.kind);
                 float v[64], next[64];
                 load(0, v);
                 load(1, next);
