@@ -517,7 +517,11 @@ LHS_API int lhs_loss(const lhs_table *t, const void *d_x, int32_t x_dtype, int64
  * accumulate once more for what dtable held, if it is of 16 bits).  Positions
  * that take part with an lse or dloss that is not finite set
  * LHS_ERRBIT_NONFINITE and make what they reach NaN; results beyond the range
- * of f16 are +-inf.  tokens == 0 clears dtable
+ * of f16 are +-inf.  The one scale of an f16 call is that of its largest |dloss|:
+ * entries of g below 2^-29 of that are subnormal and those below 2^-40 are 0, in
+ * dx too, although its rows do not depend on one another (the targets' entries
+ * of more than 128 positions excepted).  Positions whose dloss are further apart
+ * than that belong into calls of their own, which accumulate.  bf16 has f32's range.  tokens == 0 clears dtable
  * (unless accumulate).  Ranges, errors and determinism as lhs_loss. */
 LHS_API int lhs_loss_grad_workspace(const lhs_table *t, int64_t tokens, size_t *bytes);
 LHS_API int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t x_stride,

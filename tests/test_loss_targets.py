@@ -116,3 +116,30 @@ def test_added_to_what_the_gradient_held(h, out):
     ref = r["dw"] + base.double()
     within(got, ref, dw_tol + 2.0 ** -23 * r["dw"].abs() + rounding(ref, out) * 1.01)
     assert int(err.item()) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", [90, 300])
+def test_upstream_gradients_far_apart(t):
+    """bf16: every row of dx is as accurate as if it stood alone, whatever the others' dloss.  f16: down to
+    2^-40 of the largest |dloss| (test_loss's 2^-39, doubled for what is cut off), in whose units a row is
+    off; the targets' entries of more than 128 positions are not."""
+    v, h = 700, 64
+    step = 2.0 ** -(torch.arange(t) % 46).float().cuda()
+    for dtype in HALF:
+        w, x, y, _ = make(t, v, h, dtype, masked=0.1)
+        r, dx_tol, dw_tol = bounds(w, x, y, step)
+        on = r["on"]
+        tab = table_of(w)
+        _, lse, err = lhs.lhs_loss(tab, x, y)
+        dx, dw = torch.empty((t, h), device="cuda"), torch.empty((v, h), device="cuda")
+        lhs.lhs_loss_grad(tab, x, y, lse, step, dx=dx, dtable=dw, err=err)
+        within(dx[on], r["dx"], dx_tol)
+        within(dw, r["dw"], dw_tol)
+        assert int(err.item()) == 0
+        if t > 128:  # what is left of a row that f16's g has lost: the target's part
+            far = on & (step < 2.0 ** -41)
+            alone = (torch.exp(-r["loss"]) - 1)[:, None] * step[on].double()[:, None] * w[y[on].long()].double()
+            here = (step[on] < 2.0 ** -41)
+            assert dtype == torch.bfloat16 or bool((dx[far].double() - alone[here]).abs().max() <= 2.0 ** -12 * alone[here].abs().max())
+            assert bool((dx[far] != 0).any())
