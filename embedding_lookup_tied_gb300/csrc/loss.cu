@@ -492,50 +492,6 @@ cudaError_t launch_pack(const LossArgs &a, const LossPlan &p, const DeviceInfo &
 
 }  // namespace
 
-namespace {
-
-// Pieces: small ones leave g and the table's rows in L2 between the logits and the
-// products, but add dx up more often and make pairs wait for one another more.  At
-// 8,192 x 151,936 x 896 under the power cap: 3 pieces 4.55 ms, 6 4.61, 10 4.54, 20
-// 4.42, 40 4.60, 80 4.68.  Where logits are few, pieces are at least two waves of tiles
-// (256 x 262,144 x 5,120: 4 pieces 1.45 ms, 10 1.48, 16 1.51; 1 x 151,936 x 896: 4
-// pieces 204 us, 10 249).
-constexpr int64_t kPieces = 18;
-constexpr int64_t kPieceBytes = 512ll << 20;  // of g, at most, as several pieces' is kept
-constexpr int kAhead = 3;
-constexpr int kPairs = 76;                    // of CTAs that run at once
-
-void choose_pieces(LossPlan *p) {
-    const int64_t tiles = p->Tpad / kLossTile * p->vt;
-    int64_t n = tiles / (2 * kPairs) < kPieces ? tiles / (2 * kPairs) : kPieces;
-    const int64_t least = (2 * p->Tpad * p->V + kPieceBytes - 1) / kPieceBytes;
-    if (n < least) n = least;
-    if (n > (p->vt + 1) / 2) n = (p->vt + 1) / 2;  // two tiles' rows at least
-    if (n < 1) n = 1;
-    p->piece = round_up((p->V + n - 1) / n, kLossTile);
-    p->pieces = static_cast<int>((p->V + p->piece - 1) / p->piece);
-    p->part_pitch = static_cast<int32_t>(round_up(p->H, 4));
-    const int64_t blocks = p->Tpad / kLossTile, gt = p->piece / kLossTile, ht = (p->H + kLossTile - 1) / kLossTile;
-    const int64_t kh = (p->H + 63) / 64, kp = (p->V < p->piece ? p->V + 63 : p->piece) / 64;
-    const int64_t share = (blocks * gt * kh + blocks * ht * kp + gt * ht * (p->Tpad / 64)) / kPairs + 1;
-    // a tile of dx takes no longer than a share; the logits run ahead of the products by the pieces
-    // that their tiles take
-    const int64_t most = share > 16 ? share : 16;
-    int64_t splits = (kp + most - 1) / most;
-    if (splits > 32) splits = 32;
-    if (splits > kp) splits = kp;
-    p->splits = static_cast<int>(splits < 1 ? 1 : splits);
-    const int64_t ahead = kAhead + kh / share;
-    p->ahead = static_cast<int>(ahead < 6 ? ahead : 6);
-    if (p->ahead > p->pieces) p->ahead = p->pieces;
-    p->slots = p->ahead + 2 < p->pieces ? p->ahead + 2 : p->pieces;
-    // the queue, two counters to a piece, a word to each warp's part of dx's sums
-    p->n_sync = 1 + 2ll * p->pieces + blocks * ht * p->splits * kLossSyncWarps;
-    p->items = blocks * p->vt + p->pieces * blocks * ht * p->splits + p->vt * ht;
-}
-
-}  // namespace
-
 LossPlan plan_loss(const lhs_table &t, int64_t tokens, bool grad) {
     LossPlan p = {};
     p.T = tokens;
@@ -564,6 +520,7 @@ LossPlan plan_loss(const lhs_table &t, int64_t tokens, bool grad) {
         p.off_zt = take(p.Tpad * 4);
     } else {
         choose_pieces(&p);
+        p.part_pitch = static_cast<int32_t>(round_up(p.H, 4));
         p.off_sync = take(p.n_sync * 4);
         p.off_pos = take(p.T * 4);
         p.off_lse = take(p.Tpad * 4);

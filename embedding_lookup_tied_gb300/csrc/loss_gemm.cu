@@ -51,43 +51,20 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kCtaM = 128;                    // rows of a tile that a CTA holds (TMEM lanes)
-constexpr int kTileK = 64;
 constexpr int kBoxBytes = 64 * 64 * 2;        // what one TMA load brings: 64 x 64 values
 constexpr int kOperandBytes = 2 * kBoxBytes;  // a CTA's part of A, or of B, of a stage
 constexpr int kTmemCols = 512;
 constexpr int kStoreBytes = 32 * 128;         // an epilogue warp's store: 32 rows of 128 bytes
-// The tensor cores cut their f32 sums instead of rounding them: each of a step's 17 addends at 2^-25 of
-// the largest.  512 terms of one sign fall short by 2.6e-6 of their sum in f16, whose products have that
-// many bits to lose, and by 2e-7 in bf16; a longer sum by as much for every 512 (hidden 5,376 in one sum: 5.7e-6
-// of the loss; f32 on the CUDA cores 1e-6).  Logits are summed 512 of k at a time, and those sums added up, rounded,
-// in registers: for g as for the statistics, whose lse they are compared with (one long sum for g left
-// a row's probabilities short of 1, always to one side: 6e-5 in bf16 and 8e-4 in f16 for logits
-// of 30, hidden 5,376 and terms of one sign).
-constexpr int kChunk = 512 / kTileK;
-// Sums over positions (dtable) or rows of a piece (dx) are as long as the call is (2^19 positions of one sign in
-// one sum: 1.4e-3 short in bf16, 3.1e-3 in f16), and are cut into longer parts: 2,048 terms of one sign fall
-// short by 1e-5 (f16).  (1,024: 1 x 151,936 x 896, whose dx has 1,216 in a sum, 224 -> 260 us.)
-constexpr int kLongChunk = 2048 / kTileK;
 constexpr int kQueue = 3;                     // items handed out ahead
 
-enum { kLogits = 0, kDx = 1, kDtable = 2 };
-// Stages of a tile whose products make one sum in the tensor cores.
-template <int MODE>
-__device__ __forceinline__ int chunk_of(int kind) {
-    return MODE == 0 || kind == kLogits ? kChunk : kLongChunk;
-}
 enum { kStore16 = 0, kStore32 = 1, kAdd32 = 2, kPlain = 3 };  // how dtable is written
 
-struct Params {
+struct Params : LossShape {
     const LossMeta *meta;
     const int32_t *tgt;
-    int64_t V, Tpad;
-    int H, ht;               // hidden; tiles of it
     float l2;                // log2(e) / temperature
     uint32_t *queue;         // items handed out; 0 at the start
     int32_t *err;
-    int64_t piece;           // rows of a piece, and tiles of them (statistics: one piece)
-    int pieces, piece_tiles, last_tiles;
     float2 *stats;           // statistics
     float *zt;
     float inv_t;             // 1 / temperature
@@ -97,8 +74,6 @@ struct Params {
     const int32_t *slot_of;  // dtable: [V] rows of what it makes there, [tiles] whether there is one; or null
     const float *rows;
     int64_t rows_pitch;
-    bool dx;
-    int ahead, slots, splits;
     uint32_t *g_done;        // [pieces] warps that have written a tile of g
     uint32_t *read_done;     // [pieces] products that have read it
     uint32_t *dx_done;       // [tiles of dx x splits x kLossSyncWarps] pieces added up
@@ -119,17 +94,6 @@ struct Conf {
     static constexpr int kOutBuffers = 1;
 };
 
-// A tile to work on, as the scheduler hands it out.
-struct alignas(16) Item {
-    int kind;     // -1: the end
-    int piece;
-    int m;        // tile of M: block of tokens, or of the piece's rows
-    int n;        // tile of N: of the piece's rows (logits), or of hidden
-    int split;    // dx; dtable: whether a row of the tile is a target
-    int k0, k1;   // stages
-    int width;    // N of the MMAs, a multiple of 32
-};
-static_assert(sizeof(Item) == 32, "two words of 16 bytes");
 
 template <int MODE>
 struct Smem {
@@ -363,146 +327,6 @@ __device__ __forceinline__ void put_piece(uint8_t *buf, int r, int i, uint32_t x
 }
 
 // ---------------------------------------------------------------------------
-// items
-// ---------------------------------------------------------------------------
-// The queue: g of the first `ahead` pieces; then each piece's products, dx first,
-// followed by g of the piece `ahead` of it.
-// Quotients of numbers below 2^31: with 2^(l-1) < d <= 2^l and mul = ceil(2^(31+l) / d), which is
-// below 2^32, n mul / 2^(31+l) exceeds n / d by less than n / 2^(31+l) < 1 / d.
-struct Divisor {
-    uint32_t d, mul, shift;
-    __device__ __forceinline__ void set(uint32_t d_) {
-        d = d_;
-        uint32_t l = 0;
-        while (l < 31 && (1u << l) < d) ++l;
-        shift = 31 + l;
-        mul = static_cast<uint32_t>(((1ull << shift) + d - 1) / d);
-    }
-    __device__ __forceinline__ uint32_t of(uint32_t n) const {
-        return static_cast<uint32_t>((static_cast<uint64_t>(n) * mul) >> shift);
-    }
-};
-struct Work {
-    uint32_t blocks, total;
-    int token_stages;     // k of dtable
-    int turn, gap;        // from stage `turn` on, tokens lie `gap` rows further on (the second terms)
-    uint32_t before;      // g of the first pieces
-    Divisor block, head, period, ht, splits;  // what the scheduler divides by
-};
-__device__ __forceinline__ int tiles_of(const Params &p, int piece) {
-    return piece + 1 < p.pieces ? p.piece_tiles : p.last_tiles;
-}
-__device__ __forceinline__ int stages_of(const Params &p, int piece) {
-    const int64_t rows = piece + 1 < p.pieces ? p.piece : p.V - piece * p.piece;
-    return static_cast<int>((rows + kTileK - 1) / kTileK);
-}
-__device__ __forceinline__ int splits_of(const Params &p, int piece) {
-    const int stages = stages_of(p, piece);
-    return p.splits < stages ? p.splits : stages;
-}
-__device__ __forceinline__ uint32_t n_dx_of(const Params &p, const Work &w, int piece) {
-    return p.dx ? w.blocks * p.ht * splits_of(p, piece) : 0u;
-}
-__device__ __forceinline__ uint32_t n_products_of(const Params &p, const Work &w, int piece) {
-    return n_dx_of(p, w, piece) + (p.dtable ? static_cast<uint32_t>(tiles_of(p, piece)) * p.ht : 0u);
-}
-template <int MODE>
-__device__ __forceinline__ Work work_of(const Params &p) {
-    Work w = {};
-    const int count = ld_dep(&p.meta->count);
-    w.blocks = count > 0 ? (static_cast<uint32_t>(count) + kLossTile - 1) / kLossTile : 1u;
-    w.token_stages = count > 0 ? (count + kTileK - 1) / kTileK : 1;  // (without any position one of zeros)
-    w.turn = w.token_stages;
-    if (MODE == 1 && count <= kLossTwin) {
-        w.gap = kLossTwin - w.turn * kTileK;
-        w.token_stages *= 2;
-    }
-    w.total = w.blocks * (static_cast<uint32_t>(p.pieces - 1) * p.piece_tiles + p.last_tiles);
-    if (MODE == 1) {
-        w.before = p.ahead < p.pieces ? w.blocks * p.ahead * p.piece_tiles : w.total;
-        w.total += static_cast<uint32_t>(p.pieces - 1) * n_products_of(p, w, 0) + n_products_of(p, w, p.pieces - 1);
-    }
-    return w;
-}
-template <int MODE>
-__device__ __forceinline__ void set_divisors(const Params &p, Work &w) {
-    w.block.set(w.blocks);
-    if (MODE == 1) {
-        w.head.set(w.blocks * p.piece_tiles);
-        w.period.set(n_products_of(p, w, 0) + w.blocks * p.piece_tiles);
-        w.ht.set(p.ht);
-        w.splits.set(p.splits);
-    }
-}
-__device__ __forceinline__ int width_of(int H, int tile) {
-    const int left = H - tile * kLossTile;
-    return left >= kLossTile ? kLossTile : (left + 31) / 32 * 32;
-}
-template <int MODE>
-__device__ __forceinline__ Item item_of(const Params &p, const Work &w, uint32_t i) {
-    Item t = {};
-    bool logits = true;
-    if (MODE == 1) {
-        if (i < w.before) {
-            t.piece = w.head.of(i);
-            i -= t.piece * w.head.d;
-        } else {
-            i -= w.before;
-            // pieces whose products, and the logits that follow them, are whole
-            const int whole = p.pieces - p.ahead - 1;
-            int q = 0;
-            if (whole > 0) {
-                q = static_cast<int>(w.period.of(i));
-                q = q < whole ? q : whole;
-                i -= q * w.period.d;
-            }
-            for (;; ++q) {  // a few steps at the end
-                const uint32_t nq = n_products_of(p, w, q);
-                if (i < nq) {
-                    t.piece = q;
-                    logits = false;
-                    break;
-                }
-                i -= nq;
-                const uint32_t g = q + p.ahead < p.pieces ? w.blocks * tiles_of(p, q + p.ahead) : 0u;
-                if (i < g) {
-                    t.piece = q + p.ahead;
-                    break;
-                }
-                i -= g;
-            }
-        }
-    }
-    if (logits) {
-        t.kind = kLogits;
-        t.n = w.block.of(i);
-        t.m = i - t.n * w.blocks;
-        t.k1 = (p.H + kTileK - 1) / kTileK;
-        t.width = kLossTile;
-        return t;
-    }
-    const uint32_t n_dx = n_dx_of(p, w, t.piece);
-    t.kind = i < n_dx ? kDx : kDtable;
-    if (i >= n_dx) i -= n_dx;
-    const uint32_t above = w.ht.of(i);
-    t.n = i - above * p.ht;
-    t.width = width_of(p.H, t.n);
-    if (t.kind == kDx) {
-        const int splits = splits_of(p, t.piece), stages = stages_of(p, t.piece);
-        const bool same = splits == p.splits;  // but perhaps in the last piece
-        t.m = same ? w.splits.of(above) : above / splits;
-        t.split = above - t.m * splits;
-        // (stages * splits stays far below 2^31: pieces are rows below 2^31 / 64 stages, splits at most 32)
-        t.k0 = same ? w.splits.of(stages * t.split) : stages * t.split / splits;
-        t.k1 = same ? w.splits.of(stages * (t.split + 1)) : stages * (t.split + 1) / splits;
-    } else {
-        t.m = above;
-        t.k1 = w.token_stages;
-    }
-    return t;
-}
-
-// ---------------------------------------------------------------------------
 // kernel
 // ---------------------------------------------------------------------------
 template <int MODE, bool BF>
@@ -545,7 +369,7 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
     cluster_sync_all();  // the peer's barriers exist
     const uint32_t tmem = sm.tmem_base;
     pdl_wait();
-    const Work work = work_of<MODE>(p);
+    const Work work = work_of<MODE>(p, ld_dep(&p.meta->count));
 
     // The next item, for one role (a warp, or the producer's lane); kind -1 at the end or after an abort.
     int slot = 0;
@@ -1169,10 +993,7 @@ bool common(const LossArgs &a, const LossPlan &p, Maps *m, Params *k) {
     m->g = m->g_out = m->part = m->dt = m->x;  // replaced where they are used
     k->meta = reinterpret_cast<const LossMeta *>(a.ws + p.off_meta);
     k->tgt = reinterpret_cast<const int32_t *>(a.ws + p.off_tgt);
-    k->V = p.V;
-    k->Tpad = p.Tpad;
-    k->H = p.H;
-    k->ht = (p.H + kLossTile - 1) / kLossTile;
+    shape_of(p, p.grad, a.dx != nullptr, a.dtable != nullptr, k);
     k->l2 = kLog2e * a.inv_temperature;
     k->queue = reinterpret_cast<uint32_t *>(a.ws + p.off_sync);
     k->err = a.err;
@@ -1185,9 +1006,6 @@ cudaError_t launch_loss_stats(const LossArgs &a, const LossPlan &p, cudaStream_t
     Maps m;
     Params k = {};
     if (!common(a, p, &m, &k)) return cudaErrorInvalidValue;
-    k.piece = p.V;
-    k.pieces = 1;
-    k.piece_tiles = k.last_tiles = static_cast<int>(p.vt);
     k.stats = reinterpret_cast<float2 *>(a.ws + p.off_stats);
     k.zt = reinterpret_cast<float *>(a.ws + p.off_zt);
     const uint32_t items = static_cast<uint32_t>(p.Tpad / kLossTile * p.vt);
@@ -1209,7 +1027,6 @@ cudaError_t launch_loss_products(const LossArgs &a, const LossPlan &p, cudaStrea
         k.rows = reinterpret_cast<const float *>(a.ws + p.off_rows);
         k.rows_pitch = p.rows_pitch;
     }
-    k.dx = a.dx != nullptr;
     k.dtable = a.dtable;
     k.dt_dtype = a.dtable_dtype;
     k.accumulate = a.accumulate;
@@ -1232,13 +1049,6 @@ cudaError_t launch_loss_products(const LossArgs &a, const LossPlan &p, cudaStrea
     if (!make_box(&m.g, dt, a.ws + p.off_g, p.piece, g_rows, pitch, 64, 64) ||
         !make_box(&m.g_out, dt, a.ws + p.off_g, p.piece, g_rows, pitch, 64, 32))
         return cudaErrorInvalidValue;
-    k.piece = p.piece;
-    k.pieces = p.pieces;
-    k.piece_tiles = static_cast<int>(p.piece / kLossTile);
-    k.last_tiles = static_cast<int>((p.V - (p.pieces - 1) * p.piece + kLossTile - 1) / kLossTile);
-    k.ahead = p.ahead;
-    k.slots = p.slots;
-    k.splits = p.splits;
     k.g_done = k.queue + 1;
     k.read_done = k.g_done + p.pieces;
     k.dx_done = k.read_done + p.pieces;

@@ -6,25 +6,9 @@
 #include <cuda_bf16.h>
 
 #include "decode.cuh"
+#include "loss_queue.cuh"
 
 namespace lhs {
-
-constexpr int kLossTile = 256;      // tokens, and vocabulary rows, of a tile of logits
-constexpr int kLossSyncWarps = 16;  // warps of a pair of CTAs that take a tile out
-constexpr int kLossParts = 2;       // parts of a tile's columns with statistics of their own
-
-inline int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
-
-// Up to this many positions, g is held in two 16-bit terms: a tile has as many rows again, which
-// would be empty, and they hold what the first term's rounding left.
-constexpr int kLossTwin = kLossTile / 2;
-// Of more positions g is one term, and its entries at the targets are kept apart in f32: they carry nearly all
-// of the gradient (the other entries of a position add up to as much, spread over the vocabulary), and a
-// frequent target's row of the table's gradient is a sum of many of them, with different signs.  Their
-// products with x and with the table are sums over the positions alone (dtable: T rows by target, dx:
-// a row each).  256 x 262,144 x 5,120 bf16, targets as in natural text: largest error of dtable in units
-// of max(|element|, rms) 1.05 -> 0.0078, error in norm 2.3e-3 -> 1.66e-3, one rounding of the result.  Its
-// price: 1.47 -> 1.51 ms (8,192 x 151,936 x 896 3.83 -> 3.90, 628 positions 0.50 -> 0.53).
 
 // What one call needs to know on the device, written by its first kernel.
 struct LossMeta {
@@ -35,10 +19,9 @@ struct LossMeta {
 
 // Workspace of one call.  The positions that take part are numbered 0 .. count
 // in their order ("compact"); rows of x that do not are never read again.
-struct LossPlan {
-    int64_t T, Tpad;        // positions; rounded up to whole tiles (one at least)
-    int64_t V, vt;          // vocabulary rows; tiles of them
-    int32_t H, Hp;          // hidden; rounded up to 8 (rows of whole 16-byte words)
+struct LossPlan : LossQueue {
+    int64_t T;              // positions
+    int32_t Hp;             // hidden rounded up to 8 (rows of whole 16-byte words)
     bool bf16, grad;
     size_t off_meta;        // LossMeta
     size_t off_act;         // int32 [Tpad]: position of a compact row, -1 past count
@@ -46,7 +29,6 @@ struct LossPlan {
     size_t off_x;           // [Tpad x Hp]: its residual, zeros past hidden and count
     size_t off_w;           // [V x Hp]: the table, where its rows are not whole 16-byte words
     size_t off_sync;        // uint32 [n_sync]: what CTAs tell one another; 0 at the start
-    int64_t n_sync;
     // loss
     size_t off_stats;       // float2 [vt x kLossParts x Tpad]: maximum of a part, sum of its other exponentials
     size_t off_zt;          // f32 [Tpad]: the target's logit
@@ -63,11 +45,6 @@ struct LossPlan {
     int64_t rows_pitch;     // hidden rounded up to a block of a tile's columns
     size_t off_g;           // [slots x Tpad x piece]: g of a piece of the vocabulary
     size_t off_part;        // f32 [splits x Tpad x part_pitch]: dx so far
-    int64_t piece;          // vocabulary rows of a piece, a multiple of kLossTile
-    int pieces;
-    int ahead, slots;       // pieces whose logits precede a piece's products; whose g is kept
-    int64_t items;          // tiles of all products
-    int splits;             // dx's sums are split along a piece's rows
     int32_t part_pitch;     // hidden rounded up to 4
     size_t bytes;
 };
