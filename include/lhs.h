@@ -536,8 +536,8 @@ LHS_API int lhs_loss_grad(const lhs_table *t, const void *d_x, int32_t x_dtype, 
  * the entry itself where the loss is 1e-6).  Given what lhs_loss gave for the same
  * call, g[t][y_t] is (exp(-loss[t]) - 1) * dloss[t] / temperature, which keeps its
  * relative accuracy.
- *   d_loss : f32 [tokens], or NULL: as lhs_loss_grad.  One that is not finite sets
- *            LHS_ERRBIT_NONFINITE. */
+ *   d_loss : f32 [tokens], or NULL: as lhs_loss_grad.  One that is NaN or -inf sets
+ *            LHS_ERRBIT_NONFINITE, as lse and dloss do. */
 LHS_API int lhs_loss_grad_of(const lhs_table *t, const void *d_x, int32_t x_dtype, int64_t x_stride,
                              int64_t tokens, const int32_t *d_targets, int32_t ignore,
                              float temperature, const float *d_loss, const float *d_lse,

@@ -16,7 +16,7 @@ import pytest
 import torch
 
 import embedding_lookup_tied_gb300 as lhs
-from test_loss import table_of
+from test_loss import make, table_of, within
 
 pytestmark = pytest.mark.gpu
 HALF = [torch.bfloat16, torch.float16]
@@ -97,4 +97,37 @@ def test_probabilities_sum_to_one(h, dtype, temperature):
     assert off <= tol, (off, tol)
     off, tol = float(dx[:, 7].abs().max()), (own + 3 * 2.0 ** -18 + 2.0 ** -21) / temperature
     assert off <= tol, (off, tol)
+    assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=str)
+@pytest.mark.parametrize("t,v,h", [(100, 3000, 5376), (300, 2000, 5376), (260, 9000, 2000), (150, 700, 1033)])
+def test_random_long_rows(t, v, h, dtype):
+    """Loss and gradients of values of both signs, with the logits' bound above (A the sum of magnitudes, for
+    the running sum stays below it), and the rest as in test_loss_targets."""
+    w, x, y, dl = make(t, v, h, dtype, exact=False)
+    W, X = w.double(), x.double()
+    z = X @ W.T
+    d = dz(h, float((X.abs() @ W.abs().T).max()))
+    on = y >= 0
+    n = torch.logsumexp(z, 1, keepdim=True)
+    at = y.clamp(min=0).long()[:, None]
+    want = (n - z.gather(1, at))[:, 0]
+    tab = table_of(w)
+    loss, lse, err = lhs.lhs_loss(tab, x, y)
+    tol = 2 * d + 2.0 ** -18 + (128 + v / 128) * 2.0 ** -24 + 2.0 ** -22 * z.abs().amax(1)
+    assert bool(((loss.double() - want).abs() <= tol)[on].all())
+    dx, dw = torch.empty((t, h), device="cuda"), torch.empty((v, h), device="cuda")
+    lhs.lhs_loss_grad(tab, x, y, lse, dl, dx=dx, dtable=dw, err=err)
+    dd = dl.double()[:, None] * on[:, None]
+    p = torch.exp(z - n)
+    g = (p - torch.zeros_like(p).scatter_(1, at, 1.0)) * dd
+    u = torch.finfo(dtype).eps / 2
+    dp = 2 * d + 2.0 ** -17 + (128 + v / 128) * 2.0 ** -24
+    few = int(on.sum()) <= 128
+    dg = ((u * u if few else u) + dp) * p * dd.abs() + float(dl.abs().max()) * 2.0 ** -39
+    pt = p.gather(1, at)
+    dg.scatter_(1, at, ((dp + u * u) * pt + (2.0 ** -22 + (u * u if few else 0.0)) * (1 - pt)) * dd.abs() + float(dl.abs().max()) * 2.0 ** -39)
+    within(dx, g @ W, dg @ W.abs() + v * 2.0 ** -23 * (g.abs() @ W.abs()))
+    within(dw, g.T @ X, dg.T @ X.abs() + (t + 2) * 2.0 ** -23 * (g.abs().T @ X.abs()))
     assert int(err.item()) == 0
