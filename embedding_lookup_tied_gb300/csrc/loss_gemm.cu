@@ -708,11 +708,12 @@ __global__ void __launch_bounds__(Conf<MODE>::kThreads, 1)
                         equal = 0;
                         m = top;
                     }
-                    const float shift = m == -INFINITY ? 0.0f : -m * p.l2;
+                    // (the difference first: m log2(e) by itself would be rounded to 2^-24 of itself, which is an
+                    // error of all exponentials but the maximum's alike)
                     float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        const float e = ex2(fmaf(v[k], p.l2, shift));
+                        const float e = ex2((v[k] - m) * p.l2);
                         if (v[k] == m) ++equal;
                         else s4[k & 3] += e;
                     }

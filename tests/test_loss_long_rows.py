@@ -131,3 +131,28 @@ def test_random_long_rows(t, v, h, dtype):
     within(dx, g @ W, dg @ W.abs() + v * 2.0 ** -23 * (g.abs() @ W.abs()))
     within(dw, g.T @ X, dg.T @ X.abs() + (t + 2) * 2.0 ** -23 * (g.abs().T @ X.abs()))
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("temperature", [1.0, 0.5])
+@pytest.mark.parametrize("top", [8.0, 250.0, 1000.0])
+@pytest.mark.parametrize("dtype", HALF, ids=str)
+def test_loss_of_large_logits(dtype, top, temperature):
+    """Logits top - 0, 0.5, .. 3.5, exact in f32: the loss depends on their differences alone, and is as good
+    where they are far from 0.  An exponential is good to 2^-21, its argument (a difference, scaled) to
+    2^-23 of up to 7 log2(e) in its value, their sum to 48 2^-24 (128 in four, blocks, tiles and parts), the
+    logarithm to 2^-22 of itself.  (Exponentials of z and of the maximum scaled apart: 2^-24 of
+    1,443, 6e-5, at 1,000.)"""
+    v, t, h = 3001, 9, 72
+    w = torch.zeros((v, h), dtype=dtype, device="cuda")
+    w[:, 0], w[:, 1] = 1.0, -(torch.arange(v, device="cuda") % 8 * 0.25)
+    x = torch.zeros((t, h), dtype=dtype, device="cuda")
+    x[:, 0], x[:, 1] = top, 2.0
+    y = torch.arange(t, dtype=torch.int32, device="cuda") + 5
+    loss, lse, err = lhs.lhs_loss(table_of(w), x, y, temperature=temperature)
+    z = x.double() @ w.double().T / temperature
+    want = torch.logsumexp(z - z[0, 0], 1) - (z.gather(1, y.long()[:, None])[:, 0] - z[0, 0])
+    tol = 2.0 ** -21 + 7 * 1.45 / temperature * 2.0 ** -23 + 48 * 2.0 ** -24 + 2.0 ** -22 * 16
+    off = float((loss.double() - want).abs().max())
+    assert off <= tol, (off, tol)
+    assert float((lse.double() - torch.logsumexp(z, 1)).abs().max()) <= tol + 2.0 ** -23 * (top / temperature + 8)
+    assert int(err.item()) == 0
