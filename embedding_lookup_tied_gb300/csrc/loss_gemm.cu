@@ -28,17 +28,17 @@
 // other exponentials) of each token, g as 16-bit values that the products read
 // back from L2 or HBM; of up to 128 tokens in two terms, the second in the rows of the
 // tile's other half, with the residuals there too, so that both products add them up.
-// Of more positions the targets' entries are kept apart in f32 (train.cuh): g holds what a
+// Of more positions the targets' entries are kept apart in f32 (loss_queue.cuh): g holds what a
 // logit of the tensor cores makes of one beyond that, and a tile of dtable adds the sums of
 // its targets' rows before it rounds.
 //
 // What bounds it.  Many tokens: the tensor cores and the power cap.  8,192 x
-// 151,936 x 896: statistics 1.24 ms (1,800 TFLOP/s; 1,660 for seconds on end),
-// gradient 3.8 to 4.1 ms (1,630 to 1,770; 1,515 for seconds on end, where a
-// library product of the same shape does 1,597); 2,048 x 262,144 x 5,376: 3.1 ms
-// (1,880).  256 x 262,144 x 5,120: 1.46 ms for 1.18 at the sustained rate; the
+// 151,936 x 896: statistics 1.21 ms (1,840 TFLOP/s; 1,660 for seconds on end),
+// gradient 3.95 to 4.2 ms with its small kernels (1,590 to 1,690; 1,496 for seconds on end, where
+// a library product of the same shape does 1,636); 2,048 x 262,144 x 5,376: 3.05 ms
+// (1,890).  256 x 262,144 x 5,120: 1.56 ms for 1.18 at the sustained rate; the
 // table is read twice and its gradient written, 1.2 ms of HBM.  One token, 151,936 x
-// 896: statistics 49 us, 5.6 TB/s; gradient 195 us for 80: reading the table twice,
+// 896: statistics 49 us, 5.6 TB/s; gradient 196 us for 80: reading the table twice,
 // and taking 2,376 tiles of its gradient out.
 #include <mutex>
 #include <type_traits>

@@ -29,7 +29,6 @@ constexpr int kLossTwin = kLossTile / 2;
 // a row each).  256 x 262,144 x 5,120 bf16, targets as in natural text: largest error of dtable in units
 // of max(|element|, rms) 1.05 -> 0.0078, error in norm 2.3e-3 -> 1.66e-3, one rounding of the result.  Its
 // price: 1.47 -> 1.51 ms (8,192 x 151,936 x 896 3.83 -> 3.90, 628 positions 0.50 -> 0.53).
-
 constexpr int kTileK = 64;          // of k of a stage
 // The tensor cores cut their f32 sums instead of rounding them: each of a step's 17 addends at 2^-25 of
 // the largest.  512 terms of one sign fall short by 2.6e-6 of their sum in f16, whose products have that
